@@ -40,6 +40,8 @@ MOE_BIAS_SIGN = 0
 MOE_BIAS_PROPORTIONAL = 1
 MOE_SCALE_ROW = 0
 MOE_SCALE_BLOCK128 = 128
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP32 = 1
 MOE_PAYLOAD_BF16 = 0
 MOE_PAYLOAD_FP8_ROW = 1
 MOE_PAYLOAD_FP8_BLOCK128 = 2
@@ -60,6 +62,7 @@ EXPORTED = [
     "moe_validate_pools_workspace_size", "moe_validate_pools",
     "moe_validate_compact_workspace_size", "moe_validate_compact", "moe_debug_wait_timeout",
     "moe_decode_workspace_size", "moe_decode_layer",
+    "moe_add_rms_norm", "moe_add_rms_norm_backward_workspace_size", "moe_add_rms_norm_backward",
 ]
 
 
@@ -79,6 +82,16 @@ class PoolParams(ctypes.Structure):
     _fields_ = [("n_dest", ctypes.c_int32), ("local_per_dest", ctypes.c_int32),
                 ("n_waves", ctypes.c_int32), ("pool_cap", ctypes.c_int32),
                 ("wave_policy", ctypes.c_int32)]
+
+
+class NormParams(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("d", ctypes.c_int32),
+                ("x_type", ctypes.c_int32), ("residual_type", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+    def __init__(self, n, d, x_stride=None, x_type=0, residual_type=0, group=0, eps=1e-6):
+        super().__init__(n, d if x_stride is None else x_stride, d, x_type, residual_type, group,
+                         eps)
 
 
 _P = ctypes.c_void_p
@@ -148,6 +161,10 @@ _SIGS = {
     "moe_validate_compact": (_I32, [_I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P,
                                     _P]),
     "moe_debug_wait_timeout": (_I32, [_I64, _P, _P]),
+    "moe_add_rms_norm": (_I32, [ctypes.POINTER(NormParams)] + [_P] * 10),
+    "moe_add_rms_norm_backward_workspace_size": (_SZ, [ctypes.POINTER(NormParams)]),
+    "moe_add_rms_norm_backward": (_I32, [ctypes.POINTER(NormParams), _I32] + [_P] * 9 +
+                                  [_SZ, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -534,3 +551,24 @@ def moe_debug_wait_timeout(limit_ns, dev_status, stream=None):
     _check("moe_debug_wait_timeout", lib().moe_debug_wait_timeout(
         int(limit_ns), _ptr(dev_status), _stream(stream)))
     _count(1)
+
+
+def moe_add_rms_norm(p: NormParams, x, residual, weight, residual_out, y, q=None, scales=None,
+                     rstd=None, dev_status=None, stream=None):
+    _check("moe_add_rms_norm", lib().moe_add_rms_norm(
+        ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y),
+        _ptr(q), _ptr(scales), _ptr(rstd), _ptr(dev_status), _stream(stream)))
+    _count(1 if p.n > 0 else 0)
+
+
+def moe_add_rms_norm_backward_workspace_size(p: NormParams) -> int:
+    return lib().moe_add_rms_norm_backward_workspace_size(ctypes.byref(p))
+
+
+def moe_add_rms_norm_backward(p: NormParams, dy_type, dy, h, weight, rstd, dresidual_out, dx,
+                              dresidual, dweight, ws, ws_bytes, stream=None):
+    _check("moe_add_rms_norm_backward", lib().moe_add_rms_norm_backward(
+        ctypes.byref(p), dy_type, _ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd),
+        _ptr(dresidual_out), _ptr(dx), _ptr(dresidual), _ptr(dweight), _ptr(ws), ws_bytes,
+        _stream(stream)))
+    _count(0 if p.n == 0 else (2 if dweight is not None else 1))

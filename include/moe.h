@@ -656,6 +656,67 @@ moe_status moe_validate_compact(int32_t n_src, int32_t pool_cap, int32_t d, int3
                                 void* ws, size_t ws_bytes, uint32_t* dev_status,
                                 moe_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Residual addition and RMS norm in front of the layer                     */
+/* ------------------------------------------------------------------------ */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP32 = 1 };
+
+typedef struct {
+  int64_t n;             /* rows (tokens)                                          */
+  int64_t x_stride;      /* elements from one row of x to the next (>= d)          */
+  int32_t d;             /* values per row                                         */
+  int32_t x_type;        /* MOE_DTYPE_* of x (and of its gradient dx)              */
+  int32_t residual_type; /* MOE_DTYPE_* of the residual stream and its gradient    */
+  int32_t group;         /* scale group of the codes: MOE_SCALE_ROW / _BLOCK128    */
+  float eps;             /* > 0                                                    */
+} moe_norm_params;
+
+/* The residual addition and root-mean-square norm that make the layer's input
+ * rows, in one pass over each row:
+ *   h    = round_to(residual_type, x + residual)      (residual NULL: h = x)
+ *   rstd = 1 / sqrt(mean(h^2) + eps)                  (fp32, of the rounded h)
+ *   v    = (h * rstd) * weight                        (fp32, weight fp32 [d])
+ *   y    = bf16(v)                                    the router's / bf16 experts' rows
+ *   q    = E4M3(fp32(v / s)), s = fp32(amax / 448)    the dispatch payload of
+ * moe_quantize_fp8's scale rule (a zero group has s = 1), taken from the unrounded
+ * v: q [n, d], scales [n, 1] or [n, ceil(d/128)] by `group`.
+ * x is [n, d] with row stride x_stride, residual / residual_out / y / q [n, d]
+ * contiguous.  y may be NULL, and q and scales may both be NULL, but not all
+ * three; rstd [n] may be NULL (the backward needs it); residual_out may be NULL
+ * when residual is (then residual_type must equal x_type).  residual_out may be
+ * residual itself: a row is read before it is written.  Otherwise outputs must
+ * not overlap inputs.
+ * A NaN or Inf in a quantized row sets MOE_DEV_NONFINITE_INPUT (its codes are then
+ * unspecified); without q it only propagates.  Squares are summed in fp32: values
+ * beyond about 1e18 overflow the sum and give y = 0.
+ * Limits: d % 8 == 0 (16 with q), d <= 16384, x_stride % 8 == 0, 16-byte aligned
+ * pointers (4 for scales and rstd).  n = 0 does nothing.                       */
+moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, const void* residual,
+                            const float* weight, void* residual_out, moe_bf16* y, moe_fp8* q,
+                            float* scales, float* rstd, uint32_t* dev_status,
+                            moe_stream_t stream);
+
+/* Its backward.  From dy [n, d] (dy_type; the gradient of v: through the bf16 and
+ * E4M3 roundings it passes unchanged), h [n, d] (residual_out of the forward, or a
+ * contiguous x when there was no residual; residual_type), rstd [n] and
+ * dresidual_out [n, d] (residual_type; the gradient that reaches residual_out from
+ * its other readers, or NULL):
+ *   u = weight * dy,  xh = h * rstd,
+ *   dh = rstd * (u - xh * mean(u * xh)) + dresidual_out
+ *   dx (x_type) = dresidual (residual_type) = dh, both [n, d] contiguous
+ *   dweight [d] fp32 = sum over rows of dy * xh
+ * in fp32.  Each output may be NULL (not all).  dresidual may be dresidual_out
+ * itself.  dweight is summed in an order fixed by n, d and nothing else: the same
+ * bits on every run.  With dweight, ws holds at least
+ * moe_add_rms_norm_backward_workspace_size() bytes (0 = invalid parameters).
+ * n = 0 writes dweight = 0.  Limits as the forward.                           */
+size_t moe_add_rms_norm_backward_workspace_size(const moe_norm_params* p);
+moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t dy_type, const void* dy,
+                                     const void* h, const float* weight, const float* rstd,
+                                     const void* dresidual_out, void* dx, void* dresidual,
+                                     float* dweight, void* ws, size_t ws_bytes,
+                                     moe_stream_t stream);
+
 /* Self-test of the bounded pipeline wait used by the tensor-core kernels: one
  * CTA initialises an mbarrier that nothing arrives at and waits on it with the
  * same bounded-wait routine, giving up after limit_ns nanoseconds of global
