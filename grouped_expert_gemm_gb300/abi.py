@@ -63,6 +63,7 @@ EXPORTED = [
     "moe_validate_compact_workspace_size", "moe_validate_compact", "moe_debug_wait_timeout",
     "moe_decode_workspace_size", "moe_decode_layer",
     "moe_add_rms_norm", "moe_add_rms_norm_backward_workspace_size", "moe_add_rms_norm_backward",
+    "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward",
 ]
 
 
@@ -165,6 +166,11 @@ _SIGS = {
     "moe_add_rms_norm_backward_workspace_size": (_SZ, [ctypes.POINTER(NormParams)]),
     "moe_add_rms_norm_backward": (_I32, [ctypes.POINTER(NormParams), _I32] + [_P] * 9 +
                                   [_SZ, _P]),
+    "moe_balance_loss_workspace_size": (_SZ, [ctypes.POINTER(RouteParams), _I32]),
+    "moe_balance_loss": (_I32, [ctypes.POINTER(RouteParams), _I32, _P, _P, _P, ctypes.c_float,
+                                _P, _P, _P, _P, _P, _SZ, _P, _P]),
+    "moe_route_backward": (_I32, [ctypes.POINTER(RouteParams), _I32, _P, _P, _P, _P, _P,
+                                  ctypes.c_float, _P, _P, _P, _P, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -572,3 +578,25 @@ def moe_add_rms_norm_backward(p: NormParams, dy_type, dy, h, weight, rstd, dresi
         _ptr(dresidual_out), _ptr(dx), _ptr(dresidual), _ptr(dweight), _ptr(ws), ws_bytes,
         _stream(stream)))
     _count(0 if p.n == 0 else (2 if dweight is not None else 1))
+
+
+def moe_balance_loss_workspace_size(p: RouteParams, n_seq: int) -> int:
+    return lib().moe_balance_loss_workspace_size(ctypes.byref(p), n_seq)
+
+
+def moe_balance_loss(p: RouteParams, n_seq, seq_offsets, logits, topk_ids, alpha, counts,
+                     seq_tokens, mean_probs, loss, ws, ws_bytes, dev_status=None, stream=None):
+    _check("moe_balance_loss", lib().moe_balance_loss(
+        ctypes.byref(p), n_seq, _ptr(seq_offsets), _ptr(logits), _ptr(topk_ids), float(alpha),
+        _ptr(counts), _ptr(seq_tokens), _ptr(mean_probs), _ptr(loss), _ptr(ws), ws_bytes,
+        _ptr(dev_status), _stream(stream)))
+    _count(2)
+
+
+def moe_route_backward(p: RouteParams, n_seq, seq_offsets, logits, topk_ids, gates, dgates, alpha,
+                       counts, seq_tokens, dloss, dlogits, dev_status=None, stream=None):
+    _check("moe_route_backward", lib().moe_route_backward(
+        ctypes.byref(p), n_seq, _ptr(seq_offsets), _ptr(logits), _ptr(topk_ids), _ptr(gates),
+        _ptr(dgates), float(alpha), _ptr(counts), _ptr(seq_tokens), _ptr(dloss), _ptr(dlogits),
+        _ptr(dev_status), _stream(stream)))
+    _count(1 if p.T > 0 else 0)

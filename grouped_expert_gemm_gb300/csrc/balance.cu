@@ -1,0 +1,585 @@
+// The router's balance loss with per-expert counts, and the gradient of its
+// logits (the selected gates' and the loss's in one pass).
+//
+// The auxiliary term over sequences q of L_q live tokens:
+//   p_t = softmax(z_t)            (MOE_SCORE_SOFTMAX)
+//   p_t = sigma(z_t) / sum sigma  (MOE_SCORE_SIGMOID_GROUP)
+//   f_qe = E / (k L_q) n_qe,  P_qe = sum_t p_te / L_q,
+//   loss = alpha / S' sum_q sum_e f_qe P_qe,   S' = sequences with L_q > 0
+// (the counts are constants of the gradient), so with
+//   w_e = dloss alpha / S' f_qe / L_q
+//   dz_te = p_te (w_e - sum_j p_tj w_j) [(1 - sigma_te) for the sigmoid]
+// and for the selected experts, with the gates g_j and their gradients,
+//   softmax: dz = g (dg - <g, dg>)
+//   sigmoid: dz = g (1 - sigma) (dg - <g, dg> / route_scale).
+//
+// Bound: HBM.  One warp holds a token's row in registers, so the logits are read
+// once per pass.  Forward: each block owns a tile of consecutive tokens; its warps
+// keep column sums in registers and the block writes one partial row of sums and
+// counts per sequence that the tile meets, at slot tile + sequence (that index
+// grows by one with every step to the next tile or the next sequence, so no two
+// (tile, sequence) pairs share a slot).  A second launch adds a sequence's slots
+// in order: no floating-point atomics, the same bits every time.
+#include <float.h>
+#include <math.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kMaxE = 512;
+constexpr int kMaxK = 16;
+
+struct BalArgs {
+  int T, E, k, S;
+  int sigmoid;
+  int tile;       // tokens per block
+  int vec4;       // rows may be read 16 bytes at a time
+  float alpha, route_scale;
+  const int32_t* off;  // [S + 1], or nullptr: one sequence of all tokens
+  const float* logits;
+  const int32_t* ids;
+  // forward
+  float* part_sum;     // [slots, E]
+  int32_t* part_cnt;   // [slots, E]
+  int32_t* part_tok;   // [slots]
+  int32_t* ticket;
+  double* part_loss;   // [S, expert blocks]
+  int32_t* counts;     // [S, E]
+  int32_t* tokens;     // [S + 1]
+  float* probs;        // [S, E]
+  float* loss;
+  // backward
+  const float* gates;
+  const float* dgates;
+  const float* dloss;
+  float* dlogits;
+  uint32_t* dev_status;
+};
+
+// Bounds of sequence q, inside [0, T] whatever the array holds.
+__device__ __forceinline__ int seq_bound(const BalArgs& a, int q) {
+  if (a.off == nullptr) return q == 0 ? 0 : a.T;
+  return min(max(__ldg(a.off + q), 0), a.T);
+}
+
+// Last q in [0, S) with bound(q) <= t (0 if there is none).
+__device__ __forceinline__ int seq_of(const BalArgs& a, int t) {
+  int lo = 0, hi = a.S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seq_bound(a, mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void check_offsets(const BalArgs& a) {
+  if (a.off == nullptr || blockIdx.x != 0) return;
+  bool bad = false;
+  for (int q = threadIdx.x; q <= a.S; q += blockDim.x) {
+    const int v = __ldg(a.off + q);
+    bad |= v < 0 || v > a.T || (q > 0 && v < __ldg(a.off + q - 1));
+  }
+  if (bad) report(a.dev_status, MOE_DEV_BAD_MAP);
+}
+
+// The lane's values of one row: expert VEC * (lane + 32 i) + j in v[VEC * i + j];
+// places past E hold -inf.
+template <int VEC, int N>
+__device__ __forceinline__ void load_row(const float* row, int E, int lane, float (&v)[VEC * N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = VEC * (lane + 32 * i);
+    if constexpr (VEC == 4) {
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e < E) f = __ldg(reinterpret_cast<const float4*>(row + e));
+      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+    } else {
+      v[i] = e < E ? __ldg(row + e) : -INFINITY;
+    }
+  }
+}
+
+__device__ __forceinline__ float warp_add(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return x;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
+}
+
+// A row's probabilities in place of its logits; with `slope`, 1 - sigma as well
+// (1 for the softmax).  A NaN logit counts as -inf and +inf as the largest finite
+// value, both reported; a row without a finite logit has probabilities 0.  The
+// sigmoid of an all-negative row is scaled by e^-max before it is normalised, so
+// that its sum cannot underflow.
+template <int M, bool SLOPE>
+__device__ __forceinline__ void row_probs(float (&v)[M], float (&slope)[SLOPE ? M : 1], int sigmoid,
+                                          uint32_t* dev_status) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < M; ++i) bad |= !(v[i] <= FLT_MAX);
+  if (__any_sync(0xFFFFFFFFu, bad)) {
+    if (bad) report(dev_status, MOE_DEV_NONFINITE_LOGIT);
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = isnan(v[i]) ? -INFINITY : fminf(v[i], FLT_MAX);
+  }
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < M; ++i) m = fmaxf(m, v[i]);
+  m = warp_max(m);
+  if (m == -INFINITY) m = 0.0f;  // every term is then exp(-inf) = 0
+  float sum = 0.0f;
+  if (!sigmoid) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      v[i] = expf(v[i] - m);
+      sum += v[i];
+    }
+    if constexpr (SLOPE) {
+#pragma unroll
+      for (int i = 0; i < M; ++i) slope[i] = 1.0f;
+    }
+  } else if (m >= 0.0f) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const float t = expf(fminf(-v[i], 80.0f));  // sigma below e^-80 adds nothing to a sum >= 1/2
+      const float s = v[i] == -INFINITY ? 0.0f : __fdividef(1.0f, 1.0f + t);
+      if constexpr (SLOPE) slope[i] = v[i] == -INFINITY ? 1.0f : t * s;
+      v[i] = s;
+      sum += s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      const float r = __fdividef(1.0f, 1.0f + expf(v[i]));
+      if constexpr (SLOPE) slope[i] = r;
+      v[i] = expf(v[i] - m) * r;
+      sum += v[i];
+    }
+  }
+  sum = warp_add(sum);
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int i = 0; i < M; ++i) v[i] *= inv;
+}
+
+template <int VEC, int N>
+__global__ void __launch_bounds__(kBalThreads)
+balance_tile_kernel(const BalArgs a) {
+  constexpr int M = VEC * N;
+  __shared__ float s_sum[kBalWarps][32 * M];
+  __shared__ int32_t s_cnt[kMaxE];
+  __shared__ int32_t s_tok;
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  check_offsets(a);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  const int t0 = blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
+  for (int q = seq_of(a, t0); q < a.S; ++q) {
+    const int b = max(seq_bound(a, q), t0), e = min(seq_bound(a, q + 1), t1);
+    if (b >= t1) break;
+    if (b >= e) continue;
+    for (int i = threadIdx.x; i < a.E; i += kBalThreads) s_cnt[i] = 0;
+    if (threadIdx.x == 0) s_tok = 0;
+    __syncthreads();
+    float acc[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) acc[i] = 0.0f;
+    int live_tokens = 0;
+    for (int t = b + warp; t < e; t += kBalWarps) {
+      const int id = lane < a.k ? __ldg(a.ids + static_cast<int64_t>(t) * a.k + lane)
+                                : MOE_ROUTE_MASKED;
+      if (__shfl_sync(0xFFFFFFFFu, id, 0) == MOE_ROUTE_MASKED) continue;  // padding
+      float v[M], none[1];
+      load_row<VEC, N>(a.logits + static_cast<int64_t>(t) * a.E, a.E, lane, v);
+      row_probs<M, false>(v, none, a.sigmoid, a.dev_status);
+#pragma unroll
+      for (int i = 0; i < M; ++i) acc[i] += v[i];
+      if (lane < a.k) {
+        if (id >= 0 && id < a.E) atomicAdd(&s_cnt[id], 1);
+        else if (id != MOE_ROUTE_MASKED) report(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
+      }
+      ++live_tokens;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) s_sum[warp][VEC * (lane + 32 * i) + j] = acc[VEC * i + j];
+    if (lane == 0) atomicAdd(&s_tok, live_tokens);
+    __syncthreads();
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) + q;
+    for (int i = threadIdx.x; i < a.E; i += kBalThreads) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kBalWarps; ++w) s += s_sum[w][i];
+      a.part_sum[slot * a.E + i] = s;
+      a.part_cnt[slot * a.E + i] = s_cnt[i];
+    }
+    if (threadIdx.x == 0) a.part_tok[slot] = s_tok;
+    __syncthreads();
+  }
+  pdl_trigger();
+}
+
+// One block per (32 experts, sequence): the sequence's slots in order (eight
+// interleaved groups, then the groups in order).  The block that finishes last
+// adds the loss terms in order.
+__global__ void __launch_bounds__(kBalThreads)
+balance_finish_kernel(const BalArgs a) {
+  __shared__ float s_sum[8][32];
+  __shared__ int32_t s_cnt[8][32];
+  __shared__ int32_t s_tok[8];
+  __shared__ double s_loss[kBalThreads];
+  __shared__ bool last;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int eb = gridDim.x, q = blockIdx.y;
+  const int e = blockIdx.x * 32 + lane;
+  const int b = seq_bound(a, q), end = seq_bound(a, q + 1);
+  float sum = 0.0f;
+  int cnt = 0, tok = 0;
+  if (b < end) {
+    const int64_t first = static_cast<int64_t>(b / a.tile) + q;
+    const int n = (end - 1) / a.tile - b / a.tile + 1;
+#pragma unroll 4
+    for (int i = g; i < n; i += 8) {
+      if (e < a.E) {
+        sum += a.part_sum[(first + i) * a.E + e];
+        cnt += a.part_cnt[(first + i) * a.E + e];
+      }
+    }
+    for (int i = threadIdx.x; i < n; i += kBalThreads) tok += a.part_tok[first + i];
+  }
+  tok = __reduce_add_sync(0xFFFFFFFFu, tok);
+  s_sum[g][lane] = sum;
+  s_cnt[g][lane] = cnt;
+  if (lane == 0) s_tok[g] = tok;
+  __syncthreads();
+  if (g == 0) {
+    tok = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tok += s_tok[i];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      sum += s_sum[i][lane];
+      cnt += s_cnt[i][lane];
+    }
+    const float mean = tok > 0 ? sum / static_cast<float>(tok) : 0.0f;
+    double term = 0.0;
+    if (e < a.E) {
+      a.counts[static_cast<int64_t>(q) * a.E + e] = cnt;
+      a.probs[static_cast<int64_t>(q) * a.E + e] = mean;
+      if (tok > 0) term = static_cast<double>(cnt) * mean;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, o);
+    if (lane == 0) {
+      if (blockIdx.x == 0) a.tokens[q] = tok;
+      a.part_loss[static_cast<int64_t>(q) * eb + blockIdx.x] =
+          tok > 0 ? term * a.E / (static_cast<double>(a.k) * tok) : 0.0;
+      __threadfence();
+      last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x * gridDim.y) - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) {
+    pdl_trigger();
+    return;
+  }
+  __threadfence();
+  double part = 0.0;
+  int used = 0;
+  const int64_t n_terms = static_cast<int64_t>(a.S) * eb;
+  for (int64_t i = threadIdx.x; i < n_terms; i += kBalThreads) part += __ldcg(a.part_loss + i);
+  for (int i = threadIdx.x; i < a.S; i += kBalThreads) used += __ldcg(a.tokens + i) > 0;
+  s_loss[threadIdx.x] = part;
+  s_cnt[g][lane] = used;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double total = 0.0;
+    int sequences = 0;
+    for (int i = 0; i < kBalThreads; ++i) {
+      total += s_loss[i];
+      sequences += s_cnt[i >> 5][i & 31];
+    }
+    a.tokens[a.S] = sequences;
+    *a.loss = sequences > 0 ? static_cast<float>(a.alpha * total / sequences) : 0.0f;
+  }
+  pdl_trigger();
+}
+
+template <int VEC, int N>
+__global__ void __launch_bounds__(kBalThreads)
+route_backward_kernel(const BalArgs a) {
+  constexpr int M = VEC * N;
+  // gradients of the selected logits, scattered to their experts (zero between tokens)
+  __shared__ float s_sel[kBalWarps][32 * M];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* sel = s_sel[warp];
+#pragma unroll
+  for (int i = 0; i < M; ++i) sel[lane + 32 * i] = 0.0f;
+  __syncwarp();
+  const bool balance = a.counts != nullptr;
+  float scale = 0.0f;
+  if (balance) {
+    const int used = __ldg(a.tokens + a.S);
+    scale = used > 0 ? a.alpha / used : 0.0f;
+    if (a.dloss != nullptr) scale *= __ldg(a.dloss);
+    check_offsets(a);
+  }
+  const int t0 = blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
+  int seq_b = 0, seq_e = 0;  // bounds of the sequence whose weights are in w
+  float w[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) w[i] = 0.0f;
+  for (int t = t0 + warp; t < t1; t += kBalWarps) {
+    const int64_t at = static_cast<int64_t>(t) * a.k + lane;
+    float* out = a.dlogits + static_cast<int64_t>(t) * a.E;
+    const int id = lane < a.k ? __ldg(a.ids + at) : MOE_ROUTE_MASKED;
+    float v[M], slope[M];
+    if (__shfl_sync(0xFFFFFFFFu, id, 0) == MOE_ROUTE_MASKED) {  // padding: no gradient
+#pragma unroll
+      for (int i = 0; i < M; ++i) v[i] = 0.0f;
+    } else {
+      const float* row = a.logits + static_cast<int64_t>(t) * a.E;
+      if (balance) {
+        if (t < seq_b || t >= seq_e) {
+          const int q = seq_of(a, t);
+          seq_b = seq_bound(a, q);
+          seq_e = seq_bound(a, q + 1);
+          const bool inside = t >= seq_b && t < seq_e;
+          const float L = static_cast<float>(__ldg(a.tokens + q));
+          const float c = inside && L > 0.0f ? scale * a.E / (a.k * L) / L : 0.0f;
+          if (!inside) seq_e = seq_b;  // look again at the next token
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+              const int e = VEC * (lane + 32 * i) + j;
+              w[VEC * i + j] =
+                  e < a.E ? c * __ldg(a.counts + static_cast<int64_t>(q) * a.E + e) : 0.0f;
+            }
+        }
+        load_row<VEC, N>(row, a.E, lane, v);
+        row_probs<M, true>(v, slope, a.sigmoid, a.dev_status);
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < M; ++i) dot += v[i] * w[i];
+        dot = warp_add(dot);
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = v[i] * (w[i] - dot) * slope[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < M; ++i) v[i] = 0.0f;
+      }
+      if (a.dgates != nullptr) {
+        const bool ok = id >= 0 && id < a.E;
+        if (!ok && id != MOE_ROUTE_MASKED) report(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
+        const float g = ok ? __ldg(a.gates + at) : 0.0f;
+        const float dg = ok ? __ldg(a.dgates + at) : 0.0f;
+        const float inner = warp_add(g * dg);
+        float dz = g * (dg - (a.sigmoid ? inner / a.route_scale : inner));
+        if (a.sigmoid && ok) dz *= __fdividef(1.0f, 1.0f + expf(fminf(__ldg(row + id), 80.0f)));
+        if (ok) atomicAdd(sel + id, dz);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) v[VEC * i + j] += sel[VEC * (lane + 32 * i) + j];
+        __syncwarp();
+        if (ok) sel[id] = 0.0f;
+        __syncwarp();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = VEC * (lane + 32 * i);
+      if (e < a.E) {
+        if constexpr (VEC == 4)
+          *reinterpret_cast<float4*>(out + e) =
+              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        else
+          out[e] = v[i];
+      }
+    }
+  }
+  pdl_trigger();
+}
+
+// --------------------------------- host side --------------------------------
+
+// Tokens per block: four blocks per SM, at least one token per warp.
+int tile_tokens(int T) {
+  const int64_t c = ceil_div(T, 4 * 152);
+  return static_cast<int>(c < kBalWarps ? kBalWarps : c);
+}
+
+int64_t slots(int T, int S) { return ceil_div(T, tile_tokens(T)) + S; }
+
+struct Layout {
+  size_t sum, cnt, tok, ticket, loss, total;
+};
+
+Layout layout(int T, int E, int S) {
+  Carver c;
+  Layout l;
+  const int64_t n = slots(T, S);
+  l.sum = c.take<float>(n * E);
+  l.cnt = c.take<int32_t>(n * E);
+  l.tok = c.take<int32_t>(n);
+  l.ticket = c.take<int32_t>(1);
+  l.loss = c.take<double>(static_cast<size_t>(S) * ceil_div(E, 32));
+  l.total = c.off;
+  return l;
+}
+
+moe_status check_balance(const moe_route_params* p, int32_t n_seq, const int32_t* off) {
+  if (p == nullptr || p->T < 0 || p->E <= 0 || p->k <= 0 || p->k > p->E) return MOE_ERR_INVALID_ARG;
+  if (p->score_fn != MOE_SCORE_SOFTMAX && p->score_fn != MOE_SCORE_SIGMOID_GROUP)
+    return MOE_ERR_INVALID_ARG;
+  if (p->score_fn == MOE_SCORE_SIGMOID_GROUP && !(p->route_scale > 0.0f && p->route_scale < 1e30f))
+    return MOE_ERR_INVALID_ARG;
+  if (n_seq < 1 || (off == nullptr && n_seq != 1)) return MOE_ERR_INVALID_ARG;
+  if (p->E > kMaxE || p->k > kMaxK || n_seq > 65535 ||
+      static_cast<int64_t>(p->T) * p->k >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Values per lane: 16-byte pieces where the rows allow them.
+template <template <int, int> class Launch, typename... Args>
+void by_width(int E, bool vec4, Args&&... args) {
+  if (vec4) {
+    if (E <= 128) Launch<4, 1>::go(args...);
+    else if (E <= 256) Launch<4, 2>::go(args...);
+    else if (E <= 384) Launch<4, 3>::go(args...);
+    else Launch<4, 4>::go(args...);
+  } else {
+    if (E <= 32) Launch<1, 1>::go(args...);
+    else if (E <= 64) Launch<1, 2>::go(args...);
+    else if (E <= 128) Launch<1, 4>::go(args...);
+    else if (E <= 256) Launch<1, 8>::go(args...);
+    else Launch<1, 16>::go(args...);
+  }
+}
+
+template <int VEC, int N>
+struct TileLaunch {
+  static void go(const BalArgs& a, unsigned grid, cudaStream_t s) {
+    launch(balance_tile_kernel<VEC, N>, dim3(grid), dim3(kBalThreads), 0, s, a);
+  }
+};
+
+template <int VEC, int N>
+struct BackwardLaunch {
+  static void go(const BalArgs& a, unsigned grid, cudaStream_t s) {
+    launch(route_backward_kernel<VEC, N>, dim3(grid), dim3(kBalThreads), 0, s, a);
+  }
+};
+
+BalArgs base_args(const moe_route_params* p, int32_t n_seq, const int32_t* off,
+                  const float* logits, const int32_t* ids, float alpha, uint32_t* dev_status) {
+  BalArgs a = {};
+  a.T = p->T;
+  a.E = p->E;
+  a.k = p->k;
+  a.S = n_seq;
+  a.sigmoid = p->score_fn == MOE_SCORE_SIGMOID_GROUP;
+  a.tile = tile_tokens(p->T);
+  a.alpha = alpha;
+  a.route_scale = p->route_scale;
+  a.off = off;
+  a.logits = logits;
+  a.ids = ids;
+  a.dev_status = dev_status;
+  return a;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API size_t moe_balance_loss_workspace_size(const moe_route_params* p, int32_t n_seq) {
+  const int32_t one = 0;
+  if (check_balance(p, n_seq, &one) != MOE_OK) return 0;
+  return layout(p->T, p->E, n_seq).total;
+}
+
+MOE_API moe_status moe_balance_loss(const moe_route_params* p, int32_t n_seq,
+                                    const int32_t* seq_offsets, const float* logits,
+                                    const int32_t* topk_ids, float alpha, int32_t* counts,
+                                    int32_t* seq_tokens, float* mean_probs, float* loss, void* ws,
+                                    size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream) {
+  const moe_status st = check_balance(p, n_seq, seq_offsets);
+  if (st != MOE_OK) return st;
+  if (counts == nullptr || seq_tokens == nullptr || mean_probs == nullptr || loss == nullptr ||
+      ws == nullptr || !(fabsf(alpha) <= FLT_MAX))
+    return MOE_ERR_INVALID_ARG;
+  if (p->T > 0 && (logits == nullptr || topk_ids == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(logits) || !aligned4(topk_ids) || !aligned4(seq_offsets) || !aligned4(counts) ||
+      !aligned4(seq_tokens) || !aligned4(mean_probs) || !aligned4(loss) || !aligned16(ws))
+    return MOE_ERR_UNSUPPORTED;
+  const Layout l = layout(p->T, p->E, n_seq);
+  if (ws_bytes < l.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  BalArgs a = base_args(p, n_seq, seq_offsets, logits, topk_ids, alpha, dev_status);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.part_sum = reinterpret_cast<float*>(w + l.sum);
+  a.part_cnt = reinterpret_cast<int32_t*>(w + l.cnt);
+  a.part_tok = reinterpret_cast<int32_t*>(w + l.tok);
+  a.ticket = reinterpret_cast<int32_t*>(w + l.ticket);
+  a.part_loss = reinterpret_cast<double*>(w + l.loss);
+  a.counts = counts;
+  a.tokens = seq_tokens;
+  a.probs = mean_probs;
+  a.loss = loss;
+  cudaStream_t s = as_cuda(stream);
+  const int64_t tiles = ceil_div(p->T, a.tile);
+  by_width<TileLaunch>(p->E, p->E % 4 == 0 && aligned16(logits), a,
+                       static_cast<unsigned>(tiles > 0 ? tiles : 1), s);
+  launch(balance_finish_kernel,
+         dim3(static_cast<unsigned>(ceil_div(p->E, 32)), static_cast<unsigned>(n_seq)),
+         dim3(kBalThreads), 0, s, a);
+  return launch_status();
+}
+
+MOE_API moe_status moe_route_backward(const moe_route_params* p, int32_t n_seq,
+                                      const int32_t* seq_offsets, const float* logits,
+                                      const int32_t* topk_ids, const float* gates,
+                                      const float* dgates, float alpha, const int32_t* counts,
+                                      const int32_t* seq_tokens, const float* dloss,
+                                      float* dlogits, uint32_t* dev_status, moe_stream_t stream) {
+  const moe_status st = check_balance(p, n_seq, seq_offsets);
+  if (st != MOE_OK) return st;
+  if ((counts == nullptr) != (seq_tokens == nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((dgates == nullptr && counts == nullptr) || (dgates != nullptr && gates == nullptr) ||
+      !(fabsf(alpha) <= FLT_MAX))
+    return MOE_ERR_INVALID_ARG;
+  if (p->T == 0) return MOE_OK;
+  if (logits == nullptr || topk_ids == nullptr || dlogits == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(logits) || !aligned4(topk_ids) || !aligned4(seq_offsets) || !aligned4(gates) ||
+      !aligned4(dgates) || !aligned4(counts) || !aligned4(seq_tokens) || !aligned4(dloss) ||
+      !aligned4(dlogits))
+    return MOE_ERR_UNSUPPORTED;
+  BalArgs a = base_args(p, n_seq, seq_offsets, logits, topk_ids, alpha, dev_status);
+  a.gates = gates;
+  a.dgates = dgates;
+  a.counts = const_cast<int32_t*>(counts);
+  a.tokens = const_cast<int32_t*>(seq_tokens);
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  by_width<BackwardLaunch>(p->E, p->E % 4 == 0 && aligned16(logits) && aligned16(dlogits), a,
+                           static_cast<unsigned>(ceil_div(p->T, a.tile)), as_cuda(stream));
+  return launch_status();
+}

@@ -717,6 +717,58 @@ moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t dy_type, 
                                      float* dweight, void* ws, size_t ws_bytes,
                                      moe_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Router training: balance loss, per-expert counts and the logits' gradient */
+/* ------------------------------------------------------------------------ */
+/* Balance loss of a routed batch over n_seq sequences: sequence q holds tokens
+ * [seq_offsets[q], seq_offsets[q+1]) (int32 device array of n_seq + 1
+ * non-decreasing entries in [0, T]; NULL: one sequence of all T tokens).  A token
+ * whose slot-0 id is MOE_ROUTE_MASKED is padding and takes no part, nor do tokens
+ * outside every sequence.  With L_q the live tokens of q, n_qe the routes of them
+ * that chose e, p_t = softmax(logits[t]) (MOE_SCORE_SOFTMAX) or sigmoid(logits[t])
+ * over its sum (MOE_SCORE_SIGMOID_GROUP; the groups play no part) and S' the
+ * sequences with L_q > 0:
+ *   counts[q, e]     = n_qe                       int32 [n_seq, E]
+ *   seq_tokens[q]    = L_q, seq_tokens[n_seq] = S'  int32 [n_seq + 1]
+ *   mean_probs[q, e] = sum_t p_te / L_q (0 for an empty q)  fp32 [n_seq, E]
+ *   loss[0] = alpha / S' * sum_q sum_e E / (k L_q) n_qe mean_probs[q, e]   fp32 (0 if S' = 0)
+ * The counts are of the routes chosen, before any capacity ([M6.2] 0x01I demand).
+ * Sums are fp32 (the loss's last sum fp64) in an order fixed by the sizes: the same
+ * bits on every run.
+ * A NaN logit counts as -inf and +inf as the largest finite value (both set
+ * MOE_DEV_NONFINITE_LOGIT); a row of -inf only has p = 0.  Offsets out of order or
+ * range set MOE_DEV_BAD_MAP (results unspecified, nothing outside the arrays is
+ * touched); ids outside [0, E) set MOE_DEV_BAD_EXPERT_ID and are not counted.
+ * ws: moe_balance_loss_workspace_size() bytes (0 = invalid parameters), 16-byte
+ * aligned; no state is kept in it between calls, but calls that overlap on the GPU
+ * must not share it.  Limits: E <= 512, k <= min(E, 16), n_seq <= 65535,
+ * T*k < 2^31.  topk_ids [T, k] as moe_route writes them (distinct per token).   */
+size_t moe_balance_loss_workspace_size(const moe_route_params* p, int32_t n_seq);
+moe_status moe_balance_loss(const moe_route_params* p, int32_t n_seq, const int32_t* seq_offsets,
+                            const float* logits, const int32_t* topk_ids, float alpha,
+                            int32_t* counts, int32_t* seq_tokens, float* mean_probs, float* loss,
+                            void* ws, size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
+
+/* Gradient of the router's logits: the balance loss's (with counts and seq_tokens
+ * of the forward; both NULL: left out) times *dloss (device fp32; NULL = 1), plus
+ * the gates' (with dgates [T, k], for example from moe_combine_backward, and the
+ * gates [T, k] that moe_route wrote; dgates NULL: left out):
+ *   w_e = dloss alpha / S' E / (k L_q) n_qe / L_q
+ *   dz_te  = p_te (w_e - sum_j p_tj w_j)           softmax
+ *          = p_te (1 - sigma_te) (w_e - sum_j p_tj w_j)   sigmoid
+ *   dz_sel += g (dg - <g, dg>)                     softmax over the selected
+ *          += g (1 - sigma) (dg - <g, dg> / route_scale)  sigmoid
+ * dlogits [T, E] fp32 is written in full: 0 for padding tokens, the gates' part
+ * alone for tokens outside every sequence.  The selection and its bias have no
+ * gradient ([M6.2] 0x06E: the controller moves the bias).  Errors and limits as
+ * moe_balance_loss.                                                          */
+moe_status moe_route_backward(const moe_route_params* p, int32_t n_seq,
+                              const int32_t* seq_offsets, const float* logits,
+                              const int32_t* topk_ids, const float* gates, const float* dgates,
+                              float alpha, const int32_t* counts, const int32_t* seq_tokens,
+                              const float* dloss, float* dlogits, uint32_t* dev_status,
+                              moe_stream_t stream);
+
 /* Self-test of the bounded pipeline wait used by the tensor-core kernels: one
  * CTA initialises an mbarrier that nothing arrives at and waits on it with the
  * same bounded-wait routine, giving up after limit_ns nanoseconds of global
