@@ -64,6 +64,8 @@ EXPORTED = [
     "moe_decode_workspace_size", "moe_decode_layer",
     "moe_add_rms_norm", "moe_add_rms_norm_backward_workspace_size", "moe_add_rms_norm_backward",
     "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward",
+    "moe_quantize_weights_fp8", "moe_grouped_swiglu_w8_workspace_size", "moe_grouped_swiglu_w8",
+    "moe_grouped_gate_up_w8", "moe_grouped_down_w8",
 ]
 
 
@@ -171,6 +173,11 @@ _SIGS = {
                                 _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "moe_route_backward": (_I32, [ctypes.POINTER(RouteParams), _I32, _P, _P, _P, _P, _P,
                                   ctypes.c_float, _P, _P, _P, _P, _P, _P]),
+    "moe_quantize_weights_fp8": (_I32, [_I32, _I32, _I32, _P, _P, _P, _P, _P]),
+    "moe_grouped_swiglu_w8_workspace_size": (_SZ, [_I32, _I32]),
+    "moe_grouped_swiglu_w8": (_I32, [_I32] * 4 + [_P] * 12 + [_SZ, _P, _P]),
+    "moe_grouped_gate_up_w8": (_I32, [_I32] * 4 + [_P] * 12),
+    "moe_grouped_down_w8": (_I32, [_I32] * 4 + [_P] * 9),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -600,3 +607,39 @@ def moe_route_backward(p: RouteParams, n_seq, seq_offsets, logits, topk_ids, gat
         _ptr(dgates), float(alpha), _ptr(counts), _ptr(seq_tokens), _ptr(dloss), _ptr(dlogits),
         _ptr(dev_status), _stream(stream)))
     _count(1 if p.T > 0 else 0)
+
+
+def moe_quantize_weights_fp8(n_seg, K, N, w, q, scales, dev_status=None, stream=None):
+    _check("moe_quantize_weights_fp8", lib().moe_quantize_weights_fp8(
+        n_seg, K, N, _ptr(w), _ptr(q), _ptr(scales), _ptr(dev_status), _stream(stream)))
+    _count(1)
+
+
+def moe_grouped_swiglu_w8_workspace_size(max_rows: int, I: int) -> int:
+    return lib().moe_grouped_swiglu_w8_workspace_size(max_rows, I)
+
+
+def moe_grouped_swiglu_w8(n_seg, d, I, max_rows, xq, xs, seg_begin, seg_count, wg_q, wg_s, wu_q,
+                          wu_s, wd_q, wd_s, y, ws, ws_bytes, dev_status=None, stream=None):
+    _check("moe_grouped_swiglu_w8", lib().moe_grouped_swiglu_w8(
+        n_seg, d, I, max_rows, _ptr(xq), _ptr(xs), _ptr(seg_begin), _ptr(seg_count), _ptr(wg_q),
+        _ptr(wg_s), _ptr(wu_q), _ptr(wu_s), _ptr(wd_q), _ptr(wd_s), _ptr(y), _ptr(ws), ws_bytes,
+        _ptr(dev_status), _stream(stream)))
+    _count(2 if max_rows > 0 else 0)
+
+
+def moe_grouped_gate_up_w8(n_seg, d, I, max_rows, xq, xs, seg_begin, seg_count, wg_q, wg_s, wu_q,
+                           wu_s, hq, hs, dev_status=None, stream=None):
+    _check("moe_grouped_gate_up_w8", lib().moe_grouped_gate_up_w8(
+        n_seg, d, I, max_rows, _ptr(xq), _ptr(xs), _ptr(seg_begin), _ptr(seg_count), _ptr(wg_q),
+        _ptr(wg_s), _ptr(wu_q), _ptr(wu_s), _ptr(hq), _ptr(hs), _ptr(dev_status),
+        _stream(stream)))
+    _count(1 if max_rows > 0 else 0)
+
+
+def moe_grouped_down_w8(n_seg, I, d, max_rows, hq, hs, seg_begin, seg_count, wd_q, wd_s, y,
+                        dev_status=None, stream=None):
+    _check("moe_grouped_down_w8", lib().moe_grouped_down_w8(
+        n_seg, I, d, max_rows, _ptr(hq), _ptr(hs), _ptr(seg_begin), _ptr(seg_count), _ptr(wd_q),
+        _ptr(wd_s), _ptr(y), _ptr(dev_status), _stream(stream)))
+    _count(1 if max_rows > 0 else 0)

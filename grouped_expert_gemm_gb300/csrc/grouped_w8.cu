@@ -1,0 +1,664 @@
+// Grouped SwiGLU product over ragged row segments with E4M3 rows, weights and
+// intermediate on the 5th-generation tensor cores (tcgen05.mma kind::f8f6f4).
+//
+//   X = xq * xs[row, k / 128],  W = wq * ws[n / 128, k / 128]
+//   G = X Wg^T, U = X Wu^T;  H = SiLU(G) U, hq = E4M3(H / hs), hs = amax / 448 of the
+//   row's 128 columns;  y = bf16((hq hs) Wd^T)
+// (weights stored [N, K], K contiguous: both operands are K-major).
+//
+// One reduction block of 128 is one pipeline stage, one row of the 128-byte
+// swizzle and one scale block.  The tensor core sums the block's codes into a
+// tensor-memory buffer of its own; the promotion warps read it, multiply by the
+// row's and the weight block's scales and add in fp32 registers:
+//   acc[m, n] += part[m, n] * (xs[m, kb] * ws[n / 128, kb]).
+// The scales are arbitrary fp32 values, so they cannot ride in the MMA's own
+// power-of-two scale factors.
+//
+// Tile: 128 rows x 256 weight columns (gate/up: 128 gate + the same 128 up, so a
+// tile makes one whole scale group of H; down: 256 columns of y).  Roles of the 384
+// threads, one CTA per SM, persistent over the tiles:
+//   warp 0       TMA producer: [128 x 128] codes of A, two [128 x 128] of B, 48 KB
+//                a stage, four stages
+//   warp 1       allocates tensor memory; lane 0 issues four MMAs (K = 32) a stage
+//   warps 2, 3   idle (they give their registers to the promotion warps)
+//   warps 4..11  promotion and epilogue: warp w reads lanes 32 (w % 4).., columns of
+//                half (w - 4) / 4; 128 fp32 sums per thread
+// Two tensor-memory buffers of 256 columns: block kb + 1 is summed while kb is
+// promoted.  Every wait is bounded (MOE_DEV_TIMEOUT), as in the bf16 pass.
+#include <mutex>
+
+#include "umma.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxSeg = 1024;
+constexpr int kBM = 128;                   // rows per tile
+constexpr int kBK = 128;                   // codes per stage and scale block
+constexpr int kABytes = kBM * kBK;         // 16 KB
+constexpr int kBBox = 128 * kBK;           // 16 KB: one box of 128 weight rows
+constexpr int kStageBytes = kABytes + 2 * kBBox;
+constexpr int kStages = 4;
+constexpr int kAccCols = 256;
+constexpr int kThreads = 384;
+constexpr int kRegsLaunch = 168, kRegsAcc = 208, kRegsRest = 88;
+static_assert(256 * kRegsAcc + 128 * kRegsRest <= kThreads * kRegsLaunch, "register split");
+
+constexpr float kE4M3Max = 448.0f;
+constexpr uint32_t kAbsInf = 0x7F800000u;
+
+struct W8Args {
+  const int32_t* seg_begin;
+  const int32_t* seg_count;
+  int n_seg, K, N, max_rows;
+  int GK, GN;          // scale blocks along K and N
+  const float* as;     // [max_rows, GK]
+  const float* bs0;    // [n_seg, GN, GK]: gate, or down
+  const float* bs1;    // up
+  uint8_t* hq;         // gate/up
+  float* hs;           // [max_rows, GN]
+  uint16_t* y;         // down
+  uint32_t* dev_status;
+  int m_outer;
+};
+
+struct Tile {
+  int seg, row0, rows, nb;
+};
+
+struct Table {
+  volatile int* abort_flag;
+  uint32_t* tmem_slot;
+  int* warp_tot;
+  int* start;   // [n_seg + 1] first tile of a segment
+  int* begin;
+  int* count;
+};
+constexpr int kTableInts = 8 + 3 * kMaxSeg + 8;
+
+__device__ __forceinline__ Table carve_table(int* p) {
+  Table t;
+  t.abort_flag = p;
+  t.tmem_slot = reinterpret_cast<uint32_t*>(p + 1);
+  t.warp_tot = p + 4;
+  t.start = p + 8;
+  t.begin = t.start + kMaxSeg + 1;
+  t.count = t.begin + kMaxSeg;
+  return t;
+}
+
+// Tile t: inside a segment n-block outer / m-block inner, or the reverse (m_outer).
+__device__ __forceinline__ Tile tile_of(int t, const Table& tb, int n_seg, int bm, int n_blocks,
+                                        int m_outer) {
+  int lo = 0, hi = n_seg - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tb.start[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  const int local = t - tb.start[lo];
+  const int m_blocks = (tb.count[lo] + bm - 1) / bm;
+  Tile tl;
+  tl.seg = lo;
+  tl.nb = m_outer ? local % n_blocks : local / m_blocks;
+  const int mb = m_outer ? local / n_blocks : local % m_blocks;
+  tl.row0 = tb.begin[lo] + mb * bm;
+  tl.rows = min(bm, tb.count[lo] - mb * bm);
+  return tl;
+}
+
+// Segment table by 128 threads (tid 0..127 of named barrier 1): segments outside
+// the row space are reported and treated as empty.
+__device__ __forceinline__ void build_table(const W8Args& a, int bm, int n_blocks, int tid,
+                                            const Table& tb) {
+  const int lane = tid & 31, warp = tid >> 5;
+  const int per = (a.n_seg + 127) / 128;
+  const int q0 = tid * per, q1 = min(a.n_seg, q0 + per);
+  int local = 0;
+  for (int q = q0; q < q1; ++q) {
+    int b = __ldg(a.seg_begin + q), c = __ldg(a.seg_count + q);
+    if (c < 0 || b < 0 || static_cast<int64_t>(b) + c > a.max_rows) {
+      if (c != 0) report(a.dev_status, MOE_DEV_BAD_ROW);
+      b = 0;
+      c = 0;
+    }
+    tb.begin[q] = b;
+    tb.count[q] = c;
+    local += ((c + bm - 1) / bm) * n_blocks;
+  }
+  int incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) tb.warp_tot[warp] = incl;
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  int run = incl - local;
+  for (int w = 0; w < warp; ++w) run += tb.warp_tot[w];
+  for (int q = q0; q < q1; ++q) {
+    tb.start[q] = run;
+    run += ((tb.count[q] + bm - 1) / bm) * n_blocks;
+  }
+  if (tid == 127)
+    tb.start[a.n_seg] = tb.warp_tot[0] + tb.warp_tot[1] + tb.warp_tot[2] + tb.warp_tot[3];
+}
+
+__device__ __forceinline__ float scale_of(uint32_t amax) {
+  return amax == 0 ? 1.0f : __fdiv_rn(__uint_as_float(amax), kE4M3Max);
+}
+
+// acc += part * s on 32 columns.
+__device__ __forceinline__ void promote32(const uint32_t (&part)[32], float s, float2* acc) {
+  const float2 s2 = make_float2(s, s);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    acc[i] = __ffma2_rn(make_float2(__uint_as_float(part[2 * i]), __uint_as_float(part[2 * i + 1])),
+                        s2, acc[i]);
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 1)
+grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ CUtensorMap map_b0,
+                  const __grid_constant__ CUtensorMap map_b1, const W8Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stage_base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // bars: full[S], empty[S], tfull[2], tempty[2], amax[4], drain
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage_base + kStages * kStageBytes);
+  constexpr int kBars = 2 * kStages + 9;
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(bars + kBars);  // [2][2][128]
+  const Table tb = carve_table(reinterpret_cast<int*>(s_amax + 512));
+  volatile int* abort_flag = tb.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_blocks = (a.N + (SWIGLU ? 127 : 255)) / (SWIGLU ? 128 : 256);
+
+  auto full_bar = [&](int s) { return smem_u32(bars + s); };
+  auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
+  auto tfull_bar = [&](int b) { return smem_u32(bars + 2 * kStages + b); };
+  auto tempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 2 + b); };
+  auto amax_bar = [&](int q) { return smem_u32(bars + 2 * kStages + 4 + q); };
+  const uint32_t drain_bar = smem_u32(bars + 2 * kStages + 8);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 8);  // one arrival per promotion warp
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(amax_bar(q), 2);  // the two warps of a lane quadrant
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) umma_alloc(smem_u32(tb.tmem_slot), 2 * kAccCols);
+  pdl_wait();
+  if (threadIdx.x >= 128 && threadIdx.x < 256)
+    build_table(a, kBM, n_blocks, threadIdx.x - 128, tb);
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  const uint32_t tmem = *tb.tmem_slot;
+  const int total = tb.start[a.n_seg];
+
+  if (warp < 4) {
+    reg_dec<kRegsRest>();
+    if (warp == 0 && lane == 0) {
+      // ---- TMA producer ----
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const Tile tl = tile_of(t, tb, a.n_seg, kBM, n_blocks, a.m_outer);
+        for (int kb = 0; kb < a.GK; ++kb) {
+          if (!wait_bounded(empty_bar(s), ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
+          const uint32_t st = smem_u32(stage_base + s * kStageBytes);
+          mbar_arrive_expect_tx(full_bar(s), kStageBytes);
+          tma_load_2d(st, &map_a, full_bar(s), kb * kBK, tl.row0);
+          if (SWIGLU) {
+            tma_load_3d(st + kABytes, &map_b0, full_bar(s), kb * kBK, tl.nb * 128, tl.seg);
+            tma_load_3d(st + kABytes + kBBox, &map_b1, full_bar(s), kb * kBK, tl.nb * 128, tl.seg);
+          } else {
+            tma_load_3d(st + kABytes, &map_b0, full_bar(s), kb * kBK, tl.nb * 256, tl.seg);
+            tma_load_3d(st + kABytes + kBBox, &map_b0, full_bar(s), kb * kBK, tl.nb * 256 + 128,
+                        tl.seg);
+          }
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (!ok) {  // copies in flight land before the shared memory is given up
+        for (int i = 0; i < kStages; ++i) {
+          if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+          wait_drain(full_bar(s), ph);
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ---- MMA issuer ----
+      constexpr uint32_t idesc = umma_idesc_e4m3(kBM, kAccCols);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true, issued = false;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int kb = 0; kb < a.GK; ++kb) {
+          if (!wait_bounded(tempty_bar(buf), acc_ph ^ 1u, abort_flag, a.dev_status) ||
+              !wait_bounded(full_bar(s), ph, abort_flag, a.dev_status)) {
+            ok = false;
+            break;
+          }
+          umma_fence_after();
+          const uint32_t st = smem_u32(stage_base + s * kStageBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f8(tmem + buf * kAccCols, umma_desc(st + kk * 32), umma_desc(st + kABytes + kk * 32),
+                    idesc, kk > 0);
+          issued = true;
+          umma_commit(empty_bar(s));
+          umma_commit(tfull_bar(buf));
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+          if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
+        }
+      }
+      if (!ok && issued) {
+        umma_commit(drain_bar);
+        wait_drain(drain_bar, 0);
+      }
+    }
+  } else {
+    reg_inc<kRegsAcc>();
+    // ---- promotion and epilogue ----
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int r = quad * 32 + lane;
+    const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    // columns of the two 64-wide pieces this thread sums, and their scale blocks
+    const int c0 = SWIGLU ? 64 * half : 128 * half;
+    const int c1 = SWIGLU ? 128 + 64 * half : 128 * half + 64;
+    int buf = 0, parity = 0;
+    uint32_t acc_ph = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const Tile tl = tile_of(t, tb, a.n_seg, kBM, n_blocks, a.m_outer);
+      const bool live = r < tl.rows;
+      const int64_t row = min(tl.row0 + r, a.max_rows - 1);
+      const float* as = a.as + row * a.GK;
+      const int nblk = SWIGLU ? tl.nb : min(2 * tl.nb + half, a.GN - 1);
+      const int64_t boff = (static_cast<int64_t>(tl.seg) * a.GN + nblk) * a.GK;
+      const float* b0 = a.bs0 + boff;
+      const float* b1 = SWIGLU ? a.bs1 + boff : b0;
+      float2 acc0[32], acc1[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc0[i] = acc1[i] = make_float2(0.0f, 0.0f);
+      float sa = __ldg(as), w0 = __ldg(b0), w1 = __ldg(b1);
+      for (int kb = 0; kb < a.GK; ++kb) {
+        const float s0 = sa * w0, s1 = sa * w1;
+        if (kb + 1 < a.GK) {
+          sa = __ldg(as + kb + 1);
+          w0 = __ldg(b0 + kb + 1);
+          w1 = __ldg(b1 + kb + 1);
+        }
+        if (!__all_sync(0xFFFFFFFFu,
+                        wait_bounded(tfull_bar(buf), acc_ph, abort_flag, a.dev_status))) {
+          ok = false;
+          break;
+        }
+        umma_fence_after();
+        const uint32_t ta = taddr0 + buf * kAccCols;
+        uint32_t u[32], v[32];
+        umma_ld32(ta + c0, u);
+        umma_ld_wait(u);
+        umma_ld32(ta + c0 + 32, v);
+        promote32(u, s0, acc0);
+        umma_ld_wait(v);
+        umma_ld32(ta + c1, u);
+        promote32(v, s0, acc0 + 16);
+        umma_ld_wait(u);
+        umma_ld32(ta + c1 + 32, v);
+        promote32(u, s1, acc1);
+        umma_ld_wait(v);
+        umma_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(buf));
+        promote32(v, s1, acc1 + 16);
+        if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
+      }
+      if (!ok) break;
+      if constexpr (SWIGLU) {
+        // H of 64 columns in place of the gate sums, their largest magnitude, the
+        // other half's through shared memory, then the group's codes
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          acc0[i].x = __fdividef(acc0[i].x, 1.0f + __expf(-acc0[i].x)) * acc1[i].x;
+          acc0[i].y = __fdividef(acc0[i].y, 1.0f + __expf(-acc0[i].y)) * acc1[i].y;
+          top = max(top, max(__float_as_uint(acc0[i].x) & 0x7FFFFFFFu,
+                             __float_as_uint(acc0[i].y) & 0x7FFFFFFFu));
+        }
+        uint32_t* am = s_amax + parity * 256;
+        am[half * 128 + r] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(amax_bar(quad));
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(amax_bar(quad), static_cast<uint32_t>(parity),
+                                                  abort_flag, a.dev_status)))
+          break;
+        parity ^= 1;
+        top = max(top, am[(half ^ 1) * 128 + r]);
+        if (live) {
+          const float s = scale_of(top);
+          if (top >= kAbsInf) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
+          if (half == 0) a.hs[row * a.GN + tl.nb] = s;
+          const int n0 = tl.nb * 128 + 64 * half;
+          uint8_t* dst = a.hq + row * a.N + n0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (n0 + 16 * j < a.N) {
+              uint32_t p[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 x = acc0[8 * j + 2 * i], z = acc0[8 * j + 2 * i + 1];
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+                    make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+                    make_float2(__fdiv_rn(z.x, s), __fdiv_rn(z.y, s)), __NV_SATFINITE, __NV_E4M3);
+                p[i] = lo | (hi << 16);
+              }
+              *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          }
+        }
+      } else if (live) {
+        const int n0 = tl.nb * 256 + 128 * half;
+        uint16_t* dst = a.y + row * a.N + n0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (n0 + 8 * j < a.N) {
+            const float2* v = j < 8 ? acc0 + 4 * j : acc1 + 4 * (j - 8);
+            *reinterpret_cast<uint4*>(dst + 8 * j) =
+                make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                           pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+          }
+        }
+      }
+    }
+  }
+
+  // ---- teardown ----
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    umma_dealloc(tmem, 2 * kAccCols);
+  }
+  pdl_trigger();
+}
+
+constexpr int kSmemBytes =
+    1024 + kStages * kStageBytes + (2 * kStages + 9) * 8 + 512 * 4 + kTableInts * 4;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// ------------------------------ weight quantization --------------------------
+
+// One block per 128 x 128 weight block: w [K, N] bf16 -> codes [N, K] and a scale.
+__global__ void __launch_bounds__(256)
+quantize_weights_kernel(int K, int N, const uint16_t* __restrict__ w, uint8_t* __restrict__ q,
+                        float* __restrict__ scales, uint32_t* __restrict__ dev_status) {
+  __shared__ uint32_t s_top[8];
+  __shared__ __align__(16) uint8_t s_q[128][144];  // codes [n][k], rows padded by 16
+  pdl_wait();
+  const int n0 = blockIdx.x * 128, k0 = blockIdx.y * 128;
+  const int64_t seg = blockIdx.z;
+  const int tid = threadIdx.x, col = (tid & 15) * 8, kr = tid >> 4;
+  const uint16_t* src = w + seg * K * N;
+  uint4 v[8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int k = k0 + kr + 16 * i;
+    v[i] = k < K && n0 + col < N
+               ? __ldg(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(k) * N + n0 + col))
+               : make_uint4(0, 0, 0, 0);
+    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      top = max(top, (x[j] << 16) & 0x7FFFFFFFu);
+      top = max(top, x[j] & 0x7FFF0000u);
+    }
+  }
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if ((tid & 31) == 0) s_top[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, s_top[i]);
+  const float s = scale_of(top);
+  if (tid == 0) {
+    if (top >= kAbsInf) report(dev_status, MOE_DEV_NONFINITE_INPUT);
+    scales[(seg * gridDim.x + blockIdx.x) * gridDim.y + blockIdx.y] = s;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float f[8];
+    unpack8(v[i], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      s_q[col + j][kr + 16 * i] =
+          __nv_cvt_float_to_fp8(__fdiv_rn(f[j], s), __NV_SATFINITE, __NV_E4M3);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = (tid >> 3) + 32 * i, k = (tid & 7) * 16;
+    if (n0 + n < N && k0 + k < K)
+      *reinterpret_cast<uint4*>(q + (seg * N + n0 + n) * K + k0 + k) =
+          *reinterpret_cast<const uint4*>(&s_q[n][k]);
+  }
+  pdl_trigger();
+}
+
+// ------------------------------ host side ------------------------------------
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Codes [rows, K] with boxes of box_rows x 128, zero-filled past either edge.
+bool map_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t K, uint32_t box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {K, rows};
+  const cuuint64_t strides[1] = {K};
+  const cuuint32_t box[2] = {kBK, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Weight codes [n_seg, N, K]: a dimension of its own for the segment, so a box that
+// passes N is filled with zeros and not with the next segment's rows.
+bool map_weights(CUtensorMap* m, const void* base, uint64_t n_seg, uint64_t N, uint64_t K,
+                 uint32_t box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {K, N, n_seg};
+  const cuuint64_t strides[2] = {K, K * N};
+  const cuuint32_t box[3] = {kBK, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The kernel's shared-memory opt-in, once per device.
+template <typename Kernel>
+bool opt_in(Kernel kern, int bytes, std::mutex& mu, bool (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+      return false;
+    done[dev] = true;
+  }
+  return true;
+}
+
+// As in the bf16 pass: rows inner (one weight tile shared by neighbouring CTAs)
+// unless a segment's rows outgrow the L2 while its weights fit.
+int choose_m_outer(int32_t n_seg, int32_t max_rows, int32_t K, int64_t b_cols) {
+  constexpr int64_t kL2Budget = 48ll << 20;
+  const int64_t a_seg = static_cast<int64_t>(max_rows) / n_seg * K;
+  const int64_t b_seg = static_cast<int64_t>(K) * b_cols;
+  return a_seg > kL2Budget && b_seg <= kL2Budget ? 1 : 0;
+}
+
+moe_status check_shape(int32_t n_seg, int32_t K, int32_t N, int32_t max_rows) {
+  if (n_seg <= 0 || K <= 0 || N <= 0 || max_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (n_seg > kMaxSeg || K % 16 != 0 || N % 16 != 0 || K > 65536 || N > 65536)
+    return MOE_ERR_UNSUPPORTED;
+  // tile numbers are 32-bit
+  if ((static_cast<int64_t>(max_rows) / 16 + n_seg) * ceil_div(N, 128) >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+template <bool SWIGLU>
+moe_status launch_pass(const W8Args& a, const void* x, const void* b0, const void* b1,
+                       cudaStream_t s) {
+  CUtensorMap ma, m0, m1;
+  if (!map_rows(&ma, x, a.max_rows, a.K, kBM) || !map_weights(&m0, b0, a.n_seg, a.N, a.K, 128) ||
+      !map_weights(&m1, b1, a.n_seg, a.N, a.K, 128))
+    return MOE_ERR_CUDA;
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (!opt_in(grouped_w8_kernel<SWIGLU>, kSmemBytes, mu, done)) return MOE_ERR_CUDA;
+  launch(grouped_w8_kernel<SWIGLU>, dim3(sm_count()), dim3(kThreads), kSmemBytes, s, ma, m0, m1, a);
+  return launch_status();
+}
+
+struct Pass {
+  int32_t n_seg, K, N, max_rows;
+  const int32_t *seg_begin, *seg_count;
+  const void* x;
+  const float* xs;
+  const void *w0, *w1;
+  const float *s0, *s1;
+};
+
+moe_status check_pass(const Pass& p, bool swiglu) {
+  const moe_status st = check_shape(p.n_seg, p.K, p.N, p.max_rows);
+  if (st != MOE_OK || p.max_rows == 0) return st;
+  if (p.seg_begin == nullptr || p.seg_count == nullptr || p.x == nullptr || p.xs == nullptr ||
+      p.w0 == nullptr || p.s0 == nullptr || (swiglu && (p.w1 == nullptr || p.s1 == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(p.x) || !aligned16(p.w0) || !aligned16(p.w1) || !aligned4(p.xs) ||
+      !aligned4(p.s0) || !aligned4(p.s1) || !aligned4(p.seg_begin) || !aligned4(p.seg_count))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+W8Args args_of(const Pass& p, uint32_t* dev_status, bool swiglu) {
+  W8Args a = {};
+  a.seg_begin = p.seg_begin;
+  a.seg_count = p.seg_count;
+  a.n_seg = p.n_seg;
+  a.K = p.K;
+  a.N = p.N;
+  a.max_rows = p.max_rows;
+  a.GK = static_cast<int>(ceil_div(p.K, 128));
+  a.GN = static_cast<int>(ceil_div(p.N, 128));
+  a.as = p.xs;
+  a.bs0 = p.s0;
+  a.bs1 = p.s1;
+  a.dev_status = dev_status;
+  a.m_outer = choose_m_outer(p.n_seg, p.max_rows, p.K, (swiglu ? 2ll : 1ll) * p.N);
+  return a;
+}
+
+size_t hidden_offset(int64_t max_rows, int64_t I) {
+  return static_cast<size_t>((max_rows * I + 255) & ~int64_t(255));
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API moe_status moe_quantize_weights_fp8(int32_t n_seg, int32_t K, int32_t N, const moe_bf16* w,
+                                            moe_fp8* q, float* scales, uint32_t* dev_status,
+                                            moe_stream_t stream) {
+  if (n_seg <= 0 || K <= 0 || N <= 0 || w == nullptr || q == nullptr || scales == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (n_seg > kMaxSeg || K % 16 != 0 || N % 16 != 0 || K > 65536 || N > 65536 || !aligned16(w) ||
+      !aligned16(q) || !aligned4(scales))
+    return MOE_ERR_UNSUPPORTED;
+  launch(quantize_weights_kernel,
+         dim3(static_cast<unsigned>(ceil_div(N, 128)), static_cast<unsigned>(ceil_div(K, 128)),
+              static_cast<unsigned>(n_seg)),
+         dim3(256), 0, as_cuda(stream), K, N, w, q, scales, dev_status);
+  return launch_status();
+}
+
+MOE_API moe_status moe_grouped_gate_up_w8(int32_t n_seg, int32_t d, int32_t I, int32_t max_rows,
+                                          const moe_fp8* xq, const float* xs,
+                                          const int32_t* seg_begin, const int32_t* seg_count,
+                                          const moe_fp8* wg_q, const float* wg_s,
+                                          const moe_fp8* wu_q, const float* wu_s, moe_fp8* hq,
+                                          float* hs, uint32_t* dev_status, moe_stream_t stream) {
+  const Pass p = {n_seg, d, I, max_rows, seg_begin, seg_count, xq, xs, wg_q, wu_q, wg_s, wu_s};
+  const moe_status st = check_pass(p, true);
+  if (st != MOE_OK || max_rows == 0) return st;
+  if (hq == nullptr || hs == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(hq) || !aligned4(hs)) return MOE_ERR_UNSUPPORTED;
+  W8Args a = args_of(p, dev_status, true);
+  a.hq = hq;
+  a.hs = hs;
+  return launch_pass<true>(a, xq, wg_q, wu_q, as_cuda(stream));
+}
+
+MOE_API moe_status moe_grouped_down_w8(int32_t n_seg, int32_t I, int32_t d, int32_t max_rows,
+                                       const moe_fp8* hq, const float* hs,
+                                       const int32_t* seg_begin, const int32_t* seg_count,
+                                       const moe_fp8* wd_q, const float* wd_s, moe_bf16* y,
+                                       uint32_t* dev_status, moe_stream_t stream) {
+  const Pass p = {n_seg, I, d, max_rows, seg_begin, seg_count, hq, hs, wd_q, nullptr, wd_s, nullptr};
+  const moe_status st = check_pass(p, false);
+  if (st != MOE_OK || max_rows == 0) return st;
+  if (y == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(y)) return MOE_ERR_UNSUPPORTED;
+  W8Args a = args_of(p, dev_status, false);
+  a.y = y;
+  return launch_pass<false>(a, hq, wd_q, wd_q, as_cuda(stream));
+}
+
+MOE_API size_t moe_grouped_swiglu_w8_workspace_size(int32_t max_rows, int32_t I) {
+  if (max_rows < 0 || I <= 0 || I % 16 != 0 || I > 65536) return 0;
+  return hidden_offset(max_rows, I) +
+         static_cast<size_t>(max_rows) * static_cast<size_t>(ceil_div(I, 128)) * sizeof(float) + 256;
+}
+
+MOE_API moe_status moe_grouped_swiglu_w8(int32_t n_seg, int32_t d, int32_t I, int32_t max_rows,
+                                         const moe_fp8* xq, const float* xs,
+                                         const int32_t* seg_begin, const int32_t* seg_count,
+                                         const moe_fp8* wg_q, const float* wg_s,
+                                         const moe_fp8* wu_q, const float* wu_s,
+                                         const moe_fp8* wd_q, const float* wd_s, moe_bf16* y,
+                                         void* ws, size_t ws_bytes, uint32_t* dev_status,
+                                         moe_stream_t stream) {
+  // everything is checked before the first launch
+  const Pass up = {n_seg, d, I, max_rows, seg_begin, seg_count, xq, xs, wg_q, wu_q, wg_s, wu_s};
+  moe_status st = check_pass(up, true);
+  if (st == MOE_OK) st = check_shape(n_seg, I, d, max_rows);
+  if (st != MOE_OK || max_rows == 0) return st;
+  if (wd_q == nullptr || wd_s == nullptr || y == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(wd_q) || !aligned4(wd_s) || !aligned16(y) || !aligned16(ws))
+    return MOE_ERR_UNSUPPORTED;
+  if (ws_bytes < moe_grouped_swiglu_w8_workspace_size(max_rows, I)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  moe_fp8* hq = static_cast<moe_fp8*>(ws);
+  float* hs = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + hidden_offset(max_rows, I));
+  st = moe_grouped_gate_up_w8(n_seg, d, I, max_rows, xq, xs, seg_begin, seg_count, wg_q, wg_s, wu_q,
+                              wu_s, hq, hs, dev_status, stream);
+  if (st != MOE_OK) return st;
+  return moe_grouped_down_w8(n_seg, I, d, max_rows, hq, hs, seg_begin, seg_count, wd_q, wd_s, y,
+                             dev_status, stream);
+}

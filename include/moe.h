@@ -769,6 +769,61 @@ moe_status moe_route_backward(const moe_route_params* p, int32_t n_seq,
                               const float* dloss, float* dlogits, uint32_t* dev_status,
                               moe_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Grouped SwiGLU product in E4M3 with block scales                         */
+/* ------------------------------------------------------------------------ */
+/* Weights w [n_seg, K, N] bf16 (the layout of the bf16 passes) to E4M3 with one
+ * fp32 scale per 128 x 128 block, laid out for the 8-bit passes: codes
+ * q [n_seg, N, K] (K contiguous), scales [n_seg, ceil(N/128), ceil(K/128)].
+ * s = fp32(amax / 448) of the block (1 for a zero block), q = E4M3(fp32(w / s)),
+ * the rule of moe_quantize_fp8.  A NaN or Inf sets MOE_DEV_NONFINITE_INPUT.  Done
+ * once per set of weights.  Limits: K % 16 == 0, N % 16 == 0, K, N <= 65536,
+ * n_seg <= 1024; 16-byte aligned w and q.                                     */
+moe_status moe_quantize_weights_fp8(int32_t n_seg, int32_t K, int32_t N, const moe_bf16* w,
+                                    moe_fp8* q, float* scales, uint32_t* dev_status,
+                                    moe_stream_t stream);
+
+/* moe_grouped_swiglu with every operand in E4M3 (the same segment rules): rows xq
+ * [max_rows, d] with scales xs [max_rows, ceil(d/128)] (moe_quantize_fp8 or
+ * moe_add_rms_norm with MOE_SCALE_BLOCK128, moved by moe_permute_fp8), weights
+ * wg_q, wu_q [n_seg, I, d] and wd_q [n_seg, d, I] with their block scales.  With
+ * X = xq * xs and W = q * s (each element's own block scale):
+ *   G = X W_gate, U = X W_up                      fp32
+ *   H = SiLU(G) * U                               fp32, then per row and 128 columns
+ *   hs = fp32(amax / 448) (1 if zero), hq = E4M3(H / hs)
+ *   y = bf16((hq * hs) W_down)
+ * Each 128-wide block of the reduction is summed by the tensor cores
+ * (tcgen05.mma kind::f8f6f4, fp32 accumulators) on the codes alone; its sum is
+ * multiplied by the row's and the weight block's scales and added in fp32.
+ * Only segment rows of y are written.  hq / hs live in the workspace
+ * (moe_grouped_swiglu_w8_workspace_size(max_rows, I) bytes, 16-byte aligned; 0 =
+ * invalid sizes), also only for segment rows.
+ * Limits: d % 16 == 0, I % 16 == 0, d, I <= 65536, n_seg <= 1024; 16-byte aligned
+ * codes and y, 4-byte aligned scales.  Segments outside [0, max_rows) set
+ * MOE_DEV_BAD_ROW and are skipped.  A NaN or Inf in H sets
+ * MOE_DEV_NONFINITE_INPUT (that row's codes are then unspecified).             */
+size_t moe_grouped_swiglu_w8_workspace_size(int32_t max_rows, int32_t I);
+moe_status moe_grouped_swiglu_w8(int32_t n_seg, int32_t d, int32_t I, int32_t max_rows,
+                                 const moe_fp8* xq, const float* xs, const int32_t* seg_begin,
+                                 const int32_t* seg_count, const moe_fp8* wg_q, const float* wg_s,
+                                 const moe_fp8* wu_q, const float* wu_s, const moe_fp8* wd_q,
+                                 const float* wd_s, moe_bf16* y, void* ws, size_t ws_bytes,
+                                 uint32_t* dev_status, moe_stream_t stream);
+
+/* Its two passes as separate calls: hq [max_rows, I] and hs
+ * [max_rows, ceil(I/128)] are the first one's output and the second one's input.
+ * Together they give the same y, bit for bit.                                 */
+moe_status moe_grouped_gate_up_w8(int32_t n_seg, int32_t d, int32_t I, int32_t max_rows,
+                                  const moe_fp8* xq, const float* xs, const int32_t* seg_begin,
+                                  const int32_t* seg_count, const moe_fp8* wg_q,
+                                  const float* wg_s, const moe_fp8* wu_q, const float* wu_s,
+                                  moe_fp8* hq, float* hs, uint32_t* dev_status,
+                                  moe_stream_t stream);
+moe_status moe_grouped_down_w8(int32_t n_seg, int32_t I, int32_t d, int32_t max_rows,
+                               const moe_fp8* hq, const float* hs, const int32_t* seg_begin,
+                               const int32_t* seg_count, const moe_fp8* wd_q, const float* wd_s,
+                               moe_bf16* y, uint32_t* dev_status, moe_stream_t stream);
+
 /* Self-test of the bounded pipeline wait used by the tensor-core kernels: one
  * CTA initialises an mbarrier that nothing arrives at and waits on it with the
  * same bounded-wait routine, giving up after limit_ns nanoseconds of global

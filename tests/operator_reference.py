@@ -113,7 +113,8 @@ def quantize_blocks(w):
     E, N, K = w.shape
     gn, gk = -(-N // 128), -(-K // 128)
     p = torch.nn.functional.pad(w, (0, gk * 128 - K, 0, gn * 128 - N)).view(E, gn, 128, gk, 128)
-    s = p.abs().amax(dim=(2, 4)) / torch.tensor(E4M3_MAX)
+    top = p.abs().amax(dim=(2, 4))
+    s = top / torch.full_like(top, E4M3_MAX)  # a tensor: dividing by a number multiplies by 1/448
     s = torch.where(s == 0, torch.ones_like(s), s)
     q = (p / s[:, :, None, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     return q.view(E, gn * 128, gk * 128)[:, :N, :K].contiguous(), s
@@ -124,7 +125,8 @@ def quantize_rows(x):
     n, d = x.shape
     g = -(-d // 128)
     p = torch.nn.functional.pad(x, (0, g * 128 - d)).view(n, g, 128)
-    s = p.abs().amax(dim=2) / torch.tensor(E4M3_MAX)
+    top = p.abs().amax(dim=2)
+    s = top / torch.full_like(top, E4M3_MAX)
     s = torch.where(s == 0, torch.ones_like(s), s)
     q = (p / s[:, :, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     return q.view(n, g * 128)[:, :d].contiguous(), s
