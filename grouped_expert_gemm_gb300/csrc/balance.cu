@@ -28,8 +28,9 @@
 namespace moe {
 namespace {
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBwdThreads = 256;
 constexpr int kMaxE = 512;
 constexpr int kMaxK = 16;
 
@@ -37,7 +38,7 @@ struct BalArgs {
   int T, E, k, S;
   int sigmoid;
   int tile;       // tokens per block
-  int vec4;       // rows may be read 16 bytes at a time
+  int early;      // the grid is resident at once: dependents may launch right after the wait
   float alpha, route_scale;
   const int32_t* off;  // [S + 1], or nullptr: one sequence of all tokens
   const float* logits;
@@ -109,76 +110,94 @@ __device__ __forceinline__ float warp_add(float x) {
   return x;
 }
 
+// Largest value over the warp (NaN operands are ignored).
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-  return x;
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 
-// A row's probabilities in place of its logits; with `slope`, 1 - sigma as well
-// (1 for the softmax).  A NaN logit counts as -inf and +inf as the largest finite
-// value, both reported; a row without a finite logit has probabilities 0.  The
-// sigmoid of an all-negative row is scaled by e^-max before it is normalised, so
-// that its sum cannot underflow.
-template <int M, bool SLOPE>
-__device__ __forceinline__ void row_probs(float (&v)[M], float (&slope)[SLOPE ? M : 1], int sigmoid,
-                                          uint32_t* dev_status) {
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < M; ++i) bad |= !(v[i] <= FLT_MAX);
-  if (__any_sync(0xFFFFFFFFu, bad)) {
-    if (bad) report(dev_status, MOE_DEV_NONFINITE_LOGIT);
-#pragma unroll
-    for (int i = 0; i < M; ++i) v[i] = isnan(v[i]) ? -INFINITY : fminf(v[i], FLT_MAX);
-  }
+// e^x as 2^(x log2 e): two roundings of the argument (2^-23 |x|) and the
+// instruction's 2^-22; results below the normal range are 0.
+__device__ __forceinline__ float exp_of(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504088896341f));
+  return r;
+}
+
+template <int M>
+__device__ __forceinline__ float lane_max(const float (&v)[M]) {
   float m = v[0];
 #pragma unroll
   for (int i = 1; i < M; ++i) m = fmaxf(m, v[i]);
   m = warp_max(m);
-  if (m == -INFINITY) m = 0.0f;  // every term is then exp(-inf) = 0
+  return m == -INFINITY ? 0.0f : m;  // a row of -inf: every term is then exp(-inf) = 0
+}
+
+// Unnormalised probabilities of a row in place of its logits, and the lane's part
+// of their sum.  Softmax: e^(z - max).  Sigmoid: sigma(z), in an all-negative row
+// divided by e^max so that the sum cannot underflow.  `slope` receives 1 - sigma.
+// A NaN or +inf in the row makes the warp's sum NaN (+inf: inf - inf; for the
+// sigmoid the maximum is checked), so the common path has no test per value.
+template <int M, bool SIG, bool SLOPE>
+__device__ __forceinline__ float row_terms(float (&v)[M], float (&slope)[SIG && SLOPE ? M : 1]) {
+  const float m = lane_max<M>(v);
   float sum = 0.0f;
-  if (!sigmoid) {
+  if constexpr (!SIG) {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      v[i] = expf(v[i] - m);
+      v[i] = exp_of(v[i] - m);
       sum += v[i];
     }
-    if constexpr (SLOPE) {
-#pragma unroll
-      for (int i = 0; i < M; ++i) slope[i] = 1.0f;
-    }
   } else if (m >= 0.0f) {
+    if (m > FLT_MAX) sum = NAN;
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      const float t = expf(fminf(-v[i], 80.0f));  // sigma below e^-80 adds nothing to a sum >= 1/2
-      const float s = v[i] == -INFINITY ? 0.0f : __fdividef(1.0f, 1.0f + t);
-      if constexpr (SLOPE) slope[i] = v[i] == -INFINITY ? 1.0f : t * s;
+      // a sigma below e^-80 adds nothing to a sum >= 1/2
+      const bool masked = v[i] == -INFINITY;
+      const float t = exp_of(v[i] < -80.0f ? 80.0f : -v[i]);
+      const float s = masked ? 0.0f : __fdividef(1.0f, 1.0f + t);
+      if constexpr (SLOPE) slope[i] = masked ? 1.0f : t * s;
       v[i] = s;
       sum += s;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      const float r = __fdividef(1.0f, 1.0f + expf(v[i]));
+      const float r = __fdividef(1.0f, 1.0f + exp_of(v[i]));
       if constexpr (SLOPE) slope[i] = r;
-      v[i] = expf(v[i] - m) * r;
+      v[i] = exp_of(v[i] - m) * r;
       sum += v[i];
     }
   }
-  sum = warp_add(sum);
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-  for (int i = 0; i < M; ++i) v[i] *= inv;
+  return sum;
 }
 
+// The row again with NaN as -inf and +inf as the largest finite value, reported.
 template <int VEC, int N>
-__global__ void __launch_bounds__(kBalThreads)
+__device__ __forceinline__ void reload_finite(const float* row, int E, int lane,
+                                              float (&v)[VEC * N], uint32_t* dev_status) {
+  load_row<VEC, N>(row, E, lane, v);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < VEC * N; ++i) {
+    if (!(v[i] <= FLT_MAX)) {
+      v[i] = isnan(v[i]) ? -INFINITY : FLT_MAX;
+      bad = true;
+    }
+  }
+  if (bad) report(dev_status, MOE_DEV_NONFINITE_LOGIT);
+}
+
+// A warp keeps the next token's row in flight while it works on the current one.
+template <int VEC, int N, bool SIG>
+__global__ void __launch_bounds__(kBalThreads, VEC * N <= 12 ? 2 : 1)
 balance_tile_kernel(const BalArgs a) {
   constexpr int M = VEC * N;
   __shared__ float s_sum[kBalWarps][32 * M];
   __shared__ int32_t s_cnt[kMaxE];
   __shared__ int32_t s_tok;
-  pdl_wait();
+  pdl_wait_then_trigger(a.early);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   check_offsets(a);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
@@ -190,19 +209,30 @@ balance_tile_kernel(const BalArgs a) {
     for (int i = threadIdx.x; i < a.E; i += kBalThreads) s_cnt[i] = 0;
     if (threadIdx.x == 0) s_tok = 0;
     __syncthreads();
-    float acc[M];
+    float acc[M], next[M];
 #pragma unroll
     for (int i = 0; i < M; ++i) acc[i] = 0.0f;
-    int live_tokens = 0;
+    int live_tokens = 0, next_id = MOE_ROUTE_MASKED;
+    auto fetch = [&](int t) {
+      load_row<VEC, N>(a.logits + static_cast<int64_t>(t) * a.E, a.E, lane, next);
+      next_id = lane < a.k ? __ldg(a.ids + static_cast<int64_t>(t) * a.k + lane) : MOE_ROUTE_MASKED;
+    };
+    if (b + warp < e) fetch(b + warp);
     for (int t = b + warp; t < e; t += kBalWarps) {
-      const int id = lane < a.k ? __ldg(a.ids + static_cast<int64_t>(t) * a.k + lane)
-                                : MOE_ROUTE_MASKED;
-      if (__shfl_sync(0xFFFFFFFFu, id, 0) == MOE_ROUTE_MASKED) continue;  // padding
       float v[M], none[1];
-      load_row<VEC, N>(a.logits + static_cast<int64_t>(t) * a.E, a.E, lane, v);
-      row_probs<M, false>(v, none, a.sigmoid, a.dev_status);
 #pragma unroll
-      for (int i = 0; i < M; ++i) acc[i] += v[i];
+      for (int i = 0; i < M; ++i) v[i] = next[i];
+      const int id = next_id;
+      if (t + kBalWarps < e) fetch(t + kBalWarps);
+      if (__shfl_sync(0xFFFFFFFFu, id, 0) == MOE_ROUTE_MASKED) continue;  // padding
+      float sum = warp_add(row_terms<M, SIG, false>(v, none));
+      if (isnan(sum)) {
+        reload_finite<VEC, N>(a.logits + static_cast<int64_t>(t) * a.E, a.E, lane, v, a.dev_status);
+        sum = warp_add(row_terms<M, SIG, false>(v, none));
+      }
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int i = 0; i < M; ++i) acc[i] += v[i] * inv;
       if (lane < a.k) {
         if (id >= 0 && id < a.E) atomicAdd(&s_cnt[id], 1);
         else if (id != MOE_ROUTE_MASKED) report(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
@@ -226,20 +256,20 @@ balance_tile_kernel(const BalArgs a) {
     if (threadIdx.x == 0) a.part_tok[slot] = s_tok;
     __syncthreads();
   }
-  pdl_trigger();
+  if (!a.early) pdl_trigger();
 }
 
-// One block per (32 experts, sequence): the sequence's slots in order (eight
+// One block per (32 experts, sequence): the sequence's slots in order (16
 // interleaved groups, then the groups in order).  The block that finishes last
-// adds the loss terms in order.
+// adds the loss terms, in an order fixed by their number.
 __global__ void __launch_bounds__(kBalThreads)
 balance_finish_kernel(const BalArgs a) {
-  __shared__ float s_sum[8][32];
-  __shared__ int32_t s_cnt[8][32];
-  __shared__ int32_t s_tok[8];
-  __shared__ double s_loss[kBalThreads];
+  __shared__ float s_sum[kBalWarps][32];
+  __shared__ int32_t s_cnt[kBalWarps][32];
+  __shared__ int32_t s_tok[kBalWarps];
+  __shared__ double s_loss[kBalWarps];
   __shared__ bool last;
-  pdl_wait();
+  pdl_wait_then_trigger(a.early);
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int eb = gridDim.x, q = blockIdx.y;
   const int e = blockIdx.x * 32 + lane;
@@ -249,9 +279,9 @@ balance_finish_kernel(const BalArgs a) {
   if (b < end) {
     const int64_t first = static_cast<int64_t>(b / a.tile) + q;
     const int n = (end - 1) / a.tile - b / a.tile + 1;
-#pragma unroll 4
-    for (int i = g; i < n; i += 8) {
-      if (e < a.E) {
+    if (e < a.E) {
+#pragma unroll 5
+      for (int i = g; i < n; i += kBalWarps) {
         sum += a.part_sum[(first + i) * a.E + e];
         cnt += a.part_cnt[(first + i) * a.E + e];
       }
@@ -266,9 +296,9 @@ balance_finish_kernel(const BalArgs a) {
   if (g == 0) {
     tok = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tok += s_tok[i];
+    for (int i = 0; i < kBalWarps; ++i) tok += s_tok[i];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
+    for (int i = 1; i < kBalWarps; ++i) {
       sum += s_sum[i][lane];
       cnt += s_cnt[i][lane];
     }
@@ -290,39 +320,45 @@ balance_finish_kernel(const BalArgs a) {
     }
   }
   __syncthreads();
-  if (!last) {
-    pdl_trigger();
-    return;
-  }
-  __threadfence();
-  double part = 0.0;
-  int used = 0;
-  const int64_t n_terms = static_cast<int64_t>(a.S) * eb;
-  for (int64_t i = threadIdx.x; i < n_terms; i += kBalThreads) part += __ldcg(a.part_loss + i);
-  for (int i = threadIdx.x; i < a.S; i += kBalThreads) used += __ldcg(a.tokens + i) > 0;
-  s_loss[threadIdx.x] = part;
-  s_cnt[g][lane] = used;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double total = 0.0;
-    int sequences = 0;
-    for (int i = 0; i < kBalThreads; ++i) {
-      total += s_loss[i];
-      sequences += s_cnt[i >> 5][i & 31];
+  if (last) {
+    __threadfence();
+    double part = 0.0;
+    int used = 0;
+    const int64_t n_terms = static_cast<int64_t>(a.S) * eb;
+    for (int64_t i = threadIdx.x; i < n_terms; i += kBalThreads) part += __ldcg(a.part_loss + i);
+    for (int i = threadIdx.x; i < a.S; i += kBalThreads) used += __ldcg(a.tokens + i) > 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+    used = __reduce_add_sync(0xFFFFFFFFu, used);
+    if (lane == 0) {
+      s_loss[g] = part;
+      s_tok[g] = used;
     }
-    a.tokens[a.S] = sequences;
-    *a.loss = sequences > 0 ? static_cast<float>(a.alpha * total / sequences) : 0.0f;
+    __syncthreads();
+    if (g == 0) {
+      part = lane < kBalWarps ? s_loss[lane] : 0.0;
+      used = __reduce_add_sync(0xFFFFFFFFu, lane < kBalWarps ? s_tok[lane] : 0);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+      if (lane == 0) {
+        a.tokens[a.S] = used;
+        *a.loss = used > 0 ? static_cast<float>(a.alpha * part / used) : 0.0f;
+      }
+    }
   }
-  pdl_trigger();
+  if (!a.early) pdl_trigger();
 }
 
-template <int VEC, int N>
-__global__ void __launch_bounds__(kBalThreads)
+// One warp per token.  The dot product and the sum are reduced together before the
+// row is normalised; the selected experts' terms reach their lanes through a row of
+// shared memory that is zero between tokens.
+template <int VEC, int N, bool SIG>
+__global__ void __launch_bounds__(kBwdThreads, VEC * N <= 12 ? 4 : 2)
 route_backward_kernel(const BalArgs a) {
   constexpr int M = VEC * N;
-  // gradients of the selected logits, scattered to their experts (zero between tokens)
-  __shared__ float s_sel[kBalWarps][32 * M];
-  pdl_wait();
+  constexpr int kWarps = kBwdThreads / 32;
+  __shared__ __align__(16) float s_sel[kWarps][32 * M];
+  pdl_wait_then_trigger(a.early);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* sel = s_sel[warp];
 #pragma unroll
@@ -338,89 +374,149 @@ route_backward_kernel(const BalArgs a) {
   }
   const int t0 = blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
   int seq_b = 0, seq_e = 0;  // bounds of the sequence whose weights are in w
-  float w[M];
+  float w[M], next[M];
 #pragma unroll
-  for (int i = 0; i < M; ++i) w[i] = 0.0f;
-  for (int t = t0 + warp; t < t1; t += kBalWarps) {
+  for (int i = 0; i < M; ++i) w[i] = next[i] = 0.0f;
+  int next_id = MOE_ROUTE_MASKED;
+  float next_g = 0.0f, next_dg = 0.0f;
+  auto fetch = [&](int t) {
     const int64_t at = static_cast<int64_t>(t) * a.k + lane;
-    float* out = a.dlogits + static_cast<int64_t>(t) * a.E;
-    const int id = lane < a.k ? __ldg(a.ids + at) : MOE_ROUTE_MASKED;
-    float v[M], slope[M];
-    if (__shfl_sync(0xFFFFFFFFu, id, 0) == MOE_ROUTE_MASKED) {  // padding: no gradient
+    next_id = lane < a.k ? __ldg(a.ids + at) : MOE_ROUTE_MASKED;
+    if (balance) load_row<VEC, N>(a.logits + static_cast<int64_t>(t) * a.E, a.E, lane, next);
+    next_g = next_dg = 0.0f;
+    if (a.dgates != nullptr && lane < a.k) {
+      next_g = __ldg(a.gates + at);
+      next_dg = __ldg(a.dgates + at);
+    }
+  };
+  if (t0 + warp < t1) fetch(t0 + warp);
+  for (int t = t0 + warp; t < t1; t += kWarps) {
+    float v[M], slope[SIG ? M : 1];
+    const float* row = a.logits + static_cast<int64_t>(t) * a.E;
+    const int id = next_id;
+    const bool ok = id >= 0 && id < a.E;
+    const float g = ok ? next_g : 0.0f, dg = ok ? next_dg : 0.0f;
 #pragma unroll
-      for (int i = 0; i < M; ++i) v[i] = 0.0f;
-    } else {
-      const float* row = a.logits + static_cast<int64_t>(t) * a.E;
-      if (balance) {
-        if (t < seq_b || t >= seq_e) {
-          const int q = seq_of(a, t);
-          seq_b = seq_bound(a, q);
-          seq_e = seq_bound(a, q + 1);
-          const bool inside = t >= seq_b && t < seq_e;
-          const float L = static_cast<float>(__ldg(a.tokens + q));
-          const float c = inside && L > 0.0f ? scale * a.E / (a.k * L) / L : 0.0f;
-          if (!inside) seq_e = seq_b;  // look again at the next token
+    for (int i = 0; i < M; ++i) v[i] = next[i];
+    if (t + kWarps < t1) fetch(t + kWarps);
+    const bool pad = __shfl_sync(0xFFFFFFFFu, id, 0) == MOE_ROUTE_MASKED;
+    if (balance && (t < seq_b || t >= seq_e)) {
+      const int q = seq_of(a, t);
+      seq_b = seq_bound(a, q);
+      seq_e = seq_bound(a, q + 1);
+      const bool inside = t >= seq_b && t < seq_e;
+      const float L = static_cast<float>(__ldg(a.tokens + q));
+      const float c = inside && L > 0.0f ? scale * a.E / (a.k * L) / L : 0.0f;
+      if (!inside) seq_e = seq_b;  // look again at the next token
 #pragma unroll
-          for (int i = 0; i < N; ++i)
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              const int e = VEC * (lane + 32 * i) + j;
-              w[VEC * i + j] =
-                  e < a.E ? c * __ldg(a.counts + static_cast<int64_t>(q) * a.E + e) : 0.0f;
-            }
+        for (int j = 0; j < VEC; ++j) {
+          const int e = VEC * (lane + 32 * i) + j;
+          w[VEC * i + j] =
+              e < a.E ? c * __ldg(a.counts + static_cast<int64_t>(q) * a.E + e) : 0.0f;
         }
-        load_row<VEC, N>(row, a.E, lane, v);
-        row_probs<M, true>(v, slope, a.sigmoid, a.dev_status);
-        float dot = 0.0f;
+    }
+    float inner = g * dg;
+    if (balance) {
+      float sum = row_terms<M, SIG, true>(v, slope);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < M; ++i) dot += v[i] * w[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {  // three chains side by side
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+        inner += __shfl_xor_sync(0xFFFFFFFFu, inner, o);
+      }
+      if (isnan(sum)) {
+        reload_finite<VEC, N>(row, a.E, lane, v, pad ? nullptr : a.dev_status);
+        sum = warp_add(row_terms<M, SIG, true>(v, slope));
+        dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < M; ++i) dot += v[i] * w[i];
         dot = warp_add(dot);
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = v[i] * (w[i] - dot) * slope[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < M; ++i) v[i] = 0.0f;
       }
-      if (a.dgates != nullptr) {
-        const bool ok = id >= 0 && id < a.E;
-        if (!ok && id != MOE_ROUTE_MASKED) report(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
-        const float g = ok ? __ldg(a.gates + at) : 0.0f;
-        const float dg = ok ? __ldg(a.dgates + at) : 0.0f;
-        const float inner = warp_add(g * dg);
-        float dz = g * (dg - (a.sigmoid ? inner / a.route_scale : inner));
-        if (a.sigmoid && ok) dz *= __fdividef(1.0f, 1.0f + expf(fminf(__ldg(row + id), 80.0f)));
-        if (ok) atomicAdd(sel + id, dz);
-        __syncwarp();
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float shift = dot * inv;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+      for (int i = 0; i < M; ++i) {
+        v[i] = v[i] * inv * (w[i] - shift);
+        if constexpr (SIG) v[i] *= slope[i];
+      }
+    } else {
+      inner = warp_add(inner);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) v[VEC * i + j] += sel[VEC * (lane + 32 * i) + j];
-        __syncwarp();
+      for (int i = 0; i < M; ++i) v[i] = 0.0f;
+    }
+    if (a.dgates != nullptr && !pad) {
+      if (!ok && id != MOE_ROUTE_MASKED) report(a.dev_status, MOE_DEV_BAD_EXPERT_ID);
+      float dz = g * (dg - (SIG ? inner / a.route_scale : inner));
+      if (SIG && ok) {
+        const float z = __ldg(row + id);
+        dz *= __fdividef(1.0f, 1.0f + exp_of(fminf(z, 80.0f)));
+      }
+      // each lane leaves its number at its expert: one that finds another's there
+      // shares the expert (ids that moe_route did not write), and the slots are then
+      // added one by one in slot order
+      if (ok) sel[id] = __int_as_float(lane);
+      __syncwarp();
+      const bool shared_id = ok && __float_as_int(sel[id]) != lane;
+      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, shared_id)) {
         if (ok) sel[id] = 0.0f;
         __syncwarp();
+        for (int j = 0; j < a.k; ++j) {
+          if (lane == j && ok) sel[id] += dz;
+          __syncwarp();
+        }
+      } else if (ok) {
+        sel[id] = dz;
       }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if constexpr (VEC == 4) {
+          const float4 s = *reinterpret_cast<const float4*>(sel + 4 * (lane + 32 * i));
+          v[4 * i] += s.x; v[4 * i + 1] += s.y; v[4 * i + 2] += s.z; v[4 * i + 3] += s.w;
+        } else {
+          v[i] += sel[lane + 32 * i];
+        }
+      }
+      __syncwarp();
+      if (ok) sel[id] = 0.0f;
+      __syncwarp();
     }
+    float* out = a.dlogits + static_cast<int64_t>(t) * a.E;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = VEC * (lane + 32 * i);
       if (e < a.E) {
         if constexpr (VEC == 4)
           *reinterpret_cast<float4*>(out + e) =
-              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              pad ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                  : make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         else
-          out[e] = v[i];
+          out[e] = pad ? 0.0f : v[i];
       }
     }
   }
-  pdl_trigger();
+  if (!a.early) pdl_trigger();
 }
 
 // --------------------------------- host side --------------------------------
 
-// Tokens per block: four blocks per SM, at least one token per warp.
+// Tokens per block of the forward: two blocks per SM (few slots for the second
+// launch to add), at least one token per warp.
 int tile_tokens(int T) {
-  const int64_t c = ceil_div(T, 4 * 152);
+  const int64_t c = ceil_div(T, 2 * 152);
   return static_cast<int>(c < kBalWarps ? kBalWarps : c);
+}
+
+// The backward has no slots: four blocks per SM.
+int backward_tokens(int T) {
+  const int64_t c = ceil_div(T, 4 * 152);
+  return static_cast<int>(c < kBwdThreads / 32 ? kBwdThreads / 32 : c);
 }
 
 int64_t slots(int T, int S) { return ceil_div(T, tile_tokens(T)) + S; }
@@ -458,33 +554,39 @@ moe_status check_balance(const moe_route_params* p, int32_t n_seq, const int32_t
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Values per lane: 16-byte pieces where the rows allow them.
-template <template <int, int> class Launch, typename... Args>
-void by_width(int E, bool vec4, Args&&... args) {
+template <template <int, int, bool> class Launch, bool SIG>
+void by_width(bool vec4, const BalArgs& a, unsigned grid, cudaStream_t s) {
+  const int E = a.E;
   if (vec4) {
-    if (E <= 128) Launch<4, 1>::go(args...);
-    else if (E <= 256) Launch<4, 2>::go(args...);
-    else if (E <= 384) Launch<4, 3>::go(args...);
-    else Launch<4, 4>::go(args...);
+    if (E <= 128) Launch<4, 1, SIG>::go(a, grid, s);
+    else if (E <= 256) Launch<4, 2, SIG>::go(a, grid, s);
+    else if (E <= 384) Launch<4, 3, SIG>::go(a, grid, s);
+    else Launch<4, 4, SIG>::go(a, grid, s);
   } else {
-    if (E <= 32) Launch<1, 1>::go(args...);
-    else if (E <= 64) Launch<1, 2>::go(args...);
-    else if (E <= 128) Launch<1, 4>::go(args...);
-    else if (E <= 256) Launch<1, 8>::go(args...);
-    else Launch<1, 16>::go(args...);
+    if (E <= 32) Launch<1, 1, SIG>::go(a, grid, s);
+    else if (E <= 128) Launch<1, 4, SIG>::go(a, grid, s);
+    else if (E <= 256) Launch<1, 8, SIG>::go(a, grid, s);
+    else Launch<1, 16, SIG>::go(a, grid, s);
   }
 }
 
-template <int VEC, int N>
+template <template <int, int, bool> class Launch>
+void by_score(bool vec4, const BalArgs& a, unsigned grid, cudaStream_t s) {
+  if (a.sigmoid) by_width<Launch, true>(vec4, a, grid, s);
+  else by_width<Launch, false>(vec4, a, grid, s);
+}
+
+template <int VEC, int N, bool SIG>
 struct TileLaunch {
   static void go(const BalArgs& a, unsigned grid, cudaStream_t s) {
-    launch(balance_tile_kernel<VEC, N>, dim3(grid), dim3(kBalThreads), 0, s, a);
+    launch(balance_tile_kernel<VEC, N, SIG>, dim3(grid), dim3(kBalThreads), 0, s, a);
   }
 };
 
-template <int VEC, int N>
+template <int VEC, int N, bool SIG>
 struct BackwardLaunch {
   static void go(const BalArgs& a, unsigned grid, cudaStream_t s) {
-    launch(route_backward_kernel<VEC, N>, dim3(grid), dim3(kBalThreads), 0, s, a);
+    launch(route_backward_kernel<VEC, N, SIG>, dim3(grid), dim3(kBwdThreads), 0, s, a);
   }
 };
 
@@ -496,7 +598,6 @@ BalArgs base_args(const moe_route_params* p, int32_t n_seq, const int32_t* off,
   a.k = p->k;
   a.S = n_seq;
   a.sigmoid = p->score_fn == MOE_SCORE_SIGMOID_GROUP;
-  a.tile = tile_tokens(p->T);
   a.alpha = alpha;
   a.route_scale = p->route_scale;
   a.off = off;
@@ -545,12 +646,13 @@ MOE_API moe_status moe_balance_loss(const moe_route_params* p, int32_t n_seq,
   a.probs = mean_probs;
   a.loss = loss;
   cudaStream_t s = as_cuda(stream);
-  const int64_t tiles = ceil_div(p->T, a.tile);
-  by_width<TileLaunch>(p->E, p->E % 4 == 0 && aligned16(logits), a,
-                       static_cast<unsigned>(tiles > 0 ? tiles : 1), s);
-  launch(balance_finish_kernel,
-         dim3(static_cast<unsigned>(ceil_div(p->E, 32)), static_cast<unsigned>(n_seq)),
-         dim3(kBalThreads), 0, s, a);
+  a.tile = tile_tokens(p->T);
+  const int64_t tiles = p->T > 0 ? ceil_div(p->T, a.tile) : 1;
+  a.early = one_wave(tiles);
+  by_score<TileLaunch>(p->E % 4 == 0 && aligned16(logits), a, static_cast<unsigned>(tiles), s);
+  const dim3 grid(static_cast<unsigned>(ceil_div(p->E, 32)), static_cast<unsigned>(n_seq));
+  a.early = one_wave(static_cast<int64_t>(grid.x) * grid.y);
+  launch(balance_finish_kernel, grid, dim3(kBalThreads), 0, s, a);
   return launch_status();
 }
 
@@ -579,7 +681,10 @@ MOE_API moe_status moe_route_backward(const moe_route_params* p, int32_t n_seq,
   a.tokens = const_cast<int32_t*>(seq_tokens);
   a.dloss = dloss;
   a.dlogits = dlogits;
-  by_width<BackwardLaunch>(p->E, p->E % 4 == 0 && aligned16(logits) && aligned16(dlogits), a,
-                           static_cast<unsigned>(ceil_div(p->T, a.tile)), as_cuda(stream));
+  a.tile = backward_tokens(p->T);
+  const int64_t blocks = ceil_div(p->T, a.tile);
+  a.early = one_wave(blocks);
+  by_score<BackwardLaunch>(p->E % 4 == 0 && aligned16(logits) && aligned16(dlogits), a,
+                           static_cast<unsigned>(blocks), as_cuda(stream));
   return launch_status();
 }
