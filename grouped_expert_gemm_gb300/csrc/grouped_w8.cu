@@ -15,14 +15,14 @@
 // power-of-two scale factors.
 //
 // Tile: 128 rows x 256 weight columns (gate/up: 128 gate + the same 128 up, so a
-// tile makes one whole scale group of H; down: 256 columns of y).  Roles of the 384
-// threads, one CTA per SM, persistent over the tiles:
+// tile makes one whole scale group of H; down: 256 columns of y).  Roles of the 320
+// threads (so that each may hold 200 registers), one CTA per SM, persistent over the
+// tiles:
 //   warp 0       TMA producer: [128 x 128] codes of A, two [128 x 128] of B, 48 KB
 //                a stage, four stages
 //   warp 1       allocates tensor memory; lane 0 issues four MMAs (K = 32) a stage
-//   warps 2, 3   idle (they give their registers to the promotion warps)
-//   warps 4..11  promotion and epilogue: warp w reads lanes 32 (w % 4).., columns of
-//                half (w - 4) / 4; 128 fp32 sums per thread
+//   warps 2..9   promotion and epilogue: warp w reads lanes 32 (w % 4).., columns of
+//                half (w - 2) / 4; 128 fp32 sums per thread
 // Two tensor-memory buffers of 256 columns: block kb + 1 is summed while kb is
 // promoted.  Every wait is bounded (MOE_DEV_TIMEOUT), as in the bf16 pass.
 #include <mutex>
@@ -40,9 +40,7 @@ constexpr int kBBox = 128 * kBK;           // 16 KB: one box of 128 weight rows
 constexpr int kStageBytes = kABytes + 2 * kBBox;
 constexpr int kStages = 4;
 constexpr int kAccCols = 256;
-constexpr int kThreads = 384;
-constexpr int kRegsLaunch = 168, kRegsAcc = 208, kRegsRest = 88;
-static_assert(256 * kRegsAcc + 128 * kRegsRest <= kThreads * kRegsLaunch, "register split");
+constexpr int kThreads = 320;
 
 constexpr float kE4M3Max = 448.0f;
 constexpr uint32_t kAbsInf = 0x7F800000u;
@@ -147,11 +145,11 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
   return amax == 0 ? 1.0f : __fdiv_rn(__uint_as_float(amax), kE4M3Max);
 }
 
-// acc += part * s on 32 columns.
-__device__ __forceinline__ void promote32(const uint32_t (&part)[32], float s, float2* acc) {
+// acc += part * s on 16 columns.
+__device__ __forceinline__ void promote16(const uint32_t (&part)[16], float s, float2* acc) {
   const float2 s2 = make_float2(s, s);
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 8; ++i)
     acc[i] = __ffma2_rn(make_float2(__uint_as_float(part[2 * i]), __uint_as_float(part[2 * i + 1])),
                         s2, acc[i]);
 }
@@ -196,16 +194,15 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   }
   if (warp == 1) umma_alloc(smem_u32(tb.tmem_slot), 2 * kAccCols);
   pdl_wait();
-  if (threadIdx.x >= 128 && threadIdx.x < 256)
-    build_table(a, kBM, n_blocks, threadIdx.x - 128, tb);
+  if (threadIdx.x >= 64 && threadIdx.x < 192)
+    build_table(a, kBM, n_blocks, threadIdx.x - 64, tb);
   umma_fence_before();
   __syncthreads();
   umma_fence_after();
   const uint32_t tmem = *tb.tmem_slot;
   const int total = tb.start[a.n_seg];
 
-  if (warp < 4) {
-    reg_dec<kRegsRest>();
+  if (warp < 2) {
     if (warp == 0 && lane == 0) {
       // ---- TMA producer ----
       int s = 0;
@@ -267,9 +264,8 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
       }
     }
   } else {
-    reg_inc<kRegsAcc>();
     // ---- promotion and epilogue ----
-    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
     const int r = quad * 32 + lane;
     const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     // columns of the two 64-wide pieces this thread sums, and their scale blocks
@@ -305,22 +301,20 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
         }
         umma_fence_after();
         const uint32_t ta = taddr0 + buf * kAccCols;
-        uint32_t u[32], v[32];
-        umma_ld32(ta + c0, u);
-        umma_ld_wait(u);
-        umma_ld32(ta + c0 + 32, v);
-        promote32(u, s0, acc0);
-        umma_ld_wait(v);
-        umma_ld32(ta + c1, u);
-        promote32(v, s0, acc0 + 16);
-        umma_ld_wait(u);
-        umma_ld32(ta + c1 + 32, v);
-        promote32(u, s1, acc1);
-        umma_ld_wait(v);
-        umma_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty_bar(buf));
-        promote32(v, s1, acc1 + 16);
+        // eight pieces of 16 columns, the next one on its way while one is added
+        uint32_t u[2][16];
+        umma_ld16(ta + c0, u[0]);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          umma_ld_wait(u[p & 1]);
+          if (p < 7) umma_ld16(ta + (p + 1 < 4 ? c0 : c1) + 16 * ((p + 1) & 3), u[(p + 1) & 1]);
+          if (p == 7) {
+            umma_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(buf));
+          }
+          promote16(u[p & 1], p < 4 ? s0 : s1, (p < 4 ? acc0 : acc1) + 8 * (p & 3));
+        }
         if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
       }
       if (!ok) break;
@@ -346,7 +340,13 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
         top = max(top, am[(half ^ 1) * 128 + r]);
         if (live) {
           const float s = scale_of(top);
-          if (top >= kAbsInf) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
+          // One reciprocal a row instead of 64 divisions (H itself is known to fp32
+          // rounding only; with the divisions the epilogue took 3 us a tile, a
+          // fifth of the pass at K = 4096).  A scale near the type's smallest
+          // values is taken 2^64 larger, so that its reciprocal stays finite.
+          const float k = s < 0x1p-60f ? 0x1p64f : 1.0f;
+          const float inv = __frcp_rn(s * k);
+          if (top >= kAbsInf && half == 0) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
           if (half == 0) a.hs[row * a.GN + tl.nb] = s;
           const int n0 = tl.nb * 128 + 64 * half;
           uint8_t* dst = a.hq + row * a.N + n0;
@@ -358,9 +358,9 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
               for (int i = 0; i < 4; ++i) {
                 const float2 x = acc0[8 * j + 2 * i], z = acc0[8 * j + 2 * i + 1];
                 const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                    make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)), __NV_SATFINITE, __NV_E4M3);
+                    make_float2(x.x * k * inv, x.y * k * inv), __NV_SATFINITE, __NV_E4M3);
                 const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-                    make_float2(__fdiv_rn(z.x, s), __fdiv_rn(z.y, s)), __NV_SATFINITE, __NV_E4M3);
+                    make_float2(z.x * k * inv, z.y * k * inv), __NV_SATFINITE, __NV_E4M3);
                 p[i] = lo | (hi << 16);
               }
               *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(p[0], p[1], p[2], p[3]);

@@ -242,3 +242,23 @@ def test_quantize_weights_bit_exact(n, K, N):
     w[n - 1, K - 1, N - 1] = float("inf")
     g.moe_quantize_weights_fp8(n, K, N, w, q, s, st)
     assert int(st.item()) == g.MOE_DEV_NONFINITE_INPUT
+
+
+def test_tiny_and_huge_rows():
+    """Scales near the ends of fp32: rows whose H is about 1e-38 and about 1e30."""
+    t = make(256, 256, [5, 130], seed=14)
+    t["xs"][1] *= 1e-19   # G and U about 1e-19, H about 1e-38: its scale is below 2^-126
+    t["xs"][3] *= 1e-10
+    t["xs"][7] *= 1e15
+    hq, hs, st = gate_up(t)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    for i, e in ((1, 0), (3, 0), (7, 1)):
+        x = t["xq"][i:i + 1].double() * ref.spread(t["xs"][i:i + 1].double(), 256, 128)
+        h = ref.swiglu_hidden(x, *(ref.dequant_blocks(t["w"][j][0][e], t["w"][j][1][e]) for j in (0, 1)))
+        s = ref.scales(h, 128)
+        val = hq[i:i + 1].view(F8).double() * ref.spread(hs[i:i + 1].double(), 256, 128)
+        # fp32 holds values this small to 2^-149 only, the scales among them
+        room = torch.maximum(h.abs() * 2.0 ** -4, ref.spread(s, 256, 128) * 2.0 ** -10) * 1.01
+        floor = 449 * 2.0 ** -149
+        assert ((val - h).abs() <= room + 1e-3 * h.abs().max() + floor).all()
