@@ -25,6 +25,7 @@
 //                half (w - 2) / 4; 128 fp32 sums per thread
 // Two tensor-memory buffers of 256 columns: block kb + 1 is summed while kb is
 // promoted.  Every wait is bounded (MOE_DEV_TIMEOUT), as in the bf16 pass.
+#include <algorithm>
 #include <mutex>
 
 #include "umma.cuh"
@@ -58,6 +59,7 @@ struct W8Args {
   uint16_t* y;         // down
   uint32_t* dev_status;
   int m_outer;
+  int chained;         // few-rows down pass right behind its gate/up pass
 };
 
 struct Tile {
@@ -384,6 +386,7 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   }
 
   // ---- teardown ----
+  __syncwarp();
   umma_fence_before();
   __syncthreads();
   umma_fence_after();
@@ -397,6 +400,336 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
 constexpr int kSmemBytes =
     1024 + kStages * kStageBytes + (2 * kStages + 9) * 8 + 512 * 4 + kTableInts * 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// ------------------------------- few rows a segment --------------------------
+// Decode-sized segments stream the weights; a 128-row tile would stage and sum
+// mostly foreign rows.  Here the weights are the M operand: two [128 x 128] weight
+// boxes a stage (gate and up of 128 columns, or 256 columns of down) against a box
+// of NT rows, so D^T is [2 x 128 columns] x [NT rows].  A promotion thread owns one
+// weight column and NT sums; the rows' scales come to it by shuffles.  Eight
+// promotion warps: the four lane quadrants of either box.  Four tensor-memory
+// buffers of 2 x NT columns.
+//
+// With SPLIT = 2 a cluster of two CTAs shares a tile, each taking half of the
+// reduction blocks; rank 1 hands its sums to rank 0 through distributed shared
+// memory and rank 0 adds them to its own.  Taken when the tiles are fewer than half
+// of the SMs: one SM streams about 60 GB/s, so the number of SMs that stream sets
+// the time.
+//
+// CHAINED (down pass issued by moe_grouped_swiglu_w8 right behind its gate/up pass):
+// the segment table and the first stages' weights, which the gate/up pass does not
+// write, are read before waiting for it.
+
+constexpr int kFewBufs = 4;
+constexpr int kFewThreads = 320;
+
+template <bool SWIGLU, int NT, int SPLIT>
+struct Few {
+  static constexpr int kStageBytes = 2 * kBBox + NT * kBK;
+  static constexpr int kUpBytes = SWIGLU ? NT * 128 * 4 : 0;              // up sums for the gate warps
+  static constexpr int kRedBytes = SPLIT > 1 ? 2 * NT * 128 * 4 : 0;      // rank 1's sums
+  static constexpr int kTopBytes = 2 * 4 * NT * 4;
+  // bars: full[S], empty[S], tfull[4], tempty[4], upfull, upfree, top, red, redfree, drain
+  static constexpr int kFixed = 1024 + kUpBytes + kRedBytes + kTopBytes + kTableInts * 4 + 64 * 8;
+  static constexpr int kStages = (227 * 1024 - kFixed) / kStageBytes;
+  static constexpr int kBars = 2 * kStages + 2 * kFewBufs + 6;
+  static constexpr int kTmem = kFewBufs * 2 * NT;
+  static constexpr int kSmem = kFixed + kStages * kStageBytes;
+  static_assert(kBars <= 64 && kStages >= 4 && kSmem <= 227 * 1024, "shared memory");
+  static_assert(kTmem <= 512 && kTmem >= 32, "tensor memory");
+};
+
+template <bool SWIGLU, int NT, int SPLIT>
+__global__ void __launch_bounds__(kFewThreads, 1)
+grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
+                      const __grid_constant__ CUtensorMap map_w0,
+                      const __grid_constant__ CUtensorMap map_w1, const W8Args a) {
+  using F = Few<SWIGLU, NT, SPLIT>;
+  constexpr int kStages = F::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stage_base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage_base + kStages * F::kStageBytes);
+  float* s_up = reinterpret_cast<float*>(bars + 64);                          // [NT][128]
+  float* s_red = s_up + F::kUpBytes / 4;                                      // [2][NT][128]
+  uint32_t* s_top = reinterpret_cast<uint32_t*>(s_red + F::kRedBytes / 4);    // [2][4][NT]
+  const Table tb = carve_table(reinterpret_cast<int*>(s_top + F::kTopBytes / 4));
+  volatile int* abort_flag = tb.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kCols = SWIGLU ? 128 : 256;  // output columns per tile
+  const int n_blocks = (a.N + kCols - 1) / kCols;
+  const int rank = SPLIT > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int group = static_cast<int>(blockIdx.x) / SPLIT, groups = static_cast<int>(gridDim.x) / SPLIT;
+  const int kb0 = rank * a.GK / SPLIT, kb1 = (rank + 1) * a.GK / SPLIT;
+
+  auto full_bar = [&](int s) { return smem_u32(bars + s); };
+  auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
+  auto tfull_bar = [&](int b) { return smem_u32(bars + 2 * kStages + b); };
+  auto tempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + kFewBufs + b); };
+  auto bar_of = [&](int i) { return smem_u32(bars + 2 * kStages + 2 * kFewBufs + i); };
+  const uint32_t up_full = bar_of(0), up_free = bar_of(1), top_bar = bar_of(2), red_full = bar_of(3),
+                 red_free = bar_of(4), drain_bar = bar_of(5);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < kFewBufs; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 8);
+    }
+    mbar_init(up_full, 4);
+    mbar_init(up_free, 4);
+    mbar_init(top_bar, 4);
+    mbar_init(red_full, 256);
+    mbar_init(red_free, 256);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w0)) : "memory");
+    if (SWIGLU)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w1)) : "memory");
+  }
+  if (warp == 1) umma_alloc(smem_u32(tb.tmem_slot), F::kTmem);
+  if (!a.chained) pdl_wait();
+  // one CTA per SM: all of the grid is resident once all have passed here
+  if (SWIGLU) pdl_trigger();
+  if (threadIdx.x >= 64 && threadIdx.x < 192) build_table(a, NT, n_blocks, threadIdx.x - 64, tb);
+  umma_fence_before();
+  if constexpr (SPLIT > 1) cluster_sync();  // the partner's barriers are initialised
+  else __syncthreads();
+  umma_fence_after();
+  const uint32_t tmem = *tb.tmem_slot;
+  const int total = tb.start[a.n_seg];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- TMA producer ----
+      auto load_weights = [&](const Tile& tl, int kb, int s) {
+        const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
+        mbar_arrive_expect_tx(full_bar(s), F::kStageBytes);
+        tma_load_3d(st, &map_w0, full_bar(s), kb * kBK, tl.nb * kCols, tl.seg);
+        tma_load_3d(st + kBBox, SWIGLU ? &map_w1 : &map_w0, full_bar(s), kb * kBK,
+                    SWIGLU ? tl.nb * kCols : tl.nb * kCols + 128, tl.seg);
+      };
+      int s = 0, ahead = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      if (a.chained) {
+        if (group < total) {
+          const Tile tl = tile_of(group, tb, a.n_seg, NT, n_blocks, a.m_outer);
+          ahead = min(kStages, kb1 - kb0);
+          for (int i = 0; i < ahead; ++i) load_weights(tl, kb0 + i, i);
+        }
+        pdl_wait();  // the rows are the previous pass's output
+      }
+      for (int t = group; t < total && ok; t += groups) {
+        const Tile tl = tile_of(t, tb, a.n_seg, NT, n_blocks, a.m_outer);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (ahead > 0) {
+            --ahead;
+          } else {
+            if (!wait_bounded(empty_bar(s), ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
+            load_weights(tl, kb, s);
+          }
+          tma_load_2d(smem_u32(stage_base + s * F::kStageBytes + 2 * kBBox), &map_x, full_bar(s),
+                      kb * kBK, tl.row0);
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (!ok) {
+        for (int i = 0; i < kStages; ++i) {
+          if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+          wait_drain(full_bar(s), ph);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- MMA issuer: gate (or the first 128 columns), then up (the second) ----
+      constexpr uint32_t idesc = umma_idesc_e4m3(128, NT);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true, issued = false;
+      for (int t = group; t < total && ok; t += groups) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait_bounded(tempty_bar(buf), acc_ph ^ 1u, abort_flag, a.dev_status) ||
+              !wait_bounded(full_bar(s), ph, abort_flag, a.dev_status)) {
+            ok = false;
+            break;
+          }
+          umma_fence_after();
+          const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
+          const uint32_t dst = tmem + buf * (2 * NT);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f8(dst + h * NT, umma_desc(st + h * kBBox + kk * 32),
+                      umma_desc(st + 2 * kBBox + kk * 32), idesc, kk > 0);
+          issued = true;
+          umma_commit(empty_bar(s));
+          umma_commit(tfull_bar(buf));
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+          if (++buf == kFewBufs) { buf = 0; acc_ph ^= 1u; }
+        }
+      }
+      if (!ok && issued) {
+        umma_commit(drain_bar);
+        wait_drain(drain_bar, 0);
+      }
+    }
+  } else {
+    // ---- promotion and epilogue ----
+    if (a.chained) pdl_wait();  // the rows' scales
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int m = quad * 32 + lane;
+    const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * NT;
+    constexpr int kPer = (NT + 31) / 32;  // rows whose scales this lane holds
+    int buf = 0;
+    uint32_t acc_ph = 0, tile_ph = 0;
+    bool ok = true;
+    for (int t = group; t < total; t += groups, tile_ph ^= 1u) {
+      const Tile tl = tile_of(t, tb, a.n_seg, NT, n_blocks, a.m_outer);
+      const int nblk = SWIGLU ? tl.nb : min(2 * tl.nb + half, a.GN - 1);
+      const float* ws = (SWIGLU && half ? a.bs1 : a.bs0) +
+                        (static_cast<int64_t>(tl.seg) * a.GN + nblk) * a.GK;
+      const float* xs[kPer];
+      float x[kPer], w = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        xs[i] = a.as + static_cast<int64_t>(min(tl.row0 + min(lane + 32 * i, NT - 1), a.max_rows - 1)) * a.GK;
+        x[i] = kb0 < kb1 ? __ldg(xs[i] + kb0) : 0.0f;
+      }
+      if (kb0 < kb1) w = __ldg(ws + kb0);
+      float acc[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        float p[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) p[i] = x[i] * w;
+        if (kb + 1 < kb1) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) x[i] = __ldg(xs[i] + kb + 1);
+          w = __ldg(ws + kb + 1);
+        }
+        if (!__all_sync(0xFFFFFFFFu,
+                        wait_bounded(tfull_bar(buf), acc_ph, abort_flag, a.dev_status))) {
+          ok = false;
+          break;
+        }
+        umma_fence_after();
+        const uint32_t ta = taddr0 + buf * (2 * NT);
+#pragma unroll
+        for (int c = 0; c < NT; c += 16) {
+          uint32_t u[16];
+          umma_ld16(ta + c, u);
+          umma_ld_wait(u);
+          if (c + 16 == NT) {
+            umma_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(buf));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            acc[c + j] = fmaf(__uint_as_float(u[j]),
+                              __shfl_sync(0xFFFFFFFFu, p[(c + j) / 32], (c + j) & 31), acc[c + j]);
+        }
+        if (++buf == kFewBufs) { buf = 0; acc_ph ^= 1u; }
+      }
+      if (!ok) break;
+      if constexpr (SPLIT > 1) {
+        float* mine = s_red + half * (NT * 128) + m;
+        if (rank == 1) {
+          if (!__all_sync(0xFFFFFFFFu, wait_bounded<true>(red_free, tile_ph ^ 1u, abort_flag, a.dev_status)))
+            break;
+          const uint32_t dst = map_to_rank(smem_u32(mine), 0);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) st_cluster(dst + j * 512, acc[j]);
+          mbar_arrive_cluster(map_to_rank(red_full, 0));
+          continue;
+        }
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded<true>(red_full, tile_ph, abort_flag, a.dev_status)))
+          break;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j] += mine[j * 128];
+        mbar_arrive_cluster(map_to_rank(red_free, 1));
+      }
+      if constexpr (SWIGLU) {
+        if (half == 1) {
+          if (!__all_sync(0xFFFFFFFFu, wait_bounded(up_free, tile_ph ^ 1u, abort_flag, a.dev_status)))
+            break;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) s_up[j * 128 + m] = acc[j];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(up_full);
+          continue;
+        }
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(up_full, tile_ph, abort_flag, a.dev_status))) break;
+        uint32_t* tops = s_top + tile_ph * (4 * NT);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          acc[j] = __fdividef(acc[j], 1.0f + __expf(-acc[j])) * s_up[j * 128 + m];
+          const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(acc[j]) & 0x7FFFFFFFu);
+          if (lane == (j & 31)) tops[quad * NT + j] = v;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(up_free);
+          mbar_arrive(top_bar);
+        }
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(top_bar, tile_ph, abort_flag, a.dev_status))) break;
+        float k[kPer], inv[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int j = min(lane + 32 * i, NT - 1);
+          const uint32_t top = max(max(tops[j], tops[NT + j]), max(tops[2 * NT + j], tops[3 * NT + j]));
+          const float s = scale_of(top);
+          k[i] = s < 0x1p-60f ? 0x1p64f : 1.0f;  // as in the 128-row kernel
+          inv[i] = __frcp_rn(s * k[i]);
+          if (quad == 0 && lane + 32 * i < tl.rows) {
+            if (top >= kAbsInf) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
+            a.hs[static_cast<int64_t>(tl.row0 + j) * a.GN + tl.nb] = s;
+          }
+        }
+        const int n = tl.nb * 128 + m;
+        uint8_t* dst = a.hq + static_cast<int64_t>(tl.row0) * a.N + n;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float kj = __shfl_sync(0xFFFFFFFFu, k[j / 32], j & 31);
+          const float ij = __shfl_sync(0xFFFFFFFFu, inv[j / 32], j & 31);
+          if (j < tl.rows && n < a.N)
+            dst[static_cast<int64_t>(j) * a.N] =
+                __nv_cvt_float_to_fp8(acc[j] * kj * ij, __NV_SATFINITE, __NV_E4M3);
+        }
+      } else {
+        const int n = tl.nb * 256 + half * 128 + m;
+        uint16_t* dst = a.y + static_cast<int64_t>(tl.row0) * a.N + n;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (j < tl.rows && n < a.N)
+            dst[static_cast<int64_t>(j) * a.N] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[j]));
+      }
+    }
+  }
+
+  // ---- teardown ----
+  __syncwarp();
+  umma_fence_before();
+  if constexpr (SPLIT > 1) cluster_sync();  // no CTA leaves while its partner may still reach it
+  else __syncthreads();
+  umma_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    umma_dealloc(tmem, F::kTmem);
+  }
+  pdl_trigger();
+}
 
 // ------------------------------ weight quantization --------------------------
 
@@ -522,13 +855,97 @@ moe_status check_shape(int32_t n_seg, int32_t K, int32_t N, int32_t max_rows) {
   return MOE_OK;
 }
 
+// Clusters of two CTAs that can be resident at once, read once per kernel and device.
+template <typename Kernel>
+int resident_pairs(Kernel kern, int threads, int smem, std::mutex& mu, int (&cache)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sm_count() & ~1));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = sm_count() / 2;
+    }
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+template <bool SWIGLU, int NT, int SPLIT>
+moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtensorMap& m1,
+                      const W8Args& a, cudaStream_t s) {
+  using F = Few<SWIGLU, NT, SPLIT>;
+  auto kern = grouped_w8_few_kernel<SWIGLU, NT, SPLIT>;
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (!opt_in(kern, F::kSmem, mu, done)) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  unsigned grid = static_cast<unsigned>(sm_count());
+  if constexpr (SPLIT > 1) {
+    static std::mutex mu2;
+    static int pairs[64] = {};
+    const int n = resident_pairs(kern, kFewThreads, F::kSmem, mu2, pairs);
+    if (n <= 0) return MOE_ERR_CUDA;
+    grid = static_cast<unsigned>(2 * n);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.gridDim = dim3(grid);
+  cudaLaunchKernelEx(&cfg, kern, mx, m0, m1, a);
+  return launch_status();
+}
+
+// Rows per tile: the few-rows kernel with four times the average rows a segment
+// (segments are uneven), from 16 to 64; above, the 128-row kernel.
+int choose_rows(int32_t n_seg, int32_t max_rows) {
+  const int64_t four_avg = 4 * static_cast<int64_t>(max_rows) / n_seg;
+  return four_avg <= 16 ? 16 : four_avg <= 32 ? 32 : four_avg <= 64 ? 64 : kBM;
+}
+
 template <bool SWIGLU>
-moe_status launch_pass(const W8Args& a, const void* x, const void* b0, const void* b1,
+moe_status launch_pass(W8Args a, const void* x, const void* b0, const void* b1, bool chained,
                        cudaStream_t s) {
+  const int nt = choose_rows(a.n_seg, a.max_rows);
   CUtensorMap ma, m0, m1;
-  if (!map_rows(&ma, x, a.max_rows, a.K, kBM) || !map_weights(&m0, b0, a.n_seg, a.N, a.K, 128) ||
+  if (!map_rows(&ma, x, a.max_rows, a.K, nt) || !map_weights(&m0, b0, a.n_seg, a.N, a.K, 128) ||
       !map_weights(&m1, b1, a.n_seg, a.N, a.K, 128))
     return MOE_ERR_CUDA;
+  if (nt < kBM) {
+    a.chained = chained;
+    a.m_outer = 0;
+    // tiles that hold rows, at most: split the reduction where they leave half of the
+    // SMs idle
+    const int64_t tiles = std::min<int64_t>(a.n_seg, a.max_rows) * ceil_div(a.N, SWIGLU ? 128 : 256);
+    const bool split = 2 * tiles <= sm_count() && a.GK >= 2;
+    if (nt == 16) return split ? launch_few<SWIGLU, 16, 2>(ma, m0, m1, a, s)
+                               : launch_few<SWIGLU, 16, 1>(ma, m0, m1, a, s);
+    if (nt == 32) return split ? launch_few<SWIGLU, 32, 2>(ma, m0, m1, a, s)
+                               : launch_few<SWIGLU, 32, 1>(ma, m0, m1, a, s);
+    return launch_few<SWIGLU, 64, 1>(ma, m0, m1, a, s);
+  }
   static std::mutex mu;
   static bool done[64] = {};
   if (!opt_in(grouped_w8_kernel<SWIGLU>, kSmemBytes, mu, done)) return MOE_ERR_CUDA;
@@ -613,14 +1030,14 @@ MOE_API moe_status moe_grouped_gate_up_w8(int32_t n_seg, int32_t d, int32_t I, i
   W8Args a = args_of(p, dev_status, true);
   a.hq = hq;
   a.hs = hs;
-  return launch_pass<true>(a, xq, wg_q, wu_q, as_cuda(stream));
+  return launch_pass<true>(a, xq, wg_q, wu_q, false, as_cuda(stream));
 }
 
-MOE_API moe_status moe_grouped_down_w8(int32_t n_seg, int32_t I, int32_t d, int32_t max_rows,
-                                       const moe_fp8* hq, const float* hs,
-                                       const int32_t* seg_begin, const int32_t* seg_count,
-                                       const moe_fp8* wd_q, const float* wd_s, moe_bf16* y,
-                                       uint32_t* dev_status, moe_stream_t stream) {
+namespace {
+moe_status down_pass(int32_t n_seg, int32_t I, int32_t d, int32_t max_rows, const moe_fp8* hq,
+                     const float* hs, const int32_t* seg_begin, const int32_t* seg_count,
+                     const moe_fp8* wd_q, const float* wd_s, moe_bf16* y, bool chained,
+                     uint32_t* dev_status, moe_stream_t stream) {
   const Pass p = {n_seg, I, d, max_rows, seg_begin, seg_count, hq, hs, wd_q, nullptr, wd_s, nullptr};
   const moe_status st = check_pass(p, false);
   if (st != MOE_OK || max_rows == 0) return st;
@@ -628,7 +1045,17 @@ MOE_API moe_status moe_grouped_down_w8(int32_t n_seg, int32_t I, int32_t d, int3
   if (!aligned16(y)) return MOE_ERR_UNSUPPORTED;
   W8Args a = args_of(p, dev_status, false);
   a.y = y;
-  return launch_pass<false>(a, hq, wd_q, wd_q, as_cuda(stream));
+  return launch_pass<false>(a, hq, wd_q, wd_q, chained, as_cuda(stream));
+}
+}  // namespace
+
+MOE_API moe_status moe_grouped_down_w8(int32_t n_seg, int32_t I, int32_t d, int32_t max_rows,
+                                       const moe_fp8* hq, const float* hs,
+                                       const int32_t* seg_begin, const int32_t* seg_count,
+                                       const moe_fp8* wd_q, const float* wd_s, moe_bf16* y,
+                                       uint32_t* dev_status, moe_stream_t stream) {
+  return down_pass(n_seg, I, d, max_rows, hq, hs, seg_begin, seg_count, wd_q, wd_s, y, false,
+                   dev_status, stream);
 }
 
 MOE_API size_t moe_grouped_swiglu_w8_workspace_size(int32_t max_rows, int32_t I) {
@@ -659,6 +1086,6 @@ MOE_API moe_status moe_grouped_swiglu_w8(int32_t n_seg, int32_t d, int32_t I, in
   st = moe_grouped_gate_up_w8(n_seg, d, I, max_rows, xq, xs, seg_begin, seg_count, wg_q, wg_s, wu_q,
                               wu_s, hq, hs, dev_status, stream);
   if (st != MOE_OK) return st;
-  return moe_grouped_down_w8(n_seg, I, d, max_rows, hq, hs, seg_begin, seg_count, wd_q, wd_s, y,
-                             dev_status, stream);
+  return down_pass(n_seg, I, d, max_rows, hq, hs, seg_begin, seg_count, wd_q, wd_s, y, true,
+                   dev_status, stream);
 }

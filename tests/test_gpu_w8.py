@@ -146,6 +146,14 @@ def test_many_segments(seed):
     check(make(272, 128, torch.randint(0, 150, (24,), generator=gen).tolist(), seed))
 
 
+@pytest.mark.parametrize("d,I", [(64, 128), (208, 144), (1040, 272)])
+@pytest.mark.parametrize("counts", [[0] * 30 + [40, 17, 1], [9] * 20 + [0, 100], [1] * 75 + [229], [2, 0]])
+def test_few_rows_and_uneven_segments(d, I, counts):
+    """Row tiles of 16, 32 and 64; segments longer than their tile; the reduction split over
+    two CTAs with one and with several tiles each."""
+    check(make(d, I, counts, seed=d + len(counts), gaps=3, tail=1))
+
+
 def test_one_token_of_the_decode_shape():
     counts = [0] * 128
     for e in (3, 17, 40, 41, 77, 100, 126, 127):
