@@ -147,6 +147,20 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
   return amax == 0 ? 1.0f : __fdiv_rn(__uint_as_float(amax), kE4M3Max);
 }
 
+// 32 consecutive bytes (aligned to 16): one 32-byte store where the address allows
+// it -- a whole sector per lane -- else two of 16.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&v)[8]) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    uint4* q = static_cast<uint4*>(dst);
+    q[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // acc += part * s on 16 columns.
 __device__ __forceinline__ void promote16(const uint32_t (&part)[16], float s, float2* acc) {
   const float2 s2 = make_float2(s, s);
@@ -353,32 +367,34 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
           const int n0 = tl.nb * 128 + 64 * half;
           uint8_t* dst = a.hq + row * a.N + n0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (n0 + 16 * j < a.N) {
-              uint32_t p[4];
+          for (int j = 0; j < 2; ++j) {  // 32 codes; N is a multiple of 16
+            uint32_t p[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 x = acc0[8 * j + 2 * i], z = acc0[8 * j + 2 * i + 1];
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-                    make_float2(x.x * k * inv, x.y * k * inv), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-                    make_float2(z.x * k * inv, z.y * k * inv), __NV_SATFINITE, __NV_E4M3);
-                p[i] = lo | (hi << 16);
-              }
-              *reinterpret_cast<uint4*>(dst + 16 * j) = make_uint4(p[0], p[1], p[2], p[3]);
+            for (int i = 0; i < 8; ++i) {
+              const float2 x = acc0[16 * j + 2 * i], z = acc0[16 * j + 2 * i + 1];
+              const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+                  make_float2(x.x * k * inv, x.y * k * inv), __NV_SATFINITE, __NV_E4M3);
+              const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+                  make_float2(z.x * k * inv, z.y * k * inv), __NV_SATFINITE, __NV_E4M3);
+              p[i] = lo | (hi << 16);
             }
+            if (n0 + 32 * j + 16 < a.N)
+              store32(dst + 32 * j, p);
+            else if (n0 + 32 * j < a.N)
+              *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(p[0], p[1], p[2], p[3]);
           }
         }
       } else if (live) {
         const int n0 = tl.nb * 256 + 128 * half;
         uint16_t* dst = a.y + row * a.N + n0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (n0 + 8 * j < a.N) {
-            const float2* v = j < 8 ? acc0 + 4 * j : acc1 + 4 * (j - 8);
-            *reinterpret_cast<uint4*>(dst + 8 * j) =
-                make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                           pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+        for (int j = 0; j < 8; ++j) {  // 16 columns; N is a multiple of 16
+          if (n0 + 16 * j < a.N) {
+            const float2* v = j < 4 ? acc0 + 8 * j : acc1 + 8 * (j - 4);
+            uint32_t p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = pack_bf16x2(v[i].x, v[i].y);
+            store32(dst + 16 * j, p);
           }
         }
       }
