@@ -11,9 +11,10 @@
 // layer and the backward read that stored value, so all of them see one h.  The
 // codes are taken from the unrounded fp32 v (one rounding, not bf16 then E4M3).
 //
-// Bound: HBM.  A row is read once and held in registers (V chunks of 8 values
-// per thread, NW warps a row) through both reductions, so x and r are read once
-// and every output written once.
+// Bound: HBM.  A row is read once and held in registers (V chunks of 8 values per
+// thread) through both reductions, so x and r are read once and every output
+// written once.  Blocks are persistent: the raw bits of a block's next row are on
+// their way while it works on the current one.
 #include "common.cuh"
 
 namespace moe {
@@ -22,13 +23,15 @@ namespace {
 constexpr float kE4M3Max = 448.0f;
 constexpr uint32_t kAbsInf = 0x7F800000u;
 constexpr int kMaxNormD = 16384;
+constexpr int kMaxWarps = 32;
 
 struct NormArgs {
   int64_t n, x_stride;
   int d;
-  int x32, r32;  // fp32 (else bf16) x and residual stream
   int group;     // scale group of q: MOE_SCALE_ROW or MOE_SCALE_BLOCK128
   int G;         // scales per row
+  int nw;        // warps per row
+  int early;     // the grid is resident at once: dependents may launch right after the wait
   float eps;
   const void* x;
   const void* res;   // nullptr: h = x
@@ -41,18 +44,28 @@ struct NormArgs {
   uint32_t* dev_status;
 };
 
-// 8 consecutive values of a bf16 or fp32 array.  Plain (coherent) loads: a row's
-// output may be written over its input.
-__device__ __forceinline__ void load8(const void* p, int is32, int64_t at, float f[8]) {
-  if (is32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = q[0], b = q[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at), f);
+// 8 consecutive values of a bf16 or fp32 array as raw bits.  Plain (coherent) loads:
+// a row's output may be written over its input.
+template <bool FP32>
+struct Raw {
+  uint4 v[FP32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) +
+                                                    at * (FP32 ? 4 : 2));
+    v[0] = q[0];
+    if constexpr (FP32) v[1] = q[1];
   }
-}
+  __device__ __forceinline__ void get(float f[8]) const {
+    if constexpr (FP32) {
+      f[0] = __uint_as_float(v[0].x); f[1] = __uint_as_float(v[0].y);
+      f[2] = __uint_as_float(v[0].z); f[3] = __uint_as_float(v[0].w);
+      f[4] = __uint_as_float(v[1].x); f[5] = __uint_as_float(v[1].y);
+      f[6] = __uint_as_float(v[1].z); f[7] = __uint_as_float(v[1].w);
+    } else {
+      unpack8(v[0], f);
+    }
+  }
+};
 
 __device__ __forceinline__ void store8(void* p, int is32, int64_t at, const float f[8]) {
   if (is32) {
@@ -73,40 +86,33 @@ __device__ __forceinline__ void ldg8(const float* p, int64_t at, float f[8]) {
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Sum over the nw warps of a row (every thread gets it; fixed order).  `sh` holds
+// two alternating sets of kMaxWarps values, so one barrier per reduction is enough.
+__device__ __forceinline__ float row_sum(float v, int nw, float* sh, int& phase) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
-// Sum over the NW warps of a row (every thread gets it; fixed order).  `sh` holds
-// two alternating sets of NW floats, so one barrier per reduction is enough.
-template <int NW>
-__device__ __forceinline__ float row_sum(float v, float* sh, int& phase) {
-  v = warp_sum(v);
-  if constexpr (NW > 1) {
-    float* s = sh + phase * NW;
+  if (nw > 1) {
+    float* s = sh + phase * kMaxWarps;
     phase ^= 1;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0f;
+    const int lane = threadIdx.x & 31;
+    v = lane < nw ? s[lane] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) v += s[i];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
   return v;
 }
 
-template <int NW>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, float* sh, int& phase) {
+__device__ __forceinline__ uint32_t row_max(uint32_t v, int nw, float* sh, int& phase) {
   v = __reduce_max_sync(0xFFFFFFFFu, v);
-  if constexpr (NW > 1) {
-    uint32_t* s = reinterpret_cast<uint32_t*>(sh + phase * NW);
+  if (nw > 1) {
+    uint32_t* s = reinterpret_cast<uint32_t*>(sh + phase * kMaxWarps);
     phase ^= 1;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) v = max(v, s[i]);
+    const int lane = threadIdx.x & 31;
+    v = __reduce_max_sync(0xFFFFFFFFu, lane < nw ? s[lane] : 0u);
   }
   return v;
 }
@@ -123,115 +129,127 @@ __device__ __forceinline__ float scale_of(uint32_t amax) {
   return amax == 0 ? 1.0f : __fdiv_rn(__uint_as_float(amax), kE4M3Max);
 }
 
+// 8 codes of v / s as v * (1 / s): one division a group instead of one a value (the
+// divisions were two thirds of the instructions of the 7,168-wide case).  A scale
+// near the type's smallest values is taken 2^64 larger, so that its reciprocal stays
+// finite.
 __device__ __forceinline__ uint2 quant8(const float f[8], float s) {
+  const float k = s < 0x1p-60f ? 0x1p64f : 1.0f;
+  const float inv = __frcp_rn(s * k);
   uint32_t p[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    p[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s)),
+    p[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * k * inv, f[2 * i + 1] * k * inv),
                                     __NV_SATFINITE, __NV_E4M3);
   return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
 }
 
-// NW warps hold one row (NW > 1: one row per block; NW = 1: a row per warp).
-template <int NW, int V>
-__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32)
+// A row is held by nw warps: with nw = 1 a block's warps take a row each, else the
+// whole block takes one.
+template <int V, bool X32, bool R32>
+__global__ void __launch_bounds__(V < 4 ? 1024 : 512)
 add_rms_norm_kernel(const NormArgs a) {
-  __shared__ float sh[2 * NW];
-  pdl_wait();
-  const int rows_per_block = NW == 1 ? static_cast<int>(blockDim.x >> 5) : 1;
-  const int tid = NW == 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
-  const int sub = NW == 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  __shared__ float sh[2 * kMaxWarps];
+  pdl_wait_then_trigger(a.early);
+  const int nw = a.nw, span = nw * 32;
+  const int rows_per_block = nw == 1 ? static_cast<int>(blockDim.x >> 5) : 1;
+  const int tid = nw == 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+  const int sub = nw == 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
   const int chunks = a.d / 8;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows_per_block;
   int phase = 0;
   bool bad = false;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub; row < a.n;
-       row += static_cast<int64_t>(gridDim.x) * rows_per_block) {
-    const int64_t base = row * a.d;
-    float h[V][8];
+  Raw<X32> nx[V];
+  Raw<R32> nr[V];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * NW * 32;
-      if (c < chunks) load8(a.x, a.x32, row * a.x_stride + 8 * c, h[i]);
+      const int c = tid + i * span;
+      if (c < chunks) {
+        nx[i].load(a.x, row * a.x_stride + 8 * c);
+        if (a.res != nullptr) nr[i].load(a.res, row * a.d + 8 * c);
+      }
     }
+  };
+  constexpr bool kAhead = V == 4;  // (the others are launched with a row a block)
+  int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub;
+  if (kAhead && row < a.n) fetch(row);
+  for (; row < a.n; row += step) {
+    const int64_t base = row * a.d;
+    if (!kAhead) fetch(row);
+    float h[V][8];
     float ss = 0.0f;
-    if (a.res != nullptr) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * NW * 32;
-        if (c < chunks) {
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * span;
+      if (c < chunks) {
+        nx[i].get(h[i]);
+        if (a.res != nullptr) {
           float r[8];
-          load8(a.res, a.r32, base + 8 * c, r);
+          nr[i].get(r);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             h[i][j] += r[j];
-            if (!a.r32) h[i][j] = __bfloat162float(__float2bfloat16_rn(h[i][j]));
+            if constexpr (!R32) h[i][j] = __bfloat162float(__float2bfloat16_rn(h[i][j]));
           }
         }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * NW * 32;
-      if (c < chunks) {
-        if (a.res_out != nullptr) store8(a.res_out, a.r32, base + 8 * c, h[i]);
+        if (a.res_out != nullptr) store8(a.res_out, R32, base + 8 * c, h[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss += h[i][j] * h[i][j];
       }
     }
-    ss = row_sum<NW>(ss, sh, phase);
+    if (kAhead && row + step < a.n) fetch(row + step);
+    ss = row_sum(ss, nw, sh, phase);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(ss / static_cast<float>(a.d) + a.eps));
     if (a.rstd != nullptr && tid == 0) a.rstd[row] = rstd;
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * NW * 32;
+      const int c = tid + i * span;
+      uint32_t m = 0;
       if (c < chunks) {
         float w[8];
         ldg8(a.w, 8 * c, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * rstd * w[j];
         if (a.y != nullptr) store8(a.y, 0, base + 8 * c, h[i]);
-        top = max(top, amax8(h[i]));
+        if (a.q != nullptr) m = amax8(h[i]);
       }
-    }
-    if (a.q == nullptr) continue;
-    if (a.group == MOE_SCALE_ROW) {
-      top = row_max<NW>(top, sh, phase);
-      const float s = scale_of(top);
-      if (tid == 0) a.scales[row] = s;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * NW * 32;
-        if (c < chunks) *reinterpret_cast<uint2*>(a.q + base + 8 * c) = quant8(h[i], s);
-      }
-      bad |= top >= kAbsInf;
-    } else {
-      // 16 consecutive chunks, one group, lie in one half-warp
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * NW * 32;
-        uint32_t m = c < chunks ? amax8(h[i]) : 0u;
+      if (a.q != nullptr && a.group != MOE_SCALE_ROW) {
+        // 16 consecutive chunks, one group, lie in one half-warp
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         if (c < chunks) {
           const float s = scale_of(m);
           if ((c & 15) == 0) a.scales[row * a.G + (c >> 4)] = s;
           *reinterpret_cast<uint2*>(a.q + base + 8 * c) = quant8(h[i], s);
-          bad |= m >= kAbsInf;
         }
       }
+      top = max(top, m);
     }
+    if (a.q != nullptr && a.group == MOE_SCALE_ROW) {
+      top = row_max(top, nw, sh, phase);
+      const float s = scale_of(top);
+      if (tid == 0) a.scales[row] = s;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * span;
+        if (c < chunks) *reinterpret_cast<uint2*>(a.q + base + 8 * c) = quant8(h[i], s);
+      }
+    }
+    bad |= top >= kAbsInf;
   }
   if (bad) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
-  pdl_trigger();
+  if (!a.early) pdl_trigger();
 }
 
 // --------------------------------- backward ---------------------------------
 
 struct NormBwdArgs {
   int64_t n;
-  int d;
-  int dy32, x32, r32;
+  int d, nw;
+  int early;
+  int x32;
   const void* dy;
   const void* h;
   const float* w;
@@ -244,42 +262,58 @@ struct NormBwdArgs {
 
 // The rows of a block go through it in order; each thread keeps the weight
 // gradient of its own columns in registers and the block writes one partial row.
-template <int NW, int V>
-__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32)
+template <int V, bool DY32, bool R32>
+__global__ void __launch_bounds__(512)
 rms_norm_backward_kernel(const NormBwdArgs a) {
-  __shared__ float sh[2 * NW];
-  __shared__ float sh_dw[NW == 1 ? 3 * V * 256 : 1];
-  pdl_wait();
-  const int rows_per_block = NW == 1 ? static_cast<int>(blockDim.x >> 5) : 1;
-  const int tid = NW == 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
-  const int sub = NW == 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  __shared__ float sh[2 * kMaxWarps];
+  __shared__ float sh_dw[3 * V * 256];  // (a row per warp: the other three warps' sums)
+  pdl_wait_then_trigger(a.early);
+  const int nw = a.nw, span = nw * 32;
+  const int rows_per_block = nw == 1 ? static_cast<int>(blockDim.x >> 5) : 1;
+  const int tid = nw == 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+  const int sub = nw == 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
   const int chunks = a.d / 8;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows_per_block;
   int phase = 0;
   float dw[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub; row < a.n;
-       row += static_cast<int64_t>(gridDim.x) * rows_per_block) {
+  constexpr bool kAhead = V < 4;  // (wider rows leave no registers for the next one)
+  Raw<R32> nh[V], ng[kAhead ? V : 1];
+  Raw<DY32> ndy[V];
+  float nrstd = 0.0f;
+  auto fetch = [&](int64_t row) {
+    nrstd = __ldg(a.rstd + row);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * span;
+      if (c < chunks) {
+        nh[i].load(a.h, row * a.d + 8 * c);
+        ndy[i].load(a.dy, row * a.d + 8 * c);
+        if constexpr (kAhead) if (a.dh_out != nullptr) ng[i].load(a.dh_out, row * a.d + 8 * c);
+      }
+    }
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub;
+  if (kAhead && row < a.n) fetch(row);
+  for (; row < a.n; row += step) {
     const int64_t base = row * a.d;
-    const float rstd = __ldg(a.rstd + row);
+    if (!kAhead) fetch(row);
+    const float rstd = nrstd;
     float xh[V][8], u[V][8];
+    Raw<R32> g[kAhead ? V : 1];
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * NW * 32;
-      if (c < chunks) {
-        load8(a.h, a.r32, base + 8 * c, xh[i]);
-        load8(a.dy, a.dy32, base + 8 * c, u[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * NW * 32;
+      const int c = tid + i * span;
       if (c < chunks) {
         float w[8];
         ldg8(a.w, 8 * c, w);
+        nh[i].get(xh[i]);
+        ndy[i].get(u[i]);
+        if constexpr (kAhead) g[i] = ng[i];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           xh[i][j] *= rstd;
@@ -289,26 +323,28 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
         }
       }
     }
-    dot = row_sum<NW>(dot, sh, phase) / static_cast<float>(a.d);
+    if (kAhead && row + step < a.n) fetch(row + step);
+    dot = row_sum(dot, nw, sh, phase) / static_cast<float>(a.d);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * NW * 32;
+      const int c = tid + i * span;
       if (c < chunks) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[i][j] = rstd * (u[i][j] - xh[i][j] * dot);
         if (a.dh_out != nullptr) {
-          float g[8];
-          load8(a.dh_out, a.r32, base + 8 * c, g);
+          float f[8];
+          if constexpr (!kAhead) g[0].load(a.dh_out, base + 8 * c);
+          g[kAhead ? i : 0].get(f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[i][j] += g[j];
+          for (int j = 0; j < 8; ++j) u[i][j] += f[j];
         }
         if (a.dx != nullptr) store8(a.dx, a.x32, base + 8 * c, u[i]);
-        if (a.dres != nullptr) store8(a.dres, a.r32, base + 8 * c, u[i]);
+        if (a.dres != nullptr) store8(a.dres, R32, base + 8 * c, u[i]);
       }
     }
   }
   if (a.part != nullptr) {
-    if constexpr (NW == 1) {  // the block's warps, summed in warp order
+    if (nw == 1) {  // the block's four warps, summed in warp order
       if (sub > 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -327,56 +363,93 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
     if (sub == 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = tid + i * NW * 32;
-        if (c < chunks)
-          store8(a.part, 1, static_cast<int64_t>(blockIdx.x) * a.d + 8 * c, dw[i]);
+        const int c = tid + i * span;
+        if (c < chunks) store8(a.part, 1, static_cast<int64_t>(blockIdx.x) * a.d + 8 * c, dw[i]);
       }
     }
   }
-  pdl_trigger();
+  if (!a.early) pdl_trigger();
 }
 
-// dw = column sums of the partial rows, in a fixed order: 8 interleaved groups of
+// dw = column sums of the partial rows, in a fixed order: 32 interleaved groups of
 // rows per column, then the groups in order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 weight_grad_kernel(int blocks, int d, const float* __restrict__ part, float* __restrict__ dw) {
-  __shared__ float sh[8][32];
-  pdl_wait();
+  __shared__ float sh[32][33];
+  pdl_wait_then_trigger(true);  // (at most 512 blocks of 1,024 threads, two to an SM)
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (col < d) {
-#pragma unroll 4
-    for (int b = g; b < blocks; b += 8) s += part[static_cast<int64_t>(b) * d + col];
+#pragma unroll 10
+    for (int b = g; b < blocks; b += 32) s += part[static_cast<int64_t>(b) * d + col];
   }
   sh[g][lane] = s;
   __syncthreads();
-  if (g == 0 && col < d) {
+  // warp g adds column g's 32 group sums
+  s = sh[lane][g];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sh[i][lane];
-    dw[col] = s;
-  }
-  pdl_trigger();
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + g < d) dw[blockIdx.x * 32 + g] = s;
 }
 
 // --------------------------------- host side --------------------------------
 
-constexpr int64_t kMaxGrid = 1 << 20;
+// How a pass lays its rows out: V chunks of 8 values per thread, nw warps a row
+// (one: four rows to a block), persistent blocks.
+struct Plan {
+  int V, nw, threads, blocks;
+};
 
-unsigned forward_grid(int64_t n, int rows_per_block) {
-  const int64_t b = ceil_div(n, rows_per_block);
-  return static_cast<unsigned>(b > kMaxGrid ? kMaxGrid : b);
+// sm_warps: warps of the kernel that an SM holds at once.
+Plan plan_rows(int64_t n, int d, int V, int sm_warps) {
+  Plan p;
+  p.V = V;
+  p.nw = static_cast<int>(ceil_div(d / 8, 32 * V));
+  const int warps = p.nw == 1 ? 4 : p.nw;
+  p.threads = warps * 32;
+  const int64_t want = ceil_div(n, p.nw == 1 ? 4 : 1);
+  const int64_t most = static_cast<int64_t>(152) * (sm_warps > warps ? sm_warps / warps : 1);
+  p.blocks = static_cast<int>(want < most ? want : most);
+  return p;
 }
 
-// Blocks of the backward: two per SM; each writes one partial weight gradient.
-int backward_blocks(int64_t n, int rows_per_block) {
-  const int64_t b = ceil_div(n, rows_per_block), most = 2 * 152;
-  return static_cast<int>(b < most ? b : most);
+// Forward: many rows take four chunks a thread (few warps a row, more bytes in
+// flight per thread); rows fewer than the SMs are latency-bound and take one
+// (two above 8,192 values: at most 32 warps).
+Plan plan_forward(int64_t n, int d) {
+  const int V = n > 152 ? 4 : (d <= 8192 ? 1 : 2);
+  return plan_rows(n, d, V, V == 4 ? 16 : 32);
 }
 
-// Widths up to 512 values: a row per warp, four to a block; above: a row per
-// block of 8 warps.
-bool row_per_warp(int d) { return d <= 512; }
+// Backward: two chunks a thread (a row's values, its successor's and the weight
+// gradient stay in registers; four above 8,192 values: at most 16 warps); each block
+// writes one partial row of the weight gradient.
+Plan plan_backward(int64_t n, int d) { return plan_rows(n, d, d <= 8192 ? 2 : 4, 16); }
+
+template <int V>
+void launch_forward(const NormArgs& a, bool x32, bool r32, const Plan& p, cudaStream_t s) {
+  const dim3 grid(p.blocks), block(p.threads);
+  if (x32) {
+    if (r32) launch(add_rms_norm_kernel<V, true, true>, grid, block, 0, s, a);
+    else launch(add_rms_norm_kernel<V, true, false>, grid, block, 0, s, a);
+  } else {
+    if (r32) launch(add_rms_norm_kernel<V, false, true>, grid, block, 0, s, a);
+    else launch(add_rms_norm_kernel<V, false, false>, grid, block, 0, s, a);
+  }
+}
+
+template <int V>
+void launch_backward(const NormBwdArgs& a, bool dy32, bool r32, const Plan& p, cudaStream_t s) {
+  const dim3 grid(p.blocks), block(p.threads);
+  if (dy32) {
+    if (r32) launch(rms_norm_backward_kernel<V, true, true>, grid, block, 0, s, a);
+    else launch(rms_norm_backward_kernel<V, true, false>, grid, block, 0, s, a);
+  } else {
+    if (r32) launch(rms_norm_backward_kernel<V, false, true>, grid, block, 0, s, a);
+    else launch(rms_norm_backward_kernel<V, false, false>, grid, block, 0, s, a);
+  }
+}
 
 moe_status check_norm(const moe_norm_params* p) {
   if (p == nullptr || p->n < 0 || p->d <= 0) return MOE_ERR_INVALID_ARG;
@@ -418,8 +491,6 @@ MOE_API moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, con
   a.n = p->n;
   a.x_stride = p->x_stride;
   a.d = p->d;
-  a.x32 = p->x_type == MOE_DTYPE_FP32;
-  a.r32 = p->residual_type == MOE_DTYPE_FP32;
   a.group = p->group;
   a.G = p->group == MOE_SCALE_ROW ? 1 : static_cast<int>(ceil_div(p->d, 128));
   a.eps = p->eps;
@@ -432,24 +503,19 @@ MOE_API moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, con
   a.scales = scales;
   a.rstd = rstd;
   a.dev_status = dev_status;
-  cudaStream_t s = as_cuda(stream);
-  const int chunks = p->d / 8;
-  if (row_per_warp(p->d)) {
-    launch(add_rms_norm_kernel<1, 2>, dim3(forward_grid(p->n, 4)), dim3(128), 0, s, a);
-  } else {
-    const dim3 grid(forward_grid(p->n, 1)), block(256);
-    if (chunks <= 256) launch(add_rms_norm_kernel<8, 1>, grid, block, 0, s, a);
-    else if (chunks <= 512) launch(add_rms_norm_kernel<8, 2>, grid, block, 0, s, a);
-    else if (chunks <= 1024) launch(add_rms_norm_kernel<8, 4>, grid, block, 0, s, a);
-    else launch(add_rms_norm_kernel<8, 8>, grid, block, 0, s, a);
-  }
+  const Plan pl = plan_forward(p->n, p->d);
+  a.nw = pl.nw;
+  a.early = one_wave(pl.blocks);
+  const bool x32 = p->x_type == MOE_DTYPE_FP32, r32 = p->residual_type == MOE_DTYPE_FP32;
+  if (pl.V == 1) launch_forward<1>(a, x32, r32, pl, as_cuda(stream));
+  else if (pl.V == 2) launch_forward<2>(a, x32, r32, pl, as_cuda(stream));
+  else launch_forward<4>(a, x32, r32, pl, as_cuda(stream));
   return launch_status();
 }
 
 MOE_API size_t moe_add_rms_norm_backward_workspace_size(const moe_norm_params* p) {
   if (check_norm(p) != MOE_OK) return 0;
-  return static_cast<size_t>(backward_blocks(p->n, row_per_warp(p->d) ? 4 : 1)) * p->d *
-         sizeof(float);
+  return static_cast<size_t>(plan_backward(p->n, p->d).blocks) * p->d * sizeof(float);
 }
 
 MOE_API moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t dy_type,
@@ -479,12 +545,13 @@ MOE_API moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t d
     if (ws == nullptr) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < moe_add_rms_norm_backward_workspace_size(p)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   }
+  const Plan pl = plan_backward(p->n, p->d);
   NormBwdArgs a = {};
   a.n = p->n;
   a.d = p->d;
-  a.dy32 = dy_type == MOE_DTYPE_FP32;
+  a.nw = pl.nw;
+  a.early = one_wave(pl.blocks);
   a.x32 = p->x_type == MOE_DTYPE_FP32;
-  a.r32 = p->residual_type == MOE_DTYPE_FP32;
   a.dy = dy;
   a.h = h;
   a.w = weight;
@@ -493,19 +560,12 @@ MOE_API moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t d
   a.dx = dx;
   a.dres = dresidual;
   a.part = dweight != nullptr ? static_cast<float*>(ws) : nullptr;
-  const int chunks = p->d / 8;
-  const int blocks = backward_blocks(p->n, row_per_warp(p->d) ? 4 : 1);
-  if (row_per_warp(p->d)) {
-    launch(rms_norm_backward_kernel<1, 2>, dim3(blocks), dim3(128), 0, s, a);
-  } else {
-    const dim3 grid(blocks), block(256);
-    if (chunks <= 256) launch(rms_norm_backward_kernel<8, 1>, grid, block, 0, s, a);
-    else if (chunks <= 512) launch(rms_norm_backward_kernel<8, 2>, grid, block, 0, s, a);
-    else if (chunks <= 1024) launch(rms_norm_backward_kernel<8, 4>, grid, block, 0, s, a);
-    else launch(rms_norm_backward_kernel<8, 8>, grid, block, 0, s, a);
-  }
+  const bool r32 = p->residual_type == MOE_DTYPE_FP32;
+  const bool dy32 = dy_type == MOE_DTYPE_FP32;
+  if (pl.V == 2) launch_backward<2>(a, dy32, r32, pl, s);
+  else launch_backward<4>(a, dy32, r32, pl, s);
   if (dweight != nullptr)
-    launch(weight_grad_kernel, dim3(static_cast<unsigned>(ceil_div(p->d, 32))), dim3(256), 0, s,
-           blocks, p->d, static_cast<const float*>(ws), dweight);
+    launch(weight_grad_kernel, dim3(static_cast<unsigned>(ceil_div(p->d, 32))), dim3(1024), 0, s,
+           pl.blocks, p->d, static_cast<const float*>(ws), dweight);
   return launch_status();
 }

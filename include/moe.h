@@ -677,9 +677,9 @@ typedef struct {
  *   rstd = 1 / sqrt(mean(h^2) + eps)                  (fp32, of the rounded h)
  *   v    = (h * rstd) * weight                        (fp32, weight fp32 [d])
  *   y    = bf16(v)                                    the router's / bf16 experts' rows
- *   q    = E4M3(fp32(v / s)), s = fp32(amax / 448)    the dispatch payload of
+ *   q    = E4M3(v / s), s = fp32(amax / 448)          the dispatch payload of
  * moe_quantize_fp8's scale rule (a zero group has s = 1), taken from the unrounded
- * v: q [n, d], scales [n, 1] or [n, ceil(d/128)] by `group`.
+ * v (the quotient as a product with the reciprocal, within two fp32 roundings): q [n, d], scales [n, 1] or [n, ceil(d/128)] by `group`.
  * x is [n, d] with row stride x_stride, residual / residual_out / y / q [n, d]
  * contiguous.  y may be NULL, and q and scales may both be NULL, but not all
  * three; rstd [n] may be NULL (the backward needs it); residual_out may be NULL
@@ -790,7 +790,7 @@ moe_status moe_quantize_weights_fp8(int32_t n_seg, int32_t K, int32_t N, const m
  * X = xq * xs and W = q * s (each element's own block scale):
  *   G = X W_gate, U = X W_up                      fp32
  *   H = SiLU(G) * U                               fp32, then per row and 128 columns
- *   hs = fp32(amax / 448) (1 if zero), hq = E4M3(H / hs)
+ *   hs = fp32(amax / 448) (1 if zero), hq = E4M3(H / hs) (as H times 1 / hs)
  *   y = bf16((hq * hs) W_down)
  * Each 128-wide block of the reduction is summed by the tensor cores
  * (tcgen05.mma kind::f8f6f4, fp32 accumulators) on the codes alone; its sum is
