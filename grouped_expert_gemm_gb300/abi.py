@@ -222,8 +222,16 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# torch.cuda.current_stream() builds a Stream object (3 us a call on the GB300's host);
+# the raw handle of the same stream takes 0.2 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None and _device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

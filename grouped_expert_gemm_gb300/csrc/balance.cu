@@ -311,7 +311,13 @@ balance_finish_kernel(const BalArgs a) {
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xFFFFFFFFu, term, o);
-    if (lane == 0) {
+    if (lane == 0 && gridDim.x * gridDim.y == 1) {  // nothing to wait for
+      a.tokens[0] = tok;
+      a.tokens[1] = tok > 0;
+      *a.loss = tok > 0 ? static_cast<float>(a.alpha * (term * a.E / (static_cast<double>(a.k) * tok)))
+                        : 0.0f;
+      last = false;
+    } else if (lane == 0) {
       if (blockIdx.x == 0) a.tokens[q] = tok;
       a.part_loss[static_cast<int64_t>(q) * eb + blockIdx.x] =
           tok > 0 ? term * a.E / (static_cast<double>(a.k) * tok) : 0.0;
