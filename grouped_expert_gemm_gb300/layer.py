@@ -6,7 +6,9 @@
                    rows are quantized to E4M3 + fp32 scales first and the pair is
                    permuted together; the permuted rows are then dequantized once
                    before the bf16 gate/up pass (or, with fp8_loader="fused", in
-                   the gate/up GEMM's own loader).
+                   the gate/up GEMM's own loader).  With E4M3 weights (a pair of
+                   codes and block scales each) the experts' products run on the
+                   payload as it is.
 ``DecodeBucket``   a fixed token bucket for decode steps: stable buffers, one
                    captured CUDA graph of the bucketed layer, a device-side
                    valid-token count, exact admission and an eager fallback.
@@ -40,6 +42,38 @@ def capacity_from_factor(cf: float, assignments: int, slots: int) -> int:
 PAYLOADS = {"bf16": None, "fp8_row": abi.MOE_SCALE_ROW, "fp8_block128": abi.MOE_SCALE_BLOCK128}
 
 
+def check_w8_layer(d, E, I, payload, fp8_loader, gather, decode_path, expert_passes, weights,
+                   shared):
+    """Arguments of a layer with E4M3 experts: block scales on both operands, the options of
+    the bf16 passes left at their defaults, codes and scales of the right shapes."""
+    if payload != "fp8_block128":
+        raise ValueError("E4M3 experts need payload='fp8_block128' (a scale per 128 values)")
+    if fp8_loader != "auto" or gather or decode_path not in ("auto", "separate") or \
+            expert_passes not in ("auto", "separate"):
+        raise ValueError("E4M3 experts have one form: fp8_loader, gather, decode_path and "
+                         "expert_passes do not apply")
+
+    def check(pair, n, N, K, what):
+        if not isinstance(pair, (tuple, list)) or len(pair) != 2:
+            raise ValueError(f"{what} must be a pair (codes, scales)")
+        q, s = pair
+        want = (n, -(-N // 128), -(-K // 128))
+        if tuple(q.shape) != (n, N, K) or q.element_size() != 1 or not q.is_contiguous():
+            raise ValueError(f"{what} codes must be contiguous E4M3 {(n, N, K)}")
+        if tuple(s.shape) != want or s.dtype != torch.float32 or not s.is_contiguous():
+            raise ValueError(f"{what} scales must be contiguous fp32 {want}")
+
+    for pair, N, K, what in zip(weights, (I, I, d), (d, d, I), ("w_gate", "w_up", "w_down")):
+        check(pair, E, N, K, what)
+    if shared is not None:
+        if not isinstance(shared[0], (tuple, list)):
+            raise ValueError("the shared expert of a layer with E4M3 experts is E4M3 too")
+        Is = shared[0][0].shape[1]
+        for pair, N, K, what in zip(shared, (Is, Is, d), (d, d, Is),
+                                    ("shared gate", "shared up", "shared down")):
+            check(pair, 1, N, K, what)
+
+
 def _u8(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
@@ -58,6 +92,13 @@ class MoELayer:
         self.scale_group = PAYLOADS[payload]
         self.capacity = capacity
         self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
+        # E4M3 experts: each weight a pair (codes [E, N, K], block scales), as
+        # quantize_weights makes them; both products then run in E4M3 on the payload's
+        # codes (moe_grouped_swiglu_w8), the bf16 rows never exist
+        self.w8 = isinstance(w_gate, (tuple, list))
+        if self.w8:
+            check_w8_layer(d, E, I, payload, fp8_loader, gather, decode_path, expert_passes,
+                           (w_gate, w_up, w_down), shared_weights)
         self.sel_bias = sel_bias
         self.params = abi.RouteParams(T, E, k, score_fn, n_group, topk_group, route_scale)
         R = T * k
@@ -81,7 +122,7 @@ class MoELayer:
         # operand (gate/up measured 1.22 -> 4.16 ms on the 4096 x 4096 prefill shape,
         # 120 -> 127 us on decode), while the separate copy runs at 75-83 % of HBM.
         self.gather = gather and payload == "bf16"
-        if (payload == "bf16" and not self.gather) or (payload != "bf16" and not self.fused_fp8):
+        if not self.w8 and (payload == "bf16" and not self.gather or payload != "bf16" and not self.fused_fp8):
             self.x_perm = torch.empty((max(R, 1), d), dtype=torch.bfloat16, device=dev)
         if payload != "bf16":
             G = abi.fp8_scale_groups(d, self.scale_group)
@@ -89,6 +130,8 @@ class MoELayer:
             self.xs = torch.empty((max(T, 1), G), dtype=torch.float32, device=dev)
             self.xq_perm = torch.empty((max(R, 1), d), dtype=torch.uint8, device=dev)
             self.xs_perm = torch.empty((max(R, 1), G), dtype=torch.float32, device=dev)
+            # the payload in token order: the layer's own buffers, or the caller's pair
+            self.xq_in, self.xs_in = self.xq, self.xs
         self.counts = torch.empty((E,), **i32)
         self.offsets = torch.empty((E + 1,), **i32)
         self.row_to_route = torch.empty((max(R, 1),), **i32)
@@ -98,16 +141,18 @@ class MoELayer:
         self.perm_ws_bytes = abi.moe_permute_workspace_size(T, k, E)
         self.perm_ws = _u8(self.perm_ws_bytes, dev)
         self.y = torch.empty((max(R, 1), d), dtype=torch.bfloat16, device=dev)
-        self.gemm_ws_bytes = abi.moe_grouped_swiglu_workspace_size(max(R, 1), I)
+        ws_size = abi.moe_grouped_swiglu_w8_workspace_size if self.w8 else \
+            abi.moe_grouped_swiglu_workspace_size
+        self.gemm_ws_bytes = ws_size(max(R, 1), I)
         self.gemm_ws = _u8(self.gemm_ws_bytes, dev)
         self.out = torch.empty((T, d), dtype=torch.float32, device=dev)
         self.dev_status = torch.zeros((1,), dtype=torch.int32, device=dev)
         self.shared = shared_weights
         if shared_weights is not None:
             sg, su, sd = shared_weights
-            self.I_shared = sg.shape[-1]
+            self.I_shared = sg[0].shape[1] if self.w8 else sg.shape[-1]
             self.shared_y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-            self.shared_ws_bytes = abi.moe_grouped_swiglu_workspace_size(T, self.I_shared)
+            self.shared_ws_bytes = ws_size(T, self.I_shared)
             self.shared_ws = _u8(self.shared_ws_bytes, dev)
             self.shared_begin = torch.zeros((1,), **i32)
             self.shared_count = torch.full((1,), T, **i32)
@@ -135,7 +180,7 @@ class MoELayer:
         # of 128, 1.1 and 2.1 us per step faster).
         if expert_passes not in ("auto", "separate", "onepass"):
             raise ValueError("expert_passes must be 'auto', 'separate' or 'onepass'")
-        can = payload == "bf16" and not self.gather and not self.fused
+        can = payload == "bf16" and not self.gather and not self.fused and not self.w8
         self.onepass = can and (expert_passes == "onepass" or (
             expert_passes == "auto" and abi.moe_grouped_swiglu_onepass_taken(E, d, I, max(R, 1))))
         if self.onepass:
@@ -164,7 +209,10 @@ class MoELayer:
 
     @property
     def H(self) -> torch.Tensor:
-        """The bf16 SwiGLU intermediate [T*k, I] left in the GEMM workspace."""
+        """The bf16 SwiGLU intermediate [T*k, I] left in the GEMM workspace (not with E4M3
+        experts, whose workspace holds codes and scales)."""
+        if self.w8:
+            raise AttributeError("E4M3 experts keep no bf16 intermediate")
         R = max(self.T * self.k, 1)
         return self.gemm_ws[: R * self.I * 2].view(torch.bfloat16).view(R, self.I)
 
@@ -191,13 +239,18 @@ class MoELayer:
         return self.sel_bias
 
     def quantize(self, x, stream=None):
+        if isinstance(x, (tuple, list)):  # already the payload (TokenNorm): nothing to do
+            self.xq_in, self.xs_in = x
+            return
+        self.xq_in, self.xs_in = self.xq, self.xs
         abi.moe_quantize_fp8(self.T, self.d, self.scale_group, x, self.xq, self.xs,
                              self.dev_status, stream)
 
     def permute(self, x, stream=None):
         if self.payload != "bf16":
             abi.moe_permute_fp8(self.T, self.d, self.E, self.k, self.capacity, self.scale_group,
-                                self.topk_ids, self.xq, self.xs, self.xq_perm, self.xs_perm,
+                                self.topk_ids, self.xq_in, self.xs_in, self.xq_perm,
+                                self.xs_perm,
                                 self.counts, self.offsets, self.row_to_route, self.route_to_row,
                                 self.n_dropped, self.perm_ws, self.perm_ws_bytes,
                                 self.dev_status, stream)
@@ -243,7 +296,18 @@ class MoELayer:
                                        self.counts, self.w_gate, self.w_up, self.w_down, self.H,
                                        self.y, self.onepass_sync, self.dev_status, stream)
 
+    def experts_w8(self, stream=None):
+        """Both passes on E4M3 rows and weights (layers whose weights are pairs)."""
+        R = max(self.T * self.k, 1)
+        abi.moe_grouped_swiglu_w8(self.E, self.d, self.I, R, self.xq_perm, self.xs_perm,
+                                  self.offsets, self.counts, *self.w_gate, *self.w_up,
+                                  *self.w_down, self.y, self.gemm_ws, self.gemm_ws_bytes,
+                                  self.dev_status, stream)
+
     def experts(self, stream=None, x=None):
+        if self.w8:
+            self.experts_w8(stream)
+            return
         if self.onepass:
             self.experts_onepass(stream)
             return
@@ -258,6 +322,12 @@ class MoELayer:
 
     def shared_expert(self, x, stream=None):
         sg, su, sd = self.shared
+        if self.w8:
+            abi.moe_grouped_swiglu_w8(1, self.d, self.I_shared, self.T, self.xq_in, self.xs_in,
+                                      self.shared_begin, self.shared_count, *sg, *su, *sd,
+                                      self.shared_y, self.shared_ws, self.shared_ws_bytes,
+                                      self.dev_status, stream)
+            return
         abi.moe_grouped_swiglu(1, self.d, self.I_shared, self.T, x, self.shared_begin,
                                self.shared_count, sg, su, sd, self.shared_y, self.shared_ws,
                                self.shared_ws_bytes, self.dev_status, stream)
@@ -287,16 +357,20 @@ class MoELayer:
         if self.fused:
             return [("decode_layer", lambda s: self.decode_layer(logits, x, s, out), None)]
         st = []
+        if self.w8:  # the shared expert reads the payload too
+            st.append(("quantize", lambda s: self.quantize(x, s), None))
         if self.shared is not None:
             st += [("shared_fork", self.shared_fork, None),
                    ("shared_expert", lambda s: self.shared_expert(x, self.side), self.side)]
         st.append(("route", lambda s: self.route(logits, s), None))
-        if self.payload != "bf16":
+        if self.payload != "bf16" and not self.w8:
             st.append(("quantize", lambda s: self.quantize(x, s), None))
         st.append(("permute", lambda s: self.permute(x, s), None))
-        if self.payload != "bf16" and not self.fused_fp8:
+        if self.payload != "bf16" and not self.fused_fp8 and not self.w8:
             st.append(("dequantize", self.dequantize, None))
-        if self.onepass:
+        if self.w8:
+            st.append(("experts_w8", self.experts_w8, None))
+        elif self.onepass:
             st.append(("gate_up_down", self.experts_onepass, None))
         else:
             st += [("gate_up", lambda s: self.experts_gate_up(s, x), None),
@@ -306,9 +380,23 @@ class MoELayer:
         st.append(("combine", lambda s: self.combine(s, out), None))
         return st
 
+    def _check_payload(self, x):
+        if self.payload == "bf16" or (self.shared is not None and not self.w8):
+            raise ValueError("this layer reads bf16 token rows")
+        q, s = x
+        for t, shape, size, what in ((q, (self.T, self.d), 1, "codes"),
+                                     (s, tuple(self.xs.shape), 4, "scales")):
+            if tuple(t.shape) != shape or t.element_size() != size or not t.is_contiguous() or \
+                    t.device != self.out.device:
+                raise ValueError(f"payload {what} must be contiguous {shape} on {self.out.device}")
+
     def forward(self, logits, x, stream=None, out=None) -> torch.Tensor:
         """Enqueue the whole layer on `stream`; returns the fp32 output buffer [T, d]
-        (`out` if given, else the layer's own)."""
+        (`out` if given, else the layer's own).  `x`: the bf16 token rows, or with an FP8
+        payload also the pair (codes, scales) that TokenNorm makes (the layer's scale group;
+        not with a bf16 shared expert, which reads bf16 rows)."""
+        if isinstance(x, (tuple, list)):
+            self._check_payload(x)
         for _, fn, _ in self.stages(logits, x, out):
             fn(stream)
         return self.out if out is None else out

@@ -1,0 +1,86 @@
+"""Argument checks of TokenNorm, RouterLoss and the layer with E4M3 experts: each refuses
+with ValueError before anything is enqueued (no GPU is touched)."""
+import pytest
+import torch
+
+import grouped_expert_gemm_gb300 as g
+
+F8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from grouped_expert_gemm_gb300 import build
+    build.build()
+
+
+def test_norm_arguments():
+    w = torch.ones(64)
+    n = g.TokenNorm(4, 64, w, device="cpu")
+    x, r = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((4, 64), dtype=torch.bfloat16)
+    for kw in (dict(payload="fp8"), dict(x_dtype=torch.float16), dict(residual_dtype=torch.float64)):
+        with pytest.raises(ValueError):
+            g.TokenNorm(4, 64, w, device="cpu", **kw)
+    for bad in (torch.ones(63), torch.ones(64, dtype=torch.bfloat16), torch.ones(128)[::2]):
+        with pytest.raises(ValueError):
+            g.TokenNorm(4, 64, bad, device="cpu")
+    for a, b in ((x, None), (x.float(), r), (x[:3], r), (x, r.float()), (x.t().contiguous().t(), r),
+                 (x, torch.zeros((4, 128), dtype=torch.bfloat16)[:, :64]), (None, r)):
+        with pytest.raises(ValueError):
+            n.forward(a, b)
+    with pytest.raises(ValueError):
+        n.backward(x)  # before any forward
+    with pytest.raises(ValueError):
+        g.TokenNorm(4, 64, w, residual_dtype=None, device="cpu").forward(x, r)
+
+
+def test_router_loss_arguments():
+    for kw in (dict(E=513, k=8), dict(E=8, k=9), dict(E=8, k=2, n_seq=0),
+               dict(E=8, k=2, score_fn=g.MOE_SCORE_SIGMOID_GROUP, route_scale=0.0)):
+        with pytest.raises(ValueError):
+            g.RouterLoss(4, alpha=0.1, device="cpu", **kw)
+    L = g.RouterLoss(4, 8, 2, 0.1, n_seq=2, device="cpu")
+    z, ids = torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32)
+    off = torch.tensor([0, 2, 4], dtype=torch.int32)
+    for a in ((z, ids, None), (z.double(), ids, off), (z, ids.long(), off), (z[:, :4], ids, off),
+              (z, ids, off[:2])):
+        with pytest.raises(ValueError):
+            L.forward(*a)
+    with pytest.raises(ValueError):
+        L.backward(z, ids, off, gates=torch.zeros((4, 2)))
+    with pytest.raises(ValueError):
+        L.backward(z, ids, off, dloss=torch.zeros(2))
+
+
+def pair(n, N, K):
+    return torch.zeros((n, N, K), dtype=F8), torch.ones((n, -(-N // 128), -(-K // 128)))
+
+
+def test_layer_with_e4m3_experts_arguments():
+    d, E, k, I = 256, 4, 2, 128
+    w = [pair(E, I, d), pair(E, I, d), pair(E, d, I)]
+    ok = dict(payload="fp8_block128", device="cpu")
+    g.MoELayer(8, d, E, k, I, *w, **ok)
+    for kw in (dict(payload="bf16"), dict(payload="fp8_row"), dict(fp8_loader="fused"),
+               dict(gather=True), dict(decode_path="fused"), dict(expert_passes="onepass")):
+        with pytest.raises(ValueError):
+            g.MoELayer(8, d, E, k, I, *w, **{**ok, **kw})
+    for i, bad in ((0, pair(E, d, I)), (2, pair(E, I, d)), (1, (w[1][0], w[1][1][:, :, :1])),
+                   (1, (w[1][0].float(), w[1][1])), (0, w[0][0])):
+        v = list(w)
+        v[i] = bad
+        with pytest.raises(ValueError):
+            g.MoELayer(8, d, E, k, I, *v, **ok) if isinstance(v[0], tuple) else \
+                g.MoELayer(8, d, E, k, I, (v[0],), v[1], v[2], **ok)
+    with pytest.raises(ValueError):  # a bf16 shared expert beside E4M3 experts
+        g.MoELayer(8, d, E, k, I, *w, shared_weights=[torch.zeros(1, d, I)] * 3, **ok)
+    with pytest.raises(ValueError):  # the bucket's calls have no E4M3 form
+        g.DecodeBucket(8, d, E, k, I, *w, device="cpu")
+    layer = g.MoELayer(8, d, E, k, I, *w, **ok)
+    z = torch.zeros((8, E))
+    q, s = torch.zeros((8, d), dtype=torch.uint8), torch.ones((8, 2))
+    for x in ((q[:4], s), (q, s[:, :1]), (q.float(), s), (q, s.double())):
+        with pytest.raises(ValueError):
+            layer.forward(z, x)
+    with pytest.raises(ValueError):
+        g.quantize_weights(torch.zeros((2, 16, 16)))
