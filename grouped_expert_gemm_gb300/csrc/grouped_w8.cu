@@ -441,22 +441,28 @@ constexpr int kFewThreads = 320;
 
 template <bool SWIGLU, int NT, int SPLIT>
 struct Few {
+  // Two CTAs an SM where two stages each fit: one's set-up, epilogue and launch
+  // overlap the other's streaming (the down pass's first weights the gate/up pass).
+  static constexpr int kPerSm = NT == 64 || (NT == 32 && SPLIT == 2) ? 1 : 2;
+  static constexpr int kBudget = (kPerSm == 2 ? 113 : 227) * 1024;
   static constexpr int kStageBytes = 2 * kBBox + NT * kBK;
-  static constexpr int kUpBytes = SWIGLU ? NT * 128 * 4 : 0;              // up sums for the gate warps
-  static constexpr int kRedBytes = SPLIT > 1 ? 2 * NT * 128 * 4 : 0;      // rank 1's sums
+  // rank 1's sums ([2][NT / 4][128][4]), and the up sums for the gate warps (in the
+  // second half of that buffer, or one of their own)
+  static constexpr int kRedBytes = SPLIT > 1 ? 2 * NT * 128 * 4 : 0;
+  static constexpr int kUpBytes = SWIGLU && SPLIT == 1 ? NT * 128 * 4 : 0;
   static constexpr int kTopBytes = 2 * 4 * NT * 4;
   // bars: full[S], empty[S], tfull[4], tempty[4], upfull, upfree, top, red, redfree, drain
   static constexpr int kFixed = 1024 + kUpBytes + kRedBytes + kTopBytes + kTableInts * 4 + 64 * 8;
-  static constexpr int kStages = (227 * 1024 - kFixed) / kStageBytes;
+  static constexpr int kStages = (kBudget - kFixed) / kStageBytes;
   static constexpr int kBars = 2 * kStages + 2 * kFewBufs + 6;
   static constexpr int kTmem = kFewBufs * 2 * NT;
   static constexpr int kSmem = kFixed + kStages * kStageBytes;
-  static_assert(kBars <= 64 && kStages >= 4 && kSmem <= 227 * 1024, "shared memory");
-  static_assert(kTmem <= 512 && kTmem >= 32, "tensor memory");
+  static_assert(kBars <= 64 && kStages >= 2 && kSmem <= kBudget, "shared memory");
+  static_assert(kTmem * kPerSm <= 512 && kTmem >= 32, "tensor memory");
 };
 
 template <bool SWIGLU, int NT, int SPLIT>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(kFewThreads, Few<SWIGLU, NT, SPLIT>::kPerSm)
 grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
                       const __grid_constant__ CUtensorMap map_w0,
                       const __grid_constant__ CUtensorMap map_w1, const W8Args a) {
@@ -466,9 +472,9 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
   uint8_t* stage_base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage_base + kStages * F::kStageBytes);
-  float* s_up = reinterpret_cast<float*>(bars + 64);                          // [NT][128]
-  float* s_red = s_up + F::kUpBytes / 4;                                      // [2][NT][128]
-  uint32_t* s_top = reinterpret_cast<uint32_t*>(s_red + F::kRedBytes / 4);    // [2][4][NT]
+  float4* s_red = reinterpret_cast<float4*>(bars + 64);                       // [2][NT/4][128]
+  float4* s_up = SPLIT > 1 ? s_red + NT / 4 * 128 : s_red;                    // [NT/4][128]
+  uint32_t* s_top = reinterpret_cast<uint32_t*>(s_red + (F::kRedBytes + F::kUpBytes) / 16);  // [2][4][NT]
   const Table tb = carve_table(reinterpret_cast<int*>(s_top + F::kTopBytes / 4));
   volatile int* abort_flag = tb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -498,8 +504,8 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
     mbar_init(up_full, 4);
     mbar_init(up_free, 4);
     mbar_init(top_bar, 4);
-    mbar_init(red_full, 256);
-    mbar_init(red_free, 256);
+    mbar_init(red_full, 1);
+    mbar_init(red_free, SWIGLU ? 128 : 256);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -512,7 +518,7 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
   }
   if (warp == 1) umma_alloc(smem_u32(tb.tmem_slot), F::kTmem);
   if (!a.chained) pdl_wait();
-  // one CTA per SM: all of the grid is resident once all have passed here
+  // the grid fits the GPU at once: all of it is resident once all have passed here
   if (SWIGLU) pdl_trigger();
   if (threadIdx.x >= 64 && threadIdx.x < 192) build_table(a, NT, n_blocks, threadIdx.x - 64, tb);
   umma_fence_before();
@@ -611,6 +617,7 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
     bool ok = true;
     for (int t = group; t < total; t += groups, tile_ph ^= 1u) {
       const Tile tl = tile_of(t, tb, a.n_seg, NT, n_blocks, a.m_outer);
+      if (SPLIT > 1 && rank == 0 && threadIdx.x == 64) mbar_arrive_expect_tx(red_full, F::kRedBytes);
       const int nblk = SWIGLU ? tl.nb : min(2 * tl.nb + half, a.GN - 1);
       const float* ws = (SWIGLU && half ? a.bs1 : a.bs0) +
                         (static_cast<int64_t>(tl.seg) * a.GN + nblk) * a.GK;
@@ -659,29 +666,34 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
         if (++buf == kFewBufs) { buf = 0; acc_ph ^= 1u; }
       }
       if (!ok) break;
+      const bool more = t + groups < total;  // rank 1 will need the buffer again
       if constexpr (SPLIT > 1) {
-        float* mine = s_red + half * (NT * 128) + m;
+        float4* mine = s_red + half * (NT / 4 * 128) + m;
         if (rank == 1) {
           if (!__all_sync(0xFFFFFFFFu, wait_bounded<true>(red_free, tile_ph ^ 1u, abort_flag, a.dev_status)))
             break;
-          const uint32_t dst = map_to_rank(smem_u32(mine), 0);
+          const uint32_t dst = map_to_rank(smem_u32(mine), 0), bar = map_to_rank(red_full, 0);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) st_cluster(dst + j * 512, acc[j]);
-          mbar_arrive_cluster(map_to_rank(red_full, 0));
+          for (int j = 0; j < NT; j += 4)
+            st_async4(dst + j * 512, bar, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
           continue;
         }
         if (!__all_sync(0xFFFFFFFFu, wait_bounded<true>(red_full, tile_ph, abort_flag, a.dev_status)))
           break;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j] += mine[j * 128];
-        mbar_arrive_cluster(map_to_rank(red_free, 1));
+        for (int j = 0; j < NT; j += 4) {
+          const float4 v = mine[j / 4 * 128];
+          acc[j] += v.x; acc[j + 1] += v.y; acc[j + 2] += v.z; acc[j + 3] += v.w;
+        }
+        if (!SWIGLU && more) mbar_arrive_cluster(map_to_rank(red_free, 1));
       }
       if constexpr (SWIGLU) {
         if (half == 1) {
           if (!__all_sync(0xFFFFFFFFu, wait_bounded(up_free, tile_ph ^ 1u, abort_flag, a.dev_status)))
             break;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) s_up[j * 128 + m] = acc[j];
+          for (int j = 0; j < NT; j += 4)
+            s_up[j / 4 * 128 + m] = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
           __syncwarp();
           if (lane == 0) mbar_arrive(up_full);
           continue;
@@ -689,8 +701,15 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
         if (!__all_sync(0xFFFFFFFFu, wait_bounded(up_full, tile_ph, abort_flag, a.dev_status))) break;
         uint32_t* tops = s_top + tile_ph * (4 * NT);
 #pragma unroll
+        for (int j = 0; j < NT; j += 4) {
+          const float4 v = s_up[j / 4 * 128 + m];
+          const float up[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[j + i] = __fdividef(acc[j + i], 1.0f + __expf(-acc[j + i])) * up[i];
+        }
+#pragma unroll
         for (int j = 0; j < NT; ++j) {
-          acc[j] = __fdividef(acc[j], 1.0f + __expf(-acc[j])) * s_up[j * 128 + m];
           const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(acc[j]) & 0x7FFFFFFFu);
           if (lane == (j & 31)) tops[quad * NT + j] = v;
         }
@@ -699,6 +718,7 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
           mbar_arrive(up_free);
           mbar_arrive(top_bar);
         }
+        if (SPLIT > 1 && more) mbar_arrive_cluster(map_to_rank(red_free, 1));
         if (!__all_sync(0xFFFFFFFFu, wait_bounded(top_bar, tile_ph, abort_flag, a.dev_status))) break;
         float k[kPer], inv[kPer];
 #pragma unroll
@@ -916,12 +936,13 @@ moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtens
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  unsigned grid = static_cast<unsigned>(sm_count());
+  unsigned grid = static_cast<unsigned>(F::kPerSm * sm_count());
   if constexpr (SPLIT > 1) {
     static std::mutex mu2;
     static int pairs[64] = {};
-    const int n = resident_pairs(kern, kFewThreads, F::kSmem, mu2, pairs);
+    int n = resident_pairs(kern, kFewThreads, F::kSmem, mu2, pairs);
     if (n <= 0) return MOE_ERR_CUDA;
+    if (n > sm_count() / 2) n = sm_count() / 2;  // one CTA an SM streams as fast as two
     grid = static_cast<unsigned>(2 * n);
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;

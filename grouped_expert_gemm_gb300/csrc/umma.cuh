@@ -141,8 +141,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
                : "memory");
 }
 
-__device__ __forceinline__ void st_cluster(uint32_t addr_cluster, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr_cluster), "f"(v) : "memory");
+// Four floats into another CTA's shared memory, counted as 16 bytes on that CTA's
+// mbarrier: no fence of the sender's (a release at cluster scope takes about 1,500
+// cycles).
+__device__ __forceinline__ void st_async4(uint32_t addr_cluster, uint32_t bar_cluster, float a,
+                                          float b, float c, float d) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(
+          addr_cluster),
+      "r"(bar_cluster), "f"(a), "f"(b), "f"(c), "f"(d)
+      : "memory");
 }
 
 }  // namespace
