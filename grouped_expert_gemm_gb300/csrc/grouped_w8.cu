@@ -74,16 +74,16 @@ struct Table {
   int* begin;
   int* count;
 };
-constexpr int kTableInts = 8 + 3 * kMaxSeg + 8;
+__host__ __device__ constexpr int table_bytes(int n_seg) { return (8 + 3 * n_seg + 8) * 4; }
 
-__device__ __forceinline__ Table carve_table(int* p) {
+__device__ __forceinline__ Table carve_table(int* p, int n_seg) {
   Table t;
   t.abort_flag = p;
   t.tmem_slot = reinterpret_cast<uint32_t*>(p + 1);
   t.warp_tot = p + 4;
   t.start = p + 8;
-  t.begin = t.start + kMaxSeg + 1;
-  t.count = t.begin + kMaxSeg;
+  t.begin = t.start + n_seg + 1;
+  t.count = t.begin + n_seg;
   return t;
 }
 
@@ -182,7 +182,7 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage_base + kStages * kStageBytes);
   constexpr int kBars = 2 * kStages + 9;
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(bars + kBars);  // [2][2][128]
-  const Table tb = carve_table(reinterpret_cast<int*>(s_amax + 512));
+  const Table tb = carve_table(reinterpret_cast<int*>(s_amax + 512), a.n_seg);
   volatile int* abort_flag = tb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_blocks = (a.N + (SWIGLU ? 127 : 255)) / (SWIGLU ? 128 : 256);
@@ -414,7 +414,7 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
 }
 
 constexpr int kSmemBytes =
-    1024 + kStages * kStageBytes + (2 * kStages + 9) * 8 + 512 * 4 + kTableInts * 4;
+    1024 + kStages * kStageBytes + (2 * kStages + 9) * 8 + 512 * 4 + table_bytes(kMaxSeg);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 // ------------------------------- few rows a segment --------------------------
@@ -442,7 +442,8 @@ constexpr int kFewThreads = 320;
 template <bool SWIGLU, int NT, int SPLIT>
 struct Few {
   // Two CTAs an SM where two stages each fit: one's set-up, epilogue and launch
-  // overlap the other's streaming (the down pass's first weights the gate/up pass).
+  // overlap the other's streaming.  The split passes share an SM with each other: a
+  // gate/up CTA of three stages beside a down CTA that holds its first two.
   static constexpr int kPerSm = NT == 64 || (NT == 32 && SPLIT == 2) ? 1 : 2;
   static constexpr int kBudget = (kPerSm == 2 ? 113 : 227) * 1024;
   static constexpr int kStageBytes = 2 * kBBox + NT * kBK;
@@ -452,12 +453,14 @@ struct Few {
   static constexpr int kUpBytes = SWIGLU && SPLIT == 1 ? NT * 128 * 4 : 0;
   static constexpr int kTopBytes = 2 * 4 * NT * 4;
   // bars: full[S], empty[S], tfull[4], tempty[4], upfull, upfree, top, red, redfree, drain
-  static constexpr int kFixed = 1024 + kUpBytes + kRedBytes + kTopBytes + kTableInts * 4 + 64 * 8;
-  static constexpr int kStages = (kBudget - kFixed) / kStageBytes;
+  static constexpr int kFixed = 1024 + kUpBytes + kRedBytes + kTopBytes + 64 * 8;  // + the table
+  static constexpr int kStages = NT == 16 && SPLIT == 2 ? (SWIGLU ? 3 : 2)
+                                     : (kBudget - kFixed - table_bytes(kMaxSeg)) / kStageBytes;
   static constexpr int kBars = 2 * kStages + 2 * kFewBufs + 6;
   static constexpr int kTmem = kFewBufs * 2 * NT;
   static constexpr int kSmem = kFixed + kStages * kStageBytes;
-  static_assert(kBars <= 64 && kStages >= 2 && kSmem <= kBudget, "shared memory");
+  static_assert(kBars <= 64 && kStages >= 2, "stages");
+  static_assert(kSmem + table_bytes(kMaxSeg) <= 227 * 1024, "shared memory");
   static_assert(kTmem * kPerSm <= 512 && kTmem >= 32, "tensor memory");
 };
 
@@ -475,7 +478,7 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
   float4* s_red = reinterpret_cast<float4*>(bars + 64);                       // [2][NT/4][128]
   float4* s_up = SPLIT > 1 ? s_red + NT / 4 * 128 : s_red;                    // [NT/4][128]
   uint32_t* s_top = reinterpret_cast<uint32_t*>(s_red + (F::kRedBytes + F::kUpBytes) / 16);  // [2][4][NT]
-  const Table tb = carve_table(reinterpret_cast<int*>(s_top + F::kTopBytes / 4));
+  const Table tb = carve_table(reinterpret_cast<int*>(s_top + F::kTopBytes / 4), a.n_seg);
   volatile int* abort_flag = tb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCols = SWIGLU ? 128 : 256;  // output columns per tile
@@ -926,10 +929,10 @@ moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtens
   auto kern = grouped_w8_few_kernel<SWIGLU, NT, SPLIT>;
   static std::mutex mu;
   static bool done[64] = {};
-  if (!opt_in(kern, F::kSmem, mu, done)) return MOE_ERR_CUDA;
+  if (!opt_in(kern, F::kSmem + table_bytes(kMaxSeg), mu, done)) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.dynamicSmemBytes = F::kSmem + table_bytes(a.n_seg);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -940,7 +943,7 @@ moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtens
   if constexpr (SPLIT > 1) {
     static std::mutex mu2;
     static int pairs[64] = {};
-    int n = resident_pairs(kern, kFewThreads, F::kSmem, mu2, pairs);
+    int n = resident_pairs(kern, kFewThreads, F::kSmem + table_bytes(kMaxSeg), mu2, pairs);
     if (n <= 0) return MOE_ERR_CUDA;
     if (n > sm_count() / 2) n = sm_count() / 2;  // one CTA an SM streams as fast as two
     grid = static_cast<unsigned>(2 * n);
