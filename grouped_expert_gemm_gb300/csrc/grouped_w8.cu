@@ -6,6 +6,14 @@
 //   row's 128 columns;  y = bf16((hq hs) Wd^T)
 // (weights stored [N, K], K contiguous: both operands are K-major).
 //
+// Bound: decode sizes HBM (the touched experts' weights), 93 us for the 128 experts of
+// the 2048 x 768 decode bucket (604 MB, 98 % of the copy rate); large segments the
+// tensor memory: a block's MMAs take about 735 cycles a CTA (a product without the
+// per-block sums reaches 3.07 PFLOP/s), and reading its 128 KB of sums another 195,
+// during which the MMAs wait for the port -- whether 8 or 16 warps read, and however
+// fast they add; together 930 cycles, 2.5 PFLOP/s, where the down pass of 8 x 1024
+// rows, 14336 x 4096, runs (gate/up with its SwiGLU and codes: 2.4).
+//
 // One reduction block of 128 is one pipeline stage, one row of the 128-byte
 // swizzle and one scale block.  The tensor core sums the block's codes into a
 // tensor-memory buffer of its own; the promotion warps read it, multiply by the
@@ -421,16 +429,16 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 // Decode-sized segments stream the weights; a 128-row tile would stage and sum
 // mostly foreign rows.  Here the weights are the M operand: two [128 x 128] weight
 // boxes a stage (gate and up of 128 columns, or 256 columns of down) against a box
-// of NT rows, so D^T is [2 x 128 columns] x [NT rows].  A promotion thread owns one
+// of NT rows (16 or 32), so D^T is [2 x 128 columns] x [NT rows].  A promotion thread owns one
 // weight column and NT sums; the rows' scales come to it by shuffles.  Eight
 // promotion warps: the four lane quadrants of either box.  Four tensor-memory
 // buffers of 2 x NT columns.
 //
-// With SPLIT = 2 a cluster of two CTAs shares a tile, each taking half of the
-// reduction blocks; rank 1 hands its sums to rank 0 through distributed shared
-// memory and rank 0 adds them to its own.  Taken when the tiles are fewer than half
-// of the SMs: one SM streams about 60 GB/s, so the number of SMs that stream sets
-// the time.
+// With SPLIT = 2 or 4 a cluster of that many CTAs shares a tile, each taking its part
+// of the reduction blocks; the others hand their sums to rank 0 through distributed
+// shared memory and rank 0 adds them in rank order.  One SM streams about 60 GB/s, so
+// where the tiles are fewer than half (a fifth) of the SMs the number of SMs that
+// stream sets the time: see launch_pass.
 //
 // CHAINED (down pass issued by moe_grouped_swiglu_w8 right behind its gate/up pass):
 // the segment table and the first stages' weights, which the gate/up pass does not
@@ -442,14 +450,15 @@ constexpr int kFewThreads = 320;
 template <bool SWIGLU, int NT, int SPLIT>
 struct Few {
   // Two CTAs an SM where two stages each fit: one's set-up, epilogue and launch
-  // overlap the other's streaming.  The split passes share an SM with each other: a
-  // gate/up CTA of three stages beside a down CTA that holds its first two.
-  static constexpr int kPerSm = NT == 64 || (NT == 32 && SPLIT == 2) ? 1 : 2;
+  // overlap the other's streaming (decode bucket 102 -> 98 us).  The passes split in
+  // two share an SM with each other: a gate/up CTA of three stages beside a down CTA
+  // that holds its first two.
+  static constexpr int kPerSm = SPLIT == 4 || (NT == 32 && SPLIT == 2) ? 1 : 2;
   static constexpr int kBudget = (kPerSm == 2 ? 113 : 227) * 1024;
   static constexpr int kStageBytes = 2 * kBBox + NT * kBK;
-  // rank 1's sums ([2][NT / 4][128][4]), and the up sums for the gate warps (in the
-  // second half of that buffer, or one of their own)
-  static constexpr int kRedBytes = SPLIT > 1 ? 2 * NT * 128 * 4 : 0;
+  // the other ranks' sums ([SPLIT - 1][2][NT / 4][128][4]), and the up sums for the gate
+  // warps (in rank 1's second half, or a buffer of their own)
+  static constexpr int kRedBytes = (SPLIT - 1) * 2 * NT * 128 * 4;
   static constexpr int kUpBytes = SWIGLU && SPLIT == 1 ? NT * 128 * 4 : 0;
   static constexpr int kTopBytes = 2 * 4 * NT * 4;
   // bars: full[S], empty[S], tfull[4], tempty[4], upfull, upfree, top, red, redfree, drain
@@ -475,7 +484,7 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
   uint8_t* stage_base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage_base + kStages * F::kStageBytes);
-  float4* s_red = reinterpret_cast<float4*>(bars + 64);                       // [2][NT/4][128]
+  float4* s_red = reinterpret_cast<float4*>(bars + 64);                       // [SPLIT-1][2][NT/4][128]
   float4* s_up = SPLIT > 1 ? s_red + NT / 4 * 128 : s_red;                    // [NT/4][128]
   uint32_t* s_top = reinterpret_cast<uint32_t*>(s_red + (F::kRedBytes + F::kUpBytes) / 16);  // [2][4][NT]
   const Table tb = carve_table(reinterpret_cast<int*>(s_top + F::kTopBytes / 4), a.n_seg);
@@ -615,6 +624,10 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
     const int m = quad * 32 + lane;
     const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * NT;
     constexpr int kPer = (NT + 31) / 32;  // rows whose scales this lane holds
+    auto free_partners = [&]() {
+#pragma unroll
+      for (int o = 1; o < SPLIT; ++o) mbar_arrive_cluster(map_to_rank(red_free, o));
+    };
     int buf = 0;
     uint32_t acc_ph = 0, tile_ph = 0;
     bool ok = true;
@@ -669,13 +682,14 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
         if (++buf == kFewBufs) { buf = 0; acc_ph ^= 1u; }
       }
       if (!ok) break;
-      const bool more = t + groups < total;  // rank 1 will need the buffer again
+      const bool more = t + groups < total;  // the other ranks will need the buffer again
       if constexpr (SPLIT > 1) {
         float4* mine = s_red + half * (NT / 4 * 128) + m;
-        if (rank == 1) {
+        if (rank > 0) {
           if (!__all_sync(0xFFFFFFFFu, wait_bounded<true>(red_free, tile_ph ^ 1u, abort_flag, a.dev_status)))
             break;
-          const uint32_t dst = map_to_rank(smem_u32(mine), 0), bar = map_to_rank(red_full, 0);
+          const uint32_t dst = map_to_rank(smem_u32(mine + (rank - 1) * (NT / 2 * 128)), 0);
+          const uint32_t bar = map_to_rank(red_full, 0);
 #pragma unroll
           for (int j = 0; j < NT; j += 4)
             st_async4(dst + j * 512, bar, acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
@@ -684,11 +698,13 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
         if (!__all_sync(0xFFFFFFFFu, wait_bounded<true>(red_full, tile_ph, abort_flag, a.dev_status)))
           break;
 #pragma unroll
-        for (int j = 0; j < NT; j += 4) {
-          const float4 v = mine[j / 4 * 128];
-          acc[j] += v.x; acc[j + 1] += v.y; acc[j + 2] += v.z; acc[j + 3] += v.w;
-        }
-        if (!SWIGLU && more) mbar_arrive_cluster(map_to_rank(red_free, 1));
+        for (int o = 0; o < SPLIT - 1; ++o)
+#pragma unroll
+          for (int j = 0; j < NT; j += 4) {
+            const float4 v = mine[(o * (NT / 2) + j / 4) * 128];
+            acc[j] += v.x; acc[j + 1] += v.y; acc[j + 2] += v.z; acc[j + 3] += v.w;
+          }
+        if (!SWIGLU && more) free_partners();
       }
       if constexpr (SWIGLU) {
         if (half == 1) {
@@ -721,7 +737,7 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
           mbar_arrive(up_free);
           mbar_arrive(top_bar);
         }
-        if (SPLIT > 1 && more) mbar_arrive_cluster(map_to_rank(red_free, 1));
+        if (SPLIT > 1 && more) free_partners();
         if (!__all_sync(0xFFFFFFFFu, wait_bounded(top_bar, tile_ph, abort_flag, a.dev_status))) break;
         float k[kPer], inv[kPer];
 #pragma unroll
@@ -888,26 +904,27 @@ moe_status check_shape(int32_t n_seg, int32_t K, int32_t N, int32_t max_rows) {
   if (n_seg <= 0 || K <= 0 || N <= 0 || max_rows < 0) return MOE_ERR_INVALID_ARG;
   if (n_seg > kMaxSeg || K % 16 != 0 || N % 16 != 0 || K > 65536 || N > 65536)
     return MOE_ERR_UNSUPPORTED;
-  // tile numbers are 32-bit
-  if ((static_cast<int64_t>(max_rows) / 16 + n_seg) * ceil_div(N, 128) >= (int64_t(1) << 31))
+  // row and tile numbers are 32-bit, a tile's last row among them
+  if (max_rows > INT32_MAX - 1024 ||
+      (static_cast<int64_t>(max_rows) / 16 + n_seg) * ceil_div(N, 128) >= (int64_t(1) << 31))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
-// Clusters of two CTAs that can be resident at once, read once per kernel and device.
+// Clusters that can be resident at once, read once per kernel and device.
 template <typename Kernel>
-int resident_pairs(Kernel kern, int threads, int smem, std::mutex& mu, int (&cache)[64]) {
+int resident_clusters(Kernel kern, int cluster, int smem, std::mutex& mu, int (&cache)[64]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (cache[dev] == 0) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(sm_count() & ~1));
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = dim3(static_cast<unsigned>(sm_count() / cluster * cluster));
+    cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -915,9 +932,10 @@ int resident_pairs(Kernel kern, int threads, int smem, std::mutex& mu, int (&cac
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
-      n = sm_count() / 2;
+      n = sm_count() / cluster;
     }
-    cache[dev] = n;
+    // one CTA an SM streams as fast as two
+    cache[dev] = n < sm_count() / cluster ? n : sm_count() / cluster;
   }
   return cache[dev];
 }
@@ -942,13 +960,12 @@ moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtens
   unsigned grid = static_cast<unsigned>(F::kPerSm * sm_count());
   if constexpr (SPLIT > 1) {
     static std::mutex mu2;
-    static int pairs[64] = {};
-    int n = resident_pairs(kern, kFewThreads, F::kSmem + table_bytes(kMaxSeg), mu2, pairs);
+    static int clusters[64] = {};
+    const int n = resident_clusters(kern, SPLIT, F::kSmem + table_bytes(kMaxSeg), mu2, clusters);
     if (n <= 0) return MOE_ERR_CUDA;
-    if (n > sm_count() / 2) n = sm_count() / 2;  // one CTA an SM streams as fast as two
-    grid = static_cast<unsigned>(2 * n);
+    grid = static_cast<unsigned>(SPLIT * n);
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = SPLIT;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
@@ -958,11 +975,17 @@ moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtens
   return launch_status();
 }
 
-// Rows per tile: the few-rows kernel with four times the average rows a segment
-// (segments are uneven), from 16 to 64; above, the 128-row kernel.
+// Rows per tile by the average rows of a segment: 16 up to 8, 32 up to 32 (segments are
+// uneven; a longer one takes several tiles), above that the 128-row kernel.  A single
+// segment is as long as the batch: four times those bounds.  Measured (us of both
+// passes, 16 / 32 / 128 rows; 64 was slower than 128 everywhere): 128 experts,
+// 2048 x 768: average 4: 94 / 95 / 97, 8: 95 / 100 / 103, 12: 105 / 100 / 105,
+// 32: 142 / 114 / 117, 48: 175 / 134 / 122; one expert, 7168 x 2048: 24 rows 30 / 33 / 39,
+// 64: 36 / 34 / 40, 128: 57 / 40 / 41, 160: 77 / 56 / 42; eight experts, 4096 x 4096
+// (more blocks a tile than stages): average 4: 79 / 80 / 75, 16: 92 / 82 / 77.
 int choose_rows(int32_t n_seg, int32_t max_rows) {
-  const int64_t four_avg = 4 * static_cast<int64_t>(max_rows) / n_seg;
-  return four_avg <= 16 ? 16 : four_avg <= 32 ? 32 : four_avg <= 64 ? 64 : kBM;
+  const int64_t avg = static_cast<int64_t>(max_rows) / (n_seg == 1 ? 4 : n_seg);
+  return avg <= 8 ? 16 : avg <= 32 ? 32 : kBM;
 }
 
 template <bool SWIGLU>
@@ -976,15 +999,19 @@ moe_status launch_pass(W8Args a, const void* x, const void* b0, const void* b1, 
   if (nt < kBM) {
     a.chained = chained;
     a.m_outer = 0;
-    // tiles that hold rows, at most: split the reduction where they leave half of the
-    // SMs idle
+    // Tiles that hold rows, at most.  The reduction split over 1 / 2 / 4 CTAs (us of both
+    // passes): 16 tiles, K = 7168: 46 / 28 / 21, K = 4096: 28 / 20 / 17; 48 tiles
+    // 19 / 17 / 20; 64: 50 / 31 / 28; from half of the SMs on it only adds the hand-over
+    // (96 tiles: 22 / 24 / 29).
     const int64_t tiles = std::min<int64_t>(a.n_seg, a.max_rows) * ceil_div(a.N, SWIGLU ? 128 : 256);
-    const bool split = 2 * tiles <= sm_count() && a.GK >= 2;
-    if (nt == 16) return split ? launch_few<SWIGLU, 16, 2>(ma, m0, m1, a, s)
-                               : launch_few<SWIGLU, 16, 1>(ma, m0, m1, a, s);
-    if (nt == 32) return split ? launch_few<SWIGLU, 32, 2>(ma, m0, m1, a, s)
-                               : launch_few<SWIGLU, 32, 1>(ma, m0, m1, a, s);
-    return launch_few<SWIGLU, 64, 1>(ma, m0, m1, a, s);
+    const int split = 5 * tiles <= sm_count() && a.GK >= 8 ? 4 : 2 * tiles <= sm_count() && a.GK >= 2 ? 2 : 1;
+    if (nt == 16) {
+      if (split == 4) return launch_few<SWIGLU, 16, 4>(ma, m0, m1, a, s);
+      if (split == 2) return launch_few<SWIGLU, 16, 2>(ma, m0, m1, a, s);
+      return launch_few<SWIGLU, 16, 1>(ma, m0, m1, a, s);
+    }
+    if (split > 1) return launch_few<SWIGLU, 32, 2>(ma, m0, m1, a, s);
+    return launch_few<SWIGLU, 32, 1>(ma, m0, m1, a, s);
   }
   static std::mutex mu;
   static bool done[64] = {};

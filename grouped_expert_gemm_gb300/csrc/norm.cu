@@ -374,9 +374,10 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
 // dw = column sums of the partial rows, in a fixed order: 32 interleaved groups of
 // rows per column, then the groups in order.
 __global__ void __launch_bounds__(1024)
-weight_grad_kernel(int blocks, int d, const float* __restrict__ part, float* __restrict__ dw) {
+weight_grad_kernel(int blocks, int d, const float* __restrict__ part, float* __restrict__ dw,
+                   int early) {
   __shared__ float sh[32][33];
-  pdl_wait_then_trigger(true);  // (at most 512 blocks of 1,024 threads, two to an SM)
+  pdl_wait_then_trigger(early);
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   float s = 0.0f;
@@ -391,6 +392,7 @@ weight_grad_kernel(int blocks, int d, const float* __restrict__ part, float* __r
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if (lane == 0 && blockIdx.x * 32 + g < d) dw[blockIdx.x * 32 + g] = s;
+  if (!early) pdl_trigger();
 }
 
 // --------------------------------- host side --------------------------------
@@ -566,6 +568,7 @@ MOE_API moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t d
   else launch_backward<4>(a, dy32, r32, pl, s);
   if (dweight != nullptr)
     launch(weight_grad_kernel, dim3(static_cast<unsigned>(ceil_div(p->d, 32))), dim3(1024), 0, s,
-           pl.blocks, p->d, static_cast<const float*>(ws), dweight);
+           pl.blocks, p->d, static_cast<const float*>(ws), dweight,
+           static_cast<int>(one_wave(ceil_div(p->d, 32))));
   return launch_status();
 }

@@ -147,10 +147,10 @@ def test_many_segments(seed):
 
 
 @pytest.mark.parametrize("d,I", [(64, 128), (208, 144), (1040, 272)])
-@pytest.mark.parametrize("counts", [[0] * 30 + [40, 17, 1], [9] * 20 + [0, 100], [1] * 75 + [229], [2, 0]])
+@pytest.mark.parametrize("counts", [[0] * 30 + [40, 17, 1], [9] * 20 + [0, 100], [1] * 75 + [229], [2, 0], [40], [100]])
 def test_few_rows_and_uneven_segments(d, I, counts):
-    """Row tiles of 16, 32 and 64; segments longer than their tile; the reduction split over
-    two CTAs with one and with several tiles each."""
+    """Row tiles of 16 and 32; segments longer than their tile; the reduction split over two
+    and four CTAs with one and with several tiles each."""
     check(make(d, I, counts, seed=d + len(counts), gaps=3, tail=1))
 
 
@@ -164,6 +164,13 @@ def test_one_token_of_the_decode_shape():
 def test_decode_bucket():
     gen = torch.Generator().manual_seed(9)
     check(make(2048, 768, torch.randint(0, 17, (64,), generator=gen).tolist(), seed=5))
+
+
+@pytest.mark.parametrize("counts", [[1], [7, 0, 1], [16], [33], [120], [1] * 14 + [150]])
+def test_split_reductions(counts):
+    """Few tiles and many reduction blocks: clusters of two and four, uneven parts (33
+    blocks over four CTAs), segments of several tiles."""
+    check(make(4112, 1168, counts, seed=20 + len(counts)))
 
 
 def test_long_reduction():
