@@ -359,7 +359,7 @@ balance_finish_kernel(const BalArgs a) {
 // row is normalised; the selected experts' terms reach their lanes through a row of
 // shared memory that is zero between tokens.
 template <int VEC, int N, bool SIG>
-__global__ void __launch_bounds__(kBwdThreads, VEC * N <= 12 ? 4 : 2)
+__global__ void __launch_bounds__(kBwdThreads, VEC * N <= 8 ? 4 : VEC * N <= 12 ? 4 : 2)
 route_backward_kernel(const BalArgs a) {
   constexpr int M = VEC * N;
   constexpr int kWarps = kBwdThreads / 32;
@@ -444,10 +444,10 @@ route_backward_kernel(const BalArgs a) {
         dot = warp_add(dot);
       }
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-      const float shift = dot * inv;
+      const float shift = dot * inv * inv;
 #pragma unroll
       for (int i = 0; i < M; ++i) {
-        v[i] = v[i] * inv * (w[i] - shift);
+        v[i] *= fmaf(w[i], inv, -shift);
         if constexpr (SIG) v[i] *= slope[i];
       }
     } else {

@@ -117,30 +117,42 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, int nw, float* sh, int& 
   return v;
 }
 
-// Largest |v| of 8 values as fp32 bits (integer order; NaN above Inf).
+// Largest |v| of 8 values; NaN if one is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t amax8(const float f[8]) {
-  uint32_t m = 0;
+  float m = fabsf(f[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-  return m;
+  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[i]));
+  return __float_as_uint(m) & 0x7FFFFFFFu;  // as bits: integer order, NaN above Inf
 }
 
 __device__ __forceinline__ float scale_of(uint32_t amax) {
   return amax == 0 ? 1.0f : __fdiv_rn(__uint_as_float(amax), kE4M3Max);
 }
 
-// 8 codes of v / s as v * (1 / s): one division a group instead of one a value (the
-// divisions were two thirds of the instructions of the 7,168-wide case).  A scale
-// near the type's smallest values is taken 2^64 larger, so that its reciprocal stays
-// finite.
+// 8 codes of v / s as v * (1 / s): one reciprocal a group instead of a division a value
+// (with the divisions the 7,168-wide case was bound by instructions, 148 us).  Scales
+// below the normal range, whose reciprocal could overflow, divide.
 __device__ __forceinline__ uint2 quant8(const float f[8], float s) {
-  const float k = s < 0x1p-60f ? 0x1p64f : 1.0f;
-  const float inv = __frcp_rn(s * k);
+  float v[8];
+  if (s >= 0x1p-126f) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f[i] * inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(f[i], s);
+  }
   uint32_t p[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    p[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * k * inv, f[2 * i + 1] * k * inv),
-                                    __NV_SATFINITE, __NV_E4M3);
+    p[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
 }
 
@@ -188,12 +200,17 @@ add_rms_norm_kernel(const NormArgs a) {
           float r[8];
           nr[i].get(r);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            h[i][j] += r[j];
-            if constexpr (!R32) h[i][j] = __bfloat162float(__float2bfloat16_rn(h[i][j]));
-          }
+          for (int j = 0; j < 8; ++j) h[i][j] += r[j];
         }
-        if (a.res_out != nullptr) store8(a.res_out, R32, base + 8 * c, h[i]);
+        if constexpr (R32) {
+          if (a.res_out != nullptr) store8(a.res_out, 1, base + 8 * c, h[i]);
+        } else {  // the stored bf16 sum is what is normalised
+          const uint4 p = make_uint4(pack_bf16x2(h[i][0], h[i][1]), pack_bf16x2(h[i][2], h[i][3]),
+                                     pack_bf16x2(h[i][4], h[i][5]), pack_bf16x2(h[i][6], h[i][7]));
+          if (a.res_out != nullptr)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.res_out) + base + 8 * c) = p;
+          unpack8(p, h[i]);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss += h[i][j] * h[i][j];
       }
