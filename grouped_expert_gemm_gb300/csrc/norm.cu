@@ -494,12 +494,11 @@ MOE_API moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, con
                                     moe_fp8* q, float* scales, float* rstd, uint32_t* dev_status,
                                     moe_stream_t stream) {
   const moe_status st = check_norm(p);
-  if (st != MOE_OK) return st;
+  if (st != MOE_OK || p->n == 0) return st;
   if (residual == nullptr && p->residual_type != p->x_type) return MOE_ERR_INVALID_ARG;
   if (residual != nullptr && residual_out == nullptr) return MOE_ERR_INVALID_ARG;
   if ((q == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARG;
   if (y == nullptr && q == nullptr) return MOE_ERR_INVALID_ARG;
-  if (p->n == 0) return MOE_OK;
   if (x == nullptr || weight == nullptr) return MOE_ERR_INVALID_ARG;
   if (q != nullptr && p->d % 16 != 0) return MOE_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
@@ -545,14 +544,14 @@ MOE_API moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t d
   const moe_status st = check_norm(p);
   if (st != MOE_OK) return st;
   if (dy_type != MOE_DTYPE_BF16 && dy_type != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
-  if (dx == nullptr && dresidual == nullptr && dweight == nullptr) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = as_cuda(stream);
-  if (p->n == 0) {
+  if (p->n == 0) {  // (empty tensors have no address)
     if (dweight != nullptr &&
         cudaMemsetAsync(dweight, 0, static_cast<size_t>(p->d) * sizeof(float), s) != cudaSuccess)
       return MOE_ERR_CUDA;
     return MOE_OK;
   }
+  if (dx == nullptr && dresidual == nullptr && dweight == nullptr) return MOE_ERR_INVALID_ARG;
   if (dy == nullptr || h == nullptr || weight == nullptr || rstd == nullptr)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(dresidual_out) ||

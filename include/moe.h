@@ -797,8 +797,12 @@ moe_status moe_quantize_weights_fp8(int32_t n_seg, int32_t K, int32_t N, const m
  * multiplied by the row's and the weight block's scales and added in fp32.
  * Only segment rows of y are written.  hq / hs live in the workspace
  * (moe_grouped_swiglu_w8_workspace_size(max_rows, I) bytes, 16-byte aligned; 0 =
- * invalid sizes), also only for segment rows.
- * Limits: d % 16 == 0, I % 16 == 0, d, I <= 65536, n_seg <= 1024; 16-byte aligned
+ * invalid sizes), also only for segment rows: calls, and replays of graphs that
+ * captured them, that overlap on the GPU must not share it.  The segment table and
+ * the weights are read before the gate/up pass has ended: nothing enqueued after that
+ * pass may write them (the call itself enqueues both).
+ * Limits: d % 16 == 0, I % 16 == 0, d, I <= 65536, n_seg <= 1024, max_rows below
+ * 2^31 - 1024; 16-byte aligned
  * codes and y, 4-byte aligned scales.  Segments outside [0, max_rows) set
  * MOE_DEV_BAD_ROW and are skipped.  A NaN or Inf in H sets
  * MOE_DEV_NONFINITE_INPUT (that row's codes are then unspecified).             */

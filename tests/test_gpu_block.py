@@ -194,3 +194,19 @@ def test_block_captured_and_replayed():
     torch.cuda.synchronize()
     assert torch.equal(layer.out, want) and torch.equal(loss.dlogits, want_dz)
     assert torch.equal(norm._grads[0], want_dx)
+
+
+def test_empty_batch():
+    g = G()
+    w = torch.ones(64, device=DEV)
+    for payload in ("bf16", "fp8_block128"):
+        norm = g.TokenNorm(0, 64, w, x_dtype=torch.float32, payload=payload, device=DEV)
+        x, res = torch.empty((0, 64), device=DEV), torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+        norm.forward(x, res)
+        dx, dres, dw = norm.backward(x, res)
+        assert dx.shape == (0, 64) and dres.shape == (0, 64) and (dw == 0).all()
+    loss = g.RouterLoss(0, 8, 2, 0.1, device=DEV)
+    z, ids = torch.empty((0, 8), device=DEV), torch.empty((0, 2), dtype=torch.int32, device=DEV)
+    assert float(loss.forward(z, ids)) == 0 and (loss.counts == 0).all()
+    assert loss.backward(z, ids).shape == (0, 8)
+    torch.cuda.synchronize()

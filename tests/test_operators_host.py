@@ -22,6 +22,8 @@ def test_norm_refusals(g):
 
     ok = N(0, 64)
     assert fwd(ok) == g.MOE_OK  # no rows: nothing launches
+    # an empty batch has no addresses: nothing to refuse, whatever the types
+    assert fwd(N(0, 64, x_type=1), x=None, res=None, ro=None, y=None) == g.MOE_OK
     assert L.moe_add_rms_norm(None, 16, 16, 16, 16, 16, None, None, None, None, None) == ARG
     for p in (N(-1, 64), N(1, 0), N(1, -8), N(1, 64, x_type=2), N(1, 64, residual_type=-1),
               N(1, 64, group=64), N(1, 64, eps=0.0), N(1, 64, eps=-1.0), N(1, 64, eps=math.nan),
@@ -42,7 +44,7 @@ def test_norm_refusals(g):
     def bwd(p, t=0, dy=16, h=16, w=16, rstd=16, dro=None, dx=16, dr=None, dw=None, ws=None, nb=0):
         return L.moe_add_rms_norm_backward(p, t, dy, h, w, rstd, dro, dx, dr, dw, ws, nb, None)
 
-    assert bwd(ok) == g.MOE_OK
+    assert bwd(ok) == g.MOE_OK and bwd(ok, dy=None, h=None, rstd=None, dx=None) == g.MOE_OK
     assert bwd(p, t=2) == ARG and bwd(p, dx=None) == ARG
     for k in ("dy", "h", "w", "rstd"):
         assert bwd(p, **{k: None}) == ARG
