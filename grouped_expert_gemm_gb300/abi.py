@@ -217,9 +217,10 @@ def lib() -> ctypes.CDLL:
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:  # an address
         return t
-    return t.data_ptr()
 
 
 # torch.cuda.current_stream() builds a Stream object (3 us a call on the GB300's host);
