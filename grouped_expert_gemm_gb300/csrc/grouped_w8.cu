@@ -24,15 +24,18 @@
 //
 // Tile: 128 rows x 256 weight columns (gate/up: 128 gate + the same 128 up, so a
 // tile makes one whole scale group of H; down: 256 columns of y).  Roles of the 320
-// threads (so that each may hold 200 registers), one CTA per SM, persistent over the
-// tiles:
+// threads, one CTA per SM, persistent over the tiles:
 //   warp 0       TMA producer: [128 x 128] codes of A, two [128 x 128] of B, 48 KB
 //                a stage, four stages
 //   warp 1       allocates tensor memory; lane 0 issues four MMAs (K = 32) a stage
 //   warps 2..9   promotion and epilogue: warp w reads lanes 32 (w % 4).., columns of
 //                half (w - 2) / 4; 128 fp32 sums per thread
 // Two tensor-memory buffers of 256 columns: block kb + 1 is summed while kb is
-// promoted.  Every wait is bounded (MOE_DEV_TIMEOUT), as in the bf16 pass.
+// promoted.  With few tiles and a long reduction a cluster of two or four CTAs takes each
+// tile, a part of the blocks to a CTA; every CTA then sends its sums of the other CTAs'
+// rows to them through distributed shared memory and finishes its own quarter or half
+// (two rounds of a tree, with rank 0 alone in the epilogue, took 2 us longer a pass).
+// Every wait is bounded (MOE_DEV_TIMEOUT), as in the bf16 pass.
 #include <algorithm>
 #include <mutex>
 
@@ -50,6 +53,8 @@ constexpr int kStageBytes = kABytes + 2 * kBBox;
 constexpr int kStages = 4;
 constexpr int kAccCols = 256;
 constexpr int kThreads = 320;
+constexpr int kBars = 2 * kStages + 14;  // (an even number)
+constexpr int kWarpSums = 32 * 128 * 4;  // a promotion warp's sums, in bytes
 
 constexpr float kE4M3Max = 448.0f;
 constexpr uint32_t kAbsInf = 0x7F800000u;
@@ -178,7 +183,7 @@ __device__ __forceinline__ void promote16(const uint32_t (&part)[16], float s, f
                         s2, acc[i]);
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
                   const __grid_constant__ CUtensorMap map_b0,
@@ -186,13 +191,15 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stage_base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // bars: full[S], empty[S], tfull[2], tempty[2], amax[4], drain
+  // bars: full[S], empty[S], tfull[2], tempty[2], amax[4], drain, go[4], red
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage_base + kStages * kStageBytes);
-  constexpr int kBars = 2 * kStages + 9;
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(bars + kBars);  // [2][2][128]
   const Table tb = carve_table(reinterpret_cast<int*>(s_amax + 512), a.n_seg);
   volatile int* abort_flag = tb.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = SPLIT > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / SPLIT, step = static_cast<int>(gridDim.x) / SPLIT;
+  const int kb0 = rank * a.GK / SPLIT, kb1 = (rank + 1) * a.GK / SPLIT;
   const int n_blocks = (a.N + (SWIGLU ? 127 : 255)) / (SWIGLU ? 128 : 256);
 
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
@@ -201,6 +208,8 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   auto tempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 2 + b); };
   auto amax_bar = [&](int q) { return smem_u32(bars + 2 * kStages + 4 + q); };
   const uint32_t drain_bar = smem_u32(bars + 2 * kStages + 8);
+  auto go_bar = [&](int i) { return smem_u32(bars + 2 * kStages + 9 + i); };
+  const uint32_t red_bar = smem_u32(bars + 2 * kStages + 13);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -213,6 +222,8 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
     }
     for (int q = 0; q < 4; ++q) mbar_init(amax_bar(q), 2);  // the two warps of a lane quadrant
     mbar_init(drain_bar, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(go_bar(i), 1);
+    mbar_init(red_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -221,10 +232,15 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   if (threadIdx.x >= 64 && threadIdx.x < 192)
     build_table(a, kBM, n_blocks, threadIdx.x - 64, tb);
   umma_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT > 1) cluster_sync();  // the partners' barriers are initialised
+  else __syncthreads();
   umma_fence_after();
   const uint32_t tmem = *tb.tmem_slot;
-  const int total = tb.start[a.n_seg];
+  int total = tb.start[a.n_seg];
+  if (SPLIT > 1 && total > step) {  // only segments that overlap have more tiles than clusters
+    if (threadIdx.x == 0) report(a.dev_status, MOE_DEV_BAD_ROW);
+    total = step;
+  }
 
   if (warp < 2) {
     if (warp == 0 && lane == 0) {
@@ -232,9 +248,9 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      for (int t = first; t < total && ok; t += step) {
         const Tile tl = tile_of(t, tb, a.n_seg, kBM, n_blocks, a.m_outer);
-        for (int kb = 0; kb < a.GK; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(empty_bar(s), ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
           const uint32_t st = smem_u32(stage_base + s * kStageBytes);
           mbar_arrive_expect_tx(full_bar(s), kStageBytes);
@@ -262,8 +278,8 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
       int s = 0, buf = 0;
       uint32_t ph = 0, acc_ph = 0;
       bool ok = true, issued = false;
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        for (int kb = 0; kb < a.GK; ++kb) {
+      for (int t = first; t < total && ok; t += step) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(tempty_bar(buf), acc_ph ^ 1u, abort_flag, a.dev_status) ||
               !wait_bounded(full_bar(s), ph, abort_flag, a.dev_status)) {
             ok = false;
@@ -278,6 +294,8 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
           issued = true;
           umma_commit(empty_bar(s));
           umma_commit(tfull_bar(buf));
+          if constexpr (SPLIT > 1)
+            if (kb + 1 == kb1) umma_commit_multicast(go_bar(rank), (1 << SPLIT) - 1);
           if (++s == kStages) { s = 0; ph ^= 1u; }
           if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
         }
@@ -296,9 +314,9 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
     const int c0 = SWIGLU ? 64 * half : 128 * half;
     const int c1 = SWIGLU ? 128 + 64 * half : 128 * half + 64;
     int buf = 0, parity = 0;
-    uint32_t acc_ph = 0;
+    uint32_t acc_ph = 0, tile_ph = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    for (int t = first; t < total && ok; t += step) {
       const Tile tl = tile_of(t, tb, a.n_seg, kBM, n_blocks, a.m_outer);
       const bool live = r < tl.rows;
       const int64_t row = min(tl.row0 + r, a.max_rows - 1);
@@ -310,10 +328,10 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
       float2 acc0[32], acc1[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc0[i] = acc1[i] = make_float2(0.0f, 0.0f);
-      float sa = __ldg(as), w0 = __ldg(b0), w1 = __ldg(b1);
-      for (int kb = 0; kb < a.GK; ++kb) {
+      float sa = __ldg(as + kb0), w0 = __ldg(b0 + kb0), w1 = __ldg(b1 + kb0);
+      for (int kb = kb0; kb < kb1; ++kb) {
         const float s0 = sa * w0, s1 = sa * w1;
-        if (kb + 1 < a.GK) {
+        if (kb + 1 < kb1) {
           sa = __ldg(as + kb + 1);
           w0 = __ldg(b0 + kb + 1);
           w1 = __ldg(b1 + kb + 1);
@@ -342,6 +360,53 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
         if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
       }
       if (!ok) break;
+      if constexpr (SPLIT > 1) {
+        // Each rank finishes the rows of 4 / SPLIT lane quadrants: every warp of another
+        // quadrant sends its sums there, into the stages, once the receiver's MMAs have read
+        // them for the last time (a cluster has one tile) and its commit says so here.
+        constexpr int kOwn = 4 / SPLIT;
+        const int owner = quad / kOwn;
+        if (threadIdx.x == 64) mbar_arrive_expect_tx(red_bar, (SPLIT - 1) * kOwn * 2 * kWarpSums);
+        __syncwarp();
+        // The slot of sender `from` for this warp: its distance behind the owner, the warp's
+        // quadrant in the owner's, its half of the columns.
+        auto slot = [&](int dist) {
+          return stage_base + (((dist - 1) * kOwn + quad % kOwn) * 2 + half) * kWarpSums + lane * 16;
+        };
+        if (owner != rank) {
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded<true>(go_bar(owner), tile_ph, abort_flag, a.dev_status));
+          if (ok) {
+            const uint32_t dst = map_to_rank(smem_u32(slot((rank - owner + SPLIT) % SPLIT)), owner);
+            const uint32_t bar = map_to_rank(red_bar, owner);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              st_async4(dst + j * 512, bar, acc0[2 * j].x, acc0[2 * j].y, acc0[2 * j + 1].x,
+                        acc0[2 * j + 1].y);
+              st_async4(dst + (16 + j) * 512, bar, acc1[2 * j].x, acc1[2 * j].y, acc1[2 * j + 1].x,
+                        acc1[2 * j + 1].y);
+            }
+          }
+        } else {
+          ok = __all_sync(0xFFFFFFFFu, wait_bounded<true>(red_bar, tile_ph, abort_flag, a.dev_status));
+          if (ok) {
+#pragma unroll
+            for (int i = 1; i < SPLIT; ++i) {
+              const float4* in = reinterpret_cast<const float4*>(slot(i));
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float4 v = in[j * 32], w = in[(16 + j) * 32];
+                acc0[2 * j].x += v.x; acc0[2 * j].y += v.y;
+                acc0[2 * j + 1].x += v.z; acc0[2 * j + 1].y += v.w;
+                acc1[2 * j].x += w.x; acc1[2 * j].y += w.y;
+                acc1[2 * j + 1].x += w.z; acc1[2 * j + 1].y += w.w;
+              }
+            }
+          }
+        }
+        tile_ph ^= 1u;
+        if (!ok) break;
+        if (owner != rank) continue;
+      }
       if constexpr (SWIGLU) {
         // H of 64 columns in place of the gate sums, their largest magnitude, the
         // other half's through shared memory, then the group's codes
@@ -412,7 +477,8 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   // ---- teardown ----
   __syncwarp();
   umma_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT > 1) cluster_sync();  // no CTA leaves while a partner may still reach it
+  else __syncthreads();
   umma_fence_after();
   if (warp == 1) {
     __syncwarp();
@@ -422,8 +488,9 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
 }
 
 constexpr int kSmemBytes =
-    1024 + kStages * kStageBytes + (2 * kStages + 9) * 8 + 512 * 4 + table_bytes(kMaxSeg);
+    1024 + kStages * kStageBytes + kBars * 8 + 512 * 4 + table_bytes(kMaxSeg);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+static_assert(kStages * kStageBytes >= 6 * kWarpSums, "a partner's sums fit the stages");
 
 // ------------------------------- few rows a segment --------------------------
 // Decode-sized segments stream the weights; a 128-row tile would stage and sum
@@ -445,7 +512,6 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 // write, are read before waiting for it.
 
 constexpr int kFewBufs = 4;
-constexpr int kFewThreads = 320;
 
 template <bool SWIGLU, int NT, int SPLIT>
 struct Few {
@@ -474,7 +540,7 @@ struct Few {
 };
 
 template <bool SWIGLU, int NT, int SPLIT>
-__global__ void __launch_bounds__(kFewThreads, Few<SWIGLU, NT, SPLIT>::kPerSm)
+__global__ void __launch_bounds__(kThreads, Few<SWIGLU, NT, SPLIT>::kPerSm)
 grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
                       const __grid_constant__ CUtensorMap map_w0,
                       const __grid_constant__ CUtensorMap map_w1, const W8Args a) {
@@ -929,7 +995,7 @@ int resident_clusters(Kernel kern, int cluster, int smem, std::mutex& mu, int (&
   if (cache[dev] == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(sm_count() / cluster * cluster));
-    cfg.blockDim = dim3(kFewThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -949,6 +1015,28 @@ int resident_clusters(Kernel kern, int cluster, int smem, std::mutex& mu, int (&
   return cache[dev];
 }
 
+// The library's launch (programmatic dependent launch), with clusters of `cluster` CTAs.
+template <typename Kernel>
+void launch_clustered(Kernel kern, unsigned grid, int smem, int cluster, cudaStream_t s,
+                      const CUtensorMap& m, const CUtensorMap& m0, const CUtensorMap& m1,
+                      const W8Args& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, kern, m, m0, m1, a);
+}
+
 template <bool SWIGLU, int NT, int SPLIT>
 moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtensorMap& m1,
                       const W8Args& a, cudaStream_t s) {
@@ -957,15 +1045,6 @@ moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtens
   static std::mutex mu;
   static bool done[64] = {};
   if (!opt_in(kern, F::kSmem + table_bytes(kMaxSeg), mu, done)) return MOE_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = F::kSmem + table_bytes(a.n_seg);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   unsigned grid = static_cast<unsigned>(F::kPerSm * sm_count());
   if constexpr (SPLIT > 1) {
     static std::mutex mu2;
@@ -973,28 +1052,47 @@ moe_status launch_few(const CUtensorMap& mx, const CUtensorMap& m0, const CUtens
     const int n = resident_clusters(kern, SPLIT, F::kSmem + table_bytes(kMaxSeg), mu2, clusters);
     if (n <= 0) return MOE_ERR_CUDA;
     grid = static_cast<unsigned>(SPLIT * n);
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = SPLIT;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
   }
-  cfg.gridDim = dim3(grid);
-  cudaLaunchKernelEx(&cfg, kern, mx, m0, m1, a);
+  launch_clustered(kern, grid, F::kSmem + table_bytes(a.n_seg), SPLIT, s, mx, m0, m1, a);
   return launch_status();
 }
 
-// Rows per tile by the average rows of a segment: 16 up to 8, 32 up to 32 (segments are
+// The 128-row kernel; with SPLIT > 1 only where every cluster has one tile at most, else
+// false and nothing launched.
+template <bool SWIGLU, int SPLIT>
+bool launch_rows(const CUtensorMap& ma, const CUtensorMap& m0, const CUtensorMap& m1,
+                 const W8Args& a, int64_t most_tiles, cudaStream_t s, moe_status& st) {
+  auto kern = grouped_w8_kernel<SWIGLU, SPLIT>;
+  unsigned grid = static_cast<unsigned>(sm_count());
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (!opt_in(kern, kSmemBytes, mu, done)) {
+    st = MOE_ERR_CUDA;
+    return true;
+  }
+  if constexpr (SPLIT > 1) {
+    static std::mutex mu2;
+    static int clusters[64] = {};
+    if (most_tiles > resident_clusters(kern, SPLIT, kSmemBytes, mu2, clusters)) return false;
+    grid = static_cast<unsigned>(SPLIT * most_tiles);
+  }
+  launch_clustered(kern, grid, kSmemBytes, SPLIT, s, ma, m0, m1, a);
+  st = launch_status();
+  return true;
+}
+
+// Rows per tile by the average rows of a segment: 16 up to 8, 32 up to 16 (segments are
 // uneven; a longer one takes several tiles), above that the 128-row kernel.  A single
-// segment is as long as the batch: four times those bounds.  Measured (us of both
+// segment is as long as the batch: 16 up to 32 rows, else 128.  Measured (us of both
 // passes, 16 / 32 / 128 rows; 64 was slower than 128 everywhere): 128 experts,
-// 2048 x 768: average 4: 94 / 95 / 97, 8: 95 / 100 / 103, 12: 105 / 100 / 105,
-// 32: 142 / 114 / 117, 48: 175 / 134 / 122; one expert, 7168 x 2048: 24 rows 30 / 33 / 39,
-// 64: 36 / 34 / 40, 128: 57 / 40 / 41, 160: 77 / 56 / 42; eight experts, 4096 x 4096
-// (more blocks a tile than stages): average 4: 79 / 80 / 75, 16: 92 / 82 / 77.
+// 2048 x 768: average 8: 93 / 98 / 102, 16: 106 / 100 / 105, 32: 142 / 114 / 117; 32 experts,
+// 4096 x 2048: 8: 117 / 123 / 139, 16: 144 / 130 / 142, 24: 170 / 161 / 144; eight experts,
+// 4096 x 1024: 8: 24 / 26 / 27, 16: 35 / 28 / 26, 32: 51 / 38 / 28; one expert, 7168 x 2048:
+// 32 rows 25 / 33 / 27, 48: 37 / 33 / 27, 128: 57 / 40 / 27.
 int choose_rows(int32_t n_seg, int32_t max_rows) {
-  const int64_t avg = static_cast<int64_t>(max_rows) / (n_seg == 1 ? 4 : n_seg);
-  return avg <= 8 ? 16 : avg <= 32 ? 32 : kBM;
+  if (n_seg == 1) return max_rows <= 32 ? 16 : kBM;
+  const int32_t avg = max_rows / n_seg;
+  return avg <= 8 ? 16 : avg <= 16 ? 32 : kBM;
 }
 
 template <bool SWIGLU>
@@ -1022,11 +1120,20 @@ moe_status launch_pass(W8Args a, const void* x, const void* b0, const void* b1, 
     if (split > 1) return launch_few<SWIGLU, 32, 2>(ma, m0, m1, a, s);
     return launch_few<SWIGLU, 32, 1>(ma, m0, m1, a, s);
   }
-  static std::mutex mu;
-  static bool done[64] = {};
-  if (!opt_in(grouped_w8_kernel<SWIGLU>, kSmemBytes, mu, done)) return MOE_ERR_CUDA;
-  launch(grouped_w8_kernel<SWIGLU>, dim3(sm_count()), dim3(kThreads), kSmemBytes, s, ma, m0, m1, a);
-  return launch_status();
+  // 128-row tiles, at most (each segment may end one).  From 16 blocks on the reduction is
+  // split over the largest cluster of which one round holds them all (us of both passes,
+  // 1 / 2 / 4 CTAs): one expert, 7168 x 2048, 128 rows: 41 / 32 / 27; 4096 x 14336:
+  // 83 / 62 / 51; 2048 x 2048: 23.4 / 21.8 / 20.9; with 8 blocks it only adds the hand-over
+  // (eight experts, 1024 x 1024, 128 rows each: 17.5 / 18.7).
+  const int64_t segs = std::min<int64_t>(a.n_seg, a.max_rows);
+  const int64_t tiles = (a.max_rows + 127 * segs) / 128 * ceil_div(a.N, SWIGLU ? 128 : 256);
+  moe_status st = MOE_OK;
+  if (a.GK >= 16) {
+    if (launch_rows<SWIGLU, 4>(ma, m0, m1, a, tiles, s, st)) return st;
+    if (launch_rows<SWIGLU, 2>(ma, m0, m1, a, tiles, s, st)) return st;
+  }
+  launch_rows<SWIGLU, 1>(ma, m0, m1, a, tiles, s, st);
+  return st;
 }
 
 struct Pass {

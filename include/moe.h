@@ -804,7 +804,8 @@ moe_status moe_quantize_weights_fp8(int32_t n_seg, int32_t K, int32_t N, const m
  * Limits: d % 16 == 0, I % 16 == 0, d, I <= 65536, n_seg <= 1024, max_rows below
  * 2^31 - 1024; 16-byte aligned
  * codes and y, 4-byte aligned scales.  Segments outside [0, max_rows) set
- * MOE_DEV_BAD_ROW and are skipped.  A NaN or Inf in H sets
+ * MOE_DEV_BAD_ROW and are skipped; segments that overlap (not allowed) may set it and
+ * leave rows unwritten.  A NaN or Inf in H sets
  * MOE_DEV_NONFINITE_INPUT (that row's codes are then unspecified).             */
 size_t moe_grouped_swiglu_w8_workspace_size(int32_t max_rows, int32_t I);
 moe_status moe_grouped_swiglu_w8(int32_t n_seg, int32_t d, int32_t I, int32_t max_rows,

@@ -173,6 +173,51 @@ def test_split_reductions(counts):
     check(make(4112, 1168, counts, seed=20 + len(counts)))
 
 
+@pytest.mark.parametrize("d,I", [(2064, 2064), (4112, 1168), (2048, 2192), (1936, 2048)])
+@pytest.mark.parametrize("counts", [[33], [128], [129], [300], [40, 0, 200], [64, 70, 1], [17, 9], [500, 12]])
+def test_split_reductions_of_long_segments(d, I, counts):
+    """128-row tiles few enough for clusters of four or two, beside reductions too short or
+    tiles too many for them; 15 to 33 blocks, uneven parts; a tile's last rows and columns."""
+    check(make(d, I, counts, seed=d + sum(counts), gaps=2, tail=1))
+
+
+def test_split_reduction_repeats_bit_for_bit():
+    """Two captured calls at once, replayed: the parts are added in one order."""
+    cases = [make(4096, 2048, [150], seed=31), make(2048, 4096, [40, 90], seed=32)]
+    g = G()
+    runs = []
+    for v in cases:
+        want = swiglu(v)[0]
+        nb = g.moe_grouped_swiglu_w8_workspace_size(v["R"], v["I"])
+        ws = torch.empty((nb,), dtype=torch.uint8, device=DEV)
+        y = torch.full((v["R"], v["d"]), -7.0, dtype=torch.bfloat16, device=DEV)
+        (g0, s0), (g1, s1), (g2, s2) = v["w"]
+        torch.cuda.synchronize()
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=stream):
+            g.moe_grouped_swiglu_w8(v["n"], v["d"], v["I"], v["R"], v["xq"], v["xs"], v["b"], v["c"], g0,
+                                    s0, g1, s1, g2, s2, y, ws, nb)
+        runs.append((graph, stream, y, want, ws))
+    for _ in range(20):
+        for graph, stream, y, _, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, y, want, _ in runs:
+        assert torch.equal(y, want)
+
+
+def test_overlapping_segments_are_reported_where_they_exceed_the_tiles():
+    """Two segments of the same 256 rows: four tiles a column block where 256 rows in two
+    segments have three."""
+    t = make(2048, 2048, [256], seed=33)
+    u = dict(t, n=2, w=[(q.repeat(2, 1, 1), s.repeat(2, 1, 1)) for q, s in t["w"]],
+             b=t["b"].repeat(2), c=t["c"].repeat(2))
+    _, st = swiglu(u)
+    torch.cuda.synchronize()
+    assert int(st.item()) == G().MOE_DEV_BAD_ROW
+
+
 def test_long_reduction():
     check(make(4096, 2064, [150, 260], seed=6))
 
