@@ -387,7 +387,7 @@ class MoELayer:
         for t, shape, size, what in ((q, (self.T, self.d), 1, "codes"),
                                      (s, tuple(self.xs.shape), 4, "scales")):
             if tuple(t.shape) != shape or t.element_size() != size or not t.is_contiguous() or \
-                    t.device != self.out.device:
+                    t.device != self.out.device or (size == 4 and t.dtype != torch.float32):
                 raise ValueError(f"payload {what} must be contiguous {shape} on {self.out.device}")
 
     def forward(self, logits, x, stream=None, out=None) -> torch.Tensor:

@@ -84,3 +84,11 @@ def test_layer_with_e4m3_experts_arguments():
             layer.forward(z, x)
     with pytest.raises(ValueError):
         g.quantize_weights(torch.zeros((2, 16, 16)))
+
+
+def test_payload_scales_are_fp32():
+    w = [pair(4, 128, 256), pair(4, 128, 256), pair(4, 256, 128)]
+    layer = g.MoELayer(8, 256, 4, 2, 128, *w, payload="fp8_block128", device="cpu")
+    q, s = torch.zeros((8, 256), dtype=torch.uint8), torch.ones((8, 2), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        layer.forward(torch.zeros((8, 4)), (q, s))
