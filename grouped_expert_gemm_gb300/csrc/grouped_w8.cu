@@ -156,8 +156,11 @@ __device__ __forceinline__ void build_table(const W8Args& a, int bm, int n_block
     tb.start[a.n_seg] = tb.warp_tot[0] + tb.warp_tot[1] + tb.warp_tot[2] + tb.warp_tot[3];
 }
 
+// amax / 448; 1 where that is zero, which it also is for an amax below 2^-141 (codes of
+// v / 0 would be infinite or NaN; of v / 1 they are 0).
 __device__ __forceinline__ float scale_of(uint32_t amax) {
-  return amax == 0 ? 1.0f : __fdiv_rn(__uint_as_float(amax), kE4M3Max);
+  const float s = __fdiv_rn(__uint_as_float(amax), kE4M3Max);
+  return s == 0.0f ? 1.0f : s;
 }
 
 // 32 consecutive bytes (aligned to 16): one 32-byte store where the address allows

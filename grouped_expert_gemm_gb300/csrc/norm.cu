@@ -131,8 +131,11 @@ __device__ __forceinline__ uint32_t amax8(const float f[8]) {
   return __float_as_uint(m) & 0x7FFFFFFFu;  // as bits: integer order, NaN above Inf
 }
 
+// amax / 448; 1 where that is zero, which it also is for an amax below 2^-141 (codes of
+// v / 0 would be infinite or NaN; of v / 1 they are 0).
 __device__ __forceinline__ float scale_of(uint32_t amax) {
-  return amax == 0 ? 1.0f : __fdiv_rn(__uint_as_float(amax), kE4M3Max);
+  const float s = __fdiv_rn(__uint_as_float(amax), kE4M3Max);
+  return s == 0.0f ? 1.0f : s;
 }
 
 // 8 codes of v / s as v * (1 / s): one reciprocal a group instead of a division a value

@@ -678,8 +678,9 @@ typedef struct {
  *   v    = (h * rstd) * weight                        (fp32, weight fp32 [d])
  *   y    = bf16(v)                                    the router's / bf16 experts' rows
  *   q    = E4M3(v / s), s = fp32(amax / 448)          the dispatch payload of
- * moe_quantize_fp8's scale rule (a zero group has s = 1), taken from the unrounded
- * v (the quotient as a product with the reciprocal, within two fp32 roundings): q [n, d], scales [n, 1] or [n, ceil(d/128)] by `group`.
+ * moe_quantize_fp8's scale rule, taken from the unrounded v (the quotient as a product
+ * with the reciprocal, within two fp32 roundings); a group whose amax / 448 is zero in
+ * fp32 has s = 1.  q [n, d], scales [n, 1] or [n, ceil(d/128)] by `group`.
  * x is [n, d] with row stride x_stride, residual / residual_out / y / q [n, d]
  * contiguous.  y may be NULL, and q and scales may both be NULL, but not all
  * three; rstd [n] may be NULL (the backward needs it); residual_out may be NULL
@@ -708,7 +709,8 @@ moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, const void*
  * in fp32.  Each output may be NULL (not all).  dresidual may be dresidual_out
  * itself.  dweight is summed in an order fixed by n, d and nothing else: the same
  * bits on every run.  With dweight, ws holds at least
- * moe_add_rms_norm_backward_workspace_size() bytes (0 = invalid parameters).
+ * moe_add_rms_norm_backward_workspace_size() bytes (0 = invalid parameters); calls, and
+ * replays of graphs that captured them, that overlap on the GPU must not share it.
  * n = 0 writes dweight = 0.  Limits as the forward.                           */
 size_t moe_add_rms_norm_backward_workspace_size(const moe_norm_params* p);
 moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t dy_type, const void* dy,
@@ -790,7 +792,7 @@ moe_status moe_quantize_weights_fp8(int32_t n_seg, int32_t K, int32_t N, const m
  * X = xq * xs and W = q * s (each element's own block scale):
  *   G = X W_gate, U = X W_up                      fp32
  *   H = SiLU(G) * U                               fp32, then per row and 128 columns
- *   hs = fp32(amax / 448) (1 if zero), hq = E4M3(H / hs) (as H times 1 / hs)
+ *   hs = fp32(amax / 448) (1 if that is zero), hq = E4M3(H / hs) (as H times 1 / hs)
  *   y = bf16((hq * hs) W_down)
  * Each 128-wide block of the reduction is summed by the tensor cores
  * (tcgen05.mma kind::f8f6f4, fp32 accumulators) on the codes alone; its sum is
@@ -802,8 +804,7 @@ moe_status moe_quantize_weights_fp8(int32_t n_seg, int32_t K, int32_t N, const m
  * the weights are read before the gate/up pass has ended: nothing enqueued after that
  * pass may write them (the call itself enqueues both).
  * Limits: d % 16 == 0, I % 16 == 0, d, I <= 65536, n_seg <= 1024, max_rows below
- * 2^31 - 1024; 16-byte aligned
- * codes and y, 4-byte aligned scales.  Segments outside [0, max_rows) set
+ * 2^31 - 1024; 16-byte aligned codes and y, 4-byte aligned scales.  Segments outside [0, max_rows) set
  * MOE_DEV_BAD_ROW and are skipped; segments that overlap (not allowed) may set it and
  * leave rows unwritten.  A NaN or Inf in H sets
  * MOE_DEV_NONFINITE_INPUT (that row's codes are then unspecified).             */

@@ -240,3 +240,22 @@ def test_captured_replays_and_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(h, want["h"]) and torch.equal(y, want["y"])
     assert torch.equal(q, want["q"]) and torch.equal(sc, want["s"])
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("n", [3, 300])
+def test_a_scale_that_underflows_counts_as_zero(n, group):
+    """v of about 1e-44 (amax / 448 is 0 in fp32): scale 1 and zero codes, nothing reported;
+    zeros among them stay zero."""
+    g = G()
+    d = 256
+    x = torch.ones((n, d), dtype=torch.bfloat16, device=DEV)
+    x[:, 5] = 0
+    w = torch.full((d,), 1e-44, device=DEV)
+    assert (w > 0).all()
+    p = g.NormParams(n, d, d, 0, 0, group, EPS)
+    q = torch.full((n, d), 0x55, dtype=torch.uint8, device=DEV)
+    sc = torch.zeros((n, 1 if group == 0 else 2), device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    g.moe_add_rms_norm(p, x, None, w, None, None, q, sc, None, st)
+    assert (sc == 1).all() and (q == 0).all() and int(st.item()) == 0

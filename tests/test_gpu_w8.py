@@ -322,3 +322,20 @@ def test_tiny_and_huge_rows():
         room = torch.maximum(h.abs() * 2.0 ** -4, ref.spread(s, 256, 128) * 2.0 ** -10) * 1.01
         floor = 449 * 2.0 ** -149
         assert ((val - h).abs() <= room + 1e-3 * h.abs().max() + floor).all()
+
+
+def test_a_scale_that_underflows_counts_as_zero():
+    """Rows whose H is below 1e-43 (amax / 448 is 0 in fp32): scale 1 and zero codes."""
+    for counts in ([5], [130]):  # a few rows, and the 128-row tiles
+        t = make(256, 256, counts, seed=15)
+        # G and U so small that H is G U / 2: its largest value set to 2e-43
+        x = t["xq"][1:2].double()
+        gu = [x @ ref.dequant_blocks(q[0], s[0]).T for q, s in t["w"][:2]]
+        top = (gu[0] * gu[1] / 2).abs()
+        t["xs"][1] = (2e-43 / top.max()).sqrt().float()
+        assert (top[:, :128].max() > 0.1 * top.max()) and (top[:, 128:].max() > 0.1 * top.max())
+        hq, hs, st = gate_up(t)
+        y, st2 = down(t, hq, hs)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and int(st2.item()) == 0
+        assert (hs[1] == 1).all() and (hq[1] & 0x7F == 0).all() and (y[1] == 0).all()
