@@ -628,7 +628,8 @@ moe_status check_balance(const moe_route_params* p, int32_t n_seq, const int32_t
   if (p->score_fn == MOE_SCORE_SIGMOID_GROUP && !(p->route_scale > 0.0f && p->route_scale < 1e30f))
     return MOE_ERR_INVALID_ARG;
   if (n_seq < 1 || (off == nullptr && n_seq != 1)) return MOE_ERR_INVALID_ARG;
-  if (p->E > kMaxE || p->k > kMaxK || n_seq > 65535 ||
+  // (token indexes run up to a tile past T: T / 304 and a few rows, below 2^23)
+  if (p->E > kMaxE || p->k > kMaxK || n_seq > 65535 || p->T > INT32_MAX - (1 << 23) ||
       static_cast<int64_t>(p->T) * p->k >= (int64_t(1) << 31))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

@@ -744,7 +744,7 @@ moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t dy_type, 
  * ws: moe_balance_loss_workspace_size() bytes (0 = invalid parameters), 16-byte
  * aligned; no state is kept in it between calls, but calls that overlap on the GPU
  * must not share it.  Limits: E <= 512, k <= min(E, 16), n_seq <= 65535,
- * T*k < 2^31.  topk_ids [T, k] as moe_route writes them (distinct per token).   */
+ * T*k < 2^31, T < 2^31 - 2^23.  topk_ids [T, k] as moe_route writes them (distinct per token).   */
 size_t moe_balance_loss_workspace_size(const moe_route_params* p, int32_t n_seq);
 moe_status moe_balance_loss(const moe_route_params* p, int32_t n_seq, const int32_t* seq_offsets,
                             const float* logits, const int32_t* topk_ids, float alpha,

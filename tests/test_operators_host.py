@@ -124,3 +124,12 @@ def test_expert_refusals(g):
     q = L.moe_quantize_weights_fp8
     assert q(0, 16, 16, 16, 16, 16, None, None) == ARG and q(1, 16, 16, None, 16, 16, None, None) == ARG
     assert q(1, 24, 16, 16, 16, 16, None, None) == UNS and q(1, 16, 16, 24, 16, 16, None, None) == UNS
+
+
+def test_balance_token_indexes_stay_in_32_bits(g):
+    """A tile past T must not pass 2^31."""
+    for T, ok in (((1 << 31) - 1, False), ((1 << 31) - (1 << 23), False), ((1 << 31) - (1 << 23) - 1, True)):
+        p = g.RouteParams(T, 8, 1, 0, 1, 1, 1.0)
+        assert (g.moe_balance_loss_workspace_size(p, 1) > 0) == ok
+        st = g.abi.lib().moe_route_backward(p, 1, None, None, 16, 16, 16, 0.1, 16, 16, None, 16, None, None)
+        assert st == (g.MOE_ERR_INVALID_ARG if ok else g.MOE_ERR_UNSUPPORTED)  # (no logits)
