@@ -238,6 +238,7 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   if constexpr (SPLIT > 1) cluster_sync();  // the partners' barriers are initialised
   else __syncthreads();
   umma_fence_after();
+  bool awaited = false;  // the partners' sums
   const uint32_t tmem = *tb.tmem_slot;
   int total = tb.start[a.n_seg];
   if (SPLIT > 1 && total > step) {  // only segments that overlap have more tiles than clusters
@@ -370,6 +371,7 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
         constexpr int kOwn = 4 / SPLIT;
         const int owner = quad / kOwn;
         if (threadIdx.x == 64) mbar_arrive_expect_tx(red_bar, (SPLIT - 1) * kOwn * 2 * kWarpSums);
+        awaited = true;
         __syncwarp();
         // The slot of sender `from` for this warp: its distance behind the owner, the warp's
         // quadrant in the owner's, its half of the columns.
@@ -480,8 +482,13 @@ grouped_w8_kernel(const __grid_constant__ CUtensorMap map_a,
   // ---- teardown ----
   __syncwarp();
   umma_fence_before();
-  if constexpr (SPLIT > 1) cluster_sync();  // no CTA leaves while a partner may still reach it
-  else __syncthreads();
+  if constexpr (SPLIT > 1) {
+    cluster_sync();  // no CTA leaves while a partner may still reach it
+    // (after a wait that gave up: nor before the sums that were on their way)
+    if (threadIdx.x == 64 && awaited && *abort_flag) wait_drain(red_bar, 0);
+  } else {
+    __syncthreads();
+  }
   umma_fence_after();
   if (warp == 1) {
     __syncwarp();
@@ -606,6 +613,8 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
   if constexpr (SPLIT > 1) cluster_sync();  // the partner's barriers are initialised
   else __syncthreads();
   umma_fence_after();
+  bool awaited = false;  // the partners' sums, in phase
+  uint32_t awaited_ph = 0;
   const uint32_t tmem = *tb.tmem_slot;
   const int total = tb.start[a.n_seg];
 
@@ -706,7 +715,10 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
     bool ok = true;
     for (int t = group; t < total; t += groups, tile_ph ^= 1u) {
       const Tile tl = tile_of(t, tb, a.n_seg, NT, n_blocks, a.m_outer);
-      if (SPLIT > 1 && rank == 0 && threadIdx.x == 64) mbar_arrive_expect_tx(red_full, (SPLIT - 1) * 2 * 128 * 16 * ((min(tl.rows, NT) + 3) / 4));
+      if (SPLIT > 1 && rank == 0 && threadIdx.x == 64)
+        mbar_arrive_expect_tx(red_full, (SPLIT - 1) * 2 * 128 * 16 * ((min(tl.rows, NT) + 3) / 4));
+      awaited = true;
+      awaited_ph = tile_ph;
       const int nblk = SWIGLU ? tl.nb : min(2 * tl.nb + half, a.GN - 1);
       const float* ws = (SWIGLU && half ? a.bs1 : a.bs0) +
                         (static_cast<int64_t>(tl.seg) * a.GN + nblk) * a.GK;
@@ -854,8 +866,13 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
   // ---- teardown ----
   __syncwarp();
   umma_fence_before();
-  if constexpr (SPLIT > 1) cluster_sync();  // no CTA leaves while its partner may still reach it
-  else __syncthreads();
+  if constexpr (SPLIT > 1) {
+    cluster_sync();  // no CTA leaves while its partner may still reach it
+    // (after a wait that gave up: nor before the sums that were on their way)
+    if (threadIdx.x == 64 && rank == 0 && awaited && *abort_flag) wait_drain(red_full, awaited_ph);
+  } else {
+    __syncthreads();
+  }
   umma_fence_after();
   if (warp == 1) {
     __syncwarp();
