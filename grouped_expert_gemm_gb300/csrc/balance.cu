@@ -24,9 +24,7 @@
 #include <float.h>
 #include <math.h>
 
-#include <mutex>
-
-#include "common.cuh"
+#include "smem.cuh"
 
 namespace moe {
 namespace {
@@ -657,21 +655,6 @@ template <template <int, int, bool> class Launch>
 moe_status by_score(bool vec4, const BalArgs& a, unsigned grid, cudaStream_t s) {
   return a.sigmoid ? by_width<Launch, true>(vec4, a, grid, s)
                    : by_width<Launch, false>(vec4, a, grid, s);
-}
-
-// The kernel's shared-memory opt-in, once per device.
-template <typename Kernel>
-bool opt_in(Kernel kern, int bytes, std::mutex& mu, bool (&done)[64]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-        cudaSuccess)
-      return false;
-    done[dev] = true;
-  }
-  return true;
 }
 
 template <int VEC, int N, bool SIG>

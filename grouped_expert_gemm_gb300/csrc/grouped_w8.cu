@@ -37,8 +37,8 @@
 // (two rounds of a tree, with rank 0 alone in the epilogue, took 2 us longer a pass).
 // Every wait is bounded (MOE_DEV_TIMEOUT), as in the bf16 pass.
 #include <algorithm>
-#include <mutex>
 
+#include "smem.cuh"
 #include "umma.cuh"
 
 namespace moe {
@@ -969,21 +969,6 @@ bool map_weights(CUtensorMap* m, const void* base, uint64_t n_seg, uint64_t N, u
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The kernel's shared-memory opt-in, once per device.
-template <typename Kernel>
-bool opt_in(Kernel kern, int bytes, std::mutex& mu, bool (&done)[64]) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-        cudaSuccess)
-      return false;
-    done[dev] = true;
-  }
-  return true;
 }
 
 // As in the bf16 pass: rows inner (one weight tile shared by neighbouring CTAs)

@@ -13,9 +13,13 @@
 //
 // Bound: HBM.  A row is read once and held in registers (V chunks of 8 values per
 // thread) through both reductions, so x and r are read once and every output
-// written once.  Blocks are persistent: the raw bits of a block's next row are on
-// their way while it works on the current one.
-#include "common.cuh"
+// written once.  Blocks are persistent; their next rows are on their way into shared
+// memory (bulk copies, the forward and wide backward rows) or registers (the backward
+// up to 8,192 values).  Forward, 8,192 x 7,168 (of the copy rate 6.7 TB/s): bf16 83.5 us
+// (6.3 TB/s), fp32 residual 128 (6.0), fp32 both 141 (6.2); backward 96 (6.1), 144 (6.5), 174 (6.1).
+#include <algorithm>
+
+#include "smem.cuh"
 
 namespace moe {
 namespace {
@@ -24,6 +28,12 @@ constexpr float kE4M3Max = 448.0f;
 constexpr uint32_t kAbsInf = 0x7F800000u;
 constexpr int kMaxNormD = 16384;
 constexpr int kMaxWarps = 32;
+// The rings: warps an SM holds (64 registers), its shared memory, what of it a block takes
+// beside its rows (at most), rows a row group has on their way (at most).
+constexpr int kRingWarps = 32;
+constexpr int kSmBytes = 227 * 1024;
+constexpr int kBlockBytes = 2048;
+constexpr int kMaxDepth = 4;
 
 struct NormArgs {
   int64_t n, x_stride;
@@ -31,6 +41,7 @@ struct NormArgs {
   int group;     // scale group of q: MOE_SCALE_ROW or MOE_SCALE_BLOCK128
   int G;         // scales per row
   int nw;        // warps per row
+  int depth;     // rows of a row group's ring
   int early;     // the grid is resident at once: dependents may launch right after the wait
   float eps;
   const void* x;
@@ -55,6 +66,11 @@ struct Raw {
     v[0] = q[0];
     if constexpr (FP32) v[1] = q[1];
   }
+  __device__ __forceinline__ void load_shared(const uint8_t* row, int chunk) {
+    const uint4* q = reinterpret_cast<const uint4*>(row) + chunk * (FP32 ? 2 : 1);
+    v[0] = q[0];
+    if constexpr (FP32) v[1] = q[1];
+  }
   __device__ __forceinline__ void get(float f[8]) const {
     if constexpr (FP32) {
       f[0] = __uint_as_float(v[0].x); f[1] = __uint_as_float(v[0].y);
@@ -69,9 +85,15 @@ struct Raw {
 
 __device__ __forceinline__ void store8(void* p, int is32, int64_t at, const float f[8]) {
   if (is32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    float* q = static_cast<float*>(p) + at;
+    if ((reinterpret_cast<uintptr_t>(q) & 31u) == 0) {  // a whole sector per lane
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(f[0]),
+                   "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                   : "memory");
+    } else {
+      reinterpret_cast<float4*>(q)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(q)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
   } else {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
         make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
@@ -159,49 +181,106 @@ __device__ __forceinline__ uint2 quant8(const float f[8], float s) {
   return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
 }
 
+// A row group's ring in shared memory: slots of one row's operands, filled by one bulk
+// copy an operand and counted on the slot's barrier.
+struct Ring {
+  uint8_t* base;
+  uint32_t bars;  // of its slots
+  int depth, bytes;
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ const uint8_t* here() const {
+    return base + static_cast<size_t>(slot) * bytes;
+  }
+  // (A wait that gives up has reported it; the row is then whatever the slot holds.)
+  __device__ __forceinline__ void wait(volatile int* abort_flag, uint32_t* dev_status) const {
+    wait_bounded(bars + 8 * slot, phase, abort_flag, dev_status);
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == depth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  // After a wait that gave up: copies on their way land before the block leaves.
+  __device__ __forceinline__ void drain() {
+    for (int i = 0; i < depth; ++i, next()) wait_drain(bars + 8 * slot, phase ^ 1u);
+  }
+};
+
+__device__ __forceinline__ void init_ring_bars(uint64_t* bars, int n, int* abort_flag) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < n; ++i) mbar_init(smem_u32(bars + i), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+}
+
 // A row is held by nw warps: with nw = 1 a block's warps take a row each, else the
-// whole block takes one.
-template <int V, bool X32, bool R32>
-__global__ void __launch_bounds__(V < 4 ? 1024 : 512)
+// whole block takes one.  RING: blocks are persistent and each row group has `depth`
+// rows on their way into shared memory, the next one issued as soon as all have taken
+// the current row into registers.  (With the next row in registers instead, four chunks a
+// thread, 128 registers: 8,192 x 7,168, block codes, bf16 86 us against 83.5, fp32 residual
+// 171 against 128, both fp32 203 against 141, no residual 72 against 62.)
+template <int V, bool X32, bool R32, bool RING>
+__global__ void __launch_bounds__(1024)
 add_rms_norm_kernel(const NormArgs a) {
   __shared__ float sh[2 * kMaxWarps];
-  pdl_wait_then_trigger(a.early);
+  __shared__ __align__(8) uint64_t bars[4 * kMaxDepth];
+  __shared__ int s_abort;
+  extern __shared__ __align__(128) uint8_t s_rows[];
+  volatile int* abort_flag = &s_abort;
   const int nw = a.nw, span = nw * 32;
   const int rows_per_block = nw == 1 ? static_cast<int>(blockDim.x >> 5) : 1;
   const int tid = nw == 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
   const int sub = nw == 1 ? static_cast<int>(threadIdx.x >> 5) : 0;
+  if constexpr (RING) init_ring_bars(bars, rows_per_block * a.depth, &s_abort);
+  pdl_wait_then_trigger(a.early);
   const int chunks = a.d / 8;
   const int64_t step = static_cast<int64_t>(gridDim.x) * rows_per_block;
+  const int x_bytes = a.d * (X32 ? 4 : 2), r_bytes = a.res != nullptr ? a.d * (R32 ? 4 : 2) : 0;
+  Ring ring = {s_rows + static_cast<size_t>(sub) * a.depth * (x_bytes + r_bytes),
+               smem_u32(bars + sub * a.depth), a.depth, x_bytes + r_bytes};
   int phase = 0;
   bool bad = false;
-  Raw<X32> nx[V];
-  Raw<R32> nr[V];
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * span;
-      if (c < chunks) {
-        nx[i].load(a.x, row * a.x_stride + 8 * c);
-        if (a.res != nullptr) nr[i].load(a.res, row * a.d + 8 * c);
-      }
-    }
+  Raw<X32> nx[RING ? 1 : V];
+  Raw<R32> nr[RING ? 1 : V];
+  auto issue = [&](int64_t row, int to) {
+    const uint32_t bar = ring.bars + 8 * to, dst = smem_u32(ring.base) + to * ring.bytes;
+    mbar_arrive_expect_tx(bar, ring.bytes);
+    bulk_load(dst, static_cast<const uint8_t*>(a.x) + row * a.x_stride * (X32 ? 4 : 2), x_bytes, bar);
+    if (r_bytes != 0)
+      bulk_load(dst + x_bytes, static_cast<const uint8_t*>(a.res) + row * r_bytes, r_bytes, bar);
   };
-  constexpr bool kAhead = V == 4;  // (the others are launched with a row a block)
   int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub;
-  if (kAhead && row < a.n) fetch(row);
+  if (RING && tid == 0)
+    for (int i = 0; i < a.depth && row + i * step < a.n; ++i) issue(row + i * step, i);
   for (; row < a.n; row += step) {
     const int64_t base = row * a.d;
-    if (!kAhead) fetch(row);
+    if constexpr (RING) ring.wait(abort_flag, a.dev_status);
+    if constexpr (!RING) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * span;
+        if (c < chunks) {
+          nx[i].load(a.x, row * a.x_stride + 8 * c);
+          if (a.res != nullptr) nr[i].load(a.res, base + 8 * c);
+        }
+      }
+    }
     float h[V][8];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * span;
       if (c < chunks) {
-        nx[i].get(h[i]);
+        if constexpr (RING) nx[0].load_shared(ring.here(), c);
+        nx[RING ? 0 : i].get(h[i]);
         if (a.res != nullptr) {
           float r[8];
-          nr[i].get(r);
+          if constexpr (RING) nr[0].load_shared(ring.here() + x_bytes, c);
+          nr[RING ? 0 : i].get(r);
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[i][j] += r[j];
         }
@@ -218,8 +297,12 @@ add_rms_norm_kernel(const NormArgs a) {
         for (int j = 0; j < 8; ++j) ss += h[i][j] * h[i][j];
       }
     }
-    if (kAhead && row + step < a.n) fetch(row + step);
-    ss = row_sum(ss, nw, sh, phase);
+    ss = row_sum(ss, nw, sh, phase);  // (every thread has read the slot)
+    if constexpr (RING) {
+      if (tid == 0 && row + a.depth * step < a.n && !*abort_flag)
+        issue(row + a.depth * step, ring.slot);
+      ring.next();
+    }
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(ss / static_cast<float>(a.d) + a.eps));
     if (a.rstd != nullptr && tid == 0) a.rstd[row] = rstd;
     uint32_t top = 0;
@@ -259,6 +342,7 @@ add_rms_norm_kernel(const NormArgs a) {
     }
     bad |= top >= kAbsInf;
   }
+  if (RING && tid == 0 && *abort_flag) ring.drain();
   if (bad) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
   if (!a.early) pdl_trigger();
 }
@@ -268,6 +352,7 @@ add_rms_norm_kernel(const NormArgs a) {
 struct NormBwdArgs {
   int64_t n;
   int d, nw;
+  int depth;  // of the ring (wide rows)
   int early;
   int x32;
   const void* dy;
@@ -280,11 +365,43 @@ struct NormBwdArgs {
   float* part;         // [gridDim.x, d] partial weight gradients, or nullptr
 };
 
+// The block's weight gradient as one partial row.
+template <int V>
+__device__ __forceinline__ void store_partial(const NormBwdArgs& a, float (&dw)[V][8], float* sh_dw,
+                                              int rows_per_block, int sub, int tid, int span) {
+  if (a.nw == 1) {  // the block's four warps, summed in warp order
+    if (sub > 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sh_dw[((sub - 1) * V + i) * 256 + j * 32 + tid] = dw[i][j];
+    }
+    __syncthreads();
+    if (sub == 0) {
+      for (int s = 0; s < rows_per_block - 1; ++s)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dw[i][j] += sh_dw[(s * V + i) * 256 + j * 32 + tid];
+    }
+  }
+  if (sub == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * span;
+      if (c < a.d / 8) store8(a.part, 1, static_cast<int64_t>(blockIdx.x) * a.d + 8 * c, dw[i]);
+    }
+  }
+}
+
 // The rows of a block go through it in order; each thread keeps the weight
-// gradient of its own columns in registers and the block writes one partial row.
-template <int V, bool DY32, bool R32>
+// gradient of its own columns in registers and the block writes one partial row.  The
+// next row's values wait in registers (by way of a ring, as in the forward: 8,192 x 7,168
+// bf16 104 us against 97, its second pass over the slot's values).
+template <bool DY32, bool R32>
 __global__ void __launch_bounds__(512)
 rms_norm_backward_kernel(const NormBwdArgs a) {
+  constexpr int V = 2;
   __shared__ float sh[2 * kMaxWarps];
   __shared__ float sh_dw[3 * V * 256];  // (a row per warp: the other three warps' sums)
   pdl_wait_then_trigger(a.early);
@@ -300,8 +417,7 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  constexpr bool kAhead = V < 4;  // (wider rows leave no registers for the next one)
-  Raw<R32> nh[V], ng[kAhead ? V : 1];
+  Raw<R32> nh[V], ng[V];
   Raw<DY32> ndy[V];
   float nrstd = 0.0f;
   auto fetch = [&](int64_t row) {
@@ -312,18 +428,17 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
       if (c < chunks) {
         nh[i].load(a.h, row * a.d + 8 * c);
         ndy[i].load(a.dy, row * a.d + 8 * c);
-        if constexpr (kAhead) if (a.dh_out != nullptr) ng[i].load(a.dh_out, row * a.d + 8 * c);
+        if (a.dh_out != nullptr) ng[i].load(a.dh_out, row * a.d + 8 * c);
       }
     }
   };
   int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_block + sub;
-  if (kAhead && row < a.n) fetch(row);
+  if (row < a.n) fetch(row);
   for (; row < a.n; row += step) {
     const int64_t base = row * a.d;
-    if (!kAhead) fetch(row);
     const float rstd = nrstd;
     float xh[V][8], u[V][8];
-    Raw<R32> g[kAhead ? V : 1];
+    Raw<R32> g[V];
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -333,7 +448,7 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
         ldg8(a.w, 8 * c, w);
         nh[i].get(xh[i]);
         ndy[i].get(u[i]);
-        if constexpr (kAhead) g[i] = ng[i];
+        g[i] = ng[i];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           xh[i][j] *= rstd;
@@ -343,7 +458,7 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
         }
       }
     }
-    if (kAhead && row + step < a.n) fetch(row + step);
+    if (row + step < a.n) fetch(row + step);
     dot = row_sum(dot, nw, sh, phase) / static_cast<float>(a.d);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -353,8 +468,7 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
         for (int j = 0; j < 8; ++j) u[i][j] = rstd * (u[i][j] - xh[i][j] * dot);
         if (a.dh_out != nullptr) {
           float f[8];
-          if constexpr (!kAhead) g[0].load(a.dh_out, base + 8 * c);
-          g[kAhead ? i : 0].get(f);
+          g[i].get(f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) u[i][j] += f[j];
         }
@@ -363,31 +477,113 @@ rms_norm_backward_kernel(const NormBwdArgs a) {
       }
     }
   }
-  if (a.part != nullptr) {
-    if (nw == 1) {  // the block's four warps, summed in warp order
-      if (sub > 0) {
+  if (a.part != nullptr) store_partial<2>(a, dw, sh_dw, rows_per_block, sub, tid, span);
+  if (!a.early) pdl_trigger();
+}
+
+// Rows above 8,192 values, whose threads have no registers for the next row: a ring as in
+// the forward.  A row's h, dy and dh_out stay in its slot through both phases, so the slot
+// is refilled behind the next row's reduction.  4,096 x 12,288 bf16: 96 us; without a
+// next row on its way 173.
+template <bool DY32, bool R32>
+__global__ void __launch_bounds__(1024)
+rms_norm_backward_wide_kernel(const NormBwdArgs a) {
+  __shared__ float sh[2 * kMaxWarps];
+  __shared__ __align__(8) uint64_t bars[kMaxDepth];
+  __shared__ int s_abort;
+  extern __shared__ __align__(128) uint8_t s_rows[];
+  volatile int* abort_flag = &s_abort;
+  constexpr int V = 2;
+  const int nw = a.nw, span = nw * 32, tid = static_cast<int>(threadIdx.x);
+  init_ring_bars(bars, a.depth, &s_abort);
+  pdl_wait_then_trigger(a.early);
+  const int chunks = a.d / 8;
+  const int64_t step = gridDim.x;
+  const int h_bytes = a.d * (R32 ? 4 : 2), dy_bytes = a.d * (DY32 ? 4 : 2);
+  const int g_bytes = a.dh_out != nullptr ? h_bytes : 0;
+  Ring ring = {s_rows, smem_u32(bars), a.depth, h_bytes + dy_bytes + g_bytes};
+  auto issue = [&](int64_t row, int to) {
+    const uint32_t bar = ring.bars + 8 * to, dst = smem_u32(ring.base) + to * ring.bytes;
+    mbar_arrive_expect_tx(bar, ring.bytes);
+    bulk_load(dst, static_cast<const uint8_t*>(a.h) + row * h_bytes, h_bytes, bar);
+    bulk_load(dst + h_bytes, static_cast<const uint8_t*>(a.dy) + row * dy_bytes, dy_bytes, bar);
+    if (g_bytes != 0)
+      bulk_load(dst + h_bytes + dy_bytes, static_cast<const uint8_t*>(a.dh_out) + row * g_bytes,
+                g_bytes, bar);
+  };
+  int phase = 0;
+  float dw[V][8];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sh_dw[((sub - 1) * V + i) * 256 + j * 32 + tid] = dw[i][j];
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  const int64_t first = blockIdx.x;
+  int64_t row = first;
+  if (tid == 0)
+    for (int i = 0; i < a.depth && row + i * step < a.n; ++i) issue(row + i * step, i);
+  float next_rstd = row < a.n ? __ldg(a.rstd + row) : 0.0f;
+  for (; row < a.n; row += step) {
+    const int64_t base = row * a.d;
+    const float rstd = next_rstd;
+    if (row + step < a.n) next_rstd = __ldg(a.rstd + row + step);
+    ring.wait(abort_flag, nullptr);
+    const uint8_t* here = ring.here();
+    Raw<R32> h;
+    Raw<DY32> dy;
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * span;
+      if (c < chunks) {
+        float w[8], xh[8], u[8];
+        ldg8(a.w, 8 * c, w);
+        h.load_shared(here, c);
+        h.get(xh);
+        dy.load_shared(here + h_bytes, c);
+        dy.get(u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          xh[j] *= rstd;
+          dw[i][j] += u[j] * xh[j];
+          dot += u[j] * w[j] * xh[j];
+        }
       }
+    }
+    dot = row_sum(dot, nw, sh, phase) / static_cast<float>(a.d);
+    // all are past the row before: its slot takes the row a ring further
+    if (tid == 0 && a.depth > 1 && row != first && row + (a.depth - 1) * step < a.n && !*abort_flag)
+      issue(row + (a.depth - 1) * step, ring.slot == 0 ? a.depth - 1 : ring.slot - 1);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * span;
+      if (c < chunks) {
+        float w[8], xh[8], u[8];
+        ldg8(a.w, 8 * c, w);
+        h.load_shared(here, c);
+        h.get(xh);
+        dy.load_shared(here + h_bytes, c);
+        dy.get(u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = rstd * (u[j] * w[j] - xh[j] * rstd * dot);
+        if (a.dh_out != nullptr) {
+          float f[8];
+          h.load_shared(here + h_bytes + dy_bytes, c);
+          h.get(f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] += f[j];
+        }
+        if (a.dx != nullptr) store8(a.dx, a.x32, base + 8 * c, u);
+        if (a.dres != nullptr) store8(a.dres, R32, base + 8 * c, u);
+      }
+    }
+    if (a.depth == 1) {  // (rows of which two do not fit)
       __syncthreads();
-      if (sub == 0) {
-        for (int s = 0; s < rows_per_block - 1; ++s)
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dw[i][j] += sh_dw[(s * V + i) * 256 + j * 32 + tid];
-      }
+      if (tid == 0 && row + step < a.n && !*abort_flag) issue(row + step, 0);
     }
-    if (sub == 0) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = tid + i * span;
-        if (c < chunks) store8(a.part, 1, static_cast<int64_t>(blockIdx.x) * a.d + 8 * c, dw[i]);
-      }
-    }
+    ring.next();
   }
+  if (tid == 0 && *abort_flag) ring.drain();
+  if (a.part != nullptr) store_partial<V>(a, dw, nullptr, 1, 0, tid, span);
   if (!a.early) pdl_trigger();
 }
 
@@ -418,59 +614,96 @@ weight_grad_kernel(int blocks, int d, const float* __restrict__ part, float* __r
 // --------------------------------- host side --------------------------------
 
 // How a pass lays its rows out: V chunks of 8 values per thread, nw warps a row
-// (one: four rows to a block), persistent blocks.
+// (one: four rows to a block), and for the ring persistent blocks.
 struct Plan {
   int V, nw, threads, blocks;
+  int depth = 0, smem = 0;  // of the ring
 };
 
-// sm_warps: warps of the kernel that an SM holds at once.
-Plan plan_rows(int64_t n, int d, int V, int sm_warps) {
+// Two chunks a thread (four: 86.6 us at 8,192 x 7,168 bf16, fewer warps to hide the
+// reductions).  Blocks on an SM: as many as its warps and shared memory hold with two rows
+// each on their way, or with one where that holds the whole batch.
+Plan plan_ring(int64_t n, int d, int row_bytes, int block_bytes) {
   Plan p;
-  p.V = V;
-  p.nw = static_cast<int>(ceil_div(d / 8, 32 * V));
-  const int warps = p.nw == 1 ? 4 : p.nw;
-  p.threads = warps * 32;
-  const int64_t want = ceil_div(n, p.nw == 1 ? 4 : 1);
-  const int64_t most = static_cast<int64_t>(152) * (sm_warps > warps ? sm_warps / warps : 1);
-  p.blocks = static_cast<int>(want < most ? want : most);
+  p.V = 2;
+  p.nw = static_cast<int>(ceil_div(d / 8, 64));
+  const int groups = p.nw == 1 ? 4 : 1, rows = groups * row_bytes;
+  p.threads = 32 * groups * p.nw;
+  auto fit = [&](int depth) {
+    int per_sm = kRingWarps / (p.threads / 32);
+    while (per_sm > 1 && per_sm * (depth * rows + block_bytes) > kSmBytes) --per_sm;
+    return per_sm;
+  };
+  const int64_t want = ceil_div(n, groups);
+  int per_sm = fit(1);
+  if (want > static_cast<int64_t>(sm_count()) * per_sm) per_sm = fit(2);
+  p.depth = std::min(kMaxDepth, (kSmBytes / per_sm - block_bytes) / rows);
+  p.smem = p.depth * rows;
+  p.blocks = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(sm_count()) * per_sm));
   return p;
 }
 
-// Forward: many rows take four chunks a thread (few warps a row, more bytes in
-// flight per thread); rows fewer than the SMs are latency-bound and take one
-// (two above 8,192 values: at most 32 warps).
-Plan plan_forward(int64_t n, int d) {
-  const int V = n > 152 ? 4 : (d <= 8192 ? 1 : 2);
-  return plan_rows(n, d, V, V == 4 ? 16 : 32);
+// Forward: rows fewer than the SMs are latency-bound and take one chunk a thread straight
+// from global memory.
+Plan plan_forward(int64_t n, int d, int row_bytes) {
+  if (n > sm_count() || d > 8192) return plan_ring(n, d, row_bytes, kBlockBytes);
+  Plan p;
+  p.V = 1;
+  p.nw = static_cast<int>(ceil_div(d / 8, 32));
+  p.threads = 32 * (p.nw == 1 ? 4 : p.nw);
+  p.blocks = static_cast<int>(ceil_div(n, p.nw == 1 ? 4 : 1));
+  return p;
 }
 
-// Backward: two chunks a thread (a row's values, its successor's and the weight
-// gradient stay in registers; four above 8,192 values: at most 16 warps); each block
-// writes one partial row of the weight gradient.
-Plan plan_backward(int64_t n, int d) { return plan_rows(n, d, d <= 8192 ? 2 : 4, 16); }
-
-template <int V>
-void launch_forward(const NormArgs& a, bool x32, bool r32, const Plan& p, cudaStream_t s) {
-  const dim3 grid(p.blocks), block(p.threads);
-  if (x32) {
-    if (r32) launch(add_rms_norm_kernel<V, true, true>, grid, block, 0, s, a);
-    else launch(add_rms_norm_kernel<V, true, false>, grid, block, 0, s, a);
-  } else {
-    if (r32) launch(add_rms_norm_kernel<V, false, true>, grid, block, 0, s, a);
-    else launch(add_rms_norm_kernel<V, false, false>, grid, block, 0, s, a);
-  }
+// Backward: two chunks a thread, each block writes one partial row of the weight
+// gradient.  Wide rows count as if dh_out were given, so that the order of the sums does
+// not depend on it.
+Plan plan_backward(int64_t n, int d, bool dy32, bool r32) {
+  if (d > 8192) return plan_ring(n, d, d * ((dy32 ? 4 : 2) + (r32 ? 8 : 4)), kBlockBytes);
+  Plan p;
+  p.V = 2;
+  p.nw = static_cast<int>(ceil_div(d / 8, 64));
+  const int warps = p.nw == 1 ? 4 : p.nw;
+  p.threads = 32 * warps;
+  const int per_sm = std::max(1, 16 / warps);
+  p.blocks = static_cast<int>(std::min<int64_t>(ceil_div(n, p.nw == 1 ? 4 : 1),
+                                                static_cast<int64_t>(sm_count()) * per_sm));
+  return p;
 }
 
-template <int V>
-void launch_backward(const NormBwdArgs& a, bool dy32, bool r32, const Plan& p, cudaStream_t s) {
-  const dim3 grid(p.blocks), block(p.threads);
-  if (dy32) {
-    if (r32) launch(rms_norm_backward_kernel<V, true, true>, grid, block, 0, s, a);
-    else launch(rms_norm_backward_kernel<V, true, false>, grid, block, 0, s, a);
-  } else {
-    if (r32) launch(rms_norm_backward_kernel<V, false, true>, grid, block, 0, s, a);
-    else launch(rms_norm_backward_kernel<V, false, false>, grid, block, 0, s, a);
+template <int V, bool X32, bool R32, bool RING>
+bool launch_forward_as(const NormArgs& a, const Plan& p, cudaStream_t s) {
+  auto kern = add_rms_norm_kernel<V, X32, R32, RING>;
+  if constexpr (RING) {
+    static std::mutex mu;
+    static bool done[64] = {};
+    if (!opt_in(kern, kSmBytes - kBlockBytes, mu, done)) return false;
   }
+  launch(kern, dim3(p.blocks), dim3(p.threads), p.smem, s, a);
+  return true;
+}
+
+template <int V, bool RING>
+bool launch_forward(const NormArgs& a, bool x32, bool r32, const Plan& p, cudaStream_t s) {
+  if (x32)
+    return r32 ? launch_forward_as<V, true, true, RING>(a, p, s)
+               : launch_forward_as<V, true, false, RING>(a, p, s);
+  return r32 ? launch_forward_as<V, false, true, RING>(a, p, s)
+             : launch_forward_as<V, false, false, RING>(a, p, s);
+}
+
+template <bool DY32, bool R32>
+bool launch_backward(const NormBwdArgs& a, const Plan& p, cudaStream_t s) {
+  if (p.depth == 0) {
+    launch(rms_norm_backward_kernel<DY32, R32>, dim3(p.blocks), dim3(p.threads), 0, s, a);
+    return true;
+  }
+  auto kern = rms_norm_backward_wide_kernel<DY32, R32>;
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (!opt_in(kern, kSmBytes - kBlockBytes, mu, done)) return false;
+  launch(kern, dim3(p.blocks), dim3(p.threads), p.smem, s, a);
+  return true;
 }
 
 moe_status check_norm(const moe_norm_params* p) {
@@ -524,19 +757,23 @@ MOE_API moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, con
   a.scales = scales;
   a.rstd = rstd;
   a.dev_status = dev_status;
-  const Plan pl = plan_forward(p->n, p->d);
-  a.nw = pl.nw;
-  a.early = one_wave(pl.blocks);
   const bool x32 = p->x_type == MOE_DTYPE_FP32, r32 = p->residual_type == MOE_DTYPE_FP32;
-  if (pl.V == 1) launch_forward<1>(a, x32, r32, pl, as_cuda(stream));
-  else if (pl.V == 2) launch_forward<2>(a, x32, r32, pl, as_cuda(stream));
-  else launch_forward<4>(a, x32, r32, pl, as_cuda(stream));
-  return launch_status();
+  const Plan pl =
+      plan_forward(p->n, p->d, p->d * ((x32 ? 4 : 2) + (residual == nullptr ? 0 : r32 ? 4 : 2)));
+  a.nw = pl.nw;
+  a.depth = pl.depth;
+  a.early = one_wave(pl.blocks);
+  const cudaStream_t s = as_cuda(stream);
+  const bool ok = pl.V == 1 ? launch_forward<1, false>(a, x32, r32, pl, s)
+                            : launch_forward<2, true>(a, x32, r32, pl, s);
+  return ok ? launch_status() : MOE_ERR_CUDA;
 }
 
 MOE_API size_t moe_add_rms_norm_backward_workspace_size(const moe_norm_params* p) {
   if (check_norm(p) != MOE_OK) return 0;
-  return static_cast<size_t>(plan_backward(p->n, p->d).blocks) * p->d * sizeof(float);
+  // (of the two types of dy the narrower one has more blocks)
+  const int blocks = plan_backward(p->n, p->d, false, p->residual_type == MOE_DTYPE_FP32).blocks;
+  return static_cast<size_t>(blocks) * p->d * sizeof(float);
 }
 
 MOE_API moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t dy_type,
@@ -566,11 +803,13 @@ MOE_API moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t d
     if (ws == nullptr) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < moe_add_rms_norm_backward_workspace_size(p)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   }
-  const Plan pl = plan_backward(p->n, p->d);
+  const bool r32 = p->residual_type == MOE_DTYPE_FP32, dy32 = dy_type == MOE_DTYPE_FP32;
+  const Plan pl = plan_backward(p->n, p->d, dy32, r32);
   NormBwdArgs a = {};
   a.n = p->n;
   a.d = p->d;
   a.nw = pl.nw;
+  a.depth = pl.depth;
   a.early = one_wave(pl.blocks);
   a.x32 = p->x_type == MOE_DTYPE_FP32;
   a.dy = dy;
@@ -581,10 +820,9 @@ MOE_API moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t d
   a.dx = dx;
   a.dres = dresidual;
   a.part = dweight != nullptr ? static_cast<float*>(ws) : nullptr;
-  const bool r32 = p->residual_type == MOE_DTYPE_FP32;
-  const bool dy32 = dy_type == MOE_DTYPE_FP32;
-  if (pl.V == 2) launch_backward<2>(a, dy32, r32, pl, s);
-  else launch_backward<4>(a, dy32, r32, pl, s);
+  const bool ok = dy32 ? (r32 ? launch_backward<true, true>(a, pl, s) : launch_backward<true, false>(a, pl, s))
+                       : (r32 ? launch_backward<false, true>(a, pl, s) : launch_backward<false, false>(a, pl, s));
+  if (!ok) return MOE_ERR_CUDA;
   if (dweight != nullptr)
     launch(weight_grad_kernel, dim3(static_cast<unsigned>(ceil_div(p->d, 32))), dim3(1024), 0, s,
            pl.blocks, p->d, static_cast<const float*>(ws), dweight,

@@ -707,7 +707,7 @@ moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, const void*
  *   dx (x_type) = dresidual (residual_type) = dh, both [n, d] contiguous
  *   dweight [d] fp32 = sum over rows of dy * xh
  * in fp32.  Each output may be NULL (not all).  dresidual may be dresidual_out
- * itself.  dweight is summed in an order fixed by n, d and nothing else: the same
+ * itself.  dweight is summed in an order fixed by n, d and the types: the same
  * bits on every run.  With dweight, ws holds at least
  * moe_add_rms_norm_backward_workspace_size() bytes (0 = invalid parameters); calls, and
  * replays of graphs that captured them, that overlap on the GPU must not share it.

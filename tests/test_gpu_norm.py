@@ -259,3 +259,57 @@ def test_a_scale_that_underflows_counts_as_zero(n, group):
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     g.moe_add_rms_norm(p, x, None, w, None, None, q, sc, None, st)
     assert (sc == 1).all() and (q == 0).all() and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("xt,rt", [("bf16", "bf16"), ("fp32", "bf16"), ("bf16", "fp32"),
+                                   ("fp32", "fp32"), ("bf16", None), ("fp32", None)])
+@pytest.mark.parametrize("n,d", [(153, 16), (155, 7168), (9001, 64), (2500, 512), (2600, 528),
+                                 (1300, 2064), (1000, 7168), (480, 12288), (400, 16384)])
+def test_forward_of_several_rows_a_block(n, d, xt, rt, group):
+    """Rings of one to four slots that wrap, a row to a warp and to a block."""
+    x, res, w, _ = make(n, d, xt, rt, seed=n + d)
+    _, o = forward(x, res, w, xt, rt, group)
+    check_forward(x, res, w, rt, group, o)
+    assert int(o["st"].item()) == 0
+
+
+@pytest.mark.parametrize("xt,rt", [("bf16", "bf16"), ("fp32", "fp32")])
+def test_strided_rows_and_residual_in_place_of_several_rows_a_block(xt, rt):
+    g = G()
+    wide, res, w, _ = make(1500, 2080, xt, rt, seed=41)
+    x, res, w = wide[:, 16:1056], res[:, :1040].contiguous(), w[:1040].contiguous()
+    x[7, 3] = float("nan")
+    _, o = forward(x.contiguous(), res, w, xt, rt, 128)
+    assert int(o["st"].item()) == g.MOE_DEV_NONFINITE_INPUT
+    p = g.NormParams(1500, 1040, 2080, kind(xt), kind(rt), 128, EPS)
+    r2, y2, q2, s2 = res.clone(), torch.empty_like(o["y"]), torch.empty_like(o["q"]), torch.empty_like(o["s"])
+    g.moe_add_rms_norm(p, x, r2, w, r2, y2, q2, s2)
+    keep = torch.arange(1500, device=DEV) != 7
+    for a, b in ((r2, o["h"]), (y2, o["y"]), (q2, o["q"]), (s2, o["s"])):
+        assert torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.parametrize("dyt", ["bf16", "fp32"])
+@pytest.mark.parametrize("xt,rt", [("bf16", "bf16"), ("fp32", "bf16"), ("bf16", "fp32"), ("fp32", None)])
+@pytest.mark.parametrize("n,d", [(1, 8200), (700, 8208), (480, 12288), (330, 16384)])
+def test_backward_of_wide_rows(n, d, xt, rt, dyt):
+    test_backward(n, d, xt, rt, dyt)
+
+
+@pytest.mark.parametrize("rt", ["bf16", "fp32"])
+def test_backward_of_wide_rows_in_place_and_without_parts(rt):
+    g = G()
+    n, d = 500, 12288
+    x, res, w, gen = make(n, d, "bf16", rt, seed=43)
+    p, o = forward(x, res, w, "bf16", rt, 128, q=False)
+    dy = torch.randn((n, d), generator=gen, device=DEV).to(torch.bfloat16)
+    dres = torch.randn((n, d), generator=gen, device=DEV).to(TYPES[rt])
+    nb = g.moe_add_rms_norm_backward_workspace_size(p)
+    ws = torch.empty((nb,), dtype=torch.uint8, device=DEV)
+    dr, dw, dw2 = torch.empty_like(dres), torch.empty_like(w), torch.empty_like(w)
+    g.moe_add_rms_norm_backward(p, 0, dy, o["h"], w, o["rstd"], dres, None, dr, dw, ws, nb)
+    g.moe_add_rms_norm_backward(p, 0, dy, o["h"], w, o["rstd"], None, None, None, dw2, ws, nb)
+    assert torch.equal(dw, dw2)  # the order of the sums does not depend on dres
+    g.moe_add_rms_norm_backward(p, 0, dy, o["h"], w, o["rstd"], dres, None, dres, None, None, 0)
+    assert torch.equal(dres, dr)
