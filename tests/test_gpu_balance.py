@@ -244,3 +244,83 @@ def test_a_repeated_id_sums_its_slots(sigmoid):
     o = run(z, ids, gates, dg, None, sigmoid, balance=False)
     want = ref.gate_grad(z, ids, gates, dg, sigmoid, 2.5)
     assert ((o["dz"].double() - want).abs() <= 2e-5 * gates.abs().max() * dg.abs().max()).all()
+
+
+SIDE_BY_SIDE = [(4, 2), (8, 8), (12, 3), (16, 16), (20, 5), (32, 16), (36, 7), (64, 16), (68, 4),
+                (128, 8), (132, 16), (192, 8), (6, 6), (13, 13)]
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,k", SIDE_BY_SIDE)
+def test_several_tokens_a_warp(E, k, sigmoid):
+    for T in (1, 37, 1500):
+        z, ids, gates, dg = make(T, E, k, sigmoid, seed=T + E, pad=0.2)
+        for off in (None, [0, min(5, T), min(5, T), T // 2 + 1, T] if T > 9 else [0, 0, T]):
+            o = run(z, ids, gates, dg, off, sigmoid, dloss=1.5)
+            check(z, ids, gates, dg, off, sigmoid, o, dloss=1.5)
+            assert int(o["st"].item()) == 0
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,k", [(8, 2), (16, 4), (24, 9), (48, 4), (100, 6), (160, 8), (7, 3)])
+def test_nonfinite_logits_beside_other_tokens(E, k, sigmoid):
+    """NaN counts as -inf and +inf as the largest finite value; in padding tokens neither is
+    reported; the tokens beside them in the warp are as without."""
+    z, ids, gates, dg = make(90, E, k, sigmoid, seed=E, pad=0.3)
+    pad = ids[:, 0] == -1
+    z2 = z.clone()
+    z2[pad] = float("nan")
+    o = run(z2, ids, gates, dg, None, sigmoid)
+    assert int(o["st"].item()) == 0
+    check(z, ids, gates, dg, None, sigmoid, o)
+    rows = torch.nonzero(~pad)[:, 0]
+    free = int(torch.nonzero(~(torch.arange(E, device=DEV)[:, None] == ids[rows[3]]).any(1))[0])
+    z2[rows[3], free] = float("nan")   # a place that was not selected
+    free = int(torch.nonzero(~(torch.arange(E, device=DEV)[:, None] == ids[rows[10]]).any(1))[0])
+    z2[rows[10], free] = float("inf")
+    zr = torch.nan_to_num(z2, nan=float("-inf"), posinf=torch.finfo(torch.float32).max)
+    zr[pad] = 0
+    o = run(z2, ids, gates, dg, None, sigmoid)
+    assert int(o["st"].item()) == G().MOE_DEV_NONFINITE_LOGIT
+    check(zr, ids, gates, dg, None, sigmoid, o)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,k", [(8, 7), (16, 16), (32, 12), (64, 16), (96, 5)])
+def test_repeated_and_bad_ids_of_several_tokens_a_warp(E, k, sigmoid):
+    z, ids, gates, dg = make(75, E, k, sigmoid, seed=5)
+    ids[5] = 3
+    ids[6, :2] = 1
+    ids[40, -1] = ids[40, 0]
+    o = run(z, ids, gates, dg, None, sigmoid, balance=False)
+    want = ref.gate_grad(z, ids, gates, dg, sigmoid, 2.5)
+    # gates and their gradients as large as their largest, k of them added
+    assert ((o["dz"].double() - want).abs() <= 2e-5 * k * gates.abs().max() * dg.abs().max()).all()
+    ids[9, 1] = E
+    o = run(z, ids, gates, dg, None, sigmoid)
+    assert int(o["st"].item()) == G().MOE_DEV_BAD_EXPERT_ID
+    assert int(o["counts"].sum()) == 75 * k - 1
+
+
+def test_unaligned_rows_of_few_experts():
+    z, ids, gates, dg = make(333, 8, 2, False, seed=21)
+    zo = torch.empty((333 * 8 + 1,), device=DEV)[1:].view(333, 8).copy_(z)
+    o = run(zo, ids, gates, dg, None, False)
+    check(z, ids, gates, dg, None, False, o)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,k,S", [(64, 4, 130), (100, 6, 200), (40, 3, 1200), (384, 8, 64)])
+def test_many_sequences(E, k, S, sigmoid):
+    """A block a sequence in the second stage: one long sequence, short and empty ones."""
+    T = 3000
+    z, ids, gates, dg = make(T, E, k, sigmoid, seed=S, pad=0.1)
+    gen = torch.Generator().manual_seed(S)
+    cuts = torch.sort(torch.randint(1800, T + 1, (S - 2,), generator=gen)).values.tolist()
+    off = [0, 1700] + cuts + [T]
+    o = run(z, ids, gates, dg, off, sigmoid)
+    check(z, ids, gates, dg, off, sigmoid, o)
+    assert int(o["st"].item()) == 0
+    again = run(z, ids, gates, dg, off, sigmoid)
+    for name in ("loss", "probs", "dz"):
+        assert torch.equal(o[name], again[name])
