@@ -13,8 +13,8 @@
 //   softmax: dz = g (dg - <g, dg>)
 //   sigmoid: dz = g (1 - sigma) (dg - <g, dg> / route_scale).
 //
-// Bound: HBM.  One warp holds a token's row in registers, so the logits are read
-// once per pass.  Forward: each block owns a tile of consecutive tokens; its warps
+// Bound: HBM from about 256 experts on, instructions below.  A warp (or up to 192 experts a
+// part of one) holds a token's row in registers, so the logits are read once per pass.  Forward: each block owns a tile of consecutive tokens; its warps
 // keep column sums in registers and the block writes one partial row of sums and
 // counts per sequence that the tile meets, at slot tile + sequence (that index
 // grows by one with every step to the next tile or the next sequence, so no two
@@ -530,7 +530,7 @@ balance_finish_many_kernel(const BalArgs a, int cols) {
   if (!a.early) pdl_trigger();
 }
 
-// One warp per token, the rows of its next tokens on their way into the warp's ring
+// The rows of a warp's next tokens on their way into the warp's ring
 // (65,536 x 384: 35.5 us, 87 % of HBM, against 38.6 with one row ahead in registers,
 // which left the last ones spilled).  The dot product and the sum are reduced together
 // before the row is normalised; the selected experts' terms reach their lanes through a
@@ -734,10 +734,7 @@ route_backward_kernel(const BalArgs a) {
 // --------------------------------- host side --------------------------------
 
 // Lanes that hold a token.
-int lanes(int E) {
-  if (E % 4 != 0) return E <= 8 ? 8 : E <= 16 ? 16 : 32;
-  return E <= 8 ? 2 : E <= 16 ? 4 : E <= 64 ? 8 : E <= 192 ? 16 : 32;
-}
+int lanes(int E) { return E <= 8 ? 2 : E <= 16 ? 4 : E <= 64 ? 8 : E <= 192 ? 16 : 32; }
 
 // Tokens per block of the forward: two blocks per SM (few slots for the second
 // launch to add), at least one token per group of lanes.
@@ -788,7 +785,8 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // Values per lane, in 16-byte pieces where the rows allow them, and lanes per token.
 // 65,536 tokens, forward + backward, with a warp a token / so: 8 experts 13.5 + 20.7 /
 // 7.2 + 4.0 us, 64: 15.9 + 20.6 / 11.9 + 8.6, 128: 19.1 + 20.9 / 16.7 + 13.9, 192: 20.5 + 25.4 /
-// 18.1 + 18.2; 256 with half a warp: 20.9 + 25.8 / 23.4 + 26.6.
+// 18.1 + 18.2; 256 with half a warp: 20.9 + 25.8 / 23.4 + 26.6; single values, 31 experts:
+// 15.3 + 17.1 / 11.8 + 8.0.
 template <template <int, int, int, bool> class Launch, bool SIG>
 moe_status by_width(bool vec4, const BalArgs& a, unsigned grid, cudaStream_t s) {
   const int E = a.E;
@@ -803,10 +801,12 @@ moe_status by_width(bool vec4, const BalArgs& a, unsigned grid, cudaStream_t s) 
     if (E <= 384) return Launch<4, 3, 32, SIG>::go(a, grid, s);
     return Launch<4, 4, 32, SIG>::go(a, grid, s);
   }
-  if (E <= 8) return Launch<1, 1, 8, SIG>::go(a, grid, s);
-  if (E <= 16) return Launch<1, 1, 16, SIG>::go(a, grid, s);
-  if (E <= 32) return Launch<1, 1, 32, SIG>::go(a, grid, s);
-  if (E <= 128) return Launch<1, 4, 32, SIG>::go(a, grid, s);
+  if (E <= 8) return Launch<1, 4, 2, SIG>::go(a, grid, s);
+  if (E <= 16) return Launch<1, 4, 4, SIG>::go(a, grid, s);
+  if (E <= 32) return Launch<1, 4, 8, SIG>::go(a, grid, s);
+  if (E <= 64) return Launch<1, 8, 8, SIG>::go(a, grid, s);
+  if (E <= 128) return Launch<1, 8, 16, SIG>::go(a, grid, s);
+  if (E <= 192) return Launch<1, 12, 16, SIG>::go(a, grid, s);
   if (E <= 256) return Launch<1, 8, 32, SIG>::go(a, grid, s);
   return Launch<1, 16, 32, SIG>::go(a, grid, s);
 }
