@@ -15,8 +15,8 @@
 // thread) through both reductions, so x and r are read once and every output
 // written once.  Blocks are persistent; their next rows are on their way into shared
 // memory (bulk copies, the forward and wide backward rows) or registers (the backward
-// up to 8,192 values).  Forward, 8,192 x 7,168 (of the copy rate 6.7 TB/s): bf16 83.5 us
-// (6.3 TB/s), fp32 residual 128 (6.0), fp32 both 141 (6.2); backward 96 (6.1), 144 (6.5), 174 (6.1).
+// up to 8,192 values).  Forward, 8,192 x 7,168 (of the copy rate 6.7 TB/s): bf16 84 us
+// (6.3 TB/s), fp32 residual 125 (6.1), fp32 both 144 (6.1); backward 96 (6.1), 144 (6.5), 174 (6.1).
 #include <algorithm>
 
 #include "smem.cuh"
@@ -221,8 +221,8 @@ __device__ __forceinline__ void init_ring_bars(uint64_t* bars, int n, int* abort
 // whole block takes one.  RING: blocks are persistent and each row group has `depth`
 // rows on their way into shared memory, the next one issued as soon as all have taken
 // the current row into registers.  (With the next row in registers instead, four chunks a
-// thread, 128 registers: 8,192 x 7,168, block codes, bf16 86 us against 83.5, fp32 residual
-// 171 against 128, both fp32 203 against 141, no residual 72 against 62.)
+// thread, 128 registers: 8,192 x 7,168, block codes, bf16 86 us against 84, fp32 residual
+// 171 against 125, both fp32 203 against 144, no residual 72 against 62.)
 template <int V, bool X32, bool R32, bool RING>
 __global__ void __launch_bounds__(1024)
 add_rms_norm_kernel(const NormArgs a) {
@@ -621,32 +621,30 @@ struct Plan {
 };
 
 // Two chunks a thread (four: 86.6 us at 8,192 x 7,168 bf16, fewer warps to hide the
-// reductions).  Blocks on an SM: as many as its warps and shared memory hold with two rows
-// each on their way, or with one where that holds the whole batch.
-Plan plan_ring(int64_t n, int d, int row_bytes, int block_bytes) {
+// reductions).  As many blocks on an SM as its warps and shared memory hold with one row
+// each on its way (its copy then runs behind the second half of the row before); only
+// where a block has an SM to itself, rows above 8,192 values, does it take more (4,096 x
+// 12,288 bf16 forward 75 us, with one 79).  With more everywhere the forward alone is the
+// same, but 4,096 x 4,096 forward and backward in turn took 63 to 72 us against 62.
+Plan plan_ring(int64_t n, int d, int row_bytes) {
   Plan p;
   p.V = 2;
   p.nw = static_cast<int>(ceil_div(d / 8, 64));
   const int groups = p.nw == 1 ? 4 : 1, rows = groups * row_bytes;
   p.threads = 32 * groups * p.nw;
-  auto fit = [&](int depth) {
-    int per_sm = kRingWarps / (p.threads / 32);
-    while (per_sm > 1 && per_sm * (depth * rows + block_bytes) > kSmBytes) --per_sm;
-    return per_sm;
-  };
-  const int64_t want = ceil_div(n, groups);
-  int per_sm = fit(1);
-  if (want > static_cast<int64_t>(sm_count()) * per_sm) per_sm = fit(2);
-  p.depth = std::min(kMaxDepth, (kSmBytes / per_sm - block_bytes) / rows);
+  int per_sm = kRingWarps / (p.threads / 32);
+  while (per_sm > 1 && per_sm * (rows + kBlockBytes) > kSmBytes) --per_sm;
+  p.depth = per_sm > 1 ? 1 : std::min(kMaxDepth, (kSmBytes - kBlockBytes) / rows);
   p.smem = p.depth * rows;
-  p.blocks = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(sm_count()) * per_sm));
+  p.blocks = static_cast<int>(
+      std::min<int64_t>(ceil_div(n, groups), static_cast<int64_t>(sm_count()) * per_sm));
   return p;
 }
 
 // Forward: rows fewer than the SMs are latency-bound and take one chunk a thread straight
 // from global memory.
 Plan plan_forward(int64_t n, int d, int row_bytes) {
-  if (n > sm_count() || d > 8192) return plan_ring(n, d, row_bytes, kBlockBytes);
+  if (n > sm_count() || d > 8192) return plan_ring(n, d, row_bytes);
   Plan p;
   p.V = 1;
   p.nw = static_cast<int>(ceil_div(d / 8, 32));
@@ -659,7 +657,7 @@ Plan plan_forward(int64_t n, int d, int row_bytes) {
 // gradient.  Wide rows count as if dh_out were given, so that the order of the sums does
 // not depend on it.
 Plan plan_backward(int64_t n, int d, bool dy32, bool r32) {
-  if (d > 8192) return plan_ring(n, d, d * ((dy32 ? 4 : 2) + (r32 ? 8 : 4)), kBlockBytes);
+  if (d > 8192) return plan_ring(n, d, d * ((dy32 ? 4 : 2) + (r32 ? 8 : 4)));
   Plan p;
   p.V = 2;
   p.nw = static_cast<int>(ceil_div(d / 8, 64));
