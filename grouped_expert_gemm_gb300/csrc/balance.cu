@@ -179,13 +179,17 @@ __device__ __forceinline__ float group_max(float x) {
   }
 }
 
-// e^x as 2^(x log2 e): two roundings of the argument (2^-23 |x|) and the
-// instruction's 2^-22; results below the normal range are 0.
-__device__ __forceinline__ float exp_of(float x) {
+constexpr float kLog2E = 1.44269504088896341f;
+
+// The instruction errs by 2^-22; results below the normal range are 0.
+__device__ __forceinline__ float exp2_of(float x) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504088896341f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// e^x as 2^(x log2 e): two more roundings of the argument (2^-23 |x|).
+__device__ __forceinline__ float exp_of(float x) { return exp2_of(x * kLog2E); }
 
 template <int M, int L>
 __device__ __forceinline__ float row_max(const float (&v)[M]) {
@@ -206,10 +210,21 @@ __device__ __forceinline__ float row_terms(float (&v)[M], float (&slope)[SIG && 
   const float m = row_max<M, L>(v);
   float sum = 0.0f;
   if constexpr (!SIG) {
+    // e^(z - m) as 2^(z log2 e - c): the rounding of c = m log2 e is the row's own factor,
+    // which the sum takes out again.  (Not where c would overflow.)
+    if (fabsf(m) < 1e38f) {
+      const float c = m * kLog2E;
 #pragma unroll
-    for (int i = 0; i < M; ++i) {
-      v[i] = exp_of(v[i] - m);
-      sum += v[i];
+      for (int i = 0; i < M; ++i) {
+        v[i] = exp2_of(fmaf(v[i], kLog2E, -c));
+        sum += v[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        v[i] = exp_of(v[i] - m);
+        sum += v[i];
+      }
     }
   } else if (m >= 0.0f) {
     if (m > FLT_MAX) sum = NAN;
@@ -304,9 +319,9 @@ balance_tile_kernel(const BalArgs a) {
       for (int i = 0; i < kIds; ++i) id[i] = next_id[i];
       if (tw + kStep < e) fetch(tw + kStep + g);
       const bool live = __shfl_sync(0xFFFFFFFFu, id[0], lane - gl) != MOE_ROUTE_MASKED;  // no padding
-      if (!__any_sync(0xFFFFFFFFu, live)) continue;
+      if (L == 32 ? !live : !__any_sync(0xFFFFFFFFu, live)) continue;
       float sum = group_add<L>(row_terms<M, L, SIG, false>(v, none));
-      if (__any_sync(0xFFFFFFFFu, live && isnan(sum))) {
+      if (L == 32 ? isnan(sum) : __any_sync(0xFFFFFFFFu, live && isnan(sum))) {
         const int t = min(tw + g, e - 1);
         reload_finite<VEC, N, L>(a.logits + static_cast<int64_t>(t) * a.E, a.E, gl, v,
                                  live ? a.dev_status : nullptr);
@@ -640,7 +655,7 @@ route_backward_kernel(const BalArgs a) {
         dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
         inner += __shfl_xor_sync(0xFFFFFFFFu, inner, o);
       }
-      if (__any_sync(0xFFFFFFFFu, in && isnan(sum))) {
+      if (L == 32 ? isnan(sum) : __any_sync(0xFFFFFFFFu, in && isnan(sum))) {
         reload_finite<VEC, N, L>(row, a.E, gl, v, pad || !in ? nullptr : a.dev_status);
         sum = group_add<L>(row_terms<M, L, SIG, true>(v, slope));
         dot = 0.0f;
@@ -660,7 +675,7 @@ route_backward_kernel(const BalArgs a) {
 #pragma unroll
       for (int i = 0; i < M; ++i) v[i] = 0.0f;
     }
-    if (a.dgates != nullptr && __any_sync(0xFFFFFFFFu, !pad)) {
+    if (a.dgates != nullptr && (L == 32 ? !pad : __any_sync(0xFFFFFFFFu, !pad))) {
       // each slot leaves its number at its expert: one that finds another's there shares
       // the expert (ids that moe_route did not write), and the slots are then added one by
       // one in slot order
