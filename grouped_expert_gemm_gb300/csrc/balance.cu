@@ -748,18 +748,22 @@ route_backward_kernel(const BalArgs a) {
 
 // --------------------------------- host side --------------------------------
 
+// Few tokens spread over more lanes of more blocks, at least eight lanes a token (256 x 8,
+// forward + backward: 8.25 us against 8.53 with two).
+int width(int T, int E) { return T <= 1024 ? std::max(E, 17) : E; }
+
 // Lanes that hold a token.
 int lanes(int E) { return E <= 8 ? 2 : E <= 16 ? 4 : E <= 64 ? 8 : E <= 192 ? 16 : 32; }
 
 // Tokens per block of the forward: two blocks per SM (few slots for the second
 // launch to add), at least one token per group of lanes.
 int tile_tokens(int T, int E) {
-  return static_cast<int>(std::max<int64_t>(ceil_div(T, 2 * 152), kBalWarps * 32 / lanes(E)));
+  return static_cast<int>(std::max<int64_t>(ceil_div(T, 2 * 152), kBalWarps * 32 / lanes(width(T, E))));
 }
 
 // The backward has no slots: four blocks per SM.
 int backward_tokens(int T, int E) {
-  return static_cast<int>(std::max<int64_t>(ceil_div(T, 4 * 152), kBwdThreads / lanes(E)));
+  return static_cast<int>(std::max<int64_t>(ceil_div(T, 4 * 152), kBwdThreads / lanes(width(T, E))));
 }
 
 int64_t slots(int T, int E, int S) { return ceil_div(T, tile_tokens(T, E)) + S; }
@@ -804,7 +808,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // 15.3 + 17.1 / 11.8 + 8.0.
 template <template <int, int, int, bool> class Launch, bool SIG>
 moe_status by_width(bool vec4, const BalArgs& a, unsigned grid, cudaStream_t s) {
-  const int E = a.E;
+  const int E = width(a.T, a.E);
   if (vec4) {
     if (E <= 8) return Launch<4, 1, 2, SIG>::go(a, grid, s);
     if (E <= 16) return Launch<4, 1, 4, SIG>::go(a, grid, s);
