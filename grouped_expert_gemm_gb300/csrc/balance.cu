@@ -13,14 +13,15 @@
 //   softmax: dz = g (dg - <g, dg>)
 //   sigmoid: dz = g (1 - sigma) (dg - <g, dg> / route_scale).
 //
-// Bound: HBM from about 256 experts on, instructions below.  A warp (or up to 192 experts a
-// part of one) holds a token's row in registers, so the logits are read once per pass.  Forward: each block owns a tile of consecutive tokens; its warps
-// keep column sums in registers and the block writes one partial row of sums and
-// counts per sequence that the tile meets, at slot tile + sequence (that index
-// grows by one with every step to the next tile or the next sequence, so no two
-// (tile, sequence) pairs share a slot).  A second launch adds a sequence's slots
-// in order: no floating-point atomics, the same bits every time.  65,536 x 384: forward
-// 26.4 us (3.9 TB/s; 22 us the tiles), backward 35.5 us (5.8 TB/s, 87 % of the copy rate).
+// Bound: HBM from about 256 experts on, instructions below.  A warp (or, up to 192 experts,
+// a part of one) holds a token's row in registers, so the logits are read once per pass.
+// Forward: each block owns a tile of consecutive tokens; its warps keep column sums in
+// registers and the block writes one partial row of sums and counts per sequence that the
+// tile meets, at slot tile + sequence (that index grows by one with every step to the next
+// tile or the next sequence, so no two (tile, sequence) pairs share a slot).  A second
+// launch adds a sequence's slots in order: no floating-point atomics, the same bits every
+// time.  65,536 x 384: forward 26.4 us (3.9 TB/s; 22 us the tiles), backward 35.5 us
+// (5.8 TB/s, 87 % of the copy rate).
 #include <float.h>
 #include <math.h>
 
