@@ -181,6 +181,7 @@ __device__ __forceinline__ float group_max(float x) {
 }
 
 constexpr float kLog2E = 1.44269504088896341f;
+constexpr float kFoldedMax = 0x1p20f;
 
 // The instruction errs by 2^-22; results below the normal range are 0.
 __device__ __forceinline__ float exp2_of(float x) {
@@ -211,9 +212,10 @@ __device__ __forceinline__ float row_terms(float (&v)[M], float (&slope)[SIG && 
   const float m = row_max<M, L>(v);
   float sum = 0.0f;
   if constexpr (!SIG) {
-    // e^(z - m) as 2^(z log2 e - c): the rounding of c = m log2 e is the row's own factor,
-    // which the sum takes out again.  (Not where c would overflow.)
-    if (fabsf(m) < 1e38f) {
+    // e^(z - m) as 2^(z log2 e - c): the rounding of c = m log2 e is the row's own factor
+    // 2^(half an ulp of c), which the sum takes out again while it is near one: 2^(1/16) at
+    // most here (from |m| of about 2^30 on it would leave the type's range).
+    if (fabsf(m) < kFoldedMax) {
       const float c = m * kLog2E;
 #pragma unroll
       for (int i = 0; i < M; ++i) {
