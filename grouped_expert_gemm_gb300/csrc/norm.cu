@@ -17,6 +17,8 @@
 // memory (bulk copies, the forward and wide backward rows) or registers (the backward
 // up to 8,192 values).  Forward, 8,192 x 7,168 (of the copy rate 6.7 TB/s): bf16 84 us
 // (6.3 TB/s), fp32 residual 125 (6.1), fp32 both 144 (6.1); backward 96 (6.1), 144 (6.5), 174 (6.1).
+#include <math.h>
+
 #include <algorithm>
 
 #include "smem.cuh"
@@ -192,9 +194,10 @@ struct Ring {
   __device__ __forceinline__ const uint8_t* here() const {
     return base + static_cast<size_t>(slot) * bytes;
   }
-  // (A wait that gives up has reported it; the row is then whatever the slot holds.)
-  __device__ __forceinline__ void wait(volatile int* abort_flag, uint32_t* dev_status) const {
-    wait_bounded(bars + 8 * slot, phase, abort_flag, dev_status);
+  // False: the wait gave up (reported where there is a status word), and the row is
+  // whatever the slot holds.
+  __device__ __forceinline__ bool wait(volatile int* abort_flag, uint32_t* dev_status) const {
+    return wait_bounded(bars + 8 * slot, phase, abort_flag, dev_status);
   }
   __device__ __forceinline__ void next() {
     if (++slot == depth) {
@@ -522,11 +525,16 @@ rms_norm_backward_wide_kernel(const NormBwdArgs a) {
   if (tid == 0)
     for (int i = 0; i < a.depth && row + i * step < a.n; ++i) issue(row + i * step, i);
   float next_rstd = row < a.n ? __ldg(a.rstd + row) : 0.0f;
+  bool read = true;
   for (; row < a.n; row += step) {
     const int64_t base = row * a.d;
-    const float rstd = next_rstd;
+    float rstd = next_rstd;
     if (row + step < a.n) next_rstd = __ldg(a.rstd + row + step);
-    ring.wait(abort_flag, nullptr);
+    // the call has no status word: from a wait that gave up on, the block's rows become
+    // NaN, and with them its weight gradient (a slot that is not refilled any more looks
+    // full every other time round, so later waits are not asked)
+    read = read && ring.wait(abort_flag, nullptr);
+    if (!read) rstd = NAN;
     const uint8_t* here = ring.here();
     Raw<R32> h;
     Raw<DY32> dy;

@@ -689,7 +689,8 @@ typedef struct {
  * not overlap inputs.
  * A NaN or Inf in a quantized row sets MOE_DEV_NONFINITE_INPUT (its codes are then
  * unspecified); without q it only propagates.  Squares are summed in fp32: values
- * beyond about 1e18 overflow the sum and give y = 0.
+ * beyond about 1e18 overflow the sum and give y = 0.  A bounded wait that gives up
+ * sets MOE_DEV_TIMEOUT.
  * Limits: d % 8 == 0 (16 with q), d <= 16384, x_stride % 8 == 0, 16-byte aligned
  * pointers (4 for scales and rstd).  n = 0 does nothing.                       */
 moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, const void* residual,
@@ -711,7 +712,9 @@ moe_status moe_add_rms_norm(const moe_norm_params* p, const void* x, const void*
  * bits on every run.  With dweight, ws holds at least
  * moe_add_rms_norm_backward_workspace_size() bytes (0 = invalid parameters); calls, and
  * replays of graphs that captured them, that overlap on the GPU must not share it.
- * n = 0 writes dweight = 0.  Limits as the forward.                           */
+ * n = 0 writes dweight = 0.  Limits as the forward.  The call has no status word: where
+ * a bounded wait gives up (MOE_DEV_TIMEOUT elsewhere), the rows from there on that its
+ * block would write and the columns of dweight that miss them are NaN.        */
 size_t moe_add_rms_norm_backward_workspace_size(const moe_norm_params* p);
 moe_status moe_add_rms_norm_backward(const moe_norm_params* p, int32_t dy_type, const void* dy,
                                      const void* h, const float* weight, const float* rstd,
