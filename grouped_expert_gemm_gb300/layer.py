@@ -39,6 +39,8 @@ def capacity_from_factor(cf: float, assignments: int, slots: int) -> int:
 
 
 # dispatch payload of the expert input rows -> scale group of the FP8 forms
+# types that hold E4M3 codes: torch's own, and the raw bytes the payload buffers have
+E4M3_CODES = (torch.float8_e4m3fn, torch.uint8)
 PAYLOADS = {"bf16": None, "fp8_row": abi.MOE_SCALE_ROW, "fp8_block128": abi.MOE_SCALE_BLOCK128}
 
 
@@ -58,7 +60,7 @@ def check_w8_layer(d, E, I, payload, fp8_loader, gather, decode_path, expert_pas
             raise ValueError(f"{what} must be a pair (codes, scales)")
         q, s = pair
         want = (n, -(-N // 128), -(-K // 128))
-        if tuple(q.shape) != (n, N, K) or q.element_size() != 1 or not q.is_contiguous():
+        if tuple(q.shape) != (n, N, K) or q.dtype not in E4M3_CODES or not q.is_contiguous():
             raise ValueError(f"{what} codes must be contiguous E4M3 {(n, N, K)}")
         if tuple(s.shape) != want or s.dtype != torch.float32 or not s.is_contiguous():
             raise ValueError(f"{what} scales must be contiguous fp32 {want}")
@@ -384,11 +386,12 @@ class MoELayer:
         if self.payload == "bf16" or (self.shared is not None and not self.w8):
             raise ValueError("this layer reads bf16 token rows")
         q, s = x
-        for t, shape, size, what in ((q, (self.T, self.d), 1, "codes"),
-                                     (s, tuple(self.xs.shape), 4, "scales")):
-            if tuple(t.shape) != shape or t.element_size() != size or not t.is_contiguous() or \
-                    t.device != self.out.device or (size == 4 and t.dtype != torch.float32):
-                raise ValueError(f"payload {what} must be contiguous {shape} on {self.out.device}")
+        for t, shape, types, what in ((q, (self.T, self.d), E4M3_CODES, "codes"),
+                                      (s, tuple(self.xs.shape), (torch.float32,), "scales")):
+            if tuple(t.shape) != shape or t.dtype not in types or not t.is_contiguous() or \
+                    t.device != self.out.device:
+                raise ValueError(f"payload {what} must be contiguous {types[0]} {shape} on "
+                                 f"{self.out.device}")
 
     def forward(self, logits, x, stream=None, out=None) -> torch.Tensor:
         """Enqueue the whole layer on `stream`; returns the fp32 output buffer [T, d]

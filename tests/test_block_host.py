@@ -92,3 +92,23 @@ def test_payload_scales_are_fp32():
     q, s = torch.zeros((8, 256), dtype=torch.uint8), torch.ones((8, 2), dtype=torch.int32)
     with pytest.raises(ValueError):
         layer.forward(torch.zeros((8, 4)), (q, s))
+
+
+@pytest.mark.parametrize("other", [torch.float8_e5m2, torch.int8, torch.bool])
+def test_codes_of_another_one_byte_type_are_refused(other):
+    """They would be read as E4M3."""
+    d, E, k, I = 256, 4, 2, 128
+    w = [pair(E, I, d), pair(E, I, d), pair(E, d, I)]
+    sh = [pair(1, I, d), pair(1, I, d), pair(1, d, I)]
+    ok = dict(payload="fp8_block128", device="cpu")
+    raw = [(q.view(torch.uint8), s) for q, s in w]
+    layer = g.MoELayer(8, d, E, k, I, *raw, **ok)  # raw bytes are codes
+    for i in range(3):
+        v = list(w)
+        v[i] = (w[i][0].view(torch.uint8).to(other), w[i][1])
+        with pytest.raises(ValueError):
+            g.MoELayer(8, d, E, k, I, *v, **ok)
+    with pytest.raises(ValueError):
+        g.MoELayer(8, d, E, k, I, *w, shared_weights=[(sh[0][0].view(torch.uint8).to(other), sh[0][1]), *sh[1:]], **ok)
+    with pytest.raises(ValueError):
+        layer.forward(torch.zeros((8, E)), (torch.zeros((8, d), dtype=torch.uint8).to(other), torch.ones((8, 2))))
