@@ -44,10 +44,19 @@ E4M3_CODES = (torch.float8_e4m3fn, torch.uint8)
 PAYLOADS = {"bf16": None, "fp8_row": abi.MOE_SCALE_ROW, "fp8_block128": abi.MOE_SCALE_BLOCK128}
 
 
+def _same_device(a: torch.device, b: torch.device) -> bool:
+    """Whether two devices are one ("cuda" is the current GPU)."""
+    def index(d):
+        return torch.cuda.current_device() if d.type == "cuda" and d.index is None else d.index
+
+    return a.type == b.type and index(a) == index(b)
+
+
 def check_w8_layer(d, E, I, payload, fp8_loader, gather, decode_path, expert_passes, weights,
-                   shared):
+                   shared, device):
     """Arguments of a layer with E4M3 experts: block scales on both operands, the options of
-    the bf16 passes left at their defaults, codes and scales of the right shapes."""
+    the bf16 passes left at their defaults, codes and scales of the right shapes and on the
+    layer's device."""
     if payload != "fp8_block128":
         raise ValueError("E4M3 experts need payload='fp8_block128' (a scale per 128 values)")
     if fp8_loader != "auto" or gather or decode_path not in ("auto", "separate") or \
@@ -59,6 +68,9 @@ def check_w8_layer(d, E, I, payload, fp8_loader, gather, decode_path, expert_pas
         if not isinstance(pair, (tuple, list)) or len(pair) != 2:
             raise ValueError(f"{what} must be a pair (codes, scales)")
         q, s = pair
+        for t in (q, s):
+            if not isinstance(t, torch.Tensor) or not _same_device(t.device, device):
+                raise ValueError(f"{what} codes and scales must be tensors on {device}")
         want = (n, -(-N // 128), -(-K // 128))
         if tuple(q.shape) != (n, N, K) or q.dtype not in E4M3_CODES or not q.is_contiguous():
             raise ValueError(f"{what} codes must be contiguous E4M3 {(n, N, K)}")
@@ -100,7 +112,7 @@ class MoELayer:
         self.w8 = isinstance(w_gate, (tuple, list))
         if self.w8:
             check_w8_layer(d, E, I, payload, fp8_loader, gather, decode_path, expert_passes,
-                           (w_gate, w_up, w_down), shared_weights)
+                           (w_gate, w_up, w_down), shared_weights, torch.device(device))
         self.sel_bias = sel_bias
         self.params = abi.RouteParams(T, E, k, score_fn, n_group, topk_group, route_scale)
         R = T * k
@@ -388,8 +400,8 @@ class MoELayer:
         q, s = x
         for t, shape, types, what in ((q, (self.T, self.d), E4M3_CODES, "codes"),
                                       (s, tuple(self.xs.shape), (torch.float32,), "scales")):
-            if tuple(t.shape) != shape or t.dtype not in types or not t.is_contiguous() or \
-                    t.device != self.out.device:
+            if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or \
+                    t.dtype not in types or not t.is_contiguous() or t.device != self.out.device:
                 raise ValueError(f"payload {what} must be contiguous {types[0]} {shape} on "
                                  f"{self.out.device}")
 

@@ -112,3 +112,45 @@ def test_codes_of_another_one_byte_type_are_refused(other):
         g.MoELayer(8, d, E, k, I, *w, shared_weights=[(sh[0][0].view(torch.uint8).to(other), sh[0][1]), *sh[1:]], **ok)
     with pytest.raises(ValueError):
         layer.forward(torch.zeros((8, E)), (torch.zeros((8, d), dtype=torch.uint8).to(other), torch.ones((8, 2))))
+
+
+def test_codes_and_scales_on_another_device_are_refused():
+    """Their addresses would go to the kernels as they are.  (The meta device stands for
+    another one; the shared expert's pairs and the payload's are looked at too.)"""
+    d, E, k, I = 256, 4, 2, 128
+    w = [pair(E, I, d), pair(E, I, d), pair(E, d, I)]
+    sh = [pair(1, I, d), pair(1, I, d), pair(1, d, I)]
+    ok = dict(payload="fp8_block128", device="cpu")
+    layer = g.MoELayer(8, d, E, k, I, *w, **ok)
+
+    def away(p, i):
+        p = list(p)
+        p[i] = p[i].to("meta")
+        return tuple(p)
+
+    for i in range(3):
+        for part in range(2):
+            v = list(w)
+            v[i] = away(w[i], part)
+            with pytest.raises(ValueError, match="on cpu"):
+                g.MoELayer(8, d, E, k, I, *v, **ok)
+            v = list(sh)
+            v[i] = away(sh[i], part)
+            with pytest.raises(ValueError, match="on cpu"):
+                g.MoELayer(8, d, E, k, I, *w, shared_weights=v, **ok)
+    payload = (torch.zeros((8, d), dtype=torch.uint8), torch.ones((8, 2)))
+    for part in range(2):
+        with pytest.raises(ValueError, match="on cpu"):
+            layer.forward(torch.zeros((8, E)), away(payload, part))
+    for bad in ((payload[0], None), (payload[0].numpy(), payload[1])):
+        with pytest.raises(ValueError):
+            layer.forward(torch.zeros((8, E)), bad)
+
+
+def test_devices_of_one_name(monkeypatch):
+    """"cuda" is the current GPU."""
+    from grouped_expert_gemm_gb300 import layer
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    dev = torch.device
+    assert layer._same_device(dev("cuda"), dev("cuda", 1)) and layer._same_device(dev("cpu"), dev("cpu"))
+    assert not layer._same_device(dev("cuda", 0), dev("cuda")) and not layer._same_device(dev("cpu"), dev("cuda"))
