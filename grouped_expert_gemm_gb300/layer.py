@@ -44,6 +44,11 @@ E4M3_CODES = (torch.float8_e4m3fn, torch.uint8)
 PAYLOADS = {"bf16": None, "fp8_row": abi.MOE_SCALE_ROW, "fp8_block128": abi.MOE_SCALE_BLOCK128}
 
 
+def is_pair(*weights) -> bool:
+    """Whether some of the weights have the E4M3 form, a pair (codes, block scales)."""
+    return any(isinstance(w, (tuple, list)) for w in weights)
+
+
 def _same_device(a: torch.device, b: torch.device) -> bool:
     """Whether two devices are one ("cuda" is the current GPU)."""
     def index(d):
@@ -82,6 +87,8 @@ def check_w8_layer(d, E, I, payload, fp8_loader, gather, decode_path, expert_pas
     if shared is not None:
         if not isinstance(shared[0], (tuple, list)):
             raise ValueError("the shared expert of a layer with E4M3 experts is E4M3 too")
+        if len(shared[0]) != 2 or getattr(shared[0][0], "ndim", 0) != 3:
+            raise ValueError("shared gate must be a pair (codes [1, I, d], scales)")
         Is = shared[0][0].shape[1]
         for pair, N, K, what in zip(shared, (Is, Is, d), (d, d, Is),
                                     ("shared gate", "shared up", "shared down")):
@@ -109,7 +116,9 @@ class MoELayer:
         # E4M3 experts: each weight a pair (codes [E, N, K], block scales), as
         # quantize_weights makes them; both products then run in E4M3 on the payload's
         # codes (moe_grouped_swiglu_w8), the bf16 rows never exist
-        self.w8 = isinstance(w_gate, (tuple, list))
+        self.w8 = is_pair(w_gate, w_up, w_down)
+        if not self.w8 and shared_weights is not None and is_pair(*shared_weights):
+            raise ValueError("the shared expert of a layer with bf16 experts is bf16 too")
         if self.w8:
             check_w8_layer(d, E, I, payload, fp8_loader, gather, decode_path, expert_passes,
                            (w_gate, w_up, w_down), shared_weights, torch.device(device))

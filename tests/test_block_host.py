@@ -154,3 +154,23 @@ def test_devices_of_one_name(monkeypatch):
     dev = torch.device
     assert layer._same_device(dev("cuda"), dev("cuda", 1)) and layer._same_device(dev("cpu"), dev("cpu"))
     assert not layer._same_device(dev("cuda", 0), dev("cuda")) and not layer._same_device(dev("cpu"), dev("cuda"))
+
+
+def test_pairs_beside_bf16_weights_are_refused():
+    """In the constructor, not in the first forward."""
+    d, E, k, I = 256, 4, 2, 128
+    w = [pair(E, I, d), pair(E, I, d), pair(E, d, I)]
+    bf = [torch.zeros(s, dtype=torch.bfloat16) for s in ((E, d, I), (E, d, I), (E, I, d))]
+    for payload in ("bf16", "fp8_block128"):
+        for i in range(3):
+            for a, b in ((w, bf), (bf, w)):
+                v = list(a)
+                v[i] = b[i]
+                with pytest.raises(ValueError):
+                    g.MoELayer(8, d, E, k, I, *v, payload=payload, device="cpu")
+        with pytest.raises(ValueError):
+            g.MoELayer(8, d, E, k, I, *bf, shared_weights=[pair(1, I, d), pair(1, I, d), pair(1, d, I)],
+                       payload=payload, device="cpu")
+    for bad in ((), (w[0][0],), (None, w[0][1])):  # a shared gate that is no pair
+        with pytest.raises(ValueError):
+            g.MoELayer(8, d, E, k, I, *w, shared_weights=[bad, *w[1:]], payload="fp8_block128", device="cpu")
