@@ -459,6 +459,8 @@ class PooledMoELayer:
                  n_waves: int, pool_cap: int, local_cap: int, w_gate, w_up, w_down,
                  wave_policy: int = abi.MOE_WAVE_STRIPE, first_source: int = 0, device="cuda",
                  overlap: bool = True):
+        if is_pair(w_gate, w_up, w_down):
+            raise ValueError("the pooled layer's experts are bf16: no E4M3 pairs")
         self.T, self.d, self.k, self.I = T, d, k, I
         self.E = n_dest * local_per_dest
         self.n_dest, self.L, self.n_waves = n_dest, local_per_dest, n_waves
@@ -756,6 +758,8 @@ class DecodeBucket:
     def __init__(self, B: int, d: int, E: int, k: int, I: int, w_gate, w_up, w_down,
                  capacity: int = -1, score_fn: int = abi.MOE_SCORE_SOFTMAX, n_group: int = 1,
                  topk_group: int = 1, route_scale: float = 1.0, sel_bias=None, device="cuda"):
+        if is_pair(w_gate, w_up, w_down):
+            raise ValueError("a bucket's experts are bf16: its permute has no form for E4M3 rows")
         self.B, self.d, self.E, self.k, self.I = B, d, E, k, I
         self.cfg = dict(d=d, E=E, k=k, I=I, w_gate=w_gate, w_up=w_up, w_down=w_down,
                         capacity=capacity, score_fn=score_fn, n_group=n_group,

@@ -174,3 +174,13 @@ def test_pairs_beside_bf16_weights_are_refused():
     for bad in ((), (w[0][0],), (None, w[0][1])):  # a shared gate that is no pair
         with pytest.raises(ValueError):
             g.MoELayer(8, d, E, k, I, *w, shared_weights=[bad, *w[1:]], payload="fp8_block128", device="cpu")
+
+
+@pytest.mark.parametrize("overlap", [False, True])
+def test_pooled_layer_and_buckets_refuse_pairs(overlap):
+    d, L, k, I = 256, 4, 2, 128
+    w = [pair(L, I, d), pair(L, I, d), pair(L, d, I)]
+    with pytest.raises(ValueError, match="E4M3"):
+        g.PooledMoELayer(8, d, k, I, 2, L, 1, 16, 16, *w, device="cpu", overlap=overlap)
+    with pytest.raises(ValueError, match="E4M3"):
+        g.DecodeBucketLadder([1, 4], d, L, k, I, *w, device="cpu")
