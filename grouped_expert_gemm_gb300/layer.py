@@ -408,7 +408,7 @@ class MoELayer:
             raise ValueError("this layer reads bf16 token rows")
         q, s = x
         for t, shape, types, what in ((q, (self.T, self.d), E4M3_CODES, "codes"),
-                                      (s, tuple(self.xs.shape), (torch.float32,), "scales")):
+                                      (s, (self.T, self.xs.shape[1]), (torch.float32,), "scales")):
             if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or \
                     t.dtype not in types or not t.is_contiguous() or t.device != self.out.device:
                 raise ValueError(f"payload {what} must be contiguous {types[0]} {shape} on "

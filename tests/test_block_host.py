@@ -184,3 +184,15 @@ def test_pooled_layer_and_buckets_refuse_pairs(overlap):
         g.PooledMoELayer(8, d, k, I, 2, L, 1, 16, 16, *w, device="cpu", overlap=overlap)
     with pytest.raises(ValueError, match="E4M3"):
         g.DecodeBucketLadder([1, 4], d, L, k, I, *w, device="cpu")
+
+
+@pytest.mark.parametrize("T", [0, 1, 3])
+def test_payload_has_a_row_of_scales_a_token(T):
+    """The empty batch too, whose layer keeps a row of its own."""
+    w = [pair(4, 128, 256), pair(4, 128, 256), pair(4, 256, 128)]
+    layer = g.MoELayer(T, 256, 4, 2, 128, *w, payload="fp8_block128", device="cpu")
+    norm = g.TokenNorm(T, 256, torch.ones(256), payload="fp8_block128", device="cpu")
+    layer._check_payload(norm.output)
+    for n in {T + 1, max(T - 1, 0)} - {T}:
+        with pytest.raises(ValueError):
+            layer._check_payload((norm.xq, torch.ones((n, 2))))

@@ -210,3 +210,15 @@ def test_empty_batch():
     assert float(loss.forward(z, ids)) == 0 and (loss.counts == 0).all()
     assert loss.backward(z, ids).shape == (0, 8)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("shared_I", [0, 128])
+def test_empty_batch_through_the_layer(shared_I):
+    """No tokens: the norm's empty pair goes into the layer, by itself and captured."""
+    layer, norm, _, rnd, _, _ = make(0, 256, 8, 2, 128, False, shared_I=shared_I)
+    x, res = torch.empty((0, 256), device=DEV), torch.empty((0, 256), dtype=torch.bfloat16, device=DEV)
+    logits = torch.empty((0, 8), device=DEV)
+    assert layer.forward(logits, norm.forward(x, res)).shape == (0, 256)
+    torch.cuda.synchronize()
+    assert (layer.counts == 0).all() and (layer.offsets == 0).all()
+    assert int(layer.dev_status.item()) == 0
