@@ -219,8 +219,10 @@ def _ptr(t) -> Optional[int]:
         return None
     try:
         return t.data_ptr()
-    except AttributeError:  # an address
-        return t
+    except AttributeError:
+        if isinstance(t, int):  # an address
+            return t
+        raise TypeError(f"expected a tensor, an address or None, got {type(t).__name__}") from None
 
 
 # torch.cuda.current_stream() builds a Stream object (3 us a call on the GB300's host);

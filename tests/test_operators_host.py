@@ -133,3 +133,13 @@ def test_balance_token_indexes_stay_in_32_bits(g):
         assert (g.moe_balance_loss_workspace_size(p, 1) > 0) == ok
         st = g.abi.lib().moe_route_backward(p, 1, None, None, 16, 16, 16, 0.1, 16, 16, None, 16, None, None)
         assert st == (g.MOE_ERR_INVALID_ARG if ok else g.MOE_ERR_UNSUPPORTED)  # (no logits)
+
+
+@pytest.mark.parametrize("other", [b"\0" * 64, "16", 16.0, (16, 16), [16]],
+                         ids=["bytes", "str", "float", "tuple", "list"])
+def test_arguments_that_are_neither_tensor_nor_address(g, other):
+    """Bytes and strings would pass as the address of their own storage."""
+    with pytest.raises(TypeError, match="expected a tensor"):
+        g.moe_add_rms_norm(g.NormParams(0, 64), other, None, 16, None, 16)
+    with pytest.raises(TypeError, match="expected a tensor"):
+        g.moe_quantize_weights_fp8(0, 16, 16, 16, other, 16)
