@@ -13,6 +13,7 @@ graph.  Arguments are checked here (type, shape, device, contiguity) with ValueE
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -44,15 +45,27 @@ def _device(device) -> torch.device:
     return d
 
 
+def _memory_of(stream, device):
+    """Where a call allocates: new memory belongs to the stream that the call runs on, since
+    the current stream's may still be in use by work queued there."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
 def quantize_weights(w: torch.Tensor, dev_status=None, stream=None):
     """Expert weights bf16 [E, K, N] (the layout of the bf16 passes) to (codes [E, N, K]
-    float8_e4m3fn, scales fp32 [E, ceil(N/128), ceil(K/128)]); done once per set of weights."""
+    float8_e4m3fn, scales fp32 [E, ceil(N/128), ceil(K/128)]), allocated on the call's stream;
+    done once per set of weights."""
     if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dtype == torch.bfloat16 and
             w.dim() == 3 and w.is_contiguous()):
         raise ValueError("weights must be a contiguous bf16 device tensor [E, K, N]")
     E, K, N = w.shape
-    q = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=w.device)
-    s = torch.empty((E, -(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
+    with _memory_of(stream, w.device):
+        q = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=w.device)
+        s = torch.empty((E, -(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
     abi.moe_quantize_weights_fp8(E, K, N, w, q, s, dev_status, stream)
     return q, s
 
@@ -129,12 +142,13 @@ class TokenNorm:
         if self._grads is None:
             new = dict(device=self.device)
             ws_bytes = abi.moe_add_rms_norm_backward_workspace_size(self.params)
-            self._grads = (
-                torch.empty((self.n, self.d), dtype=self.x_dtype, **new),
-                None if self.residual_dtype is None else
-                torch.empty((self.n, self.d), dtype=self.residual_dtype, **new),
-                torch.empty((self.d,), dtype=torch.float32, **new),
-                torch.empty((max(ws_bytes, 16),), dtype=torch.uint8, **new), ws_bytes)
+            with _memory_of(stream, self.device):
+                self._grads = (
+                    torch.empty((self.n, self.d), dtype=self.x_dtype, **new),
+                    None if self.residual_dtype is None else
+                    torch.empty((self.n, self.d), dtype=self.residual_dtype, **new),
+                    torch.empty((self.d,), dtype=torch.float32, **new),
+                    torch.empty((max(ws_bytes, 16),), dtype=torch.uint8, **new), ws_bytes)
         dx, dres, dw, ws, ws_bytes = self._grads
         abi.moe_add_rms_norm_backward(self.params, _KIND[dy.dtype], dy, self._h, self.weight,
                                       self.rstd, dresidual_out, dx, dres, dw, ws, ws_bytes, stream)

@@ -196,3 +196,21 @@ def test_payload_has_a_row_of_scales_a_token(T):
     for n in {T + 1, max(T - 1, 0)} - {T}:
         with pytest.raises(ValueError):
             layer._check_payload((norm.xq, torch.ones((n, 2))))
+
+
+def test_calls_allocate_on_their_own_stream(monkeypatch):
+    """What a call allocates belongs to the stream it is given: memory of the current one may
+    still be in use there."""
+    from grouped_expert_gemm_gb300 import block
+    asked = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: asked.append(s) or block.contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device: ("external", s, device))
+    cuda = torch.device("cuda", 0)
+    for stream, want in ((None, []), ("s", ["s"]), (1234, [("external", 1234, cuda)])):
+        asked.clear()
+        with block._memory_of(stream, cuda):
+            pass
+        assert asked == want
+    with block._memory_of("s", torch.device("cpu")):
+        pass
+    assert len(asked) == 1

@@ -214,7 +214,7 @@ def test_empty_batch():
 
 @pytest.mark.parametrize("shared_I", [0, 128])
 def test_empty_batch_through_the_layer(shared_I):
-    """No tokens: the norm's empty pair goes into the layer, by itself and captured."""
+    """No tokens: the norm's empty pair goes into the layer."""
     layer, norm, _, rnd, _, _ = make(0, 256, 8, 2, 128, False, shared_I=shared_I)
     x, res = torch.empty((0, 256), device=DEV), torch.empty((0, 256), dtype=torch.bfloat16, device=DEV)
     logits = torch.empty((0, 8), device=DEV)
@@ -222,3 +222,34 @@ def test_empty_batch_through_the_layer(shared_I):
     torch.cuda.synchronize()
     assert (layer.counts == 0).all() and (layer.offsets == 0).all()
     assert int(layer.dev_status.item()) == 0
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_buffers_made_in_a_call_belong_to_its_stream(handle):
+    """The current stream's freed memory, still in use by work queued there, is not taken."""
+    g = G()
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    w = torch.randn((4, 256, 512), generator=gen, device=DEV).to(torch.bfloat16)
+    x = torch.randn((64, 512), generator=gen, device=DEV)
+    res, dy = x.to(torch.bfloat16), torch.randn((64, 512), generator=gen, device=DEV)
+    want = g.quantize_weights(w)
+    norms = [g.TokenNorm(64, 512, torch.ones(512, device=DEV), x_dtype=torch.float32, device=DEV)
+             for _ in range(2)]
+    for n in norms:
+        n.forward(x, res)
+    want_dx, want_dres, want_dw = norms[0].backward(dy)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if handle else s
+    torch.cuda._sleep(20_000_000)  # some ms of the current stream's own work
+    olds = [torch.empty_like(t) for t in (*want, want_dx, want_dres, want_dw, norms[0]._grads[3])]
+    at = {t.data_ptr() for t in olds}
+    for t in olds:
+        t.view(torch.uint8).fill_(0x33)
+    del t, olds
+    q, sc = g.quantize_weights(w, stream=stream)
+    dx, dres, dw = norms[1].backward(dy, stream=stream)
+    assert not at & {t.data_ptr() for t in (q, sc, dx, dres, dw, norms[1]._grads[3])}
+    torch.cuda.synchronize()
+    assert torch.equal(q.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(sc, want[1])
+    assert torch.equal(dx, want_dx) and torch.equal(dres, want_dres) and torch.equal(dw, want_dw)
