@@ -231,6 +231,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", None)
 
 
+def check_current_device(device: torch.device):
+    """Kernels are enqueued on the current device: buffers of another one are refused."""
+    if device.type == "cuda" and device.index is not None:
+        now = _device() if _device is not None and torch.cuda.is_initialized() \
+            else torch.cuda.current_device()
+        if now != device.index:
+            raise ValueError(f"the buffers are on {device}, the current device is cuda:{now}")
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         if _raw_stream is not None and _device is not None and torch.cuda.is_initialized():

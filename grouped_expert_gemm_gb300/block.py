@@ -9,7 +9,8 @@
 
 Like the layers, each object owns its buffers (allocated once) and a call only enqueues
 kernels on the given stream (default: the current one), so calls can be captured into a CUDA
-graph.  Arguments are checked here (type, shape, device, contiguity) with ValueError.
+graph.  Arguments are checked here (type, shape, device, contiguity) with ValueError; the
+object's device must be the current one.
 """
 from __future__ import annotations
 
@@ -62,6 +63,7 @@ def quantize_weights(w: torch.Tensor, dev_status=None, stream=None):
     if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dtype == torch.bfloat16 and
             w.dim() == 3 and w.is_contiguous()):
         raise ValueError("weights must be a contiguous bf16 device tensor [E, K, N]")
+    abi.check_current_device(w.device)
     E, K, N = w.shape
     with _memory_of(stream, w.device):
         q = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=w.device)
@@ -114,6 +116,7 @@ class TokenNorm:
     def forward(self, x, residual=None, stream=None):
         """Returns ``output``; the sum that becomes the residual stream is
         ``residual_out``."""
+        abi.check_current_device(self.device)
         check_tensor("x", x, (self.n, self.d), self.x_dtype, self.device, rows_strided=True)
         if (residual is None) != (self.residual_dtype is None):
             raise ValueError("residual must be given exactly when residual_dtype is")
@@ -130,6 +133,7 @@ class TokenNorm:
         """Gradients of the last forward: (dx, dresidual or None, dweight).  dy is [n, d]
         bf16 or fp32; dresidual_out the gradient that reaches residual_out from its other
         readers (None: none).  The buffers are the object's own."""
+        abi.check_current_device(self.device)
         if self._h is None:
             raise ValueError("backward needs a forward before it")
         if not isinstance(dy, torch.Tensor) or dy.dtype not in _KIND:
@@ -182,6 +186,7 @@ class RouterLoss:
         self.dev_status = torch.zeros((1,), dtype=torch.int32, **new)
 
     def _inputs(self, logits, topk_ids, seq_offsets):
+        abi.check_current_device(self.device)
         check_tensor("logits", logits, (self.T, self.E), torch.float32, self.device)
         check_tensor("topk_ids", topk_ids, (self.T, self.k), torch.int32, self.device)
         if seq_offsets is not None:

@@ -419,6 +419,8 @@ class MoELayer:
         (`out` if given, else the layer's own).  `x`: the bf16 token rows, or with an FP8
         payload also the pair (codes, scales) that TokenNorm makes (the layer's scale group;
         not with a bf16 shared expert, which reads bf16 rows)."""
+        if self.w8:
+            abi.check_current_device(self.out.device)
         if isinstance(x, (tuple, list)):
             self._check_payload(x)
         for _, fn, _ in self.stages(logits, x, out):

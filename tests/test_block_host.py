@@ -214,3 +214,35 @@ def test_calls_allocate_on_their_own_stream(monkeypatch):
     with block._memory_of("s", torch.device("cpu")):
         pass
     assert len(asked) == 1
+
+
+def test_the_current_device_must_be_the_objects(monkeypatch):
+    """Kernels go to the current device's stream, whichever GPU the buffers are on."""
+    from grouped_expert_gemm_gb300 import abi
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(abi, "_device", lambda: 0)
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    norm = g.TokenNorm(4, 64, torch.ones(64), device="cpu")
+    loss = g.RouterLoss(4, 8, 2, 0.1, device="cpu")
+    z, ids = torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32)
+    norm.device = loss.device = torch.device("cuda", 1)
+    for call in (lambda: norm.forward(x, x), lambda: norm.backward(x), lambda: loss.forward(z, ids),
+                 lambda: loss.backward(z, ids)):
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            call()
+    abi.check_current_device(torch.device("cuda", 0))
+    abi.check_current_device(torch.device("cpu"))
+    monkeypatch.setattr(abi, "_device", None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 2)
+    with pytest.raises(ValueError, match="current device is cuda:2"):
+        abi.check_current_device(torch.device("cuda", 1))
+    abi.check_current_device(torch.device("cuda", 2))
+
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+
+    w = [pair(4, 128, 256), pair(4, 128, 256), pair(4, 256, 128)]
+    layer = g.MoELayer(8, 256, 4, 2, 128, *w, payload="fp8_block128", device="cpu")
+    layer.out = Elsewhere()
+    with pytest.raises(ValueError, match="current device is cuda:2"):
+        layer.forward(torch.zeros((8, 4)), torch.zeros((8, 256), dtype=torch.bfloat16))
