@@ -119,8 +119,15 @@ __device__ __forceinline__ Tile tile_of(int t, const Table& tb, int n_seg, int b
   return tl;
 }
 
+// Tile counts of segments that overlap (not allowed, but nothing outside the arrays is to be
+// touched) may pass 2^31: sums stop there.  Both operands are below 2^31.
+__device__ __forceinline__ int add_tiles(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), 0x7FFFFFFFu));
+}
+
 // Segment table by 128 threads (tid 0..127 of named barrier 1): segments outside
-// the row space are reported and treated as empty.
+// the row space are reported and treated as empty, and all of them where they have more
+// tiles than numbers (check_shape: not if they are disjoint).
 __device__ __forceinline__ void build_table(const W8Args& a, int bm, int n_blocks, int tid,
                                             const Table& tb) {
   const int lane = tid & 31, warp = tid >> 5;
@@ -136,24 +143,31 @@ __device__ __forceinline__ void build_table(const W8Args& a, int bm, int n_block
     }
     tb.begin[q] = b;
     tb.count[q] = c;
-    local += ((c + bm - 1) / bm) * n_blocks;
+    local = add_tiles(local, ((c + bm - 1) / bm) * n_blocks);
   }
   int incl = local;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += v;
+    if (lane >= o) incl = add_tiles(incl, v);
   }
   if (lane == 31) tb.warp_tot[warp] = incl;
   asm volatile("bar.sync 1, 128;" ::: "memory");
   int run = incl - local;
-  for (int w = 0; w < warp; ++w) run += tb.warp_tot[w];
+  for (int w = 0; w < warp; ++w) run = add_tiles(run, tb.warp_tot[w]);
   for (int q = q0; q < q1; ++q) {
     tb.start[q] = run;
-    run += ((tb.count[q] + bm - 1) / bm) * n_blocks;
+    run = add_tiles(run, ((tb.count[q] + bm - 1) / bm) * n_blocks);
   }
-  if (tid == 127)
-    tb.start[a.n_seg] = tb.warp_tot[0] + tb.warp_tot[1] + tb.warp_tot[2] + tb.warp_tot[3];
+  if (tid == 127) {
+    int total = add_tiles(add_tiles(tb.warp_tot[0], tb.warp_tot[1]),
+                          add_tiles(tb.warp_tot[2], tb.warp_tot[3]));
+    if (total > 0x7FFFFFFF - 0x10000) {  // (and a CTA's next tile's number is one too)
+      report(a.dev_status, MOE_DEV_BAD_ROW);
+      total = 0;
+    }
+    tb.start[a.n_seg] = total;
+  }
 }
 
 // amax / 448; 1 where that is zero, which it also is for an amax below 2^-141 (codes of

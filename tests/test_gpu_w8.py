@@ -339,3 +339,26 @@ def test_a_scale_that_underflows_counts_as_zero():
         torch.cuda.synchronize()
         assert int(st.item()) == 0 and int(st2.item()) == 0
         assert (hs[1] == 1).all() and (hq[1] & 0x7F == 0).all() and (y[1] == 0).all()
+
+
+def test_overlapping_segments_of_more_tiles_than_numbers():
+    """1,024 segments of the same 2^28 rows have 2^31 tiles: reported, and nothing is written."""
+    g = G()
+    n, R, I, d = 1024, 1 << 28, 16, 16
+    hq = torch.empty((R, I), dtype=torch.uint8, device=DEV)
+    hs = torch.empty((R, 1), device=DEV)
+    y = torch.empty((R, d), dtype=torch.bfloat16, device=DEV)
+    ends = [y[:4096], y[-4096:]]
+    for t in ends:
+        t.fill_(-7.0)
+    b = torch.zeros((n,), dtype=torch.int32, device=DEV)
+    c = torch.full((n,), R, dtype=torch.int32, device=DEV)
+    q = torch.zeros((n, d, I), dtype=torch.uint8, device=DEV)
+    s = torch.ones((n, 1, 1), device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    g.moe_grouped_down_w8(n, I, d, R, hq, hs, b, c, q, s, y, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == g.MOE_DEV_BAD_ROW
+    assert all((t == -7.0).all() for t in ends)
+    del hq, hs, y, ends, t
+    torch.cuda.empty_cache()
