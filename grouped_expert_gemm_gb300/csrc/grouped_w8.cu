@@ -6,13 +6,15 @@
 //   row's 128 columns;  y = bf16((hq hs) Wd^T)
 // (weights stored [N, K], K contiguous: both operands are K-major).
 //
-// Bound: decode sizes HBM (the touched experts' weights), 93 us for the 128 experts of
-// the 2048 x 768 decode bucket (604 MB, 98 % of the copy rate); large segments the
-// tensor memory: a block's MMAs take about 735 cycles a CTA (a product without the
-// per-block sums reaches 3.07 PFLOP/s), and reading its 128 KB of sums another 195,
-// during which the MMAs wait for the port -- whether 8 or 16 warps read, and however
-// fast they add; together 930 cycles, 2.5 PFLOP/s, where the down pass of 8 x 1024
-// rows, 14336 x 4096, runs (gate/up with its SwiGLU and codes: 2.4).
+// Bound: decode sizes HBM (the touched experts' weights), 94 us for the 115 to 120 touched
+// experts of a 2048 x 768 decode bucket (562 MB, 6.0 TB/s, 89 % of the copy rate).  Large
+// segments: the MMAs.  A product without the per-block sums takes 735 cycles a block and CTA
+// (3.07 PFLOP/s); the down pass of 8 x 1024 rows, 14336 x 4096, takes 895 (2.4 to 2.5 PFLOP/s),
+// gate/up with its SwiGLU and codes 984 (2.3).  Clock stamps there: the promotion warps
+// wait 170 to 215 cycles a block for its sums and hand its buffer back 400 to 455 after they
+// came, well before the other buffer's MMAs end; the issuer waits 150 for a buffer and 85
+// for operands.  Why the MMAs are slower beside the reads is not shown (the port of the
+// tensor memory was busy a third of the time).
 //
 // One reduction block of 128 is one pipeline stage, one row of the 128-byte
 // swizzle and one scale block.  The tensor core sums the block's codes into a
@@ -898,6 +900,8 @@ grouped_w8_few_kernel(const __grid_constant__ CUtensorMap map_x,
 // ------------------------------ weight quantization --------------------------
 
 // One block per 128 x 128 weight block: w [K, N] bf16 -> codes [N, K] and a scale.
+// 128 experts of 2048 x 768: 375 us, 1.6 TB/s, what bounds it not looked into: it runs once
+// per set of weights.
 __global__ void __launch_bounds__(256)
 quantize_weights_kernel(int K, int N, const uint16_t* __restrict__ w, uint8_t* __restrict__ q,
                         float* __restrict__ scales, uint32_t* __restrict__ dev_status) {
@@ -1125,10 +1129,15 @@ moe_status launch_pass(W8Args a, const void* x, const void* b0, const void* b1, 
   if (nt < kBM) {
     a.chained = chained;
     a.m_outer = 0;
-    // Tiles that hold rows, at most.  The reduction split over 1 / 2 / 4 CTAs (us of both
-    // passes): 16 tiles, K = 7168: 46 / 28 / 21, K = 4096: 28 / 20 / 17; 48 tiles
-    // 19 / 17 / 20; 64: 50 / 31 / 28; from half of the SMs on it only adds the hand-over
-    // (96 tiles: 22 / 24 / 29).
+    // Tiles that hold rows, at most.  The reduction split over 1 / 2 / 4 CTAs, us of one pass
+    // (one segment, 16-row tiles).  Gate/up, K = 2048: 16 tiles 14.6 / 9.8 / 8.0, 32: 15.5 /
+    // 10.6 / 9.5, 40: 15.6 / 10.9 / 12.6, 64: 16.5 / 11.9 / 13.0; K = 7168: 16: 43.0 / 20.4 /
+    // 13.9, 32: 43.4 / 21.1 / 15.2, 40: 43.9 / 21.5 / 25.3, 64: 45.6 / 24.5 / 25.8.  Down, 28
+    // tiles, K = 2048: 14.8 / 11.0 / 9.0.  (So four would serve up to the 36 clusters that one
+    // round holds; the rule stops at a fifth of the SMs, 30 tiles.)  From half of the SMs on
+    // the split only adds the hand-over: both passes at 96 tiles 22 / 24 / 29.  Short reductions
+    // gain little or lose: down, 64 tiles of eight segments, K = 256: 4.9 / 6.3, 768: 9.3 / 9.3,
+    // 1024: 10.7 / 10.1.
     const int64_t tiles = std::min<int64_t>(a.n_seg, a.max_rows) * ceil_div(a.N, SWIGLU ? 128 : 256);
     const int split = 5 * tiles <= sm_count() && a.GK >= 8 ? 4 : 2 * tiles <= sm_count() && a.GK >= 2 ? 2 : 1;
     if (nt == 16) {
@@ -1136,6 +1145,8 @@ moe_status launch_pass(W8Args a, const void* x, const void* b0, const void* b1, 
       if (split == 2) return launch_few<SWIGLU, 16, 2>(ma, m0, m1, a, s);
       return launch_few<SWIGLU, 16, 1>(ma, m0, m1, a, s);
     }
+    // (32-row tiles have no split over four.  Gate/up, eight segments of 12 rows, 1 / 2 / 4
+    // CTAs: 16 tiles, K = 2048 15.4 / 10.9 / 9.0, K = 7168 43.2 / 22.6 / 15.4.)
     if (split > 1) return launch_few<SWIGLU, 32, 2>(ma, m0, m1, a, s);
     return launch_few<SWIGLU, 32, 1>(ma, m0, m1, a, s);
   }
