@@ -38,9 +38,9 @@ def capacity_from_factor(cf: float, assignments: int, slots: int) -> int:
     return abi.moe_capacity(fr.numerator, fr.denominator, assignments, slots)
 
 
-# dispatch payload of the expert input rows -> scale group of the FP8 forms
 # types that hold E4M3 codes: torch's own, and the raw bytes the payload buffers have
 E4M3_CODES = (torch.float8_e4m3fn, torch.uint8)
+# dispatch payload of the expert input rows -> scale group of the FP8 forms
 PAYLOADS = {"bf16": None, "fp8_row": abi.MOE_SCALE_ROW, "fp8_block128": abi.MOE_SCALE_BLOCK128}
 
 
