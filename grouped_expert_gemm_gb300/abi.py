@@ -29,6 +29,7 @@ MOE_DEV_BAD_ROW = 8
 MOE_DEV_TIMEOUT = 16
 MOE_DEV_NONFINITE_INPUT = 32
 MOE_DEV_BAD_MAP = 64
+MOE_DEV_BAD_ADAPTER = 128
 
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID_GROUP = 1
@@ -66,6 +67,9 @@ EXPORTED = [
     "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward",
     "moe_quantize_weights_fp8", "moe_grouped_swiglu_w8_workspace_size", "moe_grouped_swiglu_w8",
     "moe_grouped_gate_up_w8", "moe_grouped_down_w8",
+    "moe_adapter_project", "moe_adapter_project_backward_workspace_size",
+    "moe_adapter_project_backward", "moe_grad_plan", "moe_clip_grads_workspace_size",
+    "moe_clip_grads",
 ]
 
 
@@ -95,6 +99,23 @@ class NormParams(ctypes.Structure):
     def __init__(self, n, d, x_stride=None, x_type=0, residual_type=0, group=0, eps=1e-6):
         super().__init__(n, d if x_stride is None else x_stride, d, x_type, residual_type, group,
                          eps)
+
+
+class AdapterParams(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("r", ctypes.c_int32), ("n_adapters", ctypes.c_int32), ("n_seg", ctypes.c_int32),
+                ("y_type", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64)]
+
+    def __init__(self, T, d, n, r, n_adapters, n_seg, y_type=0, x_stride=None, y_stride=None):
+        super().__init__(T, d, n, r, n_adapters, n_seg, y_type, d if x_stride is None else x_stride,
+                         n if y_stride is None else y_stride)
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("first_chunk", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -178,6 +199,13 @@ _SIGS = {
     "moe_grouped_swiglu_w8": (_I32, [_I32] * 4 + [_P] * 12 + [_SZ, _P, _P]),
     "moe_grouped_gate_up_w8": (_I32, [_I32] * 4 + [_P] * 12),
     "moe_grouped_down_w8": (_I32, [_I32] * 4 + [_P] * 9),
+    "moe_adapter_project": (_I32, [ctypes.POINTER(AdapterParams)] + [_P] * 11),
+    "moe_adapter_project_backward_workspace_size": (_SZ, [ctypes.POINTER(AdapterParams)]),
+    "moe_adapter_project_backward": (_I32, [ctypes.POINTER(AdapterParams)] + [_P] * 12 +
+                                     [_I32, _P, _SZ, _P, _P]),
+    "moe_grad_plan": (_I32, [_I32, ctypes.POINTER(GradTensor), _I32, ctypes.POINTER(_I64)]),
+    "moe_clip_grads_workspace_size": (_SZ, [_I32]),
+    "moe_clip_grads": (_I32, [_I32, _P, _I64, _I32, ctypes.c_float, _P, _P, _SZ, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -663,3 +691,47 @@ def moe_grouped_down_w8(n_seg, I, d, max_rows, hq, hs, seg_begin, seg_count, wd_
         n_seg, I, d, max_rows, _ptr(hq), _ptr(hs), _ptr(seg_begin), _ptr(seg_count), _ptr(wd_q),
         _ptr(wd_s), _ptr(y), _ptr(dev_status), _stream(stream)))
     _count(1 if max_rows > 0 else 0)
+
+
+def moe_adapter_project(p: AdapterParams, seg_offsets, seg_adapter, x, w, a, b, scale, u, y,
+                        dev_status=None, stream=None):
+    _check("moe_adapter_project", lib().moe_adapter_project(
+        ctypes.byref(p), _ptr(seg_offsets), _ptr(seg_adapter), _ptr(x), _ptr(w), _ptr(a), _ptr(b),
+        _ptr(scale), _ptr(u), _ptr(y), _ptr(dev_status), _stream(stream)))
+    _count(2 if p.T > 0 else 0)
+
+
+def moe_adapter_project_backward_workspace_size(p: AdapterParams) -> int:
+    return lib().moe_adapter_project_backward_workspace_size(ctypes.byref(p))
+
+
+def moe_adapter_project_backward(p: AdapterParams, seg_offsets, seg_adapter, x, w, a, b, scale, u,
+                                 dy, dx, da, db, accumulate, ws, ws_bytes, dev_status=None,
+                                 stream=None):
+    _check("moe_adapter_project_backward", lib().moe_adapter_project_backward(
+        ctypes.byref(p), _ptr(seg_offsets), _ptr(seg_adapter), _ptr(x), _ptr(w), _ptr(a), _ptr(b),
+        _ptr(scale), _ptr(u), _ptr(dy), _ptr(dx), _ptr(da), _ptr(db), accumulate, _ptr(ws),
+        ws_bytes, _ptr(dev_status), _stream(stream)))
+    if p.T > 0:
+        _count(int(dx is not None or da is not None) + sum(t is not None for t in (dx, da, db)))
+
+
+def moe_grad_plan(tensors, n_groups: int) -> int:
+    """tensors: a ctypes array of GradTensor on the host (first_chunk is filled in); returns
+    the number of chunks."""
+    chunks = ctypes.c_int64()
+    _check("moe_grad_plan", lib().moe_grad_plan(len(tensors), tensors, n_groups,
+                                                ctypes.byref(chunks)))
+    return chunks.value
+
+
+def moe_clip_grads_workspace_size(n_groups: int) -> int:
+    return lib().moe_clip_grads_workspace_size(n_groups)
+
+
+def moe_clip_grads(n_tensors, tensors, n_chunks, n_groups, max_norm, norms, ws, ws_bytes,
+                   dev_status=None, stream=None):
+    _check("moe_clip_grads", lib().moe_clip_grads(
+        n_tensors, _ptr(tensors), n_chunks, n_groups, max_norm, _ptr(norms), _ptr(ws), ws_bytes,
+        _ptr(dev_status), _stream(stream)))
+    _count(2 if n_chunks > 0 else 1)

@@ -1,0 +1,1031 @@
+// Low-rank adapters of many requests beside a shared projection, forward and backward.
+//
+//   u = s (x A^T)              y = round(x W + u B)
+//   v = s (dy B^T)             dx = round(dy W^T + v A)
+//   dA = sum_t v_t^T x_t       dB = sum_t u_t^T dy_t
+// with an adapter (A [r, d], B [r, n], s) or none for every segment of token rows.  u and v
+// are fp32, so an adapter's part of y is as exact as the projection itself.
+//
+// Three kernels serve both directions (A and B, d and n, x and dy change places):
+//   shrink   u: rows against the r rows of one table, reduction over the long side.
+//   project  y: the projection on the tensor cores, the adapter's part added before the one
+//            rounding.
+//   grads    dA, dB: the sums over an adapter's tokens.
+#include <algorithm>
+
+#include "smem.cuh"
+#include "umma.cuh"
+
+namespace moe {
+namespace {
+
+struct Segments {
+  const int32_t* offsets;  // [n_seg + 1], or nullptr: one segment of all rows
+  const int32_t* adapter;  // [n_seg]
+  int n_seg, T, n_adapters;
+};
+
+constexpr int kOutside = -2;  // a row of no segment
+constexpr int kNone = -1;     // a segment without an adapter
+
+__device__ __forceinline__ int seg_begin(const Segments& s, int q) {
+  return s.offsets == nullptr ? (q == 0 ? 0 : s.T) : __ldg(s.offsets + q);
+}
+
+// Rows [b, e) of segment q inside [0, T); empty where the offsets are out of order.
+__device__ __forceinline__ void seg_rows(const Segments& s, int q, int& b, int& e) {
+  b = max(seg_begin(s, q), 0);
+  e = min(seg_begin(s, q + 1), s.T);
+}
+
+// The last segment that starts at or before row t (0 if none does): with ordered offsets the
+// only one that can hold t.
+__device__ __forceinline__ int seg_of(const Segments& s, int t) {
+  int lo = 0, hi = s.n_seg - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seg_begin(s, mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Adapter of segment q; an id outside the tables counts as none.
+__device__ __forceinline__ int seg_adapter(const Segments& s, int q) {
+  const int a = __ldg(s.adapter + q);
+  return a >= 0 && a < s.n_adapters ? a : kNone;
+}
+
+// Adapter of row t, kNone, or kOutside.
+__device__ __forceinline__ int row_adapter(const Segments& s, int t) {
+  if (t >= s.T) return kOutside;
+  const int q = seg_of(s, t);
+  if (t < seg_begin(s, q) || t >= seg_begin(s, q + 1)) return kOutside;
+  return seg_adapter(s, q);
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// --------------------------------- shrink ------------------------------------
+//
+// One CTA (or a cluster, which splits the reduction) takes the segments j, j + J, ... of a
+// tile of 8 NB rows.  The table's rows are the M operand, the tokens N = 8 at a time, so a
+// segment of one token costs one column block and nothing is shared between segments.  Both
+// operands come from global memory as 16 bytes a lane: lane t of a row takes values
+// 8t .. 8t+7 of 32, and the MMA's slots are dealt from those in the same order on both sides
+// (a sum does not mind the order of its terms).
+
+constexpr int kShrinkWarps = 8;
+
+struct ShrinkArgs {
+  Segments seg;
+  int K, r;
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint16_t* table;  // [n_adapters, r, K]
+  const float* scale;     // [n_adapters]
+  float* u;               // [T, r]
+  int J;
+  uint32_t* dev_status;
+};
+
+template <int MB, int NB>
+struct Shrink {
+  static constexpr int kRankGroups = MB > 4 ? 2 : 1;  // warps that share the rows of the table
+  static constexpr int kMB = MB / kRankGroups;
+  static constexpr int kSlices = kShrinkWarps / kRankGroups;  // of the reduction
+  static constexpr int kRows = 8 * NB;
+  static constexpr int kElems = 16 * MB * kRows;
+  static constexpr int kSmem = kSlices * kElems * 4 + kElems * 4;
+};
+
+template <int MB, int NB>
+__global__ void __launch_bounds__(32 * kShrinkWarps)
+shrink_kernel(const ShrinkArgs a, int split) {
+  using P = Shrink<MB, NB>;
+  extern __shared__ float s_part[];            // [kSlices][16 MB][8 NB]
+  float* s_sum = s_part + P::kSlices * P::kElems;  // [16 MB][8 NB]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int row0 = static_cast<int>(blockIdx.x) / split * P::kRows;
+  const int row1 = min(row0 + P::kRows, a.seg.T);
+  const int group = warp % P::kRankGroups, slice = warp / P::kRankGroups;
+  const int chunks = (a.K + 31) / 32;
+  const int c0 = rank * chunks / split, c1 = (rank + 1) * chunks / split;
+
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the segment table, looked over once
+    for (int q = threadIdx.x; q < a.seg.n_seg; q += blockDim.x) {
+      const int b = seg_begin(a.seg, q), e = seg_begin(a.seg, q + 1);
+      if (b < 0 || e < b || e > a.seg.T) report(a.dev_status, MOE_DEV_BAD_MAP);
+      const int id = __ldg(a.seg.adapter + q);
+      if (id < kNone || id >= a.seg.n_adapters) report(a.dev_status, MOE_DEV_BAD_ADAPTER);
+    }
+  }
+
+  int nth = 0;
+  for (int q = seg_of(a.seg, row0); q < a.seg.n_seg && seg_begin(a.seg, q) < row1; ++q) {
+    int b, e;
+    seg_rows(a.seg, q, b, e);
+    b = max(b, row0);
+    e = min(e, row1);
+    if (b >= e) continue;
+    if (nth++ % a.J != static_cast<int>(blockIdx.y)) continue;
+    const int id = seg_adapter(a.seg, q);
+    if (id < 0) {
+      if (rank == 0)
+        for (int i = threadIdx.x; i < (e - b) * a.r; i += blockDim.x)
+          a.u[static_cast<int64_t>(b) * a.r + i] = 0.0f;
+      continue;
+    }
+    float acc[P::kMB][NB][4];
+#pragma unroll
+    for (int i = 0; i < P::kMB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.0f;
+    const uint16_t* tab = a.table + static_cast<int64_t>(id) * a.r * a.K;
+    const int m0 = group * P::kMB * 16;
+    for (int c = c0 + slice; c < c1; c += P::kSlices) {
+      const int k = c * 32 + 8 * t4;
+      const bool in = k < a.K;  // K is a multiple of 8
+      uint4 xv[NB];
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int row = row0 + 8 * j + g;
+        xv[j] = in && row >= b && row < e
+                    ? __ldg(reinterpret_cast<const uint4*>(a.x + row * a.x_stride + k))
+                    : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < P::kMB; ++i) {
+        const int m = m0 + 16 * i + g;
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        if (in && m < a.r)
+          lo = __ldg(reinterpret_cast<const uint4*>(tab + static_cast<int64_t>(m) * a.K + k));
+        if (in && m + 8 < a.r)
+          hi = __ldg(reinterpret_cast<const uint4*>(tab + static_cast<int64_t>(m + 8) * a.K + k));
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          mma_16816(acc[i][j], lo.x, hi.x, lo.y, hi.y, xv[j].x, xv[j].y);
+          mma_16816(acc[i][j], lo.z, hi.z, lo.w, hi.w, xv[j].z, xv[j].w);
+        }
+      }
+    }
+    // the slices of this CTA, then those of the cluster, in order
+    float* mine = s_part + slice * P::kElems;
+#pragma unroll
+    for (int i = 0; i < P::kMB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int m = m0 + 16 * i + g, n = 8 * j + 2 * t4;
+        *reinterpret_cast<float2*>(mine + m * P::kRows + n) = make_float2(acc[i][j][0], acc[i][j][1]);
+        *reinterpret_cast<float2*>(mine + (m + 8) * P::kRows + n) =
+            make_float2(acc[i][j][2], acc[i][j][3]);
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < P::kElems; i += blockDim.x) {
+      float v = s_part[i];
+#pragma unroll
+      for (int s = 1; s < P::kSlices; ++s) v += s_part[s * P::kElems + i];
+      s_sum[i] = v;
+    }
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+    const float scale = __ldg(a.scale + id);
+    const int n = (e - b) * a.r;
+    for (int i = rank * blockDim.x + threadIdx.x; i < n; i += split * blockDim.x) {
+      const int row = b + i / a.r, m = i % a.r;
+      const int at = m * P::kRows + row - row0;
+      float v = 0.0f;
+      if (split > 1) {
+        const uint32_t addr = smem_u32(s_sum + at);
+        for (int o = 0; o < split; ++o) v += ld_cluster(map_to_rank(addr, o));
+      } else {
+        v = s_sum[at];
+      }
+      a.u[static_cast<int64_t>(row) * a.r + m] = scale * v;
+    }
+    if (split > 1) cluster_sync();  // before the sums are written again, or given up
+    else __syncthreads();
+  }
+}
+
+// --------------------------------- project -----------------------------------
+//
+// D^T = W^T X^T: the weight's columns are the M operand (128 a CTA), the tokens N, so a
+// decode batch is a narrow tile and the weight streams once.  Tiles of TN tokens by 128
+// columns, two accumulator buffers in tensor memory.
+//   warp 0       TMA producer: [64 k x 128] of the weight (16 KB), [TN x 64 k] of x a stage
+//   warp 1       tensor memory; lane 0 issues four MMAs (K = 16) a stage
+//   warps 2..9   the adapters' part of the tile into shared memory (fp32, each token with its
+//                own adapter's rows, while the MMAs run), then the epilogue
+// S > 1: a cluster shares a tile, each CTA a part of the reduction; the CTA of rank c finishes
+// tokens [c TN / S, (c + 1) TN / S) and gets the others' sums through distributed shared
+// memory.  The weight and x are staged before shrink has ended; u is waited for.
+
+struct ProjectArgs {
+  Segments seg;
+  int K, N, r;
+  const float* u;         // [T, r]
+  const uint16_t* table;  // [n_adapters, r, N]
+  void* y;
+  int64_t y_stride;
+  int y_fp32;
+  int n_blocks, t_blocks, n_inner;
+  uint32_t* dev_status;
+};
+
+constexpr int kThreads = 320;
+constexpr int kWBytes = 128 * 64 * 2;
+constexpr int kWBox = 64 * 64 * 2;
+
+template <int TN, int S>
+struct Flat {
+  static constexpr int kStageBytes = kWBytes + TN * 128;
+  static constexpr int kStages = TN == 128 ? 4 : TN == 64 ? 7 : 9;
+  static constexpr int kOwn = TN / S;
+  // the adapters' part [kOwn][128], and the partners' sums [S - 1][kOwn / 4][128][4]
+  static constexpr int kPartBytes = TN * 128 * 4;
+  // full[st], empty[st], tfull[2], tempty[2], red, drain
+  static constexpr int kBars = 2 * kStages + 6;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kPartBytes + 32 * 8 + TN * 4 + 16;
+  static_assert(kBars <= 32 && kSmem <= 227 * 1024, "shared memory");
+  static_assert(kOwn % 4 == 0, "four tokens to a store");
+};
+
+__device__ __forceinline__ void put(const ProjectArgs& a, int row, int n, float v) {
+  const int64_t at = row * a.y_stride + n;
+  if (a.y_fp32) static_cast<float*>(a.y)[at] = v;
+  else static_cast<uint16_t*>(a.y)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+__device__ __forceinline__ void fma4(float4& acc, float u, const float4& b) {
+  acc.x = fmaf(u, b.x, acc.x);
+  acc.y = fmaf(u, b.y, acc.y);
+  acc.z = fmaf(u, b.z, acc.z);
+  acc.w = fmaf(u, b.w, acc.w);
+}
+
+// u B of C consecutive rows of one adapter, columns n .. n + 3 of this lane.
+template <int C>
+__device__ __forceinline__ void expand(const ProjectArgs& a, int id, int row, int lane, int n,
+                                       float4 (&acc)[4], int first) {
+  const uint16_t* tab = a.table + static_cast<int64_t>(id) * a.r * a.N + n;
+  const bool in = n < a.N;
+  for (int c = 0; c < a.r; c += 32) {
+    float u[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      u[i] = c + lane < a.r ? a.u[static_cast<int64_t>(row + i) * a.r + c + lane] : 0.0f;
+    const int m = min(32, a.r - c);  // a multiple of 8
+    for (int k = 0; k < m; k += 8) {
+      uint2 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = in ? __ldg(reinterpret_cast<const uint2*>(tab + static_cast<int64_t>(c + k + j) * a.N))
+                  : make_uint2(0, 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 b = make_float4(__uint_as_float(v[j].x << 16), __uint_as_float(v[j].x & 0xFFFF0000u),
+                                     __uint_as_float(v[j].y << 16), __uint_as_float(v[j].y & 0xFFFF0000u));
+#pragma unroll
+        for (int i = 0; i < C; ++i) fma4(acc[C == 4 ? i : first], __shfl_sync(0xFFFFFFFFu, u[i], k + j), b);
+      }
+    }
+  }
+}
+
+// Barrier of the 256 epilogue threads: true if all of them say so.
+__device__ __forceinline__ bool all_of_group(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
+
+template <int TN, int S, bool KMAJ>
+__global__ void __launch_bounds__(kThreads, 1)
+project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+               const ProjectArgs a) {
+  using F = Flat<TN, S>;
+  constexpr int kStages = F::kStages, kOwn = F::kOwn;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stage_base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* s_part = reinterpret_cast<float*>(stage_base + kStages * F::kStageBytes);  // [kOwn][128]
+  float4* s_red = reinterpret_cast<float4*>(s_part + kOwn * 128);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_part + TN * 128);
+  int* s_tok = reinterpret_cast<int*>(bars + 32);
+  volatile int* abort_flag = s_tok + TN;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_tok + TN + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = S > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
+  const int total = a.n_blocks * a.t_blocks;
+  const int steps = (a.K + 63) / 64;
+  const int k0 = rank * steps / S, k1 = (rank + 1) * steps / S;
+
+  auto full_bar = [&](int s) { return smem_u32(bars + s); };
+  auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
+  auto tfull_bar = [&](int b) { return smem_u32(bars + 2 * kStages + b); };
+  auto tempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 2 + b); };
+  const uint32_t red_bar = smem_u32(bars + 2 * kStages + 4);
+  const uint32_t drain_bar = smem_u32(bars + 2 * kStages + 5);
+  auto tile = [&](int t, int& row0, int& n0) {
+    const int nb = a.n_inner ? t % a.n_blocks : t / a.t_blocks;
+    const int tb = a.n_inner ? t / a.n_blocks : t % a.t_blocks;
+    row0 = tb * TN;
+    n0 = nb * 128;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 8);
+    }
+    mbar_init(red_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (S > 1) mbar_arrive_expect_tx(red_bar, (S - 1) * kOwn * 128 * 4);
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+  }
+  if (warp == 1) umma_alloc(smem_u32(tmem_slot), 2 * TN);
+  umma_fence_before();
+  if constexpr (S > 1) cluster_sync();  // the partners' barriers are initialised
+  else __syncthreads();
+  umma_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool awaited = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step) {
+        int row0, n0;
+        tile(t, row0, n0);
+        for (int k = k0; k < k1; ++k) {
+          if (!wait_bounded(empty_bar(s), ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
+          const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
+          mbar_arrive_expect_tx(full_bar(s), F::kStageBytes);
+          if (KMAJ) {
+            tma_load_2d(st, &map_w, full_bar(s), k * 64, n0);
+          } else {
+            tma_load_2d(st, &map_w, full_bar(s), n0, k * 64);
+            tma_load_2d(st + kWBox, &map_w, full_bar(s), n0 + 64, k * 64);
+          }
+          tma_load_2d(st + kWBytes, &map_x, full_bar(s), k * 64, row0);
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (!ok) {  // copies in flight land before the shared memory is given up
+        for (int i = 0; i < kStages; ++i) {
+          if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+          wait_drain(full_bar(s), ph);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = umma_idesc_bf16(128, TN, !KMAJ);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true, issued = false;
+      for (int t = first; t < total && ok; t += step) {
+        if (!wait_bounded(tempty_bar(buf), acc_ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
+        umma_fence_after();
+        for (int k = k0; k < k1; ++k) {
+          if (!wait_bounded(full_bar(s), ph, abort_flag, a.dev_status)) { ok = false; break; }
+          umma_fence_after();
+          const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem + buf * TN,
+                      KMAJ ? umma_desc(st + kk * 32) : umma_desc_mn(st + kk * 16 * 128, kWBox),
+                      umma_desc(st + kWBytes + kk * 32), idesc, k > k0 || kk > 0);
+          issued = true;
+          umma_commit(empty_bar(s));
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        umma_commit(tfull_bar(buf));
+        if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
+      }
+      if (!ok && issued) {
+        umma_commit(drain_bar);
+        wait_drain(drain_bar, 0);
+      }
+    }
+  } else {
+    pdl_wait();  // u
+    const int w = warp - 2, quad = warp & 3, half = w >> 2;
+    const int tid = threadIdx.x - 64;
+    const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    int buf = 0;
+    uint32_t acc_ph = 0;
+    for (int t = first; t < total; t += step) {
+      int row0, n0;
+      tile(t, row0, n0);
+      if (tid < TN) s_tok[tid] = row_adapter(a.seg, row0 + tid);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      // ---- the adapters' part of this CTA's tokens ----
+      for (int j = 4 * w; j < kOwn; j += 32) {
+        int id[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) id[i] = s_tok[rank * kOwn + j + i];
+        float4 acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int row = row0 + rank * kOwn + j;
+        if (id[0] >= 0 && id[0] == id[1] && id[0] == id[2] && id[0] == id[3]) {
+          expand<4>(a, id[0], row, lane, n0 + 4 * lane, acc, 0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (id[i] >= 0) expand<1>(a, id[i], row + i, lane, n0 + 4 * lane, acc, i);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(s_part + (j + i) * 128 + 4 * lane) = acc[i];
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      // ---- epilogue: this thread's column of the weight, TN / 2 tokens ----
+      bool ok =
+          __all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar(buf), acc_ph, abort_flag, a.dev_status));
+      umma_fence_after();
+      const uint32_t ta = taddr0 + buf * TN + half * (TN / 2);
+      const int m = quad * 32 + lane, n = n0 + m;
+      if constexpr (S > 1) {
+        awaited = true;
+        // the partners' tokens first
+#pragma unroll
+        for (int c = 0; c < TN / 2; c += 16) {
+          if (!ok) break;
+          uint32_t v[16];
+          umma_ld16(ta + c, v);
+          umma_ld_wait(v);
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const int j = half * (TN / 2) + c + i, owner = j / kOwn;
+            if (owner == rank) continue;
+            const int from = (rank - owner + S) % S - 1;
+            const uint32_t dst = map_to_rank(
+                smem_u32(s_red + (from * (kOwn / 4) + (j - owner * kOwn) / 4) * 128 + m), owner);
+            st_async4(dst, map_to_rank(red_bar, owner), __uint_as_float(v[i]),
+                      __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+          }
+        }
+        ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded<true>(red_bar, 0, abort_flag, a.dev_status));
+      }
+#pragma unroll
+      for (int c = 0; c < TN / 2; c += 16) {
+        if (!ok) break;
+        if (S > 1 && (half * (TN / 2) + c + 16 <= rank * kOwn || half * (TN / 2) + c >= (rank + 1) * kOwn))
+          continue;
+        uint32_t v[16];
+        umma_ld16(ta + c, v);
+        umma_ld_wait(v);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const int j = half * (TN / 2) + c + i - rank * kOwn;  // among this CTA's tokens
+          if (S > 1 && (j < 0 || j >= kOwn)) continue;
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(v[i + e]);
+          if constexpr (S > 1) {
+            for (int o = 0; o < S - 1; ++o) {
+              const float4 p = s_red[(o * (kOwn / 4) + j / 4) * 128 + m];
+              f[0] += p.x; f[1] += p.y; f[2] += p.z; f[3] += p.w;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n < a.N && s_tok[rank * kOwn + j + e] != kOutside)
+              put(a, row0 + rank * kOwn + j + e, n, f[e] + s_part[(j + e) * 128 + m]);
+        }
+      }
+      umma_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty_bar(buf));
+      if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
+      // s_tok and s_part are free; a warp that gave up takes the others along
+      if (!all_of_group(ok)) break;
+    }
+  }
+
+  // ---- teardown ----
+  __syncwarp();
+  umma_fence_before();
+  if constexpr (S > 1) {
+    cluster_sync();  // no CTA leaves while a partner may still reach it
+    // (after a wait that gave up: nor before the sums that were on their way)
+    if (threadIdx.x == 64 && awaited && *abort_flag) wait_drain(red_bar, 0);
+  } else {
+    __syncthreads();
+  }
+  umma_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    umma_dealloc(tmem, 2 * TN);
+  }
+  pdl_trigger();
+}
+
+// ---------------------------------- grads ------------------------------------
+//
+// D_a[m, k] = sum over a's tokens of p[t, m] q[t, k], p fp32 [T, r] (u or v), q bf16 (dy or x).
+// A CTA takes one adapter and 128 columns (a cluster: parts of the adapter's tokens, added in
+// order).  p goes into the MMA as two bf16 numbers, the value and what its rounding left, so
+// the gradient keeps 16 bits of p.  Rows of other segments are never loaded: zeros stand in
+// their place in both operands.
+
+struct GradArgs {
+  Segments seg;
+  int K, r;
+  const float* p;
+  const uint16_t* q;
+  int64_t q_stride;
+  float* out;  // [n_adapters, r, K]
+  int accumulate;
+};
+
+constexpr int kGradTokens = 32;
+constexpr int kGradCols = 128;
+constexpr int kGradStages = 3;
+constexpr int kGradRow = kGradCols * 2 + 16;  // bytes of a staged row of q
+
+template <int MB>
+struct Grad {
+  static constexpr int kPRow = 16 * MB + 4;  // floats of a staged row of p
+  static constexpr int kStageBytes = kGradTokens * (kGradRow + kPRow * 4);
+  static constexpr int kSum = 16 * MB * kGradCols * 4;
+  static constexpr int kSmem = kGradStages * kStageBytes > kSum ? kGradStages * kStageBytes : kSum;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+
+template <int MB>
+__global__ void __launch_bounds__(256)
+grads_kernel(const GradArgs a, int split) {
+  using P = Grad<MB>;
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int col0 = static_cast<int>(blockIdx.x) / split * kGradCols;
+  const int id = blockIdx.y;
+  pdl_wait();
+  pdl_trigger();
+
+  // the adapter's tokens, in order of its segments: this CTA's part of them
+  int64_t count = 0;
+  for (int q0 = 0; q0 < a.seg.n_seg; q0 += 32) {
+    int n = 0;
+    if (q0 + lane < a.seg.n_seg && __ldg(a.seg.adapter + q0 + lane) == id) {
+      int b, e;
+      seg_rows(a.seg, q0 + lane, b, e);
+      n = max(e - b, 0);
+    }
+    count += __reduce_add_sync(0xFFFFFFFFu, n);
+  }
+  const int64_t part0 = count * rank / split, part1 = count * (rank + 1) / split;
+
+  float acc[MB][2][4];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.0f;
+
+  // The pieces of kGradTokens rows, one after the other (every warp walks the same table):
+  // `next` finds the next one.
+  int q = -1, b = 0, e = 0, cand = 0;
+  uint32_t mask = 0;
+  int q_base = -32;
+  int64_t seen = 0;  // tokens of the adapter before the current segment
+  auto next = [&](int& row, int& rows) {
+    while (true) {
+      if (b < e) {
+        row = b;
+        rows = min(e - b, kGradTokens);
+        b += rows;
+        return true;
+      }
+      while (mask == 0) {
+        q_base += 32;
+        if (q_base >= a.seg.n_seg) return false;
+        cand = q_base + lane < a.seg.n_seg ? __ldg(a.seg.adapter + q_base + lane) : -1;
+        mask = __ballot_sync(0xFFFFFFFFu, cand == id);
+      }
+      q = q_base + __ffs(mask) - 1;
+      mask &= mask - 1;
+      seg_rows(a.seg, q, b, e);
+      if (e <= b) { e = b; continue; }
+      const int n = e - b;
+      const int64_t from = part0 > seen ? part0 - seen : 0, to = part1 - seen;
+      seen += n;
+      e = b + static_cast<int>(to < n ? (to > 0 ? to : 0) : n);
+      b += static_cast<int>(from < n ? from : n);
+    }
+  };
+  auto stage_ptr = [&](int s) { return s_raw + s * P::kStageBytes; };
+  auto load = [&](int s, int row, int rows) {
+    uint8_t* st = stage_ptr(s);
+    for (int i = threadIdx.x; i < kGradTokens * (kGradCols / 8); i += 256) {
+      const int t = i / (kGradCols / 8), c = i % (kGradCols / 8) * 8;
+      const bool live = t < rows && col0 + c < a.K;
+      cp_async16(smem_u32(st + t * kGradRow + c * 2),
+                 live ? a.q + (row + t) * a.q_stride + col0 + c : a.q, live);
+    }
+    uint8_t* sp = st + kGradTokens * kGradRow;
+    for (int i = threadIdx.x; i < kGradTokens * 4 * MB; i += 256) {
+      const int t = i / (4 * MB), m = i % (4 * MB) * 4;
+      const bool live = t < rows && m < a.r;
+      cp_async16(smem_u32(sp + (t * P::kPRow + m) * 4),
+                 live ? a.p + static_cast<int64_t>(row + t) * a.r + m : a.p, live);
+    }
+  };
+  int ahead = 0;  // pieces staged and not yet used
+  bool more = count > 0;
+  for (int s = 0; s < kGradStages - 1; ++s) {
+    int row, rows;
+    if (more && (more = next(row, rows))) {
+      load(s, row, rows);
+      ++ahead;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  int s = 0;
+  while (ahead > 0) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kGradStages - 2) : "memory");
+    __syncthreads();
+    {
+      int row, rows;
+      if (more && (more = next(row, rows))) {
+        load((s + kGradStages - 1) % kGradStages, row, rows);
+        ++ahead;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    const uint8_t* st = stage_ptr(s);
+    const float* sp = reinterpret_cast<const float*>(st + kGradTokens * kGradRow);
+#pragma unroll
+    for (int kk = 0; kk < kGradTokens / 16; ++kk) {
+      // q: tokens x 16 columns of this warp, transposed on the way
+      uint32_t bq[4];
+      const uint32_t addr = smem_u32(st + (kk * 16 + (lane & 15)) * kGradRow + (warp * 16 + (lane >> 4) * 8) * 2);
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(bq[0]), "=r"(bq[1]), "=r"(bq[2]), "=r"(bq[3])
+                   : "r"(addr)
+                   : "memory");
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int m = 16 * i + g + (v & 1) * 8, t = kk * 16 + 2 * t4 + (v >> 1) * 8;
+          const float f0 = sp[t * P::kPRow + m], f1 = sp[(t + 1) * P::kPRow + m];
+          hi[v] = pack_bf16x2(f0, f1);
+          lo[v] = pack_bf16x2(f0 - __uint_as_float(hi[v] << 16),
+                              f1 - __uint_as_float(hi[v] & 0xFFFF0000u));
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          mma_16816(acc[i][j], hi[0], hi[1], hi[2], hi[3], bq[2 * j], bq[2 * j + 1]);
+          mma_16816(acc[i][j], lo[0], lo[1], lo[2], lo[3], bq[2 * j], bq[2 * j + 1]);
+        }
+      }
+    }
+    --ahead;
+    s = (s + 1) % kGradStages;
+    __syncthreads();
+  }
+
+  float* out = a.out + static_cast<int64_t>(id) * a.r * a.K;
+  if (split > 1 && count > 0) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float* s_sum = reinterpret_cast<float*>(s_raw);  // [16 MB][128]
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int m = 16 * i + g, c = warp * 16 + 8 * j + 2 * t4;
+        *reinterpret_cast<float2*>(s_sum + m * kGradCols + c) = make_float2(acc[i][j][0], acc[i][j][1]);
+        *reinterpret_cast<float2*>(s_sum + (m + 8) * kGradCols + c) =
+            make_float2(acc[i][j][2], acc[i][j][3]);
+      }
+    cluster_sync();
+    for (int i = rank * 256 + threadIdx.x; i < a.r * kGradCols; i += split * 256) {
+      const int m = i / kGradCols, c = i % kGradCols;
+      const uint32_t addr = smem_u32(s_sum + i);
+      float v = 0.0f;
+      for (int o = 0; o < split; ++o) v += ld_cluster(map_to_rank(addr, o));
+      if (col0 + c < a.K) {
+        float* dst = out + static_cast<int64_t>(m) * a.K + col0 + c;
+        *dst = a.accumulate ? *dst + v : v;
+      }
+    }
+    cluster_sync();
+    return;
+  }
+  if (rank > 0 || (count == 0 && a.accumulate)) return;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int m = 16 * i + g + 8 * h, c = col0 + warp * 16 + 8 * j + 2 * t4;
+        if (m < a.r && c < a.K) {
+          float2* dst = reinterpret_cast<float2*>(out + static_cast<int64_t>(m) * a.K + c);
+          float2 v = make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+          if (a.accumulate) {
+            const float2 old = *dst;
+            v.x += old.x;
+            v.y += old.y;
+          }
+          *dst = v;
+        }
+      }
+}
+
+// ------------------------------- host side -----------------------------------
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// bf16 [rows, cols] with `stride` values from row to row, boxes of box_rows x 64 values.
+bool map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t stride,
+            uint32_t box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {stride * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The library's launch, with clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+void launch_clustered(void (*kern)(KArgs...), dim3 grid, int threads, int smem, int cluster,
+                      cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+int pow2_at_most(int64_t v, int most) {
+  int p = 1;
+  while (2 * p <= v && 2 * p <= most) p *= 2;
+  return p;
+}
+
+template <int MB, int NB>
+moe_status launch_shrink_as(ShrinkArgs a, cudaStream_t s) {
+  using P = Shrink<MB, NB>;
+  auto kern = shrink_kernel<MB, NB>;
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (!opt_in(kern, P::kSmem, mu, done)) return MOE_ERR_CUDA;
+  const int64_t tiles = ceil_div(a.seg.T, P::kRows);
+  const int64_t per_tile = ceil_div(static_cast<int64_t>(a.seg.n_seg) * P::kRows, a.seg.T);
+  a.J = static_cast<int>(std::min<int64_t>(P::kRows, std::max<int64_t>(1, per_tile)));
+  const int split = pow2_at_most(std::min<int64_t>(4 * sm_count() / (tiles * a.J), a.K / 256), 8);
+  launch_clustered(kern, dim3(static_cast<unsigned>(tiles * split), a.J), 32 * kShrinkWarps, P::kSmem,
+                   split, s, a, split);
+  return launch_status();
+}
+
+moe_status launch_shrink(const ShrinkArgs& a, cudaStream_t s) {
+  const bool narrow = a.seg.T <= 256;
+  const int mb = (a.r + 15) / 16;
+  if (mb == 1) return narrow ? launch_shrink_as<1, 1>(a, s) : launch_shrink_as<1, 4>(a, s);
+  if (mb == 2) return narrow ? launch_shrink_as<2, 1>(a, s) : launch_shrink_as<2, 4>(a, s);
+  if (mb <= 4) return narrow ? launch_shrink_as<4, 1>(a, s) : launch_shrink_as<4, 4>(a, s);
+  return narrow ? launch_shrink_as<8, 1>(a, s) : launch_shrink_as<8, 4>(a, s);
+}
+
+template <int TN, int S, bool KMAJ>
+moe_status launch_project_as(ProjectArgs a, const void* x, int64_t x_stride, const void* w,
+                             cudaStream_t s) {
+  using F = Flat<TN, S>;
+  auto kern = project_kernel<TN, S, KMAJ>;
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (!opt_in(kern, F::kSmem, mu, done)) return MOE_ERR_CUDA;
+  CUtensorMap mw, mx;
+  // the weight is [K, N] (rows of N), or for the backward [N, K]
+  if (!(KMAJ ? map_2d(&mw, w, a.N, a.K, a.K, 128) : map_2d(&mw, w, a.K, a.N, a.N, 64)) ||
+      !map_2d(&mx, x, a.seg.T, a.K, x_stride, TN))
+    return MOE_ERR_CUDA;
+  a.n_blocks = static_cast<int>(ceil_div(a.N, 128));
+  a.t_blocks = static_cast<int>(ceil_div(a.seg.T, TN));
+  a.n_inner = 0;
+  const int64_t tiles = static_cast<int64_t>(a.n_blocks) * a.t_blocks;
+  const unsigned grid = static_cast<unsigned>(S > 1 ? S * tiles : std::min<int64_t>(tiles, sm_count()));
+  launch_clustered(kern, dim3(grid), kThreads, F::kSmem, S, s, mw, mx, a);
+  return launch_status();
+}
+
+template <bool KMAJ>
+moe_status launch_project(const ProjectArgs& a, const void* x, int64_t x_stride, const void* w,
+                          cudaStream_t s) {
+  const int64_t tiles = ceil_div(a.N, 128);
+  const int steps = (a.K + 63) / 64;
+  if (a.seg.T <= 32) {
+    const int split = pow2_at_most(std::min<int64_t>(sm_count() / tiles, steps), 8);
+    if (split == 8) return launch_project_as<32, 8, KMAJ>(a, x, x_stride, w, s);
+    if (split == 4) return launch_project_as<32, 4, KMAJ>(a, x, x_stride, w, s);
+    if (split == 2) return launch_project_as<32, 2, KMAJ>(a, x, x_stride, w, s);
+    return launch_project_as<32, 1, KMAJ>(a, x, x_stride, w, s);
+  }
+  if (a.seg.T <= 128) {
+    const int split = pow2_at_most(std::min<int64_t>(sm_count() / tiles, steps), 8);
+    if (split == 8) return launch_project_as<128, 8, KMAJ>(a, x, x_stride, w, s);
+    if (split == 4) return launch_project_as<128, 4, KMAJ>(a, x, x_stride, w, s);
+    if (split == 2) return launch_project_as<128, 2, KMAJ>(a, x, x_stride, w, s);
+  }
+  return launch_project_as<128, 1, KMAJ>(a, x, x_stride, w, s);
+}
+
+template <int MB>
+moe_status launch_grads_as(const GradArgs& a, cudaStream_t s) {
+  using P = Grad<MB>;
+  auto kern = grads_kernel<MB>;
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (!opt_in(kern, P::kSmem, mu, done)) return MOE_ERR_CUDA;
+  const int64_t blocks = ceil_div(a.K, kGradCols);
+  const int64_t active = std::min(a.seg.n_adapters, a.seg.n_seg);
+  const int split =
+      pow2_at_most(std::min<int64_t>(4 * sm_count() / (blocks * active), a.seg.T / 256), 8);
+  launch_clustered(kern, dim3(static_cast<unsigned>(blocks * split), a.seg.n_adapters), 256, P::kSmem,
+                   split, s, a, split);
+  return launch_status();
+}
+
+moe_status launch_grads(const GradArgs& a, cudaStream_t s) {
+  const int mb = (a.r + 15) / 16;
+  if (mb == 1) return launch_grads_as<1>(a, s);
+  if (mb == 2) return launch_grads_as<2>(a, s);
+  if (mb <= 4) return launch_grads_as<4>(a, s);
+  return launch_grads_as<8>(a, s);
+}
+
+constexpr int64_t kMaxStride = int64_t(1) << 31;
+
+// Sizes, strides and types of one call.
+moe_status check_params(const moe_adapter_params* p) {
+  if (p == nullptr || p->T < 0 || p->d <= 0 || p->n <= 0 || p->r <= 0 || p->n_adapters <= 0 ||
+      p->n_seg <= 0 || p->x_stride < p->d || p->y_stride < p->n ||
+      (p->y_type != MOE_DTYPE_BF16 && p->y_type != MOE_DTYPE_FP32))
+    return MOE_ERR_INVALID_ARG;
+  if (p->d % 8 != 0 || p->n % 8 != 0 || p->r % 8 != 0 || p->d > 65536 || p->n > 65536 ||
+      p->r > 128 || p->n_adapters > 65535 || p->n_seg > 65535 || p->T > INT32_MAX - 1024 ||
+      p->x_stride % 8 != 0 || p->y_stride % 8 != 0 || p->x_stride > kMaxStride ||
+      p->y_stride > kMaxStride)
+    return MOE_ERR_UNSUPPORTED;
+  // tile numbers are 32-bit
+  if (ceil_div(p->T, 8) * ceil_div(std::max(p->d, p->n), 128) >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_tables(const moe_adapter_params* p, const int32_t* seg_offsets,
+                        const int32_t* seg_adapter, const void* x, const void* w, const void* a,
+                        const void* b, const float* scale, const float* u) {
+  if (seg_adapter == nullptr || (seg_offsets == nullptr && p->n_seg != 1) || x == nullptr ||
+      w == nullptr || a == nullptr || b == nullptr || scale == nullptr || u == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(a) || !aligned16(b) || !aligned16(u) ||
+      !aligned4(scale) || !aligned4(seg_offsets) || !aligned4(seg_adapter))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+Segments segments_of(const moe_adapter_params* p, const int32_t* seg_offsets,
+                     const int32_t* seg_adapter) {
+  return Segments{seg_offsets, seg_adapter, p->n_seg, p->T, p->n_adapters};
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API moe_status moe_adapter_project(const moe_adapter_params* p, const int32_t* seg_offsets,
+                                       const int32_t* seg_adapter, const moe_bf16* x,
+                                       const moe_bf16* w, const moe_bf16* a, const moe_bf16* b,
+                                       const float* scale, float* u, void* y,
+                                       uint32_t* dev_status, moe_stream_t stream) {
+  moe_status st = check_params(p);
+  if (st != MOE_OK || p->T == 0) return st;
+  st = check_tables(p, seg_offsets, seg_adapter, x, w, a, b, scale, u);
+  if (st != MOE_OK) return st;
+  if (y == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(y)) return MOE_ERR_UNSUPPORTED;
+  const Segments seg = segments_of(p, seg_offsets, seg_adapter);
+  const cudaStream_t s = as_cuda(stream);
+  st = launch_shrink(ShrinkArgs{seg, p->d, p->r, x, p->x_stride, a, scale, u, 1, dev_status}, s);
+  if (st != MOE_OK) return st;
+  return launch_project<false>(ProjectArgs{seg, p->d, p->n, p->r, u, b, y, p->y_stride,
+                                           p->y_type == MOE_DTYPE_FP32, 0, 0, 0, dev_status},
+                               x, p->x_stride, w, s);
+}
+
+MOE_API size_t moe_adapter_project_backward_workspace_size(const moe_adapter_params* p) {
+  if (check_params(p) != MOE_OK) return 0;
+  return std::max<size_t>(static_cast<size_t>(p->T) * p->r * 4, 16);  // v
+}
+
+MOE_API moe_status moe_adapter_project_backward(
+    const moe_adapter_params* p, const int32_t* seg_offsets, const int32_t* seg_adapter,
+    const moe_bf16* x, const moe_bf16* w, const moe_bf16* a, const moe_bf16* b, const float* scale,
+    const float* u, const moe_bf16* dy, moe_bf16* dx, float* da, float* db, int32_t accumulate,
+    void* ws, size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream) {
+  moe_status st = check_params(p);
+  if (st != MOE_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  if (dx == nullptr && da == nullptr && db == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dx) || !aligned16(da) || !aligned16(db)) return MOE_ERR_UNSUPPORTED;
+  const cudaStream_t s = as_cuda(stream);
+  if (p->T == 0) {  // no tokens: zero gradients
+    if (accumulate) return MOE_OK;
+    if (da != nullptr && cudaMemsetAsync(da, 0, size_t(4) * p->n_adapters * p->r * p->d, s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    if (db != nullptr && cudaMemsetAsync(db, 0, size_t(4) * p->n_adapters * p->r * p->n, s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  st = check_tables(p, seg_offsets, seg_adapter, x, w, a, b, scale, u);
+  if (st != MOE_OK) return st;
+  if (dy == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(ws)) return MOE_ERR_UNSUPPORTED;
+  if (ws_bytes < moe_adapter_project_backward_workspace_size(p)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const Segments seg = segments_of(p, seg_offsets, seg_adapter);
+  float* v = static_cast<float*>(ws);
+  if (dx != nullptr || da != nullptr) {
+    st = launch_shrink(ShrinkArgs{seg, p->n, p->r, dy, p->y_stride, b, scale, v, 1, dev_status}, s);
+    if (st != MOE_OK) return st;
+  }
+  if (dx != nullptr) {
+    st = launch_project<true>(ProjectArgs{seg, p->n, p->d, p->r, v, a, dx, p->d, 0, 0, 0, 0, dev_status},
+                              dy, p->y_stride, w, s);
+    if (st != MOE_OK) return st;
+  }
+  if (da != nullptr) {
+    st = launch_grads(GradArgs{seg, p->d, p->r, v, x, p->x_stride, da, accumulate}, s);
+    if (st != MOE_OK) return st;
+  }
+  if (db != nullptr) return launch_grads(GradArgs{seg, p->n, p->r, u, dy, p->y_stride, db, accumulate}, s);
+  return MOE_OK;
+}

@@ -1,0 +1,334 @@
+// Gradient norms over groups of many tensors, and the tensors scaled to a largest norm.
+//
+//   norm_g = sqrt(sum x^2 over g's tensors),  c_g = min(1, max_norm / (norm_g + 1e-6))
+//   out = round(x c_g)
+//
+// Bound: HBM (the tensors twice in, once out, less what the second pass finds in the L2).
+// The elements of all tensors are one line of chunks (of kChunk elements, none across two
+// tensors), cut into as many equal parts as there are blocks.  Tensors of a group stand
+// together, so the pairs (block, group) that occur form a staircase along the line and b + g
+// numbers them without gaps or clashes: each block writes the sum of its part of group g to
+// partial[b + g], and whoever needs norm g adds the entries of g's blocks, always in the same
+// order.  No atomics, no counters: the same bits on every run, and nothing to clear.  The
+// second pass walks every part backwards: its end is what the first pass read last.
+//
+// Squares are summed in fp32 over a thread's 32 values of a chunk and in fp64 from there on;
+// where those 32 squares leave fp32's range (values beyond 2^60 or below 2^-40) the values are
+// scaled by a power of two first, so any finite tensor has its norm.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kChunk = 8192;  // elements; a power of two
+constexpr int kMaxBlocks = 1024;
+
+struct ClipArgs {
+  const moe_grad_tensor* tensors;
+  int n_tensors, n_groups;
+  int64_t n_chunks;
+  double* partial;  // [gridDim.x + n_groups - 1]
+  float max_norm;
+  float* norms;
+  uint32_t* dev_status;
+};
+
+// The last tensor whose first chunk is at or before c: the one that holds it (tensors without
+// elements have no chunk and are passed over).
+__device__ __forceinline__ int tensor_of(const ClipArgs& a, int64_t c) {
+  int lo = 0, hi = a.n_tensors - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.tensors[mid].first_chunk <= c) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int64_t part_begin(int64_t b, int64_t chunks, int64_t parts) {
+  return b * chunks / parts;
+}
+// The part that holds chunk c: the last b with part_begin(b) <= c.
+__device__ __forceinline__ int part_of(int64_t c, int64_t chunks, int64_t parts) {
+  return static_cast<int>(((c + 1) * parts + chunks - 1) / chunks - 1);
+}
+
+// One chunk of a tensor: `head` elements up to a 16-byte boundary of the source, `vecs` vectors
+// of 16 bytes, `tail` elements.
+template <typename T>
+struct Piece {
+  static constexpr int kPer = 16 / sizeof(T);
+  const T* src;
+  int head, vecs, tail;
+  __device__ __forceinline__ Piece(const moe_grad_tensor& t, int64_t chunk) {
+    const int64_t at = (chunk - t.first_chunk) * kChunk;
+    const int n = static_cast<int>(min(t.count - at, static_cast<int64_t>(kChunk)));
+    src = static_cast<const T*>(t.grad) + at;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
+    head = min(n, (kPer - off) % kPer);
+    vecs = (n - head) / kPer;
+    tail = n - head - vecs * kPer;
+  }
+};
+
+__device__ __forceinline__ float value(uint16_t v) { return bf16_bits_to_float(v); }
+__device__ __forceinline__ float value(float v) { return v; }
+
+__device__ __forceinline__ void spread(const uint4& v, float (&f)[8]) { unpack8(v, f); }
+__device__ __forceinline__ void spread(const uint4& v, float (&f)[4]) {
+  f[0] = __uint_as_float(v.x);
+  f[1] = __uint_as_float(v.y);
+  f[2] = __uint_as_float(v.z);
+  f[3] = __uint_as_float(v.w);
+}
+
+// Sum of squares of this thread's share of a chunk.
+template <typename T>
+__device__ __forceinline__ double squares(const moe_grad_tensor& t, int64_t chunk) {
+  constexpr int kPer = Piece<T>::kPer;
+  constexpr int kVecs = kChunk / kPer / kBlock;  // vectors a thread, at most
+  const Piece<T> p(t, chunk);
+  const uint4* body = reinterpret_cast<const uint4*>(p.src + p.head);
+  uint4 v[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int j = i * kBlock + threadIdx.x;
+    v[i] = j < p.vecs ? __ldg(body + j) : make_uint4(0, 0, 0, 0);
+  }
+  // the elements beside the vectors: fewer than 2 kPer
+  float edge = 0.0f;
+  if (static_cast<int>(threadIdx.x) < p.head) edge = value(p.src[threadIdx.x]);
+  else if (static_cast<int>(threadIdx.x) < p.head + p.tail)
+    edge = value(p.src[p.vecs * kPer + threadIdx.x]);
+  auto sum = [&](float k) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float f[kPer];
+      spread(v[i], f);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) s[e & 3] = fmaf(f[e] * k, f[e] * k, s[e & 3]);
+    }
+    s[0] = fmaf(edge * k, edge * k, s[0]);
+    return (s[0] + s[1]) + (s[2] + s[3]);
+  };
+  const float s = sum(1.0f);
+  if (s > 0x1p-80f && s < 0x1p126f) return static_cast<double>(s);
+  if (s >= 0x1p126f) return static_cast<double>(sum(0x1p-75f)) * 0x1p150;
+  return static_cast<double>(sum(0x1p100f)) * 0x1p-200;  // (a NaN stays one)
+}
+
+// Sum over the block, the same in every thread.
+__device__ __forceinline__ double block_sum(double v, double* s_warp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  __syncthreads();  // the last sum has been read
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kBlock / 32; ++i) s += s_warp[i];
+  return s;
+}
+
+__global__ void __launch_bounds__(kBlock) grad_squares_kernel(const ClipArgs a) {
+  __shared__ double s_warp[kBlock / 32];
+  const int64_t c0 = part_begin(blockIdx.x, a.n_chunks, gridDim.x);
+  const int64_t c1 = part_begin(blockIdx.x + 1, a.n_chunks, gridDim.x);
+  pdl_wait();
+  pdl_trigger();  // the grid is resident as a whole
+  double sum = 0.0;
+  int ti = tensor_of(a, c0);
+  moe_grad_tensor t = a.tensors[ti];
+  int group = t.group;
+  for (int64_t c = c0; c < c1; ++c) {
+    while (ti + 1 < a.n_tensors && a.tensors[ti + 1].first_chunk <= c) t = a.tensors[++ti];
+    if (t.group != group) {
+      const double s = block_sum(sum, s_warp);
+      if (threadIdx.x == 0) a.partial[blockIdx.x + group] = s;
+      sum = 0.0;
+      group = t.group;
+    }
+    sum += t.type == MOE_DTYPE_BF16 ? squares<uint16_t>(t, c) : squares<float>(t, c);
+  }
+  const double s = block_sum(sum, s_warp);
+  if (threadIdx.x == 0) a.partial[blockIdx.x + group] = s;
+}
+
+// The first tensor of group g or a later one, or n_tensors.
+__device__ __forceinline__ int first_of_group(const ClipArgs& a, int g) {
+  int lo = 0, hi = a.n_tensors;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.tensors[mid].group < g) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+
+// Norm of group g, by the whole block.
+__device__ __forceinline__ float group_norm(const ClipArgs& a, int g, double* s_warp) {
+  const int i0 = first_of_group(a, g), i1 = first_of_group(a, g + 1);
+  const int64_t c0 = i0 < a.n_tensors ? a.tensors[i0].first_chunk : a.n_chunks;
+  const int64_t c1 = i1 < a.n_tensors ? a.tensors[i1].first_chunk : a.n_chunks;
+  double v = 0.0;
+  if (c0 < c1) {
+    const int b0 = part_of(c0, a.n_chunks, gridDim.x), b1 = part_of(c1 - 1, a.n_chunks, gridDim.x);
+    for (int b = b0 + threadIdx.x; b <= b1; b += kBlock) v += a.partial[b + g];
+  }
+  return static_cast<float>(sqrt(block_sum(v, s_warp)));
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 join(const float (&f)[Piece<T>::kPer]);
+template <>
+__device__ __forceinline__ uint4 join<float>(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
+}
+template <>
+__device__ __forceinline__ uint4 join<uint16_t>(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(uint16_t* p, float v) {
+  *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_chunk(const moe_grad_tensor& t, int64_t chunk, float k) {
+  constexpr int kPer = Piece<T>::kPer;
+  constexpr int kVecs = kChunk / kPer / kBlock;
+  const Piece<T> p(t, chunk);
+  T* dst = static_cast<T*>(t.out) + (chunk - t.first_chunk) * kChunk;
+  const uint4* body = reinterpret_cast<const uint4*>(p.src + p.head);
+  T* out = dst + p.head;
+  const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+  uint4 v[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int j = i * kBlock + threadIdx.x;
+    if (j < p.vecs) v[i] = body[j];
+  }
+  int at = -1;
+  if (static_cast<int>(threadIdx.x) < p.head) at = threadIdx.x;
+  else if (static_cast<int>(threadIdx.x) < p.head + p.tail) at = p.vecs * kPer + threadIdx.x;
+  if (at >= 0) put(dst + at, value(p.src[at]) * k);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int j = i * kBlock + threadIdx.x;
+    if (j >= p.vecs) break;
+    float f[kPer];
+    spread(v[i], f);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) f[e] *= k;
+    if (aligned) {
+      reinterpret_cast<uint4*>(out)[j] = join<T>(f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) put(out + j * kPer + e, f[e]);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kBlock) grad_scale_kernel(const ClipArgs a) {
+  __shared__ double s_warp[kBlock / 32];
+  const int64_t c0 = part_begin(blockIdx.x, a.n_chunks, gridDim.x);
+  const int64_t c1 = part_begin(blockIdx.x + 1, a.n_chunks, gridDim.x);
+  pdl_wait();
+  for (int g = blockIdx.x; g < a.n_groups; g += gridDim.x) {
+    const float norm = group_norm(a, g, s_warp);
+    if (threadIdx.x == 0) {
+      a.norms[g] = norm;
+      if (!(norm < __int_as_float(0x7F800000))) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
+    }
+  }
+  int ti = -1, group = -1;
+  float k = 1.0f;
+  moe_grad_tensor t;
+  for (int64_t c = c1 - 1; c >= c0; --c) {
+    if (ti < 0 || t.first_chunk > c) {
+      ti = tensor_of(a, c);
+      t = a.tensors[ti];
+    }
+    if (t.group != group) {
+      group = t.group;
+      const float norm = group_norm(a, group, s_warp);
+      const float q = __fdiv_rn(a.max_norm, norm + 1e-6f);
+      k = q > 1.0f ? 1.0f : q;  // (a NaN stays one)
+    }
+    if (k == 1.0f && t.grad == t.out) continue;  // in place, and as it should be
+    if (t.type == MOE_DTYPE_BF16) scale_chunk<uint16_t>(t, c, k);
+    else scale_chunk<float>(t, c, k);
+  }
+  pdl_trigger();
+}
+
+// No elements at all: every norm is zero.
+__global__ void __launch_bounds__(kBlock) zero_norms_kernel(int n_groups, float* norms) {
+  pdl_wait();
+  for (int g = threadIdx.x; g < n_groups; g += kBlock) norms[g] = 0.0f;
+  pdl_trigger();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API moe_status moe_grad_plan(int32_t n_tensors, moe_grad_tensor* tensors, int32_t n_groups,
+                                 int64_t* n_chunks) {
+  if (n_tensors < 0 || n_groups <= 0 || n_chunks == nullptr || (n_tensors > 0 && tensors == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (n_groups > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    moe_grad_tensor& t = tensors[i];
+    if (t.count < 0 || (t.type != MOE_DTYPE_BF16 && t.type != MOE_DTYPE_FP32) || t.group < 0 ||
+        t.group >= n_groups || (i > 0 && t.group < tensors[i - 1].group) ||
+        (t.count > 0 && (t.grad == nullptr || t.out == nullptr)))
+      return MOE_ERR_INVALID_ARG;
+    const uintptr_t size = t.type == MOE_DTYPE_BF16 ? 2 : 4;
+    if (t.count > 0 && (reinterpret_cast<uintptr_t>(t.grad) % size != 0 ||
+                        reinterpret_cast<uintptr_t>(t.out) % size != 0))
+      return MOE_ERR_UNSUPPORTED;
+    if (t.count > (int64_t(1) << 50)) return MOE_ERR_UNSUPPORTED;
+    t.first_chunk = chunks;
+    chunks += ceil_div(t.count, kChunk);
+    if (chunks > (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+  }
+  *n_chunks = chunks;
+  return MOE_OK;
+}
+
+MOE_API size_t moe_clip_grads_workspace_size(int32_t n_groups) {
+  return n_groups <= 0 ? 0 : 8 * (static_cast<size_t>(kMaxBlocks) + n_groups);
+}
+
+MOE_API moe_status moe_clip_grads(int32_t n_tensors, const moe_grad_tensor* tensors,
+                                  int64_t n_chunks, int32_t n_groups, float max_norm, float* norms,
+                                  void* ws, size_t ws_bytes, uint32_t* dev_status,
+                                  moe_stream_t stream) {
+  if (n_tensors < 0 || n_chunks < 0 || n_groups <= 0 || !(max_norm > 0.0f) || norms == nullptr ||
+      (n_chunks > 0 && (n_tensors == 0 || tensors == nullptr || ws == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (n_groups > (1 << 20) || n_chunks > (int64_t(1) << 40) ||
+      (reinterpret_cast<uintptr_t>(tensors) & 7u) != 0 || (reinterpret_cast<uintptr_t>(ws) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(norms) & 3u) != 0)
+    return MOE_ERR_UNSUPPORTED;
+  const cudaStream_t s = as_cuda(stream);
+  if (n_chunks == 0) {
+    launch(zero_norms_kernel, dim3(1), dim3(kBlock), 0, s, n_groups, norms);
+    return launch_status();
+  }
+  if (ws_bytes < moe_clip_grads_workspace_size(n_groups)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const ClipArgs a{tensors, n_tensors, n_groups, n_chunks, static_cast<double*>(ws), max_norm, norms,
+                   dev_status};
+  const unsigned grid = static_cast<unsigned>(
+      std::min<int64_t>(n_chunks, std::min<int64_t>(4 * sm_count(), kMaxBlocks)));
+  launch(grad_squares_kernel, dim3(grid), dim3(kBlock), 0, s, a);
+  launch(grad_scale_kernel, dim3(grid), dim3(kBlock), 0, s, a);
+  return launch_status();
+}

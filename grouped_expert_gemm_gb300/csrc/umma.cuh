@@ -1,6 +1,6 @@
-// Tensor-core (tcgen05) wrappers of the 8-bit grouped product, inline PTX for
-// sm_103a: tensor-memory allocation, MMA on E4M3 operands in shared memory,
-// commits, accumulator loads, and the matrix descriptors.
+// Tensor-core (tcgen05) wrappers of the 8-bit grouped product and of the projection
+// with adapters, inline PTX for sm_103a: tensor-memory allocation, MMA on E4M3 or bf16
+// operands in shared memory, commits, accumulator loads, and the matrix descriptors.
 #pragma once
 
 #include "tma.cuh"
@@ -52,6 +52,24 @@ __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_
       : "memory");
 }
 
+// D (+)= A B on bf16 operands in shared memory, K = 16 per instruction.
+__device__ __forceinline__ void umma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f16: fp32 accumulate, bf16 A and B, B K-major, A K-major or
+// M-major (a_mn), M = m, N = n.
+__host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool a_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
 // Instruction descriptor, kind::f8f6f4: fp32 accumulate, E4M3 A and B, both
 // K-major, M = m, N = n.
 __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int m, int n) {
@@ -62,6 +80,13 @@ __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int m, int n) {
 // rows = 1024 bytes), version 1.
 __device__ __forceinline__ uint64_t umma_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The same for an M-major tile made of boxes of 64 M values (128 bytes) by some K rows:
+// `box` bytes from one 64 of M to the next, eight K rows = 1024 bytes.
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t addr, uint32_t box) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(box >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 

@@ -59,7 +59,8 @@ enum {
   MOE_DEV_BAD_ROW = 8u,         /* a map entry outside the row space; skipped        */
   MOE_DEV_TIMEOUT = 16u,        /* a bounded pipeline wait gave up; output invalid   */
   MOE_DEV_NONFINITE_INPUT = 32u, /* a NaN/Inf activation met by moe_quantize_fp8     */
-  MOE_DEV_BAD_MAP = 64u          /* a moe_validate_* call found a broken invariant    */
+  MOE_DEV_BAD_MAP = 64u,         /* a moe_validate_* call found a broken invariant    */
+  MOE_DEV_BAD_ADAPTER = 128u     /* an adapter id outside [-1, n_adapters)            */
 };
 
 #define MOE_POOL_EMPTY 0xFFFFu /* header element of an unused pool row */
@@ -832,6 +833,101 @@ moe_status moe_grouped_down_w8(int32_t n_seg, int32_t I, int32_t d, int32_t max_
                                const moe_fp8* hq, const float* hs, const int32_t* seg_begin,
                                const int32_t* seg_count, const moe_fp8* wd_q, const float* wd_s,
                                moe_bf16* y, uint32_t* dev_status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Low-rank adapters of many requests beside a shared projection            */
+/* ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t T;          /* token rows                                             */
+  int32_t d, n;       /* x [T, d], y [T, n]                                     */
+  int32_t r;          /* rank of the tables; a lower one is padded with zeros   */
+  int32_t n_adapters; /* adapters in the tables                                 */
+  int32_t n_seg;      /* segments of rows                                       */
+  int32_t y_type;     /* MOE_DTYPE_* of y (dy is bf16)                          */
+  int64_t x_stride;   /* elements from one row of x to the next (>= d)          */
+  int64_t y_stride;   /* elements from one row of y, or dy, to the next (>= n)  */
+} moe_adapter_params;
+
+/* A projection that all requests share, and each request's own low-rank change to it:
+ * segment q holds rows [seg_offsets[q], seg_offsets[q+1]) (int32 device array of n_seg + 1
+ * non-decreasing entries in [0, T]; NULL: one segment of all rows) and has adapter
+ * seg_adapter[q] (int32 device array; -1: none).  For the rows t of a segment with adapter e
+ *   u[t] = scale[e] * (x[t] a[e]^T)          fp32 [T, r]; zero rows without an adapter
+ *   y[t] = round(x[t] w + u[t] b[e])         one rounding, to y_type
+ * with x, w [d, n], a [n_adapters, r, d], b [n_adapters, r, n] bf16 and scale fp32
+ * [n_adapters].  Products are of bf16 numbers (u enters as fp32, or as the sum of two bf16
+ * numbers that holds 16 bits of it), sums fp32.  Rows of no segment are left as they are, in u
+ * and in y.  A segment may be empty, and several may name one adapter.  A row's result depends
+ * on its own x, w and its own adapter only: a NaN or Inf in one adapter's tables or in one
+ * row stays with the rows that use it.
+ * fp32 y [T, E] of w [d, E] are router logits as moe_route takes them.
+ * Offsets out of order or range set MOE_DEV_BAD_MAP (results unspecified, nothing outside
+ * the arrays is touched); an adapter outside [-1, n_adapters) sets MOE_DEV_BAD_ADAPTER and
+ * counts as none.  A bounded wait that gives up sets MOE_DEV_TIMEOUT (outputs invalid).
+ * The call enqueues two kernels; the second one reads x and w before the first has ended, so
+ * nothing enqueued after the first may write them (the call itself enqueues both).
+ * Limits: d, n, r % 8 == 0, d, n <= 65536, r <= 128, n_adapters, n_seg <= 65535, strides % 8
+ * == 0; 16-byte aligned x, w, a, b, u and y.  T = 0 does nothing.  y must not overlap the
+ * inputs.                                                                     */
+moe_status moe_adapter_project(const moe_adapter_params* p, const int32_t* seg_offsets,
+                               const int32_t* seg_adapter, const moe_bf16* x, const moe_bf16* w,
+                               const moe_bf16* a, const moe_bf16* b, const float* scale, float* u,
+                               void* y, uint32_t* dev_status, moe_stream_t stream);
+
+/* Its backward with a frozen w.  From dy [T, n] bf16 (rows y_stride apart), and x, u of the
+ * forward with the same segments:
+ *   v[t]  = scale[e] * (dy[t] b[e]^T)                fp32, in the workspace
+ *   dx[t] = bf16(dy[t] w^T + v[t] a[e])              [T, d] contiguous; NULL: left out
+ *   da[e] = sum over e's rows of v[t]^T x[t]         fp32 [n_adapters, r, d]; NULL: left out
+ *   db[e] = sum over e's rows of u[t]^T dy[t]        fp32 [n_adapters, r, n]; NULL: left out
+ * da and db are written for every adapter (zeros for one without rows), or with accumulate = 1
+ * added to.  They are summed in an order that the sizes and segments fix: the same bits on
+ * every run.  Rows of no segment of dx are left as they are.  scale has no gradient.
+ * ws: moe_adapter_project_backward_workspace_size() bytes (0 = invalid parameters), 16-byte
+ * aligned; calls, and replays of graphs that captured them, that overlap on the GPU must not
+ * share it.  T = 0 writes zero gradients (accumulate = 0).  16-byte aligned dy, dx, da and db;
+ * other limits and errors as the forward.                                    */
+size_t moe_adapter_project_backward_workspace_size(const moe_adapter_params* p);
+moe_status moe_adapter_project_backward(
+    const moe_adapter_params* p, const int32_t* seg_offsets, const int32_t* seg_adapter,
+    const moe_bf16* x, const moe_bf16* w, const moe_bf16* a, const moe_bf16* b, const float* scale,
+    const float* u, const moe_bf16* dy, moe_bf16* dx, float* da, float* db, int32_t accumulate,
+    void* ws, size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gradient norms over many tensors, and clipping                           */
+/* ------------------------------------------------------------------------ */
+typedef struct {
+  const void* grad;    /* device, contiguous                                     */
+  void* out;           /* device: grad itself, or apart from every gradient      */
+  int64_t count;       /* elements                                               */
+  int32_t type;        /* MOE_DTYPE_* of both                                    */
+  int32_t group;       /* whose norm it counts in; non-decreasing over the table */
+  int64_t first_chunk; /* written by moe_grad_plan                               */
+} moe_grad_tensor;
+
+/* Checks a table of n_tensors on the HOST (it may be copied to the device as it is
+ * afterwards), fills in first_chunk and returns the number of chunks.  Tensors of a group
+ * stand together; a tensor may have no elements (its addresses may then be NULL), and a group
+ * no tensors.  Addresses must be aligned to their type.                       */
+moe_status moe_grad_plan(int32_t n_tensors, moe_grad_tensor* tensors, int32_t n_groups,
+                         int64_t* n_chunks);
+
+/* One norm per group and the tensors scaled to it, with a planned table on the DEVICE:
+ *   norms[g] = sqrt(sum of squares over g's tensors)            fp32 [n_groups]
+ *   c_g = min(1, max_norm / (norms[g] + 1e-6)),  out = round(grad * c_g), to the tensor's type
+ * A tensor in place whose c_g is 1 is not written.  Sums of squares are held in fp64 (over 32
+ * values at a time fp32, scaled where they leave its range), in an order that the table and
+ * the GPU fix: the same bits on every run.  A norm that is not finite in fp32 sets
+ * MOE_DEV_NONFINITE_INPUT; the formula is followed (NaN: NaN everywhere in the group, Inf:
+ * zeros, and NaN where the gradient was infinite).
+ * max_norm > 0 (infinity: norms alone matter).  ws: moe_clip_grads_workspace_size(n_groups)
+ * bytes, 8-byte aligned, no state kept in it between calls; calls, and replays of graphs that
+ * captured them, that overlap on the GPU must not share it.  Limits: n_groups <= 2^20.      */
+size_t moe_clip_grads_workspace_size(int32_t n_groups);
+moe_status moe_clip_grads(int32_t n_tensors, const moe_grad_tensor* tensors, int64_t n_chunks,
+                          int32_t n_groups, float max_norm, float* norms, void* ws,
+                          size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
 
 /* Self-test of the bounded pipeline wait used by the tensor-core kernels: one
  * CTA initialises an mbarrier that nothing arrives at and waits on it with the
