@@ -228,136 +228,158 @@ shrink_kernel(const ShrinkArgs a, int split) {
 
 // --------------------------------- project -----------------------------------
 //
-// D^T = W^T X^T: the weight's columns are the M operand (128 a CTA), the tokens N, so a
-// decode batch is a narrow tile and the weight streams once.  Tiles of TN tokens by 128
-// columns, two accumulator buffers in tensor memory.
-//   warp 0       TMA producer: [64 k x 128] of the weight (16 KB), [TN x 64 k] of x a stage
+// D^T = W^T X^T: the weight's columns are the M operand, the tokens N, so a decode batch is a
+// narrow tile and the weight streams once.  Roles of the 352 threads:
+//   warp 0       TMA producer: [64 k x 128] of the weight (16 KB) and [tokens x 64 k] of x
 //   warp 1       tensor memory; lane 0 issues four MMAs (K = 16) a stage
-//   warps 2..9   the adapters' part of the tile into shared memory (fp32, each token with its
-//                own adapter's rows, while the MMAs run), then the epilogue
-// S > 1: a cluster shares a tile, each CTA a part of the reduction; the CTA of rank c finishes
-// tokens [c TN / S, (c + 1) TN / S) and gets the others' sums through distributed shared
-// memory.  The weight and x are staged before shrink has ended; u is waited for.
+//   warps 2..9   epilogue: warp (quad, sub) has the 16 weight columns at 32 quad + 16 sub
+//   warp 10      the tile's runs of rows with one adapter, and the runs' tables by TMA
+// The adapters' part is a product of mma.sync in the epilogue: u B is r / d of the work and a
+// run may be one token long, where tcgen05's narrowest tile is 16 columns by 128 rows of the
+// table.  tcgen05's 16x256b loads give the accumulators in mma.sync's own layout, 16 weight
+// columns by 8 tokens at a time, so a run's table (transposed by ldmatrix into registers, once a
+// run) is multiplied with the u of the 8 tokens onto the sums themselves.  Where several runs
+// meet in 8 tokens every column takes the result of its own run: nothing of one request, not
+// even 0 times an infinity, reaches another's rows.  u enters as two bf16 numbers.
+//
+// Shapes (choose_shape has the rule):
+//   pair   a cluster of two CTAs, 256 weight columns by 256 tokens (cta_group::2), two
+//          accumulator buffers that fill the tensor memory
+//   flat   one CTA, 128 weight columns by TN = 64 or 128 tokens; the adapters' part is made
+//          while the MMAs run and waits in tensor memory.  S > 1: a cluster shares a tile, each
+//          CTA a part of the reduction; the CTA of rank c finishes its S-th of the tokens and
+//          gets the others' sums through distributed shared memory.
+// fp32 results of long reductions are summed in pieces of kPiece: the tensor cores' own fp32
+// sums lose 2^-26 a step (7168: 8e-6 of the result, in pieces of 1024 1e-6).
+// The weight, x and the tables are staged before shrink has ended; u is waited for.
 
 struct ProjectArgs {
   Segments seg;
   int K, N, r;
-  const float* u;         // [T, r]
-  const uint16_t* table;  // [n_adapters, r, N]
+  const float* u;  // [T, r]
   void* y;
   int64_t y_stride;
   int y_fp32;
   int n_blocks, t_blocks, n_inner;
+  int slots;  // of the tables
   uint32_t* dev_status;
 };
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kWBytes = 128 * 64 * 2;
 constexpr int kWBox = 64 * 64 * 2;
+constexpr int kPiece = 16;      // steps of 64 to a piece of an fp32 result's reduction
+constexpr int kMaxSlots = 16;
+constexpr int kMaxRank = 128;
 
-template <int TN, int S>
-struct Flat {
-  static constexpr int kStageBytes = kWBytes + TN * 128;
-  static constexpr int kStages = TN == 128 ? 4 : TN == 64 ? 7 : 9;
+template <int TN, int S, int CG>
+struct Shape {
+  static constexpr int kStageBytes = kWBytes + TN / CG * 128;
+  static constexpr int kStages = CG == 2 ? 6 : TN == 128 ? (S >= 4 ? 3 : 4) : 5;
   static constexpr int kOwn = TN / S;
-  // the adapters' part [kOwn][128], and the partners' sums [S - 1][kOwn / 4][128][4]
-  static constexpr int kPartBytes = TN * 128 * 4;
-  // full[st], empty[st], tfull[2], tempty[2], red, drain
-  static constexpr int kBars = 2 * kStages + 6;
-  static constexpr int kSmem = 1024 + kStages * kStageBytes + kPartBytes + 32 * 8 + TN * 4 + 16;
-  static_assert(kBars <= 32 && kSmem <= 227 * 1024, "shared memory");
-  static_assert(kOwn % 4 == 0, "four tokens to a store");
+  static constexpr int kTableBytes = (CG == 2 ? 32 : 64) * 1024;
+  static constexpr int kRedBytes = (S - 1) * kOwn * 512;  // [S - 1][kOwn / 8][8][32] float4
+  // full[st], empty[st], tfull[2], tempty[2], jfull[2], jempty[2], tbfull[], tbempty[], red, drain
+  static constexpr int kBars = 2 * kStages + 8 + 2 * kMaxSlots + 2;
+  static constexpr int kTmem = CG == 2 ? 2 * TN : 4 * TN;  // two buffers, (flat) the sums
+  static constexpr int kSmem =
+      1024 + kStages * kStageBytes + kTableBytes + kRedBytes + kBars * 8 + 2 * kOwn * 2 + 16;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kOwn % 8 == 0 && kTmem <= 512, "shape");
+  static_assert(kTableBytes >= 256 * kMaxRank, "one table at least");
 };
 
-__device__ __forceinline__ void put(const ProjectArgs& a, int row, int n, float v) {
-  const int64_t at = row * a.y_stride + n;
-  if (a.y_fp32) static_cast<float*>(a.y)[at] = v;
-  else static_cast<uint16_t*>(a.y)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+// The table of one run in registers, and its place in the ring.
+struct Table {
+  uint32_t f[kMaxRank / 16][4];
+  int run;        // whose table f holds
+  int slot;
+  uint32_t ph;
+};
+
+__device__ __forceinline__ void load_u(const ProjectArgs& a, int64_t row, bool live, int t4,
+                                       float2 (&u)[kMaxRank / 16][2]) {
+  const float* p = a.u + row * a.r + 2 * t4;
+#pragma unroll
+  for (int k = 0; k < kMaxRank / 16; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (16 * k < a.r)
+        u[k][h] = live && 16 * k + 8 * h < a.r ? *reinterpret_cast<const float2*>(p + 16 * k + 8 * h)
+                                               : make_float2(0.0f, 0.0f);
 }
 
-__device__ __forceinline__ void fma4(float4& acc, float u, const float4& b) {
-  acc.x = fmaf(u, b.x, acc.x);
-  acc.y = fmaf(u, b.y, acc.y);
-  acc.z = fmaf(u, b.z, acc.z);
-  acc.w = fmaf(u, b.w, acc.w);
-}
-
-// u B of C consecutive rows of one adapter, columns n .. n + 3 of this lane.
-template <int C>
-__device__ __forceinline__ void expand(const ProjectArgs& a, int id, int row, int lane, int n,
-                                       float4 (&acc)[4], int first) {
-  const uint16_t* tab = a.table + static_cast<int64_t>(id) * a.r * a.N + n;
-  const bool in = n < a.N;
-  for (int c = 0; c < a.r; c += 32) {
-    float u[C];
+// Stores 16 weight columns from n by 8 tokens from row (the layout of umma_ld_frag).
+__device__ __forceinline__ void put_frag(const ProjectArgs& a, const float (&c)[4], int row, int n,
+                                         const int16_t* run, int lane) {
+  const int g = lane >> 2, t4 = lane & 3;
+  if (a.y_fp32) {
+    float* y = static_cast<float*>(a.y) + static_cast<int64_t>(row) * a.y_stride + n + g;
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-      u[i] = c + lane < a.r ? a.u[static_cast<int64_t>(row + i) * a.r + c + lane] : 0.0f;
-    const int m = min(32, a.r - c);  // a multiple of 8
-    for (int k = 0; k < m; k += 8) {
-      uint2 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = in ? __ldg(reinterpret_cast<const uint2*>(tab + static_cast<int64_t>(c + k + j) * a.N))
-                  : make_uint2(0, 0);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 b = make_float4(__uint_as_float(v[j].x << 16), __uint_as_float(v[j].x & 0xFFFF0000u),
-                                     __uint_as_float(v[j].y << 16), __uint_as_float(v[j].y & 0xFFFF0000u));
-#pragma unroll
-        for (int i = 0; i < C; ++i) fma4(acc[C == 4 ? i : first], __shfl_sync(0xFFFFFFFFu, u[i], k + j), b);
+    for (int e = 0; e < 2; ++e)
+      if (run[2 * t4 + e] != kOutside) {
+        if (n < a.N) y[(2 * t4 + e) * a.y_stride] = c[e];
+        if (n + 8 < a.N) y[(2 * t4 + e) * a.y_stride + 8] = c[2 + e];
       }
-    }
+    return;
   }
+  // rows become tokens: two 8 x 8 blocks transposed, then 4 columns to a lane
+  uint32_t d0 = pack_bf16x2(c[0], c[1]), d1 = pack_bf16x2(c[2], c[3]);
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(d0));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(d1));
+  const bool odd = t4 & 1;
+  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? d0 : d1, 1);
+  const int col = n + (odd ? 8 + 2 * (t4 - 1) : 2 * t4);
+  if (col < a.N && run[g] != kOutside)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + static_cast<int64_t>(row + g) * a.y_stride +
+                              col) = odd ? make_uint2(other, d1) : make_uint2(d0, other);
 }
 
-// Barrier of the 256 epilogue threads: true if all of them say so.
-__device__ __forceinline__ bool all_of_group(bool ok) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, 256, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"(ok ? 1u : 0u)
-      : "memory");
-  return all != 0;
-}
-
-template <int TN, int S, bool KMAJ>
+template <int TN, int S, int CG, bool KMAJ>
 __global__ void __launch_bounds__(kThreads, 1)
 project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-               const ProjectArgs a) {
-  using F = Flat<TN, S>;
+               const __grid_constant__ CUtensorMap map_t, const ProjectArgs a) {
+  using F = Shape<TN, S, CG>;
+  static_assert(CG == 1 || S == 1, "one kind of cluster");
   constexpr int kStages = F::kStages, kOwn = F::kOwn;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stage_base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* s_part = reinterpret_cast<float*>(stage_base + kStages * F::kStageBytes);  // [kOwn][128]
-  float4* s_red = reinterpret_cast<float4*>(s_part + kOwn * 128);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_part + TN * 128);
-  int* s_tok = reinterpret_cast<int*>(bars + 32);
-  volatile int* abort_flag = s_tok + TN;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_tok + TN + 1);
+  uint8_t* s_table = stage_base + kStages * F::kStageBytes;
+  uint8_t* s_red = s_table + F::kTableBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_red + F::kRedBytes);
+  int16_t* s_run = reinterpret_cast<int16_t*>(bars + F::kBars);  // [2][kOwn]
+  volatile int* abort_flag = reinterpret_cast<int*>(s_run + 2 * kOwn);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_run + 2 * kOwn) + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = S > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int first = static_cast<int>(blockIdx.x) / S, step = static_cast<int>(gridDim.x) / S;
+  constexpr int kCluster = S * CG;
+  const int rank = kCluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const bool leader = CG == 1 || rank == 0;
+  const int first = static_cast<int>(blockIdx.x) / kCluster;
+  const int step = static_cast<int>(gridDim.x) / kCluster;
   const int total = a.n_blocks * a.t_blocks;
   const int steps = (a.K + 63) / 64;
-  const int k0 = rank * steps / S, k1 = (rank + 1) * steps / S;
+  const int k0 = S > 1 ? rank * steps / S : 0, k1 = S > 1 ? (rank + 1) * steps / S : steps;
+  const int piece = CG == 1 && a.y_fp32 ? kPiece : steps;
+  const int rp = (a.r + 15) & ~15;
+  const int own0 = S > 1 ? rank * kOwn : 0;  // this CTA's tokens of the tile
 
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
   auto tfull_bar = [&](int b) { return smem_u32(bars + 2 * kStages + b); };
   auto tempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 2 + b); };
-  const uint32_t red_bar = smem_u32(bars + 2 * kStages + 4);
-  const uint32_t drain_bar = smem_u32(bars + 2 * kStages + 5);
+  auto jfull_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 4 + b); };
+  auto jempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 6 + b); };
+  auto tbfull_bar = [&](int s) { return smem_u32(bars + 2 * kStages + 8 + s); };
+  auto tbempty_bar = [&](int s) { return smem_u32(bars + 2 * kStages + 8 + kMaxSlots + s); };
+  const uint32_t red_bar = smem_u32(bars + 2 * kStages + 8 + 2 * kMaxSlots);
+  const uint32_t drain_bar = red_bar + 8;
+  // first token and first weight column of this CTA's part of tile t
   auto tile = [&](int t, int& row0, int& n0) {
     const int nb = a.n_inner ? t % a.n_blocks : t / a.t_blocks;
     const int tb = a.n_inner ? t / a.n_blocks : t % a.t_blocks;
     row0 = tb * TN;
-    n0 = nb * 128;
+    n0 = nb * 128 * CG + (CG == 2 ? rank * 128 : 0);
   };
 
   if (threadIdx.x == 0) {
@@ -367,195 +389,376 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
-      mbar_init(tempty_bar(b), 8);
+      mbar_init(tempty_bar(b), 8 * CG);  // one arrival per epilogue warp
+      mbar_init(jfull_bar(b), 1);
+      mbar_init(jempty_bar(b), 8);
+    }
+    for (int s = 0; s < kMaxSlots; ++s) {
+      mbar_init(tbfull_bar(s), 1);
+      mbar_init(tbempty_bar(s), 8);
     }
     mbar_init(red_bar, 1);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (S > 1) mbar_arrive_expect_tx(red_bar, (S - 1) * kOwn * 128 * 4);
+    if (S > 1) mbar_arrive_expect_tx(red_bar, F::kRedBytes);
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_t)) : "memory");
   }
-  if (warp == 1) umma_alloc(smem_u32(tmem_slot), 2 * TN);
+  if (warp == 1) {
+    if constexpr (CG == 2) umma_alloc_pair(smem_u32(tmem_slot), F::kTmem);
+    else umma_alloc(smem_u32(tmem_slot), F::kTmem);
+  }
   umma_fence_before();
-  if constexpr (S > 1) cluster_sync();  // the partners' barriers are initialised
-  else __syncthreads();
+  __syncthreads();
+  if constexpr (kCluster > 1) cluster_sync();  // the partners' barriers are initialised
   umma_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool awaited = false;
 
   if (warp == 0) {
     if (lane == 0) {
+      // ---- TMA producer ----
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = first; t < total && ok; t += step) {
         int row0, n0;
         tile(t, row0, n0);
+        if (CG == 2) row0 += rank * (TN / 2);
         for (int k = k0; k < k1; ++k) {
           if (!wait_bounded(empty_bar(s), ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
           const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
-          mbar_arrive_expect_tx(full_bar(s), F::kStageBytes);
-          if (KMAJ) {
-            tma_load_2d(st, &map_w, full_bar(s), k * 64, n0);
+          if constexpr (CG == 2) {
+            const uint32_t bar = map_to_rank(full_bar(s), 0);
+            if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * F::kStageBytes);
+            if (KMAJ) {
+              tma_load_2d_pair(st, &map_w, bar, k * 64, n0);
+            } else {
+              tma_load_2d_pair(st, &map_w, bar, n0, k * 64);
+              tma_load_2d_pair(st + kWBox, &map_w, bar, n0 + 64, k * 64);
+            }
+            tma_load_2d_pair(st + kWBytes, &map_x, bar, k * 64, row0);
           } else {
-            tma_load_2d(st, &map_w, full_bar(s), n0, k * 64);
-            tma_load_2d(st + kWBox, &map_w, full_bar(s), n0 + 64, k * 64);
+            mbar_arrive_expect_tx(full_bar(s), F::kStageBytes);
+            if (KMAJ) {
+              tma_load_2d(st, &map_w, full_bar(s), k * 64, n0);
+            } else {
+              tma_load_2d(st, &map_w, full_bar(s), n0, k * 64);
+              tma_load_2d(st + kWBox, &map_w, full_bar(s), n0 + 64, k * 64);
+            }
+            tma_load_2d(st + kWBytes, &map_x, full_bar(s), k * 64, row0);
           }
-          tma_load_2d(st + kWBytes, &map_x, full_bar(s), k * 64, row0);
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
       }
       if (!ok) {  // copies in flight land before the shared memory is given up
-        for (int i = 0; i < kStages; ++i) {
-          if (--s < 0) { s = kStages - 1; ph ^= 1u; }
-          wait_drain(full_bar(s), ph);
+        if (leader) {
+          for (int i = 0; i < kStages; ++i) {
+            if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+            wait_drain(full_bar(s), ph);
+          }
+        } else {  // they are counted on the leader's barriers: a fixed window
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < 2000000ull) {
+          }
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = umma_idesc_bf16(128, TN, !KMAJ);
+    if (lane == 0 && leader) {
+      // ---- MMA issuer ----
+      constexpr uint32_t idesc = umma_idesc_bf16(128 * CG, TN, !KMAJ);
       int s = 0, buf = 0;
       uint32_t ph = 0, acc_ph = 0;
       bool ok = true, issued = false;
       for (int t = first; t < total && ok; t += step) {
-        if (!wait_bounded(tempty_bar(buf), acc_ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
-        umma_fence_after();
-        for (int k = k0; k < k1; ++k) {
-          if (!wait_bounded(full_bar(s), ph, abort_flag, a.dev_status)) { ok = false; break; }
+        for (int kp = k0; kp < k1 && ok; kp += piece) {
+          if (!wait_bounded(tempty_bar(buf), acc_ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
           umma_fence_after();
-          const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
+          const int ke = min(kp + piece, k1);
+          for (int k = kp; k < ke; ++k) {
+            if (!wait_bounded(full_bar(s), ph, abort_flag, a.dev_status)) { ok = false; break; }
+            umma_fence_after();
+            const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem + buf * TN,
-                      KMAJ ? umma_desc(st + kk * 32) : umma_desc_mn(st + kk * 16 * 128, kWBox),
-                      umma_desc(st + kWBytes + kk * 32), idesc, k > k0 || kk > 0);
-          issued = true;
-          umma_commit(empty_bar(s));
-          if (++s == kStages) { s = 0; ph ^= 1u; }
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ad = KMAJ ? umma_desc(st + kk * 32) : umma_desc_mn(st + kk * 16 * 128, kWBox);
+              const uint64_t bd = umma_desc(st + kWBytes + kk * 32);
+              if constexpr (CG == 2) umma_bf16_pair(tmem + buf * TN, ad, bd, idesc, k > kp || kk > 0);
+              else umma_bf16(tmem + buf * TN, ad, bd, idesc, k > kp || kk > 0);
+            }
+            issued = true;
+            if constexpr (CG == 2) umma_commit_pair(empty_bar(s), 0x3);
+            else umma_commit(empty_bar(s));
+            if (++s == kStages) { s = 0; ph ^= 1u; }
+          }
+          if (!ok) break;
+          if constexpr (CG == 2) umma_commit_pair(tfull_bar(buf), 0x3);
+          else umma_commit(tfull_bar(buf));
+          if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
         }
-        if (!ok) break;
-        umma_commit(tfull_bar(buf));
-        if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
       }
       if (!ok && issued) {
-        umma_commit(drain_bar);
+        if constexpr (CG == 2) umma_commit_pair(drain_bar, 0x1);
+        else umma_commit(drain_bar);
         wait_drain(drain_bar, 0);
       }
     }
+  } else if (warp == 10) {
+    // ---- runs and their tables ----
+    int jb = 0, slot = 0, used = 0;
+    uint32_t jph = 0, sph = 0;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      int row0, n0;
+      tile(t, row0, n0);
+      constexpr int kChunks = (kOwn + 31) / 32;
+      int id[kChunks];
+      uint32_t starts[kChunks];
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        id[c] = 32 * c + lane < kOwn ? row_adapter(a.seg, row0 + own0 + 32 * c + lane) : kOutside;
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(jempty_bar(jb), jph ^ 1u, abort_flag, a.dev_status))) {
+        ok = false;
+        break;
+      }
+      int runs = 0, last = kOutside;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        int before = __shfl_up_sync(0xFFFFFFFFu, id[c], 1);
+        if (lane == 0) before = last;
+        last = __shfl_sync(0xFFFFFFFFu, id[c], 31);
+        starts[c] = __ballot_sync(0xFFFFFFFFu, id[c] >= 0 && id[c] != before);
+        const int run = runs + __popc(starts[c] & (0xFFFFFFFFu >> (31 - lane))) - 1;
+        if (32 * c + lane < kOwn)
+          s_run[jb * kOwn + 32 * c + lane] = static_cast<int16_t>(id[c] >= 0 ? run : id[c]);
+        runs += __popc(starts[c]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(jfull_bar(jb));
+      if (++jb == 2) { jb = 0; jph ^= 1u; }
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t m = starts[c];
+        while (m != 0 && ok) {
+          const int e = __shfl_sync(0xFFFFFFFFu, id[c], __ffs(m) - 1);
+          m &= m - 1;
+          if (!__all_sync(0xFFFFFFFFu, wait_bounded(tbempty_bar(slot), sph ^ 1u, abort_flag, a.dev_status))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            const uint32_t dst = smem_u32(s_table + slot * 256 * rp);
+            mbar_arrive_expect_tx(tbfull_bar(slot), 256 * rp);
+            tma_load_3d(dst, &map_t, tbfull_bar(slot), n0, 0, e);
+            tma_load_3d(dst + 128 * rp, &map_t, tbfull_bar(slot), n0 + 64, 0, e);
+          }
+          ++used;
+          if (++slot == a.slots) { slot = 0; sph ^= 1u; }
+        }
+      }
+    }
+    if (!ok && lane == 0)
+      for (int i = 0; i < min(used, a.slots); ++i) {
+        if (--slot < 0) { slot = a.slots - 1; sph ^= 1u; }
+        wait_drain(tbfull_bar(slot), sph);
+      }
   } else {
+    // ---- epilogue ----
     pdl_wait();  // u
-    const int w = warp - 2, quad = warp & 3, half = w >> 2;
-    const int tid = threadIdx.x - 64;
-    const uint32_t taddr0 = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    int buf = 0;
-    uint32_t acc_ph = 0;
+    const int quad = warp & 3, sub = (warp - 2) >> 2;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int m0 = 32 * quad + 16 * sub;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(m0) << 16);
+    const uint32_t sums = taddr + 2 * TN;  // (flat) [kOwn], or in pieces [TN]
+    Table tb;
+    tb.slot = 0;
+    tb.ph = 0;
+    int buf = 0, jb = 0;
+    uint32_t acc_ph = 0, jph = 0;
+    // ldmatrix: this lane's row of the four 8 x 8 blocks of (16 k, 16 columns)
+    const int lk = (lane & 7) + (lane & 16 ? 8 : 0), ln = m0 + (lane & 8);
+    const uint32_t lm = smem_u32(s_table) + (ln >> 6) * 128 * rp + lk * 128 + ((((ln & 63) >> 3) ^ (lk & 7)) << 4);
+
+    // c += u B on 8 tokens (u of token g, run[] of the 8): false if a wait gave up.
+    auto add_runs = [&](float (&c)[4], const float2 (&u)[kMaxRank / 16][2], const int16_t* run) {
+      const int mine = run[lane & 7];
+      const int hi = __reduce_max_sync(0xFFFFFFFFu, mine);
+      if (hi < 0) return true;
+      const int lo = __reduce_min_sync(0xFFFFFFFFu, mine < 0 ? 0x7FFF : mine);
+      const int r0 = run[2 * t4], r1 = run[2 * t4 + 1];
+      for (int j = lo; j <= hi; ++j) {
+        if (j != tb.run) {
+          if (!__all_sync(0xFFFFFFFFu, wait_bounded(tbfull_bar(tb.slot), tb.ph, abort_flag, a.dev_status)))
+            return false;
+          const uint32_t at = lm + tb.slot * 256 * rp;
+#pragma unroll
+          for (int k = 0; k < kMaxRank / 16; ++k)
+            if (16 * k < a.r)
+              asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(tb.f[k][0]), "=r"(tb.f[k][1]), "=r"(tb.f[k][2]), "=r"(tb.f[k][3])
+                           : "r"(at + k * 2048)
+                           : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tbempty_bar(tb.slot));
+          if (++tb.slot == a.slots) { tb.slot = 0; tb.ph ^= 1u; }
+          tb.run = j;
+        }
+        float d[4] = {c[0], c[1], c[2], c[3]};
+#pragma unroll
+        for (int k = 0; k < kMaxRank / 16; ++k)
+          if (16 * k < a.r) {
+            const uint32_t h0 = pack_bf16x2(u[k][0].x, u[k][0].y), h1 = pack_bf16x2(u[k][1].x, u[k][1].y);
+            const uint32_t l0 = pack_bf16x2(u[k][0].x - __uint_as_float(h0 << 16),
+                                            u[k][0].y - __uint_as_float(h0 & 0xFFFF0000u));
+            const uint32_t l1 = pack_bf16x2(u[k][1].x - __uint_as_float(h1 << 16),
+                                            u[k][1].y - __uint_as_float(h1 & 0xFFFF0000u));
+            mma_16816(d, tb.f[k][0], tb.f[k][1], tb.f[k][2], tb.f[k][3], h0, h1);
+            mma_16816(d, tb.f[k][0], tb.f[k][1], tb.f[k][2], tb.f[k][3], l0, l1);
+          }
+        if (r0 == j) { c[0] = d[0]; c[2] = d[2]; }
+        if (r1 == j) { c[1] = d[1]; c[3] = d[3]; }
+      }
+      return true;
+    };
+
+    bool ok = true;
     for (int t = first; t < total; t += step) {
       int row0, n0;
       tile(t, row0, n0);
-      if (tid < TN) s_tok[tid] = row_adapter(a.seg, row0 + tid);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      // ---- the adapters' part of this CTA's tokens ----
-      for (int j = 4 * w; j < kOwn; j += 32) {
-        int id[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) id[i] = s_tok[rank * kOwn + j + i];
-        float4 acc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const int row = row0 + rank * kOwn + j;
-        if (id[0] >= 0 && id[0] == id[1] && id[0] == id[2] && id[0] == id[3]) {
-          expand<4>(a, id[0], row, lane, n0 + 4 * lane, acc, 0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (id[i] >= 0) expand<1>(a, id[i], row + i, lane, n0 + 4 * lane, acc, i);
+      const int n = n0 + m0;
+      tb.run = -1;
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(jfull_bar(jb), jph, abort_flag, a.dev_status))) break;
+      const int16_t* run = s_run + jb * kOwn;
+      const int64_t row_own = row0 + own0;
+      float2 u[kMaxRank / 16][2];
+      if constexpr (CG == 2) {
+        load_u(a, row_own + g, run[g] >= 0, t4, u);
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar(buf), acc_ph, abort_flag, a.dev_status))) break;
+        umma_fence_after();
+        for (int j = 0; j < kOwn; j += 8) {
+          float c[4];
+          umma_ld_frag(taddr + buf * TN + j, c);
+          umma_ld_frag_wait(c);
+          if (!(ok = add_runs(c, u, run + j))) break;
+          if (j + 8 < kOwn) load_u(a, row_own + j + 8 + g, run[j + 8 + g] >= 0, t4, u);
+          put_frag(a, c, static_cast<int>(row_own) + j, n, run + j, lane);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4*>(s_part + (j + i) * 128 + 4 * lane) = acc[i];
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      // ---- epilogue: this thread's column of the weight, TN / 2 tokens ----
-      bool ok =
-          __all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar(buf), acc_ph, abort_flag, a.dev_status));
-      umma_fence_after();
-      const uint32_t ta = taddr0 + buf * TN + half * (TN / 2);
-      const int m = quad * 32 + lane, n = n0 + m;
-      if constexpr (S > 1) {
-        awaited = true;
-        // the partners' tokens first
-#pragma unroll
-        for (int c = 0; c < TN / 2; c += 16) {
-          if (!ok) break;
-          uint32_t v[16];
-          umma_ld16(ta + c, v);
-          umma_ld_wait(v);
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const int j = half * (TN / 2) + c + i, owner = j / kOwn;
-            if (owner == rank) continue;
-            const int from = (rank - owner + S) % S - 1;
-            const uint32_t dst = map_to_rank(
-                smem_u32(s_red + (from * (kOwn / 4) + (j - owner * kOwn) / 4) * 128 + m), owner);
-            st_async4(dst, map_to_rank(red_bar, owner), __uint_as_float(v[i]),
-                      __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-          }
-        }
-        ok = ok && __all_sync(0xFFFFFFFFu, wait_bounded<true>(red_bar, 0, abort_flag, a.dev_status));
-      }
-#pragma unroll
-      for (int c = 0; c < TN / 2; c += 16) {
         if (!ok) break;
-        if (S > 1 && (half * (TN / 2) + c + 16 <= rank * kOwn || half * (TN / 2) + c >= (rank + 1) * kOwn))
-          continue;
-        uint32_t v[16];
-        umma_ld16(ta + c, v);
-        umma_ld_wait(v);
+        umma_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(map_to_rank(tempty_bar(buf), 0));
+          mbar_arrive(jempty_bar(jb));
+        }
+        if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
+      } else {
+        load_u(a, row_own + g, run[g] >= 0, t4, u);
+        for (int j = 0; j < kOwn; j += 8) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (!(ok = add_runs(c, u, run + j))) break;
+          if (j + 8 < kOwn) load_u(a, row_own + j + 8 + g, run[j + 8 + g] >= 0, t4, u);
+          umma_st_frag(sums + own0 + j, c);
+        }
+        if (!ok) break;
+        if (S > 1 && k0 + piece < k1) {  // the other tokens' sums start at zero
+          const float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int j = 0; j < TN; j += 8)
+            if (j < own0 || j >= own0 + kOwn) umma_st_frag(sums + j, z);
+        }
+        umma_st_wait();
+        int kp = k0;
+        for (; kp + piece < k1; kp += piece) {  // every piece but the last onto the sums
+          if (!(ok = __all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar(buf), acc_ph, abort_flag, a.dev_status))))
+            break;
+          umma_fence_after();
+          for (int j = 0; j < TN; j += 8) {
+            float c[4], q[4];
+            umma_ld_frag(taddr + buf * TN + j, c);
+            umma_ld_frag(sums + j, q);
+            umma_ld_frag_wait(c);
+            umma_ld_frag_wait(q);
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const int j = half * (TN / 2) + c + i - rank * kOwn;  // among this CTA's tokens
-          if (S > 1 && (j < 0 || j >= kOwn)) continue;
-          float f[4];
+            for (int e = 0; e < 4; ++e) c[e] += q[e];
+            umma_st_frag(sums + j, c);
+          }
+          umma_st_wait();
+          umma_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty_bar(buf));
+          if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
+        }
+        if (!ok) break;
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar(buf), acc_ph, abort_flag, a.dev_status))) break;
+        umma_fence_after();
+        if constexpr (S > 1) {
+          awaited = true;
+          for (int i = 1; i < S; ++i) {  // the partners' tokens first
+            const int owner = (rank + i) % S;
+            const uint32_t bar = map_to_rank(red_bar, owner);
+            const uint32_t dst = map_to_rank(
+                smem_u32(s_red + (S - 1 - i) * kOwn * 512 + (warp - 2) * 512 + lane * 16), owner);
+            for (int j = 0; j < kOwn; j += 8) {
+              float c[4];
+              umma_ld_frag(taddr + buf * TN + owner * kOwn + j, c);
+              umma_ld_frag_wait(c);
+              if (k0 + piece < k1) {
+                float q[4];
+                umma_ld_frag(sums + owner * kOwn + j, q);
+                umma_ld_frag_wait(q);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(v[i + e]);
-          if constexpr (S > 1) {
-            for (int o = 0; o < S - 1; ++o) {
-              const float4 p = s_red[(o * (kOwn / 4) + j / 4) * 128 + m];
-              f[0] += p.x; f[1] += p.y; f[2] += p.z; f[3] += p.w;
+                for (int e = 0; e < 4; ++e) c[e] += q[e];
+              }
+              st_async4(dst + j * 512, bar, c[0], c[1], c[2], c[3]);
             }
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n < a.N && s_tok[rank * kOwn + j + e] != kOutside)
-              put(a, row0 + rank * kOwn + j + e, n, f[e] + s_part[(j + e) * 128 + m]);
+          if (!__all_sync(0xFFFFFFFFu, wait_bounded<true>(red_bar, 0, abort_flag, a.dev_status))) break;
         }
+        for (int j = 0; j < kOwn; j += 8) {
+          float c[4], q[4];
+          umma_ld_frag(taddr + buf * TN + own0 + j, c);
+          umma_ld_frag(sums + own0 + j, q);
+          umma_ld_frag_wait(c);
+          umma_ld_frag_wait(q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[e] += q[e];
+          if constexpr (S > 1) {
+            for (int o = 0; o < S - 1; ++o) {
+              const float4 p = *reinterpret_cast<const float4*>(s_red + o * kOwn * 512 + j * 512 +
+                                                                (warp - 2) * 512 + lane * 16);
+              c[0] += p.x; c[1] += p.y; c[2] += p.z; c[3] += p.w;
+            }
+          }
+          put_frag(a, c, static_cast<int>(row_own) + j, n, run + j, lane);
+        }
+        umma_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(tempty_bar(buf));
+          mbar_arrive(jempty_bar(jb));
+        }
+        if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
       }
-      umma_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty_bar(buf));
-      if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
-      // s_tok and s_part are free; a warp that gave up takes the others along
-      if (!all_of_group(ok)) break;
+      if (++jb == 2) { jb = 0; jph ^= 1u; }
     }
   }
 
   // ---- teardown ----
   __syncwarp();
   umma_fence_before();
-  if constexpr (S > 1) {
+  __syncthreads();
+  if constexpr (kCluster > 1) {
     cluster_sync();  // no CTA leaves while a partner may still reach it
     // (after a wait that gave up: nor before the sums that were on their way)
-    if (threadIdx.x == 64 && awaited && *abort_flag) wait_drain(red_bar, 0);
-  } else {
-    __syncthreads();
+    if (S > 1 && threadIdx.x == 64 && awaited && *abort_flag) wait_drain(red_bar, 0);
   }
   umma_fence_after();
   if (warp == 1) {
     __syncwarp();
-    umma_dealloc(tmem, 2 * TN);
+    if constexpr (CG == 2) umma_dealloc_pair(tmem, F::kTmem);
+    else umma_dealloc(tmem, F::kTmem);
   }
   pdl_trigger();
 }
@@ -564,8 +767,9 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
 //
 // D_a[m, k] = sum over a's tokens of p[t, m] q[t, k], p fp32 [T, r] (u or v), q bf16 (dy or x).
 // A CTA takes one adapter and 128 columns (a cluster: parts of the adapter's tokens, added in
-// order).  p goes into the MMA as two bf16 numbers, the value and what its rounding left, so
-// the gradient keeps 16 bits of p.  Rows of other segments are never loaded: zeros stand in
+// order).  p goes into the MMA as three bf16 numbers, the value and what each rounding left, and
+// every piece of kGradTokens rows is added to the sums in fp32 registers: the gradient is as
+// exact as an fp32 sum.  Rows of other segments are never loaded: zeros stand in
 // their place in both operands.
 
 struct GradArgs {
@@ -703,32 +907,42 @@ grads_kernel(const GradArgs a, int split) {
     }
     const uint8_t* st = stage_ptr(s);
     const float* sp = reinterpret_cast<const float*>(st + kGradTokens * kGradRow);
+    uint32_t bq[kGradTokens / 16][4];  // q: tokens x 16 columns of this warp, transposed on the way
 #pragma unroll
     for (int kk = 0; kk < kGradTokens / 16; ++kk) {
-      // q: tokens x 16 columns of this warp, transposed on the way
-      uint32_t bq[4];
       const uint32_t addr = smem_u32(st + (kk * 16 + (lane & 15)) * kGradRow + (warp * 16 + (lane >> 4) * 8) * 2);
       asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(bq[0]), "=r"(bq[1]), "=r"(bq[2]), "=r"(bq[3])
+                   : "=r"(bq[kk][0]), "=r"(bq[kk][1]), "=r"(bq[kk][2]), "=r"(bq[kk][3])
                    : "r"(addr)
                    : "memory");
+    }
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        uint32_t hi[4], lo[4];
+    for (int i = 0; i < MB; ++i) {
+      float d[2][4] = {};  // this piece's sums
+#pragma unroll
+      for (int kk = 0; kk < kGradTokens / 16; ++kk) {
+        uint32_t w[3][4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int m = 16 * i + g + (v & 1) * 8, t = kk * 16 + 2 * t4 + (v >> 1) * 8;
-          const float f0 = sp[t * P::kPRow + m], f1 = sp[(t + 1) * P::kPRow + m];
-          hi[v] = pack_bf16x2(f0, f1);
-          lo[v] = pack_bf16x2(f0 - __uint_as_float(hi[v] << 16),
-                              f1 - __uint_as_float(hi[v] & 0xFFFF0000u));
+          float f0 = sp[t * P::kPRow + m], f1 = sp[(t + 1) * P::kPRow + m];
+#pragma unroll
+          for (int h = 0; h < 3; ++h) {
+            w[h][v] = pack_bf16x2(f0, f1);
+            f0 -= __uint_as_float(w[h][v] << 16);
+            f1 -= __uint_as_float(w[h][v] & 0xFFFF0000u);
+          }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          mma_16816(acc[i][j], hi[0], hi[1], hi[2], hi[3], bq[2 * j], bq[2 * j + 1]);
-          mma_16816(acc[i][j], lo[0], lo[1], lo[2], lo[3], bq[2 * j], bq[2 * j + 1]);
-        }
+        for (int h = 0; h < 3; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            mma_16816(d[j], w[h][0], w[h][1], w[h][2], w[h][3], bq[kk][2 * j], bq[kk][2 * j + 1]);
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] += d[j][v];
     }
     --ahead;
     s = (s + 1) % kGradStages;
@@ -854,47 +1068,115 @@ moe_status launch_shrink(const ShrinkArgs& a, cudaStream_t s) {
   return narrow ? launch_shrink_as<8, 1>(a, s) : launch_shrink_as<8, 4>(a, s);
 }
 
-template <int TN, int S, bool KMAJ>
-moe_status launch_project_as(ProjectArgs a, const void* x, int64_t x_stride, const void* w,
-                             cudaStream_t s) {
-  using F = Flat<TN, S>;
-  auto kern = project_kernel<TN, S, KMAJ>;
+// bf16 tables [n_adapters, r, cols]: a box that passes r is filled with zeros and not with the
+// next adapter's rows.
+bool map_tables(CUtensorMap* m, const void* base, uint64_t n_adapters, uint64_t r, uint64_t cols) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {cols, r, n_adapters};
+  const cuuint64_t strides[2] = {cols * 2, cols * r * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>((r + 15) / 16 * 16), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operands {
+  const void* x;
+  int64_t x_stride;
+  const void* w;
+  const void* table;
+};
+
+// Pairs of CTAs that can be resident at once, read once per kernel and device.
+template <typename Kernel>
+int resident_pairs(Kernel kern, int smem, std::mutex& mu, int (&cache)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sm_count() & ~1));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = sm_count() / 2;
+    }
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+template <int TN, int S, int CG, bool KMAJ>
+moe_status launch_project_as(ProjectArgs a, const Operands& o, cudaStream_t s) {
+  using F = Shape<TN, S, CG>;
+  auto kern = project_kernel<TN, S, CG, KMAJ>;
   static std::mutex mu;
   static bool done[64] = {};
   if (!opt_in(kern, F::kSmem, mu, done)) return MOE_ERR_CUDA;
-  CUtensorMap mw, mx;
+  CUtensorMap mw, mx, mt;
   // the weight is [K, N] (rows of N), or for the backward [N, K]
-  if (!(KMAJ ? map_2d(&mw, w, a.N, a.K, a.K, 128) : map_2d(&mw, w, a.K, a.N, a.N, 64)) ||
-      !map_2d(&mx, x, a.seg.T, a.K, x_stride, TN))
+  if (!(KMAJ ? map_2d(&mw, o.w, a.N, a.K, a.K, 128) : map_2d(&mw, o.w, a.K, a.N, a.N, 64)) ||
+      !map_2d(&mx, o.x, a.seg.T, a.K, o.x_stride, TN / CG) ||
+      !map_tables(&mt, o.table, a.seg.n_adapters, a.r, a.N))
     return MOE_ERR_CUDA;
-  a.n_blocks = static_cast<int>(ceil_div(a.N, 128));
+  a.n_blocks = static_cast<int>(ceil_div(a.N, 128 * CG));
   a.t_blocks = static_cast<int>(ceil_div(a.seg.T, TN));
-  a.n_inner = 0;
+  a.slots = std::min(kMaxSlots, F::kTableBytes / (256 * ((a.r + 15) / 16 * 16)));
+  // Tokens inner: the weight is read once, the rows stay in the L2.  Rows that outgrow it while
+  // the weight does not: columns inner.
+  constexpr int64_t kL2Budget = 80ll << 20;
+  a.n_inner = static_cast<int64_t>(a.seg.T) * a.K * 2 > kL2Budget &&
+              static_cast<int64_t>(a.N) * a.K * 2 <= kL2Budget;
   const int64_t tiles = static_cast<int64_t>(a.n_blocks) * a.t_blocks;
-  const unsigned grid = static_cast<unsigned>(S > 1 ? S * tiles : std::min<int64_t>(tiles, sm_count()));
-  launch_clustered(kern, dim3(grid), kThreads, F::kSmem, S, s, mw, mx, a);
+  int64_t clusters = tiles;
+  if constexpr (CG == 2) {
+    static std::mutex mu2;
+    static int pairs[64] = {};
+    const int n = resident_pairs(kern, F::kSmem, mu2, pairs);
+    if (n <= 0) return MOE_ERR_CUDA;
+    clusters = std::min<int64_t>(tiles, n);
+  } else if (S == 1) {
+    clusters = std::min<int64_t>(tiles, sm_count());
+  }
+  launch_clustered(kern, dim3(static_cast<unsigned>(clusters * S * CG)), kThreads, F::kSmem, S * CG, s,
+                   mw, mx, mt, a);
   return launch_status();
 }
 
 template <bool KMAJ>
-moe_status launch_project(const ProjectArgs& a, const void* x, int64_t x_stride, const void* w,
-                          cudaStream_t s) {
-  const int64_t tiles = ceil_div(a.N, 128);
-  const int steps = (a.K + 63) / 64;
-  if (a.seg.T <= 32) {
-    const int split = pow2_at_most(std::min<int64_t>(sm_count() / tiles, steps), 8);
-    if (split == 8) return launch_project_as<32, 8, KMAJ>(a, x, x_stride, w, s);
-    if (split == 4) return launch_project_as<32, 4, KMAJ>(a, x, x_stride, w, s);
-    if (split == 2) return launch_project_as<32, 2, KMAJ>(a, x, x_stride, w, s);
-    return launch_project_as<32, 1, KMAJ>(a, x, x_stride, w, s);
+moe_status launch_project(const ProjectArgs& a, const Operands& o, cudaStream_t s) {
+  const int64_t cols = ceil_div(a.N, 128);
+  const int64_t steps = ceil_div(a.K, 64);
+  const int64_t sms = sm_count();
+  const int T = a.seg.T;
+  if (T <= 64) {
+    const int split = pow2_at_most(std::min(sms / cols, steps), 8);
+    if (split == 8) return launch_project_as<64, 8, 1, KMAJ>(a, o, s);
+    if (split == 4) return launch_project_as<64, 4, 1, KMAJ>(a, o, s);
+    if (split == 2) return launch_project_as<64, 2, 1, KMAJ>(a, o, s);
+    return launch_project_as<64, 1, 1, KMAJ>(a, o, s);
   }
-  if (a.seg.T <= 128) {
-    const int split = pow2_at_most(std::min<int64_t>(sm_count() / tiles, steps), 8);
-    if (split == 8) return launch_project_as<128, 8, KMAJ>(a, x, x_stride, w, s);
-    if (split == 4) return launch_project_as<128, 4, KMAJ>(a, x, x_stride, w, s);
-    if (split == 2) return launch_project_as<128, 2, KMAJ>(a, x, x_stride, w, s);
-  }
-  return launch_project_as<128, 1, KMAJ>(a, x, x_stride, w, s);
+  // Rounds of tiles, in units of a 128 x 128 tile's MMAs a step.
+  const int64_t tiles = cols * ceil_div(T, 128);
+  const int split = pow2_at_most(std::min(sms / tiles, steps), 8);
+  const int64_t flat = split > 1 ? ceil_div(steps, split) : ceil_div(tiles, sms) * steps;
+  const int64_t pair = ceil_div(ceil_div(a.N, 256) * ceil_div(T, 256), sms / 2) * steps * 2;
+  if (!a.y_fp32 && 10 * pair <= 13 * flat) return launch_project_as<256, 1, 2, KMAJ>(a, o, s);
+  if (split == 8) return launch_project_as<128, 8, 1, KMAJ>(a, o, s);
+  if (split == 4) return launch_project_as<128, 4, 1, KMAJ>(a, o, s);
+  if (split == 2) return launch_project_as<128, 2, 1, KMAJ>(a, o, s);
+  return launch_project_as<128, 1, 1, KMAJ>(a, o, s);
 }
 
 template <int MB>
@@ -977,9 +1259,9 @@ MOE_API moe_status moe_adapter_project(const moe_adapter_params* p, const int32_
   const cudaStream_t s = as_cuda(stream);
   st = launch_shrink(ShrinkArgs{seg, p->d, p->r, x, p->x_stride, a, scale, u, 1, dev_status}, s);
   if (st != MOE_OK) return st;
-  return launch_project<false>(ProjectArgs{seg, p->d, p->n, p->r, u, b, y, p->y_stride,
-                                           p->y_type == MOE_DTYPE_FP32, 0, 0, 0, dev_status},
-                               x, p->x_stride, w, s);
+  return launch_project<false>(ProjectArgs{seg, p->d, p->n, p->r, u, y, p->y_stride,
+                                           p->y_type == MOE_DTYPE_FP32, 0, 0, 0, 0, dev_status},
+                               Operands{x, p->x_stride, w, b}, s);
 }
 
 MOE_API size_t moe_adapter_project_backward_workspace_size(const moe_adapter_params* p) {
@@ -1018,8 +1300,8 @@ MOE_API moe_status moe_adapter_project_backward(
     if (st != MOE_OK) return st;
   }
   if (dx != nullptr) {
-    st = launch_project<true>(ProjectArgs{seg, p->n, p->d, p->r, v, a, dx, p->d, 0, 0, 0, 0, dev_status},
-                              dy, p->y_stride, w, s);
+    st = launch_project<true>(ProjectArgs{seg, p->n, p->d, p->r, v, dx, p->d, 0, 0, 0, 0, 0, dev_status},
+                              Operands{dy, p->y_stride, w, a}, s);
     if (st != MOE_OK) return st;
   }
   if (da != nullptr) {

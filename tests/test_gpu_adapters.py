@@ -87,6 +87,9 @@ SHAPES = [
     (300, [11, 60, 60, 61, 299], [0, 1, 2, 0], 328, 720, 16, 3),  # and before the first
     (1021, [0, 1, 2, 3, 500, 1000, 1021], [4, 0, -1, 2, 2, 1], 256, 256, 104, 5),
     (2048, [0, 2048], [1], 512, 392, 16, 2),
+    # tiles of two CTAs, forward and (turned around) backward
+    (2290, [3] + list(range(4, 24)) + [700, 701, 1500, 2281], [q % 8 - 1 for q in range(24)], 200, 2040, 72, 7),
+    (2290, [0, 9, 1000, 1000, 2290], [2, 1, 0, 1], 2040, 200, 16, 3),
     (700, [0] * 300 + [400] * 200 + [700], [q % 3 for q in range(500)], 128, 128, 8, 3),
 ]
 
