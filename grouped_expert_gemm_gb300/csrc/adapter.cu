@@ -38,29 +38,41 @@ __device__ __forceinline__ void seg_rows(const Segments& s, int q, int& b, int& 
   e = min(seg_begin(s, q + 1), s.T);
 }
 
-// The last segment that starts at or before row t (0 if none does): with ordered offsets the
-// only one that can hold t.
-__device__ __forceinline__ int seg_of(const Segments& s, int t) {
-  int lo = 0, hi = s.n_seg - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (seg_begin(s, mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
 // Adapter of segment q; an id outside the tables counts as none.
 __device__ __forceinline__ int seg_adapter(const Segments& s, int q) {
   const int a = __ldg(s.adapter + q);
   return a >= 0 && a < s.n_adapters ? a : kNone;
 }
 
-// Adapter of row t, kNone, or kOutside.
-__device__ __forceinline__ int row_adapter(const Segments& s, int t) {
-  if (t >= s.T) return kOutside;
-  const int q = seg_of(s, t);
-  if (t < seg_begin(s, q) || t >= seg_begin(s, q + 1)) return kOutside;
-  return seg_adapter(s, q);
+// Adapter of row row0 + lane (kNone, or kOutside), by a whole warp: a search that asks 32
+// segments at a time for the one that holds row0 (a binary one would be as many loads one after
+// the other as it has steps), then the ends of the segments behind it, 32 at a time.
+__device__ __forceinline__ int row_adapters(const Segments& s, int row0, int lane) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  int lo = 0, n = s.n_seg;  // the last segment that starts at or before row0 is in [lo, lo + n)
+  while (n > 1) {
+    const int stride = (n + 31) / 32;
+    const int q = lo + lane * stride;
+    const bool at = lane * stride < n && seg_begin(s, q) <= row0;
+    const int c = __popc(__ballot_sync(kAll, at));  // ordered offsets: the first c of them
+    const int skip = c > 0 ? (c - 1) * stride : 0;
+    lo += skip;
+    n = min(stride, n - skip);
+  }
+  const int row = row0 + lane;
+  const bool before = row < seg_begin(s, lo);  // (in front of the first segment)
+  int seg = -1;
+  for (int q0 = lo; q0 < s.n_seg; q0 += 32) {
+    const int end = q0 + lane < s.n_seg ? seg_begin(s, q0 + lane + 1) : 0x7FFFFFFF;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) c += __shfl_sync(kAll, end, i) <= row;
+    if (seg < 0 && c < 32) seg = q0 + c;
+    if (__all_sync(kAll, seg >= 0)) break;
+  }
+  if (row >= s.T || before || seg < 0 || seg >= s.n_seg) return kOutside;
+  // (offsets out of order may name a segment that does not hold the row: still inside the table)
+  return seg_adapter(s, seg);
 }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -72,6 +84,15 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Four 8 x 8 blocks of 16-bit values, transposed; lane l gives the address of row l % 8 of block
+// l / 8.
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -80,12 +101,12 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 
 // --------------------------------- shrink ------------------------------------
 //
-// One CTA (or a cluster, which splits the reduction) takes the segments j, j + J, ... of a
-// tile of 8 NB rows.  The table's rows are the M operand, the tokens N = 8 at a time, so a
-// segment of one token costs one column block and nothing is shared between segments.  Both
-// operands come from global memory as 16 bytes a lane: lane t of a row takes values
-// 8t .. 8t+7 of 32, and the MMA's slots are dealt from those in the same order on both sides
-// (a sum does not mind the order of its terms).
+// A tile of 8 NB rows holds runs of rows with one adapter; CTA j of a tile (blockIdx.y) takes its
+// runs j, j + J, ...  The table's rows are the M operand, the tokens N = 8 at a time, so a run
+// of one token costs one column block and nothing is shared between runs.  Both operands come
+// from global memory as 16 bytes a lane: lane t of a row takes values 8t .. 8t+7 of 32, and the
+// MMA's slots are dealt from those in the same order on both sides (a sum does not mind the order
+// of its terms).  The warps split the reduction (a cluster too, where there are few CTAs).
 
 constexpr int kShrinkWarps = 8;
 
@@ -97,7 +118,6 @@ struct ShrinkArgs {
   const uint16_t* table;  // [n_adapters, r, K]
   const float* scale;     // [n_adapters]
   float* u;               // [T, r]
-  int J;
   uint32_t* dev_status;
 };
 
@@ -107,24 +127,28 @@ struct Shrink {
   static constexpr int kMB = MB / kRankGroups;
   static constexpr int kSlices = kShrinkWarps / kRankGroups;  // of the reduction
   static constexpr int kRows = 8 * NB;
-  static constexpr int kElems = 16 * MB * kRows;
+  static constexpr int kPitch = kRows + 2;  // of a row of sums: consecutive ones in other banks
+  static constexpr int kElems = 16 * MB * kPitch;
   static constexpr int kSmem = kSlices * kElems * 4 + kElems * 4;
+  // 32-value pieces a warp loads at once: about a dozen 16-byte loads a lane
+  static constexpr int kAhead = kMB == 1 ? (NB == 1 ? 4 : 2) : kMB == 2 ? (NB == 1 ? 3 : 2) : NB == 1 ? 2 : 1;
 };
 
 template <int MB, int NB>
-__global__ void __launch_bounds__(32 * kShrinkWarps)
+__global__ void __launch_bounds__(32 * kShrinkWarps, 2)
 shrink_kernel(const ShrinkArgs a, int split) {
   using P = Shrink<MB, NB>;
-  extern __shared__ float s_part[];            // [kSlices][16 MB][8 NB]
-  float* s_sum = s_part + P::kSlices * P::kElems;  // [16 MB][8 NB]
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  extern __shared__ float s_part[];            // [kSlices][16 MB][kPitch]
+  float* s_sum = s_part + P::kSlices * P::kElems;  // [16 MB][kPitch]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int row0 = static_cast<int>(blockIdx.x) / split * P::kRows;
-  const int row1 = min(row0 + P::kRows, a.seg.T);
   const int group = warp % P::kRankGroups, slice = warp / P::kRankGroups;
-  const int chunks = (a.K + 31) / 32;
-  const int c0 = rank * chunks / split, c1 = (rank + 1) * chunks / split;
+  const int m0 = group * P::kMB * 16;
+  const int pieces = (a.K + 31) / 32;
+  const int c0 = rank * pieces / split, c1 = (rank + 1) * pieces / split;
 
   pdl_wait();
   pdl_trigger();
@@ -137,21 +161,25 @@ shrink_kernel(const ShrinkArgs a, int split) {
     }
   }
 
-  int nth = 0;
-  for (int q = seg_of(a.seg, row0); q < a.seg.n_seg && seg_begin(a.seg, q) < row1; ++q) {
-    int b, e;
-    seg_rows(a.seg, q, b, e);
-    b = max(b, row0);
-    e = min(e, row1);
-    if (b >= e) continue;
-    if (nth++ % a.J != static_cast<int>(blockIdx.y)) continue;
-    const int id = seg_adapter(a.seg, q);
-    if (id < 0) {
-      if (rank == 0)
-        for (int i = threadIdx.x; i < (e - b) * a.r; i += blockDim.x)
-          a.u[static_cast<int64_t>(b) * a.r + i] = 0.0f;
-      continue;
-    }
+  // runs of the tile: every warp finds them for itself
+  const int id = row_adapters(a.seg, row0, lane);
+  const uint32_t in_tile = P::kRows == 32 ? kAll : (1u << P::kRows) - 1;
+  if (blockIdx.y == 0 && rank == 0) {
+    uint32_t none = __ballot_sync(kAll, id == kNone) & in_tile;
+    for (; none != 0; none &= none - 1)
+      if (static_cast<int>(threadIdx.x) < a.r)
+        a.u[static_cast<int64_t>(row0 + __ffs(none) - 1) * a.r + threadIdx.x] = 0.0f;
+  }
+  const int before = __shfl_up_sync(kAll, id, 1);
+  uint32_t starts = __ballot_sync(kAll, id >= 0 && (lane == 0 || id != before)) & in_tile;
+  const uint32_t held = __ballot_sync(kAll, id >= 0) & in_tile;
+  for (int nth = 0; starts != 0; ++nth) {
+    const int b = __ffs(starts) - 1;  // rows b .. e - 1 of the tile
+    starts &= starts - 1;
+    const uint32_t stops = (starts | ~held) & ~((2u << b) - 1);  // later starts, rows without one
+    const int e = min(stops != 0 ? __ffs(stops) - 1 : 32, P::kRows);
+    if (nth % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
+    const int adapter = __shfl_sync(kAll, id, b);
     float acc[P::kMB][NB][4];
 #pragma unroll
     for (int i = 0; i < P::kMB; ++i)
@@ -159,67 +187,78 @@ shrink_kernel(const ShrinkArgs a, int split) {
       for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.0f;
-    const uint16_t* tab = a.table + static_cast<int64_t>(id) * a.r * a.K;
-    const int m0 = group * P::kMB * 16;
-    for (int c = c0 + slice; c < c1; c += P::kSlices) {
-      const int k = c * 32 + 8 * t4;
-      const bool in = k < a.K;  // K is a multiple of 8
-      uint4 xv[NB];
+    const uint16_t* tab = a.table + (static_cast<int64_t>(adapter) * a.r + m0 + g) * a.K;
+    const uint16_t* xr = a.x + (row0 + g) * a.x_stride;
+    for (int c = c0 + slice; c < c1; c += P::kSlices * P::kAhead) {
+      uint4 xv[P::kAhead][NB], tv[P::kAhead][P::kMB][2];
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int row = row0 + 8 * j + g;
-        xv[j] = in && row >= b && row < e
-                    ? __ldg(reinterpret_cast<const uint4*>(a.x + row * a.x_stride + k))
-                    : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < P::kAhead; ++h) {
+        const int k = (c + h * P::kSlices) * 32 + 8 * t4;
+        const bool in = c + h * P::kSlices < c1 && k < a.K;  // K is a multiple of 8
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          xv[h][j] = in && 8 * j + g >= b && 8 * j + g < e
+                         ? __ldg(reinterpret_cast<const uint4*>(xr + 8 * j * a.x_stride + k))
+                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < P::kMB; ++i)
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+            tv[h][i][o] = in && m0 + 16 * i + 8 * o + g < a.r
+                              ? __ldg(reinterpret_cast<const uint4*>(
+                                    tab + static_cast<int64_t>(16 * i + 8 * o) * a.K + k))
+                              : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int i = 0; i < P::kMB; ++i) {
-        const int m = m0 + 16 * i + g;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        if (in && m < a.r)
-          lo = __ldg(reinterpret_cast<const uint4*>(tab + static_cast<int64_t>(m) * a.K + k));
-        if (in && m + 8 < a.r)
-          hi = __ldg(reinterpret_cast<const uint4*>(tab + static_cast<int64_t>(m + 8) * a.K + k));
+      for (int h = 0; h < P::kAhead; ++h)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          mma_16816(acc[i][j], lo.x, hi.x, lo.y, hi.y, xv[j].x, xv[j].y);
-          mma_16816(acc[i][j], lo.z, hi.z, lo.w, hi.w, xv[j].z, xv[j].w);
-        }
-      }
+        for (int j = 0; j < NB; ++j)
+          if (8 * j < e && 8 * j + 8 > b) {
+#pragma unroll
+            for (int i = 0; i < P::kMB; ++i) {
+              const uint4 lo = tv[h][i][0], hi = tv[h][i][1];
+              mma_16816(acc[i][j], lo.x, hi.x, lo.y, hi.y, xv[h][j].x, xv[h][j].y);
+              mma_16816(acc[i][j], lo.z, hi.z, lo.w, hi.w, xv[h][j].z, xv[h][j].w);
+            }
+          }
     }
     // the slices of this CTA, then those of the cluster, in order
     float* mine = s_part + slice * P::kElems;
 #pragma unroll
     for (int i = 0; i < P::kMB; ++i)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int m = m0 + 16 * i + g, n = 8 * j + 2 * t4;
-        *reinterpret_cast<float2*>(mine + m * P::kRows + n) = make_float2(acc[i][j][0], acc[i][j][1]);
-        *reinterpret_cast<float2*>(mine + (m + 8) * P::kRows + n) =
-            make_float2(acc[i][j][2], acc[i][j][3]);
-      }
+      for (int j = 0; j < NB; ++j)
+        if (8 * j < e && 8 * j + 8 > b) {
+          const int m = m0 + 16 * i + g, n = 8 * j + 2 * t4;
+          *reinterpret_cast<float2*>(mine + m * P::kPitch + n) = make_float2(acc[i][j][0], acc[i][j][1]);
+          *reinterpret_cast<float2*>(mine + (m + 8) * P::kPitch + n) =
+              make_float2(acc[i][j][2], acc[i][j][3]);
+        }
     __syncthreads();
-    for (int i = threadIdx.x; i < P::kElems; i += blockDim.x) {
-      float v = s_part[i];
-#pragma unroll
-      for (int s = 1; s < P::kSlices; ++s) v += s_part[s * P::kElems + i];
-      s_sum[i] = v;
-    }
-    if (split > 1) cluster_sync();
-    else __syncthreads();
-    const float scale = __ldg(a.scale + id);
+    const float scale = __ldg(a.scale + adapter);
     const int n = (e - b) * a.r;
+    if (split > 1) {
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int at = i % a.r * P::kPitch + b + i / a.r;
+        float v = s_part[at];
+#pragma unroll
+        for (int s = 1; s < P::kSlices; ++s) v += s_part[s * P::kElems + at];
+        s_sum[at] = v;
+      }
+      cluster_sync();
+    }
     for (int i = rank * blockDim.x + threadIdx.x; i < n; i += split * blockDim.x) {
       const int row = b + i / a.r, m = i % a.r;
-      const int at = m * P::kRows + row - row0;
+      const int at = m * P::kPitch + row;
       float v = 0.0f;
       if (split > 1) {
         const uint32_t addr = smem_u32(s_sum + at);
         for (int o = 0; o < split; ++o) v += ld_cluster(map_to_rank(addr, o));
       } else {
-        v = s_sum[at];
+#pragma unroll
+        for (int s = 0; s < P::kSlices; ++s) v += s_part[s * P::kElems + at];
       }
-      a.u[static_cast<int64_t>(row) * a.r + m] = scale * v;
+      a.u[static_cast<int64_t>(row0 + row) * a.r + m] = scale * v;
     }
     if (split > 1) cluster_sync();  // before the sums are written again, or given up
     else __syncthreads();
@@ -234,6 +273,7 @@ shrink_kernel(const ShrinkArgs a, int split) {
 //   warp 1       tensor memory; lane 0 issues four MMAs (K = 16) a stage
 //   warps 2..9   epilogue: warp (quad, sub) has the 16 weight columns at 32 quad + 16 sub
 //   warp 10      the tile's runs of rows with one adapter, and the runs' tables by TMA
+//   warp 11      u, 32 tokens at a time, by TMA
 // The adapters' part is a product of mma.sync in the epilogue: u B is r / d of the work and a
 // run may be one token long, where tcgen05's narrowest tile is 16 columns by 128 rows of the
 // table.  tcgen05's 16x256b loads give the accumulators in mma.sync's own layout, 16 weight
@@ -261,32 +301,40 @@ struct ProjectArgs {
   int64_t y_stride;
   int y_fp32;
   int n_blocks, t_blocks, n_inner;
-  int slots;  // of the tables
+  int x_rows;   // rows of a box of x: those behind the batch's last are never staged
+  int slots;    // of the tables
+  int u_slots;
   uint32_t* dev_status;
 };
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kWBytes = 128 * 64 * 2;
 constexpr int kWBox = 64 * 64 * 2;
 constexpr int kPiece = 16;      // steps of 64 to a piece of an fp32 result's reduction
 constexpr int kMaxSlots = 16;
+constexpr int kUBox = 32 * 32 * 4;  // [32 tokens][32 of r] fp32
 constexpr int kMaxRank = 128;
 
 template <int TN, int S, int CG>
 struct Shape {
   static constexpr int kStageBytes = kWBytes + TN / CG * 128;
-  static constexpr int kStages = CG == 2 ? 6 : TN == 128 ? (S >= 4 ? 3 : 4) : 5;
+  static constexpr int kStages = CG == 2 ? 5 : TN == 128 ? (S == 2 ? 4 : 3) : S == 1 ? 5 : 4;
   static constexpr int kOwn = TN / S;
-  static constexpr int kTableBytes = (CG == 2 ? 32 : 64) * 1024;
+  // 64 KB of tables on their way where runs may be single tokens (32 KB: 128 tokens of as many
+  // adapters took a third longer)
+  static constexpr int kTableBytes = (CG == 2 || (TN == 128 && (S == 2 || S == 8)) ? 32 : 64) * 1024;
+  static constexpr int kUBytes = (S >= 4 ? 16 : 32) * 1024;
   static constexpr int kRedBytes = (S - 1) * kOwn * 512;  // [S - 1][kOwn / 8][8][32] float4
-  // full[st], empty[st], tfull[2], tempty[2], jfull[2], jempty[2], tbfull[], tbempty[], red, drain
-  static constexpr int kBars = 2 * kStages + 8 + 2 * kMaxSlots + 2;
+  // full[st], empty[st], tfull[2], tempty[2], jfull[2], jempty[2], tbfull[], tbempty[], ufull[],
+  // uempty[], red, drain
+  static constexpr int kBars = 2 * kStages + 8 + 4 * kMaxSlots + 2;
   static constexpr int kTmem = CG == 2 ? 2 * TN : 4 * TN;  // two buffers, (flat) the sums
   static constexpr int kSmem =
-      1024 + kStages * kStageBytes + kTableBytes + kRedBytes + kBars * 8 + 2 * kOwn * 2 + 16;
+      1024 + kStages * kStageBytes + kTableBytes + kUBytes + kRedBytes + kBars * 8 + 2 * kOwn * 2 + 2 * (kOwn / 8) * 4 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOwn % 8 == 0 && kTmem <= 512, "shape");
   static_assert(kTableBytes >= 256 * kMaxRank, "one table at least");
+  static_assert(kUBytes >= (kOwn > 32 ? 2 : 1) * kUBox * kMaxRank / 32, "two pieces of u where there are");
 };
 
 // The table of one run in registers, and its place in the ring.
@@ -296,18 +344,6 @@ struct Table {
   int slot;
   uint32_t ph;
 };
-
-__device__ __forceinline__ void load_u(const ProjectArgs& a, int64_t row, bool live, int t4,
-                                       float2 (&u)[kMaxRank / 16][2]) {
-  const float* p = a.u + row * a.r + 2 * t4;
-#pragma unroll
-  for (int k = 0; k < kMaxRank / 16; ++k)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (16 * k < a.r)
-        u[k][h] = live && 16 * k + 8 * h < a.r ? *reinterpret_cast<const float2*>(p + 16 * k + 8 * h)
-                                               : make_float2(0.0f, 0.0f);
-}
 
 // Stores 16 weight columns from n by 8 tokens from row (the layout of umma_ld_frag).
 __device__ __forceinline__ void put_frag(const ProjectArgs& a, const float (&c)[4], int row, int n,
@@ -338,7 +374,8 @@ __device__ __forceinline__ void put_frag(const ProjectArgs& a, const float (&c)[
 template <int TN, int S, int CG, bool KMAJ>
 __global__ void __launch_bounds__(kThreads, 1)
 project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-               const __grid_constant__ CUtensorMap map_t, const ProjectArgs a) {
+               const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_u,
+               const ProjectArgs a) {
   using F = Shape<TN, S, CG>;
   static_assert(CG == 1 || S == 1, "one kind of cluster");
   constexpr int kStages = F::kStages, kOwn = F::kOwn;
@@ -346,11 +383,14 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   uint8_t* stage_base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_table = stage_base + kStages * F::kStageBytes;
-  uint8_t* s_red = s_table + F::kTableBytes;
+  uint8_t* s_u = s_table + F::kTableBytes;
+  uint8_t* s_red = s_u + F::kUBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_red + F::kRedBytes);
-  int16_t* s_run = reinterpret_cast<int16_t*>(bars + F::kBars);  // [2][kOwn]
-  volatile int* abort_flag = reinterpret_cast<int*>(s_run + 2 * kOwn);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_run + 2 * kOwn) + 1;
+  int16_t* s_run = reinterpret_cast<int16_t*>(bars + F::kBars);  // [2][kOwn]: run of a token
+  // [2][kOwn / 8]: first run of 8 tokens, and in the high half the last one (-1: none)
+  int* s_span = reinterpret_cast<int*>(s_run + 2 * kOwn);
+  volatile int* abort_flag = s_span + 2 * (kOwn / 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_span + 2 * (kOwn / 8)) + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCluster = S * CG;
   const int rank = kCluster > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -363,6 +403,8 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   const int piece = CG == 1 && a.y_fp32 ? kPiece : steps;
   const int rp = (a.r + 15) & ~15;
   const int own0 = S > 1 ? rank * kOwn : 0;  // this CTA's tokens of the tile
+  const int u_bytes = (a.r + 31) / 32 * kUBox;  // a piece of u
+  const uint32_t stage_tx = kWBytes + a.x_rows * 128;
 
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
@@ -372,7 +414,9 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   auto jempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 6 + b); };
   auto tbfull_bar = [&](int s) { return smem_u32(bars + 2 * kStages + 8 + s); };
   auto tbempty_bar = [&](int s) { return smem_u32(bars + 2 * kStages + 8 + kMaxSlots + s); };
-  const uint32_t red_bar = smem_u32(bars + 2 * kStages + 8 + 2 * kMaxSlots);
+  auto ufull_bar = [&](int s) { return smem_u32(bars + 2 * kStages + 8 + 2 * kMaxSlots + s); };
+  auto uempty_bar = [&](int s) { return smem_u32(bars + 2 * kStages + 8 + 3 * kMaxSlots + s); };
+  const uint32_t red_bar = smem_u32(bars + 2 * kStages + 8 + 4 * kMaxSlots);
   const uint32_t drain_bar = red_bar + 8;
   // first token and first weight column of this CTA's part of tile t
   auto tile = [&](int t, int& row0, int& n0) {
@@ -396,6 +440,8 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     for (int s = 0; s < kMaxSlots; ++s) {
       mbar_init(tbfull_bar(s), 1);
       mbar_init(tbempty_bar(s), 8);
+      mbar_init(ufull_bar(s), 1);
+      mbar_init(uempty_bar(s), 8);
     }
     mbar_init(red_bar, 1);
     mbar_init(drain_bar, 1);
@@ -405,6 +451,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_t)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_u)) : "memory");
   }
   if (warp == 1) {
     if constexpr (CG == 2) umma_alloc_pair(smem_u32(tmem_slot), F::kTmem);
@@ -432,7 +479,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
           const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
           if constexpr (CG == 2) {
             const uint32_t bar = map_to_rank(full_bar(s), 0);
-            if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * F::kStageBytes);
+            if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * stage_tx);
             if (KMAJ) {
               tma_load_2d_pair(st, &map_w, bar, k * 64, n0);
             } else {
@@ -441,7 +488,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             }
             tma_load_2d_pair(st + kWBytes, &map_x, bar, k * 64, row0);
           } else {
-            mbar_arrive_expect_tx(full_bar(s), F::kStageBytes);
+            mbar_arrive_expect_tx(full_bar(s), stage_tx);
             if (KMAJ) {
               tma_load_2d(st, &map_w, full_bar(s), k * 64, n0);
             } else {
@@ -518,8 +565,10 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
       int id[kChunks];
       uint32_t starts[kChunks];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-        id[c] = 32 * c + lane < kOwn ? row_adapter(a.seg, row0 + own0 + 32 * c + lane) : kOutside;
+      for (int c = 0; c < kChunks; ++c) {
+        id[c] = row_adapters(a.seg, row0 + own0 + 32 * c, lane);
+        if (32 * c + lane >= kOwn) id[c] = kOutside;
+      }
       if (!__all_sync(0xFFFFFFFFu, wait_bounded(jempty_bar(jb), jph ^ 1u, abort_flag, a.dev_status))) {
         ok = false;
         break;
@@ -532,8 +581,17 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         last = __shfl_sync(0xFFFFFFFFu, id[c], 31);
         starts[c] = __ballot_sync(0xFFFFFFFFu, id[c] >= 0 && id[c] != before);
         const int run = runs + __popc(starts[c] & (0xFFFFFFFFu >> (31 - lane))) - 1;
-        if (32 * c + lane < kOwn)
-          s_run[jb * kOwn + 32 * c + lane] = static_cast<int16_t>(id[c] >= 0 ? run : id[c]);
+        const int mine = id[c] >= 0 ? run : id[c];
+        int hi = mine, lo = mine >= 0 ? mine : 0x7FFF;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+          hi = max(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+          lo = min(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        }
+        if (32 * c + lane < kOwn) {
+          s_run[jb * kOwn + 32 * c + lane] = static_cast<int16_t>(mine);
+          if ((lane & 7) == 0) s_span[jb * (kOwn / 8) + 4 * c + lane / 8] = hi < 0 ? -1 : lo | hi << 16;
+        }
         runs += __popc(starts[c]);
       }
       __syncwarp();
@@ -565,9 +623,35 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         if (--slot < 0) { slot = a.slots - 1; sph ^= 1u; }
         wait_drain(tbfull_bar(slot), sph);
       }
+  } else if (warp == 11) {
+    if (lane == 0) {
+      // ---- u ----
+      pdl_wait();
+      int s = 0, used = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step) {
+        int row0, n0;
+        tile(t, row0, n0);
+        for (int j = 0; j < kOwn; j += 32) {
+          if (!wait_bounded(uempty_bar(s), ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
+          mbar_arrive_expect_tx(ufull_bar(s), u_bytes);
+          for (int c = 0; c < a.r; c += 32)
+            tma_load_2d(smem_u32(s_u + s * u_bytes + c / 32 * kUBox), &map_u, ufull_bar(s), c,
+                        row0 + own0 + j);
+          ++used;
+          if (++s == a.u_slots) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (!ok)
+        for (int i = 0; i < min(used, a.u_slots); ++i) {
+          if (--s < 0) { s = a.u_slots - 1; ph ^= 1u; }
+          wait_drain(ufull_bar(s), ph);
+        }
+    }
   } else {
     // ---- epilogue ----
-    pdl_wait();  // u
+    pdl_wait();  // (what is written here may still be read by the kernels before)
     const int quad = warp & 3, sub = (warp - 2) >> 2;
     const int g = lane >> 2, t4 = lane & 3;
     const int m0 = 32 * quad + 16 * sub;
@@ -576,50 +660,57 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     Table tb;
     tb.slot = 0;
     tb.ph = 0;
-    int buf = 0, jb = 0;
-    uint32_t acc_ph = 0, jph = 0;
+    int buf = 0, jb = 0, us = 0;
+    uint32_t acc_ph = 0, jph = 0, uph = 0;
     // ldmatrix: this lane's row of the four 8 x 8 blocks of (16 k, 16 columns)
     const int lk = (lane & 7) + (lane & 16 ? 8 : 0), ln = m0 + (lane & 8);
     const uint32_t lm = smem_u32(s_table) + (ln >> 6) * 128 * rp + lk * 128 + ((((ln & 63) >> 3) ^ (lk & 7)) << 4);
 
-    // c += u B on 8 tokens (u of token g, run[] of the 8): false if a wait gave up.
-    auto add_runs = [&](float (&c)[4], const float2 (&u)[kMaxRank / 16][2], const int16_t* run) {
-      const int mine = run[lane & 7];
-      const int hi = __reduce_max_sync(0xFFFFFFFFu, mine);
-      if (hi < 0) return true;
-      const int lo = __reduce_min_sync(0xFFFFFFFFu, mine < 0 ? 0x7FFF : mine);
-      const int r0 = run[2 * t4], r1 = run[2 * t4 + 1];
-      for (int j = lo; j <= hi; ++j) {
-        if (j != tb.run) {
-          if (!__all_sync(0xFFFFFFFFu, wait_bounded(tbfull_bar(tb.slot), tb.ph, abort_flag, a.dev_status)))
-            return false;
-          const uint32_t at = lm + tb.slot * 256 * rp;
+    // The table of run j into registers, its slot given back: false if the wait gave up.
+    auto take = [&](int j) {
+      if (j == tb.run) return true;
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(tbfull_bar(tb.slot), tb.ph, abort_flag, a.dev_status)))
+        return false;
+      const uint32_t at = lm + tb.slot * 256 * rp;
 #pragma unroll
-          for (int k = 0; k < kMaxRank / 16; ++k)
-            if (16 * k < a.r)
-              asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(tb.f[k][0]), "=r"(tb.f[k][1]), "=r"(tb.f[k][2]), "=r"(tb.f[k][3])
-                           : "r"(at + k * 2048)
-                           : "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tbempty_bar(tb.slot));
-          if (++tb.slot == a.slots) { tb.slot = 0; tb.ph ^= 1u; }
-          tb.run = j;
-        }
-        float d[4] = {c[0], c[1], c[2], c[3]};
+      for (int k = 0; k < kMaxRank / 16; ++k)
+        if (16 * k < a.r) ldmatrix_trans(tb.f[k], at + k * 2048);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tbempty_bar(tb.slot));
+      if (++tb.slot == a.slots) { tb.slot = 0; tb.ph ^= 1u; }
+      tb.run = j;
+      return true;
+    };
+    // u of 16 ranks of a token as two bf16 numbers a value, in the layout of mma.sync's second
+    // operand: w[0..1] the values, w[2..3] what their rounding left.
+    auto split_u = [&](const uint8_t* row_u, int swz, int k, uint32_t (&w)[4]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int word = (16 * k) % 32 + 8 * h + 2 * t4;  // of the 32 of a row
+        const float2 f = *reinterpret_cast<const float2*>(
+            row_u + k / 2 * kUBox + (((word >> 2) ^ swz) << 4) + (word & 3) * 4);
+        w[h] = pack_bf16x2(f.x, f.y);
+        w[2 + h] = pack_bf16x2(f.x - __uint_as_float(w[h] << 16),
+                               f.y - __uint_as_float(w[h] & 0xFFFF0000u));
+      }
+    };
+    // c += u B on 8 tokens of several runs.
+    auto add_runs = [&](float (&c)[4], const uint8_t* row_u, const int16_t* run, int span) {
+      if (span < 0) return true;
+      const int r0 = run[2 * t4], r1 = run[2 * t4 + 1];
+      for (int j = span & 0xFFFF; j <= span >> 16; ++j) {
+        if (!take(j)) return false;
+        float d[4] = {c[0], c[1], c[2], c[3]}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < kMaxRank / 16; ++k)
           if (16 * k < a.r) {
-            const uint32_t h0 = pack_bf16x2(u[k][0].x, u[k][0].y), h1 = pack_bf16x2(u[k][1].x, u[k][1].y);
-            const uint32_t l0 = pack_bf16x2(u[k][0].x - __uint_as_float(h0 << 16),
-                                            u[k][0].y - __uint_as_float(h0 & 0xFFFF0000u));
-            const uint32_t l1 = pack_bf16x2(u[k][1].x - __uint_as_float(h1 << 16),
-                                            u[k][1].y - __uint_as_float(h1 & 0xFFFF0000u));
-            mma_16816(d, tb.f[k][0], tb.f[k][1], tb.f[k][2], tb.f[k][3], h0, h1);
-            mma_16816(d, tb.f[k][0], tb.f[k][1], tb.f[k][2], tb.f[k][3], l0, l1);
+            uint32_t w[4];
+            split_u(row_u, g, k, w);
+            mma_16816(d, tb.f[k][0], tb.f[k][1], tb.f[k][2], tb.f[k][3], w[0], w[1]);
+            mma_16816(e, tb.f[k][0], tb.f[k][1], tb.f[k][2], tb.f[k][3], w[2], w[3]);
           }
-        if (r0 == j) { c[0] = d[0]; c[2] = d[2]; }
-        if (r1 == j) { c[1] = d[1]; c[3] = d[3]; }
+        if (r0 == j) { c[0] = d[0] + e[0]; c[2] = d[2] + e[2]; }
+        if (r1 == j) { c[1] = d[1] + e[1]; c[3] = d[3] + e[3]; }
       }
       return true;
     };
@@ -632,21 +723,73 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
       tb.run = -1;
       if (!__all_sync(0xFFFFFFFFu, wait_bounded(jfull_bar(jb), jph, abort_flag, a.dev_status))) break;
       const int16_t* run = s_run + jb * kOwn;
-      const int64_t row_own = row0 + own0;
-      float2 u[kMaxRank / 16][2];
+      const int row_own = row0 + own0;
       if constexpr (CG == 2) {
-        load_u(a, row_own + g, run[g] >= 0, t4, u);
         if (!__all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar(buf), acc_ph, abort_flag, a.dev_status))) break;
         umma_fence_after();
-        for (int j = 0; j < kOwn; j += 8) {
-          float c[4];
-          umma_ld_frag(taddr + buf * TN + j, c);
-          umma_ld_frag_wait(c);
-          if (!(ok = add_runs(c, u, run + j))) break;
-          if (j + 8 < kOwn) load_u(a, row_own + j + 8 + g, run[j + 8 + g] >= 0, t4, u);
-          put_frag(a, c, static_cast<int>(row_own) + j, n, run + j, lane);
-        }
+      }
+      const int* span = s_span + jb * (kOwn / 8);
+      constexpr int kGroups = kOwn < 32 ? kOwn / 8 : 4;
+      for (int j = 0; j < kOwn && ok; j += 32) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded(ufull_bar(us), uph, abort_flag, a.dev_status));
         if (!ok) break;
+        const uint8_t* row_u = s_u + us * u_bytes + g * 128;  // (rows of 8 i + g share g's swizzle)
+        const int r0 = run[j], r1 = run[j + 8 * kGroups - 1];
+        if (r0 == r1) {  // one run, or no adapter (or outside: never stored)
+          ok = r0 < 0 || take(r0);
+          float c[kGroups][4];
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i) {
+            if constexpr (CG == 2) {
+              umma_ld_frag(taddr + buf * TN + j + 8 * i, c[i]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) c[i][e] = 0.0f;
+            }
+          }
+          if constexpr (CG == 2) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) umma_ld_frag_wait(c[i]);
+          }
+          if (r0 >= 0 && ok) {
+#pragma unroll
+            for (int k = 0; k < kMaxRank / 16; ++k)
+              if (16 * k < a.r) {
+                uint32_t w[kGroups][4];
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) split_u(row_u + i * 1024, g, k, w[i]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int i = 0; i < kGroups; ++i)
+                    mma_16816(c[i], tb.f[k][0], tb.f[k][1], tb.f[k][2], tb.f[k][3], w[i][2 * h],
+                              w[i][2 * h + 1]);
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i) {
+            if constexpr (CG == 2) put_frag(a, c[i], row_own + j + 8 * i, n, run + j + 8 * i, lane);
+            else umma_st_frag(sums + own0 + j + 8 * i, c[i]);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kGroups && ok; ++i) {
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (CG == 2) {
+              umma_ld_frag(taddr + buf * TN + j + 8 * i, c);
+              umma_ld_frag_wait(c);
+            }
+            ok = add_runs(c, row_u + i * 1024, run + j + 8 * i, span[j / 8 + i]);
+            if constexpr (CG == 2) put_frag(a, c, row_own + j + 8 * i, n, run + j + 8 * i, lane);
+            else umma_st_frag(sums + own0 + j + 8 * i, c);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(uempty_bar(us));
+        if (++us == a.u_slots) { us = 0; uph ^= 1u; }
+      }
+      if (!ok) break;
+      if constexpr (CG == 2) {
         umma_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -655,14 +798,6 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         }
         if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
       } else {
-        load_u(a, row_own + g, run[g] >= 0, t4, u);
-        for (int j = 0; j < kOwn; j += 8) {
-          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (!(ok = add_runs(c, u, run + j))) break;
-          if (j + 8 < kOwn) load_u(a, row_own + j + 8 + g, run[j + 8 + g] >= 0, t4, u);
-          umma_st_frag(sums + own0 + j, c);
-        }
-        if (!ok) break;
         if (S > 1 && k0 + piece < k1) {  // the other tokens' sums start at zero
           const float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           for (int j = 0; j < TN; j += 8)
@@ -731,7 +866,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
               c[0] += p.x; c[1] += p.y; c[2] += p.z; c[3] += p.w;
             }
           }
-          put_frag(a, c, static_cast<int>(row_own) + j, n, run + j, lane);
+          put_frag(a, c, row_own + j, n, run + j, lane);
         }
         umma_fence_before();
         __syncwarp();
@@ -784,15 +919,18 @@ struct GradArgs {
 
 constexpr int kGradTokens = 32;
 constexpr int kGradCols = 128;
-constexpr int kGradStages = 3;
+constexpr int kGradStages = 4;
 constexpr int kGradRow = kGradCols * 2 + 16;  // bytes of a staged row of q
 
 template <int MB>
 struct Grad {
-  static constexpr int kPRow = 16 * MB + 4;  // floats of a staged row of p
-  static constexpr int kStageBytes = kGradTokens * (kGradRow + kPRow * 4);
+  static constexpr int kPRow = 16 * MB * 4;         // bytes of a staged row of p
+  static constexpr int kStageBytes = kGradTokens * (kGradRow + kPRow);
+  static constexpr int kSplitRow = 16 * MB * 2 + 16;  // of one of the three bf16 parts of p
+  static constexpr int kSplitBytes = 3 * kGradTokens * kSplitRow;
   static constexpr int kSum = 16 * MB * kGradCols * 4;
-  static constexpr int kSmem = kGradStages * kStageBytes > kSum ? kGradStages * kStageBytes : kSum;
+  static constexpr int kRing = kGradStages * kStageBytes + kSplitBytes;
+  static constexpr int kSmem = kRing > kSum ? kRing : kSum;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
@@ -879,7 +1017,7 @@ grads_kernel(const GradArgs a, int split) {
     for (int i = threadIdx.x; i < kGradTokens * 4 * MB; i += 256) {
       const int t = i / (4 * MB), m = i % (4 * MB) * 4;
       const bool live = t < rows && m < a.r;
-      cp_async16(smem_u32(sp + (t * P::kPRow + m) * 4),
+      cp_async16(smem_u32(sp + t * P::kPRow + m * 4),
                  live ? a.p + static_cast<int64_t>(row + t) * a.r + m : a.p, live);
     }
   };
@@ -906,39 +1044,38 @@ grads_kernel(const GradArgs a, int split) {
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
     const uint8_t* st = stage_ptr(s);
-    const float* sp = reinterpret_cast<const float*>(st + kGradTokens * kGradRow);
+    uint8_t* parts = s_raw + kGradStages * P::kStageBytes;
+    for (int i = threadIdx.x; i < kGradTokens * 8 * MB; i += 256) {
+      const int t = i / (8 * MB), m = i % (8 * MB) * 2;
+      float2 f = *reinterpret_cast<const float2*>(st + kGradTokens * kGradRow + t * P::kPRow + m * 4);
+#pragma unroll
+      for (int h = 0; h < 3; ++h) {
+        const uint32_t w = pack_bf16x2(f.x, f.y);
+        f.x -= __uint_as_float(w << 16);
+        f.y -= __uint_as_float(w & 0xFFFF0000u);
+        *reinterpret_cast<uint32_t*>(parts + (h * kGradTokens + t) * P::kSplitRow + m * 2) = w;
+      }
+    }
+    __syncthreads();
     uint32_t bq[kGradTokens / 16][4];  // q: tokens x 16 columns of this warp, transposed on the way
 #pragma unroll
-    for (int kk = 0; kk < kGradTokens / 16; ++kk) {
-      const uint32_t addr = smem_u32(st + (kk * 16 + (lane & 15)) * kGradRow + (warp * 16 + (lane >> 4) * 8) * 2);
-      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(bq[kk][0]), "=r"(bq[kk][1]), "=r"(bq[kk][2]), "=r"(bq[kk][3])
-                   : "r"(addr)
-                   : "memory");
-    }
+    for (int kk = 0; kk < kGradTokens / 16; ++kk)
+      ldmatrix_trans(bq[kk], smem_u32(st + (kk * 16 + (lane & 15)) * kGradRow +
+                                      (warp * 16 + (lane >> 4) * 8) * 2));
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       float d[2][4] = {};  // this piece's sums
 #pragma unroll
-      for (int kk = 0; kk < kGradTokens / 16; ++kk) {
-        uint32_t w[3][4];
+      for (int kk = 0; kk < kGradTokens / 16; ++kk)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int m = 16 * i + g + (v & 1) * 8, t = kk * 16 + 2 * t4 + (v >> 1) * 8;
-          float f0 = sp[t * P::kPRow + m], f1 = sp[(t + 1) * P::kPRow + m];
-#pragma unroll
-          for (int h = 0; h < 3; ++h) {
-            w[h][v] = pack_bf16x2(f0, f1);
-            f0 -= __uint_as_float(w[h][v] << 16);
-            f1 -= __uint_as_float(w[h][v] & 0xFFFF0000u);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 3; ++h)
+        for (int h = 0; h < 3; ++h) {
+          uint32_t w[4];
+          const int t = kk * 16 + (lane & 7) + (lane & 16 ? 8 : 0), m = 16 * i + (lane & 8);
+          ldmatrix_trans(w, smem_u32(parts + (h * kGradTokens + t) * P::kSplitRow + m * 2));
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            mma_16816(d[j], w[h][0], w[h][1], w[h][2], w[h][3], bq[kk][2 * j], bq[kk][2 * j + 1]);
-      }
+            mma_16816(d[j], w[0], w[1], w[2], w[3], bq[kk][2 * j], bq[kk][2 * j + 1]);
+        }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -1003,15 +1140,16 @@ grads_kernel(const GradArgs a, int split) {
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // bf16 [rows, cols] with `stride` values from row to row, boxes of box_rows x 64 values.
+// (or fp32, boxes of 32 values)
 bool map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t stride,
-            uint32_t box_rows) {
+            uint32_t box_rows, bool fp32 = false) {
   const EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {stride * 2};
-  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint64_t strides[1] = {stride * (fp32 ? 4 : 2)};
+  const cuuint32_t box[2] = {fp32 ? 32u : 64u, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+  return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1044,18 +1182,21 @@ int pow2_at_most(int64_t v, int most) {
 }
 
 template <int MB, int NB>
-moe_status launch_shrink_as(ShrinkArgs a, cudaStream_t s) {
+moe_status launch_shrink_as(const ShrinkArgs& a, cudaStream_t s) {
   using P = Shrink<MB, NB>;
   auto kern = shrink_kernel<MB, NB>;
   static std::mutex mu;
   static bool done[64] = {};
   if (!opt_in(kern, P::kSmem, mu, done)) return MOE_ERR_CUDA;
-  const int64_t tiles = ceil_div(a.seg.T, P::kRows);
-  const int64_t per_tile = ceil_div(static_cast<int64_t>(a.seg.n_seg) * P::kRows, a.seg.T);
-  a.J = static_cast<int>(std::min<int64_t>(P::kRows, std::max<int64_t>(1, per_tile)));
-  const int split = pow2_at_most(std::min<int64_t>(4 * sm_count() / (tiles * a.J), a.K / 256), 8);
-  launch_clustered(kern, dim3(static_cast<unsigned>(tiles * split), a.J), 32 * kShrinkWarps, P::kSmem,
-                   split, s, a, split);
+  // CTAs a tile for its runs: more than it has runs only costs CTAs that end at once.  The
+  // reduction is split over a cluster where the CTAs that have work do not fill the SMs twice.
+  const int64_t tiles = ceil_div(a.seg.T, P::kRows), sms = sm_count();
+  const int64_t J = std::min<int64_t>(
+      {P::kRows, a.seg.n_seg, std::max(ceil_div(2 * static_cast<int64_t>(a.seg.n_seg), tiles), 4 * sms / tiles)});
+  const int64_t busy = std::min(tiles * J, tiles + a.seg.n_seg);
+  const int split = pow2_at_most(std::min<int64_t>(2 * sms / busy, a.K / 256), 8);
+  launch_clustered(kern, dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(std::max<int64_t>(J, 1))),
+                   32 * kShrinkWarps, P::kSmem, split, s, a, split);
   return launch_status();
 }
 
@@ -1124,15 +1265,17 @@ moe_status launch_project_as(ProjectArgs a, const Operands& o, cudaStream_t s) {
   static std::mutex mu;
   static bool done[64] = {};
   if (!opt_in(kern, F::kSmem, mu, done)) return MOE_ERR_CUDA;
-  CUtensorMap mw, mx, mt;
+  CUtensorMap mw, mx, mt, mu_;
+  a.x_rows = static_cast<int>(std::min<int64_t>(TN / CG, ceil_div(a.seg.T, 8) * 8));
   // the weight is [K, N] (rows of N), or for the backward [N, K]
   if (!(KMAJ ? map_2d(&mw, o.w, a.N, a.K, a.K, 128) : map_2d(&mw, o.w, a.K, a.N, a.N, 64)) ||
-      !map_2d(&mx, o.x, a.seg.T, a.K, o.x_stride, TN / CG) ||
-      !map_tables(&mt, o.table, a.seg.n_adapters, a.r, a.N))
+      !map_2d(&mx, o.x, a.seg.T, a.K, o.x_stride, a.x_rows) ||
+      !map_2d(&mu_, a.u, a.seg.T, a.r, a.r, 32, true) || !map_tables(&mt, o.table, a.seg.n_adapters, a.r, a.N))
     return MOE_ERR_CUDA;
   a.n_blocks = static_cast<int>(ceil_div(a.N, 128 * CG));
   a.t_blocks = static_cast<int>(ceil_div(a.seg.T, TN));
   a.slots = std::min(kMaxSlots, F::kTableBytes / (256 * ((a.r + 15) / 16 * 16)));
+  a.u_slots = std::min(kMaxSlots, F::kUBytes / ((a.r + 31) / 32 * kUBox));
   // Tokens inner: the weight is read once, the rows stay in the L2.  Rows that outgrow it while
   // the weight does not: columns inner.
   constexpr int64_t kL2Budget = 80ll << 20;
@@ -1150,7 +1293,7 @@ moe_status launch_project_as(ProjectArgs a, const Operands& o, cudaStream_t s) {
     clusters = std::min<int64_t>(tiles, sm_count());
   }
   launch_clustered(kern, dim3(static_cast<unsigned>(clusters * S * CG)), kThreads, F::kSmem, S * CG, s,
-                   mw, mx, mt, a);
+                   mw, mx, mt, mu_, a);
   return launch_status();
 }
 
@@ -1189,7 +1332,7 @@ moe_status launch_grads_as(const GradArgs& a, cudaStream_t s) {
   const int64_t blocks = ceil_div(a.K, kGradCols);
   const int64_t active = std::min(a.seg.n_adapters, a.seg.n_seg);
   const int split =
-      pow2_at_most(std::min<int64_t>(4 * sm_count() / (blocks * active), a.seg.T / 256), 8);
+      pow2_at_most(std::min<int64_t>(4 * sm_count() / (blocks * active), a.seg.T / 64), 8);
   launch_clustered(kern, dim3(static_cast<unsigned>(blocks * split), a.seg.n_adapters), 256, P::kSmem,
                    split, s, a, split);
   return launch_status();
@@ -1257,10 +1400,10 @@ MOE_API moe_status moe_adapter_project(const moe_adapter_params* p, const int32_
   if (!aligned16(y)) return MOE_ERR_UNSUPPORTED;
   const Segments seg = segments_of(p, seg_offsets, seg_adapter);
   const cudaStream_t s = as_cuda(stream);
-  st = launch_shrink(ShrinkArgs{seg, p->d, p->r, x, p->x_stride, a, scale, u, 1, dev_status}, s);
+  st = launch_shrink(ShrinkArgs{seg, p->d, p->r, x, p->x_stride, a, scale, u, dev_status}, s);
   if (st != MOE_OK) return st;
   return launch_project<false>(ProjectArgs{seg, p->d, p->n, p->r, u, y, p->y_stride,
-                                           p->y_type == MOE_DTYPE_FP32, 0, 0, 0, 0, dev_status},
+                                           p->y_type == MOE_DTYPE_FP32, 0, 0, 0, 0, 0, 0, dev_status},
                                Operands{x, p->x_stride, w, b}, s);
 }
 
@@ -1296,11 +1439,11 @@ MOE_API moe_status moe_adapter_project_backward(
   const Segments seg = segments_of(p, seg_offsets, seg_adapter);
   float* v = static_cast<float*>(ws);
   if (dx != nullptr || da != nullptr) {
-    st = launch_shrink(ShrinkArgs{seg, p->n, p->r, dy, p->y_stride, b, scale, v, 1, dev_status}, s);
+    st = launch_shrink(ShrinkArgs{seg, p->n, p->r, dy, p->y_stride, b, scale, v, dev_status}, s);
     if (st != MOE_OK) return st;
   }
   if (dx != nullptr) {
-    st = launch_project<true>(ProjectArgs{seg, p->n, p->d, p->r, v, dx, p->d, 0, 0, 0, 0, 0, dev_status},
+    st = launch_project<true>(ProjectArgs{seg, p->n, p->d, p->r, v, dx, p->d, 0, 0, 0, 0, 0, 0, 0, dev_status},
                               Operands{dy, p->y_stride, w, a}, s);
     if (st != MOE_OK) return st;
   }
