@@ -1,0 +1,723 @@
+// The projection of the rows with their adapters' part: kernel and launch of one shape.
+#pragma once
+
+#include "adapter.cuh"
+
+namespace moe {
+namespace adapter {
+namespace {
+
+// --------------------------------- project -----------------------------------
+//
+// D^T = W^T X^T: the weight's columns are the M operand, the tokens N, so a decode batch is a
+// narrow tile and the weight streams once.  Roles of the 320 threads:
+//   warp 0       TMA producer: [64 k x 128] of the weight (16 KB) and [tokens x 64 k] of x
+//   warp 1       tensor memory; lane 0 issues four MMAs (K = 16) a stage
+//   warps 2..9   epilogue: warp (quad, sub) has the 16 weight columns at 32 quad + 16 sub
+// The adapters' part is made by the epilogue warps, 32 tokens at a time: u B is r / d of the work
+// and a run of one adapter may be one token long, where tcgen05's narrowest tile is 16 columns
+// by 128 rows of the table.
+//   32 tokens of one adapter: mma.sync.  tcgen05's 16x256b loads give the accumulators in its
+//     layout, 16 weight columns by 8 tokens, so the table (16 columns, in registers, transposed
+//     by movmatrix, once a run) is multiplied with u onto the sums themselves.  u is split into
+//     two bf16 numbers a value by all warps together.
+//   otherwise: warp w takes tokens 4w .. 4w + 3, each with its own adapter's rows (four columns
+//     a lane, fp32), through shared memory.
+// Nothing of one request, not even 0 times an infinity, reaches another's rows.
+//
+// Shapes (launch_project has the rule):
+//   pair   a cluster of two CTAs, 256 weight columns by 256 tokens (cta_group::2), two
+//          accumulator buffers that fill the tensor memory
+//   flat   one CTA, 128 weight columns by TN = 64 or 128 tokens; the adapters' part is made
+//          while the MMAs run and waits in tensor memory.  S > 1: a cluster shares a tile, each
+//          CTA a part of the reduction; the CTA of rank c finishes its S-th of the tokens and
+//          gets the others' sums through distributed shared memory.
+// fp32 results of long reductions are summed in pieces of kPiece: the tensor cores' own fp32
+// sums lose 2^-26 a step (7168: 8e-6 of the result, in pieces of 1024 1e-6).
+// The weight, x and the tables are read before shrink has ended; u is waited for.
+
+constexpr int kThreads = 320;
+constexpr int kWBytes = 128 * 64 * 2;
+constexpr int kWBox = 64 * 64 * 2;
+constexpr int kPiece = 16;      // steps of 64 to a piece of an fp32 result's reduction
+constexpr int kMaxRank = 128;
+
+// 32 tokens of u: [value, remainder][32][r, padded to 16 and 8 more], so that eight rows of an
+// ldmatrix lie in other banks.
+__host__ __device__ constexpr int u_pitch(int rp) { return rp * 2 + 16; }
+// 32 tokens of the adapters' part: [32][128 columns and 4 more] fp32.
+constexpr int kPartPitch = 132;
+constexpr int kPieceBytes = 18 * 1024;  // either of them
+
+template <int TN, int S, int CG>
+struct Shape {
+  static constexpr int kStageBytes = kWBytes + TN / CG * 128;
+  static constexpr int kStages = CG == 2 ? 5 : TN == 128 ? (S == 1 ? 5 : 4) : 6;
+  static constexpr int kOwn = TN / S;
+  static constexpr int kRedBytes = (S - 1) * kOwn * 512;  // [S - 1][kOwn / 8][8][32] float4
+  // full[st], empty[st], tfull[2], tempty[2], group, red, drain
+  static constexpr int kBars = 2 * kStages + 8;
+  static constexpr int kTmem = CG == 2 ? 2 * TN : 4 * TN;  // two buffers, (flat) the sums
+  static constexpr int kSmem =
+      1024 + kStages * kStageBytes + 2 * kPieceBytes + kRedBytes + kBars * 8 + 2 * (kOwn + 8) * 4 + 16;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kOwn % 8 == 0 && kTmem <= 512, "shape");
+  static_assert(kPieceBytes >= 2 * 32 * u_pitch(kMaxRank) && kPieceBytes >= 32 * kPartPitch * 4, "pieces");
+};
+
+constexpr int kSeveral = -3;  // 32 tokens of several kinds
+
+// First token of tile t, and first weight column of this CTA's part of it.
+template <int TN, int CG>
+__device__ __forceinline__ void tile_at(const ProjectArgs& a, int t, int rank, int& row0, int& n0) {
+  const int nb = a.n_inner ? t % a.n_blocks : t / a.t_blocks;
+  const int tb = a.n_inner ? t / a.n_blocks : t % a.t_blocks;
+  row0 = tb * TN;
+  n0 = nb * 128 * CG + (CG == 2 ? rank * 128 : 0);
+}
+
+__device__ __forceinline__ void fma4(float4& acc, float u, const uint2& b) {
+  acc.x = fmaf(u, __uint_as_float(b.x << 16), acc.x);
+  acc.y = fmaf(u, __uint_as_float(b.x & 0xFFFF0000u), acc.y);
+  acc.z = fmaf(u, __uint_as_float(b.y << 16), acc.z);
+  acc.w = fmaf(u, __uint_as_float(b.y & 0xFFFF0000u), acc.w);
+}
+
+// acc += u B of four consecutive rows, columns n .. n + 3 of this lane; id: their adapters (rows
+// without one stay).  32 loads of a lane are on their way at once: 32 ranks of one adapter, or
+// eight of each of four (one row after the other, 16 ranks at a time, took three times as long).
+__device__ __forceinline__ void expand(const ProjectArgs& a, const int (&id)[4], int row, int lane,
+                                       int n, float4 (&acc)[4]) {
+  const bool same = id[0] >= 0 && id[0] == id[1] && id[0] == id[2] && id[0] == id[3];
+  const uint16_t* tab = a.table + n;
+  const int64_t table_size = static_cast<int64_t>(a.r) * a.N;
+  for (int c = 0; c < a.r; c += 32) {
+    float u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u[i] = id[i] >= 0 && c + lane < a.r ? a.u[static_cast<int64_t>(row + i) * a.r + c + lane] : 0.0f;
+    if (same) {
+      uint2 v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        v[j] = n < a.N && c + j < a.r ? __ldg(reinterpret_cast<const uint2*>(tab + id[0] * table_size +
+                                                                             static_cast<int64_t>(c + j) * a.N))
+                                      : make_uint2(0, 0);
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fma4(acc[i], __shfl_sync(0xFFFFFFFFu, u[i], j), v[j]);
+    } else {
+      for (int k = 0; k < 32 && c + k < a.r; k += 8) {  // (r is a multiple of 8)
+        uint2 v[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[i][j] = n < a.N && id[i] >= 0
+                          ? __ldg(reinterpret_cast<const uint2*>(tab + id[i] * table_size +
+                                                                 static_cast<int64_t>(c + k + j) * a.N))
+                          : make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) fma4(acc[i], __shfl_sync(0xFFFFFFFFu, u[i], k + j), v[i][j]);
+      }
+    }
+  }
+}
+
+// Stores 16 weight columns from n by 8 G tokens from row (the layout of umma_ld_frag); id: the
+// tokens'.
+template <int G>
+__device__ __forceinline__ void put_frags(const ProjectArgs& a, const float (&c)[G][4], int row, int n,
+                                          const int* id, int lane) {
+  const int g = lane >> 2, t4 = lane & 3;
+  if (a.y_fp32) {
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (id[8 * i + 2 * t4 + e] != kOutside) {
+          float* y = static_cast<float*>(a.y) + static_cast<int64_t>(row + 8 * i + 2 * t4 + e) * a.y_stride + n + g;
+          if (n < a.N) y[0] = c[i][e];
+          if (n + 8 < a.N) y[8] = c[i][2 + e];
+        }
+    return;
+  }
+  // rows become tokens: two 8 x 8 blocks transposed, then 4 columns to a lane
+  uint32_t d[G][2], other[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    d[i][0] = pack_bf16x2(c[i][0], c[i][1]);
+    d[i][1] = pack_bf16x2(c[i][2], c[i][3]);
+  }
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(d[i][h]));
+  const bool odd = t4 & 1;
+#pragma unroll
+  for (int i = 0; i < G; ++i) other[i] = __shfl_xor_sync(0xFFFFFFFFu, odd ? d[i][0] : d[i][1], 1);
+  const int col = n + (odd ? 8 + 2 * (t4 - 1) : 2 * t4);
+  uint16_t* y = static_cast<uint16_t*>(a.y) + static_cast<int64_t>(row + g) * a.y_stride + col;
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+    if (col < a.N && id[8 * i + g] != kOutside)
+      *reinterpret_cast<uint2*>(y + 8 * i * a.y_stride) =
+          odd ? make_uint2(other[i], d[i][1]) : make_uint2(d[i][0], other[i]);
+}
+
+// What the epilogue warps share.
+struct Epilogue {
+  uint8_t* piece;   // [2][kPieceBytes]
+  uint8_t* red;
+  int* id;          // [2][kOwn]: adapter of a token
+  int* whole;       // [2][8]: of 32 tokens the adapter of all, kNone where none has one, or kSeveral
+  volatile int* abort_flag;
+  uint32_t tfull, tempty, group_bar, red_bar;  // (tfull and tempty: two barriers each)
+  uint32_t tmem;
+  int first, step, total, rank, k0, k1, piece_steps;
+};
+
+// The epilogue warps' work; RB: blocks of 16 ranks.  True if partners' sums were awaited.
+template <int TN, int S, int CG, int RB>
+__device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s, int warp, int lane) {
+  constexpr int kOwn = TN / S, kChunks = (kOwn + 31) / 32, kGroups = kOwn < 32 ? kOwn / 8 : 4;
+  constexpr int kQuads = 4 * RB;                              // groups of four values of a row of u
+  constexpr int kLoads = (8 * kGroups * kQuads + 255) / 256;  // of them a thread
+  constexpr int kPitch = u_pitch(16 * RB);
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int w = warp - 2, quad = warp & 3, sub = w >> 2, tid = threadIdx.x - 64;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int m0 = 32 * quad + 16 * sub;
+  const int own0 = S > 1 ? s.rank * kOwn : 0;
+  const uint32_t taddr = s.tmem + (static_cast<uint32_t>(m0) << 16);
+  const uint32_t sums = taddr + 2 * TN;  // (flat) [kOwn], or in pieces [TN]
+  int buf = 0, par = 0, pb = 0;
+  uint32_t acc_ph = 0, group_ph = 0;
+  bool ok = true, waited = false, awaited = false;
+  // Barrier of the eight warps: false if one of them gave up.
+  auto meet = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(s.group_bar);
+    const bool all = __all_sync(kAll, wait_bounded(s.group_bar, group_ph, s.abort_flag, a.dev_status));
+    group_ph ^= 1u;
+    return all;
+  };
+  auto sums_ready = [&]() {
+    const bool all = __all_sync(kAll, wait_bounded(s.tfull + 8 * buf, acc_ph, s.abort_flag, a.dev_status));
+    umma_fence_after();
+    return all;
+  };
+  auto sums_read = [&]() {
+    umma_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (CG == 2) mbar_arrive_cluster(map_to_rank(s.tempty + 8 * buf, 0));
+      else mbar_arrive(s.tempty + 8 * buf);
+    }
+    if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
+  };
+  // 16 columns of the table of adapter `held`, mma.sync's first operand
+  uint32_t tab[RB][4];
+  int held = kNone, held_n = 0;
+  auto hold = [&](int e, int n) {
+    if (e == held && n == held_n) return;
+    held = e;
+    held_n = n;
+    const uint16_t* p = a.table + (static_cast<int64_t>(e) * a.r + g) * a.N + n + 2 * t4;
+#pragma unroll
+    for (int k = 0; k < RB; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // columns + 8 (q & 1), ranks + 8 (q >> 1)
+        const int rank_q = 16 * k + 8 * (q >> 1);
+        tab[k][q] = n + 8 * (q & 1) < a.N && rank_q < a.r
+                        ? __ldg(reinterpret_cast<const uint32_t*>(p + static_cast<int64_t>(rank_q) * a.N + 8 * (q & 1)))
+                        : 0u;
+      }
+#pragma unroll
+    for (int k = 0; k < RB; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(tab[k][q]));
+  };
+  // this thread's part of the u of 32 tokens, on its way
+  float4 ahead[kLoads];
+  auto fetch_u = [&](int row) {
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      const int i = tid + 256 * e, q = i % kQuads * 4;
+      ahead[e] = i < 8 * kGroups * kQuads && q < a.r
+                     ? *reinterpret_cast<const float4*>(a.u + static_cast<int64_t>(row + i / kQuads) * a.r + q)
+                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+  };
+  // this lane's row of the four 8 x 8 blocks of an ldmatrix of u (two of the values, two of what
+  // their rounding left): mma.sync's second operand of 8 tokens and 16 ranks
+  const uint32_t lu = smem_u32(s.piece) + (lane & 7) * kPitch + (lane & 8) * 2 + (lane & 16 ? 32 * kPitch : 0);
+
+  for (int t = s.first; t < s.total; t += s.step) {
+    int row0, n0;
+    tile_at<TN, CG>(a, t, s.rank, row0, n0);
+    const int n = n0 + m0, row_own = row0 + own0;
+    // ---- whose are the tokens: warp w finds out for 32 of them ----
+    int* ids = s.id + par * kOwn;
+    int* whole = s.whole + par * 8;
+    if (w < kChunks) {
+      const int id = row_adapters(a.seg, row_own + 32 * w, lane);
+      constexpr uint32_t kIn = kOwn < 32 ? (1u << (kOwn & 31)) - 1 : kAll;
+      const uint32_t has = __ballot_sync(kAll, id >= 0) & kIn;
+      const uint32_t same = __ballot_sync(kAll, id == __shfl_sync(kAll, id, 0)) & kIn;
+      if (32 * w + lane < kOwn) ids[32 * w + lane] = id;
+      if (lane == 0) whole[w] = has == 0 ? kNone : has == kIn && same == kIn ? id : kSeveral;
+    }
+    if (!meet()) break;
+    if (whole[0] >= 0) hold(whole[0], n);
+    if (!waited) {
+      pdl_wait();  // u; and what is written here may still be read by the kernels before
+      waited = true;
+    }
+    if (whole[0] >= 0) fetch_u(row_own);
+    if constexpr (CG == 2)
+      if (!sums_ready()) break;
+#pragma unroll 1
+    for (int ch = 0; ch < kChunks; ++ch) {
+      const int j = 32 * ch, kind = whole[ch];
+      uint8_t* piece = s.piece + pb * kPieceBytes;
+      const uint32_t at = lu + pb * kPieceBytes;
+      if (kind >= 0) {
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e) {
+          const int i = tid + 256 * e;
+          const float4 f = ahead[e];
+          const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
+          const uint32_t l0 = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
+          const uint32_t l1 = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+          if (i < 8 * kGroups * kQuads) {
+            uint8_t* dst = piece + i / kQuads * kPitch + i % kQuads * 8;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
+            *reinterpret_cast<uint2*>(dst + 32 * kPitch) = make_uint2(l0, l1);
+          }
+        }
+        hold(kind, n);
+      } else if (kind == kSeveral && 4 * w < kOwn - j) {
+        int id[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) id[i] = ids[j + 4 * w + i];
+        float4 acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int row = row_own + j + 4 * w;
+        expand(a, id, row, lane, n0 + 4 * lane, acc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(piece + ((4 * w + i) * kPartPitch + 4 * lane) * 4) = acc[i];
+      }
+      if (kind != kNone) {
+        ok = meet();
+        if (!ok) break;
+        pb ^= 1;  // (the other piece's readers have all come here)
+      }
+      if (ch + 1 < kChunks && whole[ch + 1] >= 0) fetch_u(row_own + j + 32);
+      float c[kGroups][4];
+      if constexpr (CG == 2) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) umma_ld_frag(taddr + buf * TN + j + 8 * i, c[i]);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) umma_ld_frag_wait(c[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[i][e] = 0.0f;
+      }
+      if (kind >= 0) {
+#pragma unroll
+        for (int k = 0; k < RB; ++k) {
+          uint32_t u[kGroups][4];
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i) ldmatrix(u[i], at + 8 * i * kPitch + k * 32);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+              mma_16816(c[i], tab[k][0], tab[k][1], tab[k][2], tab[k][3], u[i][2 * h], u[i][2 * h + 1]);
+        }
+      } else if (kind == kSeveral) {
+        const float* part = reinterpret_cast<const float*>(piece) + m0 + g;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            c[i][e] += part[(8 * i + 2 * t4 + (e & 1)) * kPartPitch + 8 * (e >> 1)];
+      }
+      if constexpr (CG == 2) {
+        put_frags<kGroups>(a, c, row_own + j, n, ids + j, lane);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) umma_st_frag(sums + own0 + j + 8 * i, c[i]);
+      }
+    }
+    if (!ok) break;
+    if constexpr (CG == 2) {
+      sums_read();
+    } else {
+      const bool pieces = s.k0 + s.piece_steps < s.k1;
+      if (S > 1 && pieces) {  // the other tokens' sums start at zero
+        const float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < TN; j += 8)
+          if (j < own0 || j >= own0 + kOwn) umma_st_frag(sums + j, z);
+      }
+      umma_st_wait();
+      // every piece but the last onto the sums
+      for (int kp = s.k0; kp + s.piece_steps < s.k1; kp += s.piece_steps) {
+        ok = sums_ready();
+        if (!ok) break;
+        for (int j = 0; j < TN; j += 32) {
+          float c[4][4], q[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            umma_ld_frag(taddr + buf * TN + j + 8 * i, c[i]);
+            umma_ld_frag(sums + j + 8 * i, q[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            umma_ld_frag_wait(c[i]);
+            umma_ld_frag_wait(q[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[i][e] += q[i][e];
+            umma_st_frag(sums + j + 8 * i, c[i]);
+          }
+        }
+        umma_st_wait();
+        sums_read();
+      }
+      if (!ok || !sums_ready()) break;
+      if constexpr (S > 1) {
+        awaited = true;
+        for (int i = 1; i < S; ++i) {  // the partners' tokens first
+          const int owner = (s.rank + i) % S;
+          const uint32_t bar = map_to_rank(s.red_bar, owner);
+          const uint32_t dst =
+              map_to_rank(smem_u32(s.red + (S - 1 - i) * kOwn * 512 + w * 512 + lane * 16), owner);
+          for (int j = 0; j < kOwn; j += 8) {
+            float c[4];
+            umma_ld_frag(taddr + buf * TN + owner * kOwn + j, c);
+            umma_ld_frag_wait(c);
+            if (pieces) {
+              float q[4];
+              umma_ld_frag(sums + owner * kOwn + j, q);
+              umma_ld_frag_wait(q);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) c[e] += q[e];
+            }
+            st_async4(dst + j * 512, bar, c[0], c[1], c[2], c[3]);
+          }
+        }
+        if (!__all_sync(kAll, wait_bounded<true>(s.red_bar, 0, s.abort_flag, a.dev_status))) break;
+      }
+      for (int j = 0; j < kOwn; j += 8 * kGroups) {
+        float c[kGroups][4], q[kGroups][4];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          umma_ld_frag(taddr + buf * TN + own0 + j + 8 * i, c[i]);
+          umma_ld_frag(sums + own0 + j + 8 * i, q[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+          umma_ld_frag_wait(c[i]);
+          umma_ld_frag_wait(q[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[i][e] += q[i][e];
+          if constexpr (S > 1) {
+#pragma unroll
+            for (int o = 0; o < S - 1; ++o) {
+              const float4 p = *reinterpret_cast<const float4*>(s.red + o * kOwn * 512 + (j + 8 * i) * 512 +
+                                                                w * 512 + lane * 16);
+              c[i][0] += p.x; c[i][1] += p.y; c[i][2] += p.z; c[i][3] += p.w;
+            }
+          }
+        }
+        put_frags<kGroups>(a, c, row_own + j, n, ids + j, lane);
+      }
+      sums_read();
+    }
+    par ^= 1;
+  }
+  return awaited;
+}
+
+template <int TN, int S, int CG, bool KMAJ>
+__global__ void __launch_bounds__(kThreads, 1)
+project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+               const ProjectArgs a) {
+  using F = Shape<TN, S, CG>;
+  static_assert(CG == 1 || S == 1, "one kind of cluster");
+  constexpr int kStages = F::kStages, kOwn = F::kOwn;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stage_base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_piece = stage_base + kStages * F::kStageBytes;  // two
+  uint8_t* s_red = s_piece + 2 * kPieceBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_red + F::kRedBytes);
+  int* s_id = reinterpret_cast<int*>(bars + F::kBars);  // [2][kOwn]: adapter of a token
+  // [2][8]: of 32 tokens the adapter of all, kNone where none has one, or kSeveral
+  int* s_whole = s_id + 2 * kOwn;
+  volatile int* abort_flag = s_whole + 2 * 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_whole + 2 * 8) + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kCluster = S * CG;
+  const int rank = kCluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const bool leader = CG == 1 || rank == 0;
+  const int first = static_cast<int>(blockIdx.x) / kCluster;
+  const int step = static_cast<int>(gridDim.x) / kCluster;
+  const int total = a.n_blocks * a.t_blocks;
+  const int steps = (a.K + 63) / 64;
+  const int k0 = S > 1 ? rank * steps / S : 0, k1 = S > 1 ? (rank + 1) * steps / S : steps;
+  const int piece = CG == 1 && a.y_fp32 ? kPiece : steps;
+  const uint32_t stage_tx = kWBytes + a.x_rows * 128;
+
+  auto full_bar = [&](int s) { return smem_u32(bars + s); };
+  auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
+  auto tfull_bar = [&](int b) { return smem_u32(bars + 2 * kStages + b); };
+  auto tempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 2 + b); };
+  const uint32_t group_bar = smem_u32(bars + 2 * kStages + 4);
+  const uint32_t red_bar = group_bar + 8;
+  const uint32_t drain_bar = red_bar + 8;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 8 * CG);  // one arrival per epilogue warp
+    }
+    mbar_init(group_bar, 8);
+    mbar_init(red_bar, 1);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (S > 1) mbar_arrive_expect_tx(red_bar, F::kRedBytes);
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_x)) : "memory");
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) umma_alloc_pair(smem_u32(tmem_slot), F::kTmem);
+    else umma_alloc(smem_u32(tmem_slot), F::kTmem);
+  }
+  umma_fence_before();
+  __syncthreads();
+  if constexpr (kCluster > 1) cluster_sync();  // the partners' barriers are initialised
+  umma_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool awaited = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- TMA producer ----
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step) {
+        int row0, n0;
+        tile_at<TN, CG>(a, t, rank, row0, n0);
+        if (CG == 2) row0 += rank * (TN / 2);
+        for (int k = k0; k < k1; ++k) {
+          if (!wait_bounded(empty_bar(s), ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
+          const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
+          if constexpr (CG == 2) {
+            const uint32_t bar = map_to_rank(full_bar(s), 0);
+            if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * stage_tx);
+            if (KMAJ) {
+              tma_load_2d_pair(st, &map_w, bar, k * 64, n0);
+            } else {
+              tma_load_2d_pair(st, &map_w, bar, n0, k * 64);
+              tma_load_2d_pair(st + kWBox, &map_w, bar, n0 + 64, k * 64);
+            }
+            tma_load_2d_pair(st + kWBytes, &map_x, bar, k * 64, row0);
+          } else {
+            mbar_arrive_expect_tx(full_bar(s), stage_tx);
+            if (KMAJ) {
+              tma_load_2d(st, &map_w, full_bar(s), k * 64, n0);
+            } else {
+              tma_load_2d(st, &map_w, full_bar(s), n0, k * 64);
+              tma_load_2d(st + kWBox, &map_w, full_bar(s), n0 + 64, k * 64);
+            }
+            tma_load_2d(st + kWBytes, &map_x, full_bar(s), k * 64, row0);
+          }
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (!ok) {  // copies in flight land before the shared memory is given up
+        if (leader) {
+          for (int i = 0; i < kStages; ++i) {
+            if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+            wait_drain(full_bar(s), ph);
+          }
+        } else {  // they are counted on the leader's barriers: a fixed window
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < 2000000ull) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---- MMA issuer ----
+      constexpr uint32_t idesc = umma_idesc_bf16(128 * CG, TN, !KMAJ);
+      int s = 0, buf = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true, issued = false;
+      for (int t = first; t < total && ok; t += step) {
+        for (int kp = k0; kp < k1 && ok; kp += piece) {
+          if (!wait_bounded(tempty_bar(buf), acc_ph ^ 1u, abort_flag, a.dev_status)) { ok = false; break; }
+          umma_fence_after();
+          const int ke = min(kp + piece, k1);
+          for (int k = kp; k < ke; ++k) {
+            if (!wait_bounded(full_bar(s), ph, abort_flag, a.dev_status)) { ok = false; break; }
+            umma_fence_after();
+            const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ad = KMAJ ? umma_desc(st + kk * 32) : umma_desc_mn(st + kk * 16 * 128, kWBox);
+              const uint64_t bd = umma_desc(st + kWBytes + kk * 32);
+              if constexpr (CG == 2) umma_bf16_pair(tmem + buf * TN, ad, bd, idesc, k > kp || kk > 0);
+              else umma_bf16(tmem + buf * TN, ad, bd, idesc, k > kp || kk > 0);
+            }
+            issued = true;
+            if constexpr (CG == 2) umma_commit_pair(empty_bar(s), 0x3);
+            else umma_commit(empty_bar(s));
+            if (++s == kStages) { s = 0; ph ^= 1u; }
+          }
+          if (!ok) break;
+          if constexpr (CG == 2) umma_commit_pair(tfull_bar(buf), 0x3);
+          else umma_commit(tfull_bar(buf));
+          if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
+        }
+      }
+      if (!ok && issued) {
+        if constexpr (CG == 2) umma_commit_pair(drain_bar, 0x1);
+        else umma_commit(drain_bar);
+        wait_drain(drain_bar, 0);
+      }
+    }
+  } else {
+    const Epilogue e{s_piece, s_red, s_id, s_whole, abort_flag, tfull_bar(0), tempty_bar(0), group_bar,
+                     red_bar, tmem, first, step, total, rank, k0, k1, piece};
+    awaited = a.r <= 16   ? epilogue<TN, S, CG, 1>(a, e, warp, lane)
+              : a.r <= 32 ? epilogue<TN, S, CG, 2>(a, e, warp, lane)
+              : a.r <= 64 ? epilogue<TN, S, CG, 4>(a, e, warp, lane)
+                          : epilogue<TN, S, CG, 8>(a, e, warp, lane);
+  }
+
+  // ---- teardown ----
+  __syncwarp();
+  umma_fence_before();
+  __syncthreads();
+  if constexpr (kCluster > 1) {
+    cluster_sync();  // no CTA leaves while a partner may still reach it
+    // (after a wait that gave up: nor before the sums that were on their way)
+    if (S > 1 && threadIdx.x == 64 && awaited && *abort_flag) wait_drain(red_bar, 0);
+  }
+  umma_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    if constexpr (CG == 2) umma_dealloc_pair(tmem, F::kTmem);
+    else umma_dealloc(tmem, F::kTmem);
+  }
+  pdl_trigger();
+}
+
+// bf16 [rows, cols] with `stride` values from row to row, boxes of box_rows x 64 values.
+bool map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t stride,
+            uint32_t box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {stride * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs of CTAs that can be resident at once, read once per kernel and device.
+template <typename Kernel>
+int resident_pairs(Kernel kern, int smem, std::mutex& mu, int (&cache)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sm_count() & ~1));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = sm_count() / 2;
+    }
+    cache[dev] = n;
+  }
+  return cache[dev];
+}
+
+template <int TN, int S, int CG, bool KMAJ>
+moe_status launch_project_as(ProjectArgs a, const Operands& o, cudaStream_t s) {
+  using F = Shape<TN, S, CG>;
+  auto kern = project_kernel<TN, S, CG, KMAJ>;
+  static std::mutex mu;
+  static bool done[64] = {};
+  if (!opt_in(kern, F::kSmem, mu, done)) return MOE_ERR_CUDA;
+  CUtensorMap mw, mx;
+  a.x_rows = static_cast<int>(std::min<int64_t>(TN / CG, ceil_div(a.seg.T, 8) * 8));
+  // the weight is [K, N] (rows of N), or for the backward [N, K]
+  if (!(KMAJ ? map_2d(&mw, o.w, a.N, a.K, a.K, 128) : map_2d(&mw, o.w, a.K, a.N, a.N, 64)) ||
+      !map_2d(&mx, o.x, a.seg.T, a.K, o.x_stride, a.x_rows))
+    return MOE_ERR_CUDA;
+  a.n_blocks = static_cast<int>(ceil_div(a.N, 128 * CG));
+  a.t_blocks = static_cast<int>(ceil_div(a.seg.T, TN));
+  // Tokens inner: the weight is read once, the rows stay in the L2.  Rows that outgrow it while
+  // the weight does not: columns inner.
+  constexpr int64_t kL2Budget = 80ll << 20;
+  a.n_inner = static_cast<int64_t>(a.seg.T) * a.K * 2 > kL2Budget &&
+              static_cast<int64_t>(a.N) * a.K * 2 <= kL2Budget;
+  const int64_t tiles = static_cast<int64_t>(a.n_blocks) * a.t_blocks;
+  int64_t clusters = tiles;
+  if constexpr (CG == 2) {
+    static std::mutex mu2;
+    static int pairs[64] = {};
+    const int n = resident_pairs(kern, F::kSmem, mu2, pairs);
+    if (n <= 0) return MOE_ERR_CUDA;
+    clusters = std::min<int64_t>(tiles, n);
+  } else if (S == 1) {
+    clusters = std::min<int64_t>(tiles, sm_count());
+  }
+  launch_clustered(kern, dim3(static_cast<unsigned>(clusters * S * CG)), kThreads, F::kSmem, S * CG, s,
+                   mw, mx, a);
+  return launch_status();
+}
+
+template <int TN, bool KMAJ>
+moe_status launch_flat(const ProjectArgs& a, const Operands& o, int split, cudaStream_t s) {
+  switch (split) {
+    case 8: return launch_project_as<TN, 8, 1, KMAJ>(a, o, s);
+    case 4: return launch_project_as<TN, 4, 1, KMAJ>(a, o, s);
+    case 2: return launch_project_as<TN, 2, 1, KMAJ>(a, o, s);
+    default: return launch_project_as<TN, 1, 1, KMAJ>(a, o, s);
+  }
+}
+
+}  // namespace
+}  // namespace adapter
+}  // namespace moe

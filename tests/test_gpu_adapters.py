@@ -90,6 +90,9 @@ SHAPES = [
     # tiles of two CTAs, forward and (turned around) backward
     (2290, [3] + list(range(4, 24)) + [700, 701, 1500, 2281], [q % 8 - 1 for q in range(24)], 200, 2040, 72, 7),
     (2290, [0, 9, 1000, 1000, 2290], [2, 1, 0, 1], 2040, 200, 16, 3),
+    # runs between rows without an adapter, inside 32 rows
+    (2200, [0, 34, 50, 64, 70, 2180], [-1, 1, -1, 0, -1], 200, 2040, 24, 2),
+    (100, [1, 4, 9, 40, 60, 97], [-1, 1, -1, 0, -1], 328, 136, 8, 2),
     (700, [0] * 300 + [400] * 200 + [700], [q % 3 for q in range(500)], 128, 128, 8, 3),
 ]
 
