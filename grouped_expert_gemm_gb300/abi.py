@@ -115,7 +115,8 @@ class AdapterParams(ctypes.Structure):
 class GradTensor(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
                 ("type", ctypes.c_int32), ("group", ctypes.c_int32),
-                ("first_chunk", ctypes.c_int64)]
+                ("first_chunk", ctypes.c_int64), ("group_begin", ctypes.c_int64),
+                ("group_end", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -717,7 +718,7 @@ def moe_adapter_project_backward(p: AdapterParams, seg_offsets, seg_adapter, x, 
 
 
 def moe_grad_plan(tensors, n_groups: int) -> int:
-    """tensors: a ctypes array of GradTensor on the host (first_chunk is filled in); returns
+    """tensors: a ctypes array of GradTensor on the host (its last three fields are filled in); returns
     the number of chunks."""
     chunks = ctypes.c_int64()
     _check("moe_grad_plan", lib().moe_grad_plan(len(tensors), tensors, n_groups,

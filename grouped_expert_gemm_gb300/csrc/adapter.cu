@@ -19,25 +19,16 @@ namespace {
 
 // --------------------------------- shrink ------------------------------------
 //
-// A tile of 8 NB rows holds runs of rows with one adapter; CTA j of a tile (blockIdx.y) takes its
-// runs j, j + J, ...  The table's rows are the M operand, the tokens N = 8 at a time, so a run
+// Segments of few rows (longer ones: adapter_shrink.cu).  A CTA takes a piece of 8 NB rows of
+// one segment; where there are more than kPieceSegs segments, a tile of 8 NB rows holds runs of
+// rows with one adapter, and CTA j of a tile (blockIdx.y) takes its runs j, j + J, ... (finding a
+// piece takes a look at the segments in front of it).  The table's rows are the M operand, the tokens N = 8 at a time, so a run
 // of one token costs one column block and nothing is shared between runs.  Both operands come
 // from global memory as 16 bytes a lane: lane t of a row takes values 8t .. 8t+7 of 32, and the
 // MMA's slots are dealt from those in the same order on both sides (a sum does not mind the order
 // of its terms).  The warps split the reduction (a cluster too, where there are few CTAs).
 
 constexpr int kShrinkWarps = 8;
-
-struct ShrinkArgs {
-  Segments seg;
-  int K, r;
-  const uint16_t* x;
-  int64_t x_stride;
-  const uint16_t* table;  // [n_adapters, r, K]
-  const float* scale;     // [n_adapters]
-  float* u;               // [T, r]
-  uint32_t* dev_status;
-};
 
 template <int MB, int NB>
 struct Shrink {
@@ -52,9 +43,11 @@ struct Shrink {
   static constexpr int kAhead = kMB == 1 ? (NB == 1 ? 4 : 2) : kMB == 2 ? (NB == 1 ? 3 : 2) : NB == 1 ? 2 : 1;
 };
 
+constexpr int kPieceSegs = 2048;
+
 template <int MB, int NB>
 __global__ void __launch_bounds__(32 * kShrinkWarps, 2)
-shrink_kernel(const ShrinkArgs a, int split) {
+shrink_kernel(const ShrinkArgs a, int split, int pieces_mode) {
   using P = Shrink<MB, NB>;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   extern __shared__ float s_part[];            // [kSlices][16 MB][kPitch]
@@ -62,7 +55,6 @@ shrink_kernel(const ShrinkArgs a, int split) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int row0 = static_cast<int>(blockIdx.x) / split * P::kRows;
   const int group = warp % P::kRankGroups, slice = warp / P::kRankGroups;
   const int m0 = group * P::kMB * 16;
   const int pieces = (a.K + 31) / 32;
@@ -70,18 +62,18 @@ shrink_kernel(const ShrinkArgs a, int split) {
 
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the segment table, looked over once
-    for (int q = threadIdx.x; q < a.seg.n_seg; q += blockDim.x) {
-      const int b = seg_begin(a.seg, q), e = seg_begin(a.seg, q + 1);
-      if (b < 0 || e < b || e > a.seg.T) report(a.dev_status, MOE_DEV_BAD_MAP);
-      const int id = __ldg(a.seg.adapter + q);
-      if (id < kNone || id >= a.seg.n_adapters) report(a.dev_status, MOE_DEV_BAD_ADAPTER);
-    }
-  }
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_segments(a.seg, a.dev_status);
 
   // runs of the tile: every warp finds them for itself
-  const int id = row_adapters(a.seg, row0, lane);
+  int row0 = static_cast<int>(blockIdx.x) / split * P::kRows, id;
   const uint32_t in_tile = P::kRows == 32 ? kAll : (1u << P::kRows) - 1;
+  if (pieces_mode) {
+    const Piece p = piece_of<32 * kShrinkWarps>(a.seg, static_cast<int>(blockIdx.x) / split, P::kRows);
+    row0 = p.row;
+    id = lane < p.rows ? p.adapter : kOutside;
+  } else {
+    id = row_adapters(a.seg, row0, lane);
+  }
   if (blockIdx.y == 0 && rank == 0) {
     uint32_t none = __ballot_sync(kAll, id == kNone) & in_tile;
     for (; none != 0; none &= none - 1)
@@ -424,12 +416,6 @@ grads_kernel(const GradArgs a, int split) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-int pow2_at_most(int64_t v, int most) {
-  int p = 1;
-  while (2 * p <= v && 2 * p <= most) p *= 2;
-  return p;
-}
-
 template <int MB, int NB>
 moe_status launch_shrink_as(const ShrinkArgs& a, cudaStream_t s) {
   using P = Shrink<MB, NB>;
@@ -437,19 +423,20 @@ moe_status launch_shrink_as(const ShrinkArgs& a, cudaStream_t s) {
   static std::mutex mu;
   static bool done[64] = {};
   if (!opt_in(kern, P::kSmem, mu, done)) return MOE_ERR_CUDA;
-  // CTAs a tile for its runs: more than it has runs only costs CTAs that end at once.  The
-  // reduction is split over a cluster where the CTAs that have work do not fill the SMs twice.
-  const int64_t tiles = ceil_div(a.seg.T, P::kRows), sms = sm_count();
-  const int64_t J = std::min<int64_t>(
-      {P::kRows, a.seg.n_seg, std::max(ceil_div(2 * static_cast<int64_t>(a.seg.n_seg), tiles), 4 * sms / tiles)});
-  const int64_t busy = std::min(tiles * J, tiles + a.seg.n_seg);
-  const int split = pow2_at_most(std::min<int64_t>(2 * sms / busy, a.K / 256), 8);
-  launch_clustered(kern, dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(std::max<int64_t>(J, 1))),
-                   32 * kShrinkWarps, P::kSmem, split, s, a, split);
+  // The reduction is split over a cluster where the CTAs that have work do not fill the SMs twice.
+  const int64_t tiles = ceil_div(a.seg.T, P::kRows), sms = sm_count(), n_seg = a.seg.n_seg;
+  const bool pieces = n_seg <= kPieceSegs;
+  const int64_t grid = pieces ? tiles + n_seg : tiles;
+  const int64_t J = pieces ? 1 : std::min<int64_t>(P::kRows, ceil_div(2 * n_seg, tiles));
+  const int split = pow2_at_most(std::min<int64_t>(2 * sms / (grid * J), a.K / 256), 8);
+  launch_clustered(kern, dim3(static_cast<unsigned>(grid * split), static_cast<unsigned>(J)),
+                   32 * kShrinkWarps, P::kSmem, split, s, a, split, static_cast<int>(pieces));
   return launch_status();
 }
 
 moe_status launch_shrink(const ShrinkArgs& a, cudaStream_t s) {
+  // Rows of a segment on average: from 32 on tiles of 128 rows by the tensor memory accelerator
+  if (a.seg.T >= 32 * static_cast<int64_t>(a.seg.n_seg)) return shrink_long(a, s);
   const bool narrow = a.seg.T <= 256;
   const int mb = (a.r + 15) / 16;
   if (mb == 1) return narrow ? launch_shrink_as<1, 1>(a, s) : launch_shrink_as<1, 4>(a, s);
@@ -472,7 +459,7 @@ moe_status launch_project(const ProjectArgs& a, const Operands& o, bool kmaj, cu
   const int split = pow2_at_most(std::min(sms / tiles, steps), 8);
   const int64_t flat = split > 1 ? ceil_div(steps, split) : ceil_div(tiles, sms) * steps;
   const int64_t pair = ceil_div(ceil_div(a.N, 256) * ceil_div(T, 256), sms / 2) * steps * 2;
-  if (!a.y_fp32 && 10 * pair <= 13 * flat) return project_pair(a, o, kmaj, s);
+  if (!a.y_fp32 && T >= 32 * static_cast<int64_t>(a.seg.n_seg) && 10 * pair <= 13 * flat) return project_pair(a, o, kmaj, s);
   return kmaj ? project_flat128_kmaj(a, o, split, s) : project_flat128(a, o, split, s);
 }
 

@@ -43,6 +43,21 @@ moe_status project_flat128(const ProjectArgs& a, const Operands& o, int split, c
 moe_status project_flat128_kmaj(const ProjectArgs& a, const Operands& o, int split, cudaStream_t s);
 moe_status project_pair(const ProjectArgs& a, const Operands& o, bool kmaj, cudaStream_t s);
 
+// u [T, r] = scale (x table^T) of each row's own table.
+struct ShrinkArgs {
+  Segments seg;
+  int K, r;
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint16_t* table;  // [n_adapters, r, K]
+  const float* scale;     // [n_adapters]
+  float* u;               // [T, r]
+  uint32_t* dev_status;
+};
+
+// Segments long enough for tiles of 128 rows (adapter_shrink.cu).
+moe_status shrink_long(const ShrinkArgs& a, cudaStream_t s);
+
 namespace {
 
 constexpr int kOutside = -2;  // a row of no segment
@@ -95,6 +110,60 @@ __device__ __forceinline__ int row_adapters(const Segments& s, int row0, int lan
   return seg_adapter(s, seg);
 }
 
+// The segment table, looked over once a call.
+__device__ __forceinline__ void check_segments(const Segments& s, uint32_t* dev_status) {
+  for (int q = threadIdx.x; q < s.n_seg; q += blockDim.x) {
+    const int b = seg_begin(s, q), e = seg_begin(s, q + 1);
+    if (b < 0 || e < b || e > s.T) report(dev_status, MOE_DEV_BAD_MAP);
+    const int id = __ldg(s.adapter + q);
+    if (id < kNone || id >= s.n_adapters) report(dev_status, MOE_DEV_BAD_ADAPTER);
+  }
+}
+
+// Each segment cut into pieces of `size` rows (the last one shorter): piece `index` of them all,
+// by the whole block.  There are at most n_seg + T / size (offsets out of order may name more;
+// those are left out).
+struct Piece {
+  int row, rows, adapter;  // rows = 0: there is no such piece
+};
+template <int THREADS>
+__device__ __forceinline__ Piece piece_of(const Segments& s, int index, int size) {
+  __shared__ int s_sum[THREADS / 32];
+  __shared__ Piece s_piece;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) s_piece.rows = 0;
+  int64_t before = 0;  // pieces of the segments in front of this round's
+  for (int q0 = 0; q0 < s.n_seg; q0 += THREADS) {
+    const int q = q0 + static_cast<int>(threadIdx.x);
+    int b = 0, e = 0;
+    if (q < s.n_seg) seg_rows(s, q, b, e);
+    const int n = e > b ? (e - b + size - 1) / size : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();  // (the round before has been read)
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int64_t at = before + incl - n, total = before;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) at += s_sum[w];
+      total += s_sum[w];
+    }
+    if (index >= at && index < at + n) {
+      const int row = b + static_cast<int>(index - at) * size;
+      s_piece = Piece{row, min(size, e - row), seg_adapter(s, q)};
+    }
+    before = total;
+    if (total > index) break;
+  }
+  __syncthreads();
+  return s_piece;
+}
+
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -145,6 +214,41 @@ void launch_clustered(void (*kern)(KArgs...), dim3 grid, int threads, int smem, 
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// bf16 [rows, cols] with `stride` values from row to row, boxes of box_rows x 64 values.
+inline bool map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t stride,
+            uint32_t box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {stride * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16 tables [n_adapters, r, cols], boxes of box_rows x 64 values of one adapter: one that passes
+// r is filled with zeros and not with the next adapter's rows.
+inline bool map_tables(CUtensorMap* m, const void* base, uint64_t n_adapters, uint64_t r, uint64_t cols,
+                       uint32_t box_rows) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {cols, r, n_adapters};
+  const cuuint64_t strides[2] = {cols * 2, cols * r * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline int pow2_at_most(int64_t v, int most) {
+  int p = 1;
+  while (2 * p <= v && 2 * p <= most) p *= 2;
+  return p;
 }
 
 }  // namespace

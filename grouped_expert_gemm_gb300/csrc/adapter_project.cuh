@@ -630,20 +630,6 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   pdl_trigger();
 }
 
-// bf16 [rows, cols] with `stride` values from row to row, boxes of box_rows x 64 values.
-bool map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t stride,
-            uint32_t box_rows) {
-  const EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {stride * 2};
-  const cuuint32_t box[2] = {64, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Pairs of CTAs that can be resident at once, read once per kernel and device.
 template <typename Kernel>
 int resident_pairs(Kernel kern, int smem, std::mutex& mu, int (&cache)[64]) {

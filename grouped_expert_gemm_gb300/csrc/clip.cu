@@ -4,7 +4,7 @@
 //   out = round(x c_g)
 //
 // Bound: HBM (the tensors twice in, once out, less what the second pass finds in the L2).
-// The elements of all tensors are one line of chunks (of kChunk elements, none across two
+// The elements of all tensors are one line of chunks (of kChunkBytes, none across two
 // tensors), cut into as many equal parts as there are blocks.  Tensors of a group stand
 // together, so the pairs (block, group) that occur form a staircase along the line and b + g
 // numbers them without gaps or clashes: each block writes the sum of its part of group g to
@@ -12,8 +12,8 @@
 // order.  No atomics, no counters: the same bits on every run, and nothing to clear.  The
 // second pass walks every part backwards: its end is what the first pass read last.
 //
-// Squares are summed in fp32 over a thread's 32 values of a chunk and in fp64 from there on;
-// where those 32 squares leave fp32's range (values beyond 2^60 or below 2^-40) the values are
+// Squares are summed in fp32 over a thread's 16 or 32 values of a chunk and in fp64 from there on;
+// where those squares leave fp32's range (values beyond 2^60 or below 2^-40) the values are
 // scaled by a power of two first, so any finite tensor has its norm.
 #include <algorithm>
 
@@ -23,7 +23,10 @@ namespace moe {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kChunk = 8192;  // elements; a power of two
+constexpr int kChunkBytes = 8192;
+constexpr int kBatch = 4;  // chunks of one tensor that a block loads at once
+constexpr int kVecs = kBatch * kChunkBytes / 16 / kBlock;  // their vectors a thread, at most
+constexpr int kPerSm = 2;   // blocks: more of them were slower (four: 617 us for 1.2 GB, two: 554)
 constexpr int kMaxBlocks = 1024;
 
 struct ClipArgs {
@@ -37,12 +40,16 @@ struct ClipArgs {
 };
 
 // The last tensor whose first chunk is at or before c: the one that holds it (tensors without
-// elements have no chunk and are passed over).
+// elements have no chunk and are passed over).  By the whole block, 256 tensors at a time.
 __device__ __forceinline__ int tensor_of(const ClipArgs& a, int64_t c) {
-  int lo = 0, hi = a.n_tensors - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.tensors[mid].first_chunk <= c) lo = mid; else hi = mid - 1;
+  int lo = 0, n = a.n_tensors;
+  while (n > 1) {
+    const int stride = (n + kBlock - 1) / kBlock;
+    const int at = static_cast<int>(threadIdx.x) * stride;
+    const int k = __syncthreads_count(at < n && a.tensors[lo + at].first_chunk <= c);
+    const int skip = k > 0 ? (k - 1) * stride : 0;
+    lo += skip;
+    n = min(stride, n - skip);
   }
   return lo;
 }
@@ -55,23 +62,8 @@ __device__ __forceinline__ int part_of(int64_t c, int64_t chunks, int64_t parts)
   return static_cast<int>(((c + 1) * parts + chunks - 1) / chunks - 1);
 }
 
-// One chunk of a tensor: `head` elements up to a 16-byte boundary of the source, `vecs` vectors
-// of 16 bytes, `tail` elements.
-template <typename T>
-struct Piece {
-  static constexpr int kPer = 16 / sizeof(T);
-  const T* src;
-  int head, vecs, tail;
-  __device__ __forceinline__ Piece(const moe_grad_tensor& t, int64_t chunk) {
-    const int64_t at = (chunk - t.first_chunk) * kChunk;
-    const int n = static_cast<int>(min(t.count - at, static_cast<int64_t>(kChunk)));
-    src = static_cast<const T*>(t.grad) + at;
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
-    head = min(n, (kPer - off) % kPer);
-    vecs = (n - head) / kPer;
-    tail = n - head - vecs * kPer;
-  }
-};
+__host__ __device__ constexpr int elem_bytes(int type) { return type == MOE_DTYPE_BF16 ? 2 : 4; }
+__host__ __device__ constexpr int chunk_elems(int type) { return kChunkBytes / elem_bytes(type); }
 
 __device__ __forceinline__ float value(uint16_t v) { return bf16_bits_to_float(v); }
 __device__ __forceinline__ float value(float v) { return v; }
@@ -84,41 +76,68 @@ __device__ __forceinline__ void spread(const uint4& v, float (&f)[4]) {
   f[3] = __uint_as_float(v.w);
 }
 
-// Sum of squares of this thread's share of a chunk.
-template <typename T>
-__device__ __forceinline__ double squares(const moe_grad_tensor& t, int64_t chunk) {
-  constexpr int kPer = Piece<T>::kPer;
-  constexpr int kVecs = kChunk / kPer / kBlock;  // vectors a thread, at most
-  const Piece<T> p(t, chunk);
-  const uint4* body = reinterpret_cast<const uint4*>(p.src + p.head);
+// This thread's share of up to kBatch chunks of a tensor: of their vectors of 16 bytes (`head`
+// elements behind the start, where the source is aligned) and at most one of the elements beside them (fewer than two
+// vectors' worth).
+struct Share {
   uint4 v[kVecs];
+  float edge;
+  int edge_at;  // its place, or -1
+  int head, vecs;
+  void* out;    // of the first chunk
+  int type, tensor, group;
+  bool in_place;
+  __device__ __forceinline__ void load(const moe_grad_tensor& t, int index, int64_t chunk, int chunks) {
+    type = t.type;
+    tensor = index;
+    group = t.group;
+    const int size = elem_bytes(type), per = 16 / size;
+    const int64_t at = (chunk - t.first_chunk) * chunk_elems(type);
+    const int n = static_cast<int>(min(t.count - at, static_cast<int64_t>(chunks) * chunk_elems(type)));
+    const uint8_t* src = static_cast<const uint8_t*>(t.grad) + at * size;
+    out = static_cast<uint8_t*>(t.out) + at * size;
+    in_place = t.grad == t.out;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15u) / size;
+    head = min(n, (per - off) % per);
+    vecs = (n - head) / per;
+    const int tail = n - head - vecs * per;
+    const uint4* body = reinterpret_cast<const uint4*>(src + head * size);
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int j = i * kBlock + threadIdx.x;
-    v[i] = j < p.vecs ? __ldg(body + j) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kVecs; ++i) {
+      const int j = i * kBlock + threadIdx.x;
+      v[i] = j < vecs ? body[j] : make_uint4(0, 0, 0, 0);
+    }
+    const int k = threadIdx.x;
+    edge_at = k < head ? k : k < head + tail ? vecs * per + k : -1;
+    edge = 0.0f;
+    if (edge_at >= 0)
+      edge = type == MOE_DTYPE_BF16 ? value(reinterpret_cast<const uint16_t*>(src)[edge_at])
+                                    : value(reinterpret_cast<const float*>(src)[edge_at]);
   }
-  // the elements beside the vectors: fewer than 2 kPer
-  float edge = 0.0f;
-  if (static_cast<int>(threadIdx.x) < p.head) edge = value(p.src[threadIdx.x]);
-  else if (static_cast<int>(threadIdx.x) < p.head + p.tail)
-    edge = value(p.src[p.vecs * kPer + threadIdx.x]);
-  auto sum = [&](float k) {
+  template <int PER>
+  __device__ __forceinline__ float sum(float k) const {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      float f[kPer];
+      float f[PER];
       spread(v[i], f);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) s[e & 3] = fmaf(f[e] * k, f[e] * k, s[e & 3]);
+      for (int e = 0; e < PER; ++e) s[e & 3] = fmaf(f[e] * k, f[e] * k, s[e & 3]);
     }
     s[0] = fmaf(edge * k, edge * k, s[0]);
     return (s[0] + s[1]) + (s[2] + s[3]);
-  };
-  const float s = sum(1.0f);
-  if (s > 0x1p-80f && s < 0x1p126f) return static_cast<double>(s);
-  if (s >= 0x1p126f) return static_cast<double>(sum(0x1p-75f)) * 0x1p150;
-  return static_cast<double>(sum(0x1p100f)) * 0x1p-200;  // (a NaN stays one)
-}
+  }
+  template <int PER>
+  __device__ __forceinline__ double squares_as() const {
+    const float s = sum<PER>(1.0f);
+    if (s > 0x1p-80f && s < 0x1p126f) return static_cast<double>(s);
+    if (s >= 0x1p126f) return static_cast<double>(sum<PER>(0x1p-75f)) * 0x1p150;
+    return static_cast<double>(sum<PER>(0x1p100f)) * 0x1p-200;  // (a NaN stays one)
+  }
+  __device__ __forceinline__ double squares() const {
+    return type == MOE_DTYPE_BF16 ? squares_as<8>() : squares_as<4>();
+  }
+};
 
 // Sum over the block, the same in every thread.
 __device__ __forceinline__ double block_sum(double v, double* s_warp) {
@@ -133,62 +152,58 @@ __device__ __forceinline__ double block_sum(double v, double* s_warp) {
   return s;
 }
 
-__global__ void __launch_bounds__(kBlock) grad_squares_kernel(const ClipArgs a) {
+__global__ void __launch_bounds__(kBlock, kPerSm) grad_squares_kernel(const ClipArgs a) {
   __shared__ double s_warp[kBlock / 32];
   const int64_t c0 = part_begin(blockIdx.x, a.n_chunks, gridDim.x);
   const int64_t c1 = part_begin(blockIdx.x + 1, a.n_chunks, gridDim.x);
   pdl_wait();
   pdl_trigger();  // the grid is resident as a whole
+  for (int g = blockIdx.x * kBlock + threadIdx.x; g < a.n_groups; g += gridDim.x * kBlock)
+    a.norms[g] = 0.0f;  // of a group without elements; the others are written by the second pass
   double sum = 0.0;
   int ti = tensor_of(a, c0);
   moe_grad_tensor t = a.tensors[ti];
+  auto end_of = [&]() { return t.first_chunk + (t.count + chunk_elems(t.type) - 1) / chunk_elems(t.type); };
+  int64_t end = end_of();
+  auto fetch = [&](Share& s, int64_t c) {
+    while (end <= c) {
+      t = a.tensors[++ti];
+      end = end_of();
+    }
+    const int n = static_cast<int>(min(min(end, c1) - c, static_cast<int64_t>(kBatch)));
+    s.load(t, ti, c, n);
+    return n;
+  };
   int group = t.group;
-  for (int64_t c = c0; c < c1; ++c) {
-    while (ti + 1 < a.n_tensors && a.tensors[ti + 1].first_chunk <= c) t = a.tensors[++ti];
-    if (t.group != group) {
+  for (int64_t c = c0; c < c1;) {
+    Share now;
+    c += fetch(now, c);
+    if (now.group != group) {
       const double s = block_sum(sum, s_warp);
       if (threadIdx.x == 0) a.partial[blockIdx.x + group] = s;
       sum = 0.0;
-      group = t.group;
+      group = now.group;
     }
-    sum += t.type == MOE_DTYPE_BF16 ? squares<uint16_t>(t, c) : squares<float>(t, c);
+    sum += now.squares();
   }
   const double s = block_sum(sum, s_warp);
   if (threadIdx.x == 0) a.partial[blockIdx.x + group] = s;
 }
 
-// The first tensor of group g or a later one, or n_tensors.
-__device__ __forceinline__ int first_of_group(const ClipArgs& a, int g) {
-  int lo = 0, hi = a.n_tensors;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.tensors[mid].group < g) lo = mid + 1; else hi = mid;
-  }
-  return lo;
-}
-
-// Norm of group g, by the whole block.
-__device__ __forceinline__ float group_norm(const ClipArgs& a, int g, double* s_warp) {
-  const int i0 = first_of_group(a, g), i1 = first_of_group(a, g + 1);
-  const int64_t c0 = i0 < a.n_tensors ? a.tensors[i0].first_chunk : a.n_chunks;
-  const int64_t c1 = i1 < a.n_tensors ? a.tensors[i1].first_chunk : a.n_chunks;
+// Norm of the group of tensor t, by the whole block.
+__device__ __forceinline__ float group_norm(const ClipArgs& a, const moe_grad_tensor& t, double* s_warp) {
   double v = 0.0;
-  if (c0 < c1) {
-    const int b0 = part_of(c0, a.n_chunks, gridDim.x), b1 = part_of(c1 - 1, a.n_chunks, gridDim.x);
-    for (int b = b0 + threadIdx.x; b <= b1; b += kBlock) v += a.partial[b + g];
-  }
+  const int b0 = part_of(t.group_begin, a.n_chunks, gridDim.x);
+  const int b1 = part_of(t.group_end - 1, a.n_chunks, gridDim.x);
+  for (int b = b0 + threadIdx.x; b <= b1; b += kBlock) v += __ldcg(a.partial + b + t.group);
   return static_cast<float>(sqrt(block_sum(v, s_warp)));
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 join(const float (&f)[Piece<T>::kPer]);
-template <>
-__device__ __forceinline__ uint4 join<float>(const float (&f)[4]) {
+__device__ __forceinline__ uint4 join(const float (&f)[4]) {
   return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                     __float_as_uint(f[3]));
 }
-template <>
-__device__ __forceinline__ uint4 join<uint16_t>(const float (&f)[8]) {
+__device__ __forceinline__ uint4 join(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                     pack_bf16x2(f[6], f[7]));
 }
@@ -198,34 +213,22 @@ __device__ __forceinline__ void put(uint16_t* p, float v) {
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_chunk(const moe_grad_tensor& t, int64_t chunk, float k) {
-  constexpr int kPer = Piece<T>::kPer;
-  constexpr int kVecs = kChunk / kPer / kBlock;
-  const Piece<T> p(t, chunk);
-  T* dst = static_cast<T*>(t.out) + (chunk - t.first_chunk) * kChunk;
-  const uint4* body = reinterpret_cast<const uint4*>(p.src + p.head);
-  T* out = dst + p.head;
+__device__ __forceinline__ void scale_share(const Share& s, float k) {
+  constexpr int kPer = 16 / sizeof(T);
+  T* out = static_cast<T*>(s.out);
+  if (s.edge_at >= 0) put(out + s.edge_at, s.edge * k);
+  out += s.head;
   const bool aligned = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-  uint4 v[kVecs];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
     const int j = i * kBlock + threadIdx.x;
-    if (j < p.vecs) v[i] = body[j];
-  }
-  int at = -1;
-  if (static_cast<int>(threadIdx.x) < p.head) at = threadIdx.x;
-  else if (static_cast<int>(threadIdx.x) < p.head + p.tail) at = p.vecs * kPer + threadIdx.x;
-  if (at >= 0) put(dst + at, value(p.src[at]) * k);
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int j = i * kBlock + threadIdx.x;
-    if (j >= p.vecs) break;
+    if (j >= s.vecs) break;
     float f[kPer];
-    spread(v[i], f);
+    spread(s.v[i], f);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) f[e] *= k;
     if (aligned) {
-      reinterpret_cast<uint4*>(out)[j] = join<T>(f);
+      reinterpret_cast<uint4*>(out)[j] = join(f);
     } else {
 #pragma unroll
       for (int e = 0; e < kPer; ++e) put(out + j * kPer + e, f[e]);
@@ -233,35 +236,41 @@ __device__ __forceinline__ void scale_chunk(const moe_grad_tensor& t, int64_t ch
   }
 }
 
-__global__ void __launch_bounds__(kBlock) grad_scale_kernel(const ClipArgs a) {
+__global__ void __launch_bounds__(kBlock, kPerSm) grad_scale_kernel(const ClipArgs a) {
   __shared__ double s_warp[kBlock / 32];
   const int64_t c0 = part_begin(blockIdx.x, a.n_chunks, gridDim.x);
   const int64_t c1 = part_begin(blockIdx.x + 1, a.n_chunks, gridDim.x);
-  pdl_wait();
-  for (int g = blockIdx.x; g < a.n_groups; g += gridDim.x) {
-    const float norm = group_norm(a, g, s_warp);
-    if (threadIdx.x == 0) {
-      a.norms[g] = norm;
-      if (!(norm < __int_as_float(0x7F800000))) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
-    }
-  }
-  int ti = -1, group = -1;
+  // The first pass waited for everything before it and writes only partial and norms: the
+  // table and the gradients are read before it has ended.
+  int ti = tensor_of(a, c1 - 1);
+  moe_grad_tensor t = a.tensors[ti];
+  auto fetch = [&](Share& s, int64_t c) {  // chunks up to c
+    while (t.count == 0 || t.first_chunk > c) t = a.tensors[--ti];
+    const int n = static_cast<int>(min(c + 1 - max(t.first_chunk, c0), static_cast<int64_t>(kBatch)));
+    s.load(t, ti, c + 1 - n, n);
+    return n;
+  };
+  int group = -1;
   float k = 1.0f;
-  moe_grad_tensor t;
-  for (int64_t c = c1 - 1; c >= c0; --c) {
-    if (ti < 0 || t.first_chunk > c) {
-      ti = tensor_of(a, c);
-      t = a.tensors[ti];
-    }
-    if (t.group != group) {
-      group = t.group;
-      const float norm = group_norm(a, group, s_warp);
+  for (int64_t c = c1 - 1; c >= c0;) {
+    Share now;
+    c -= fetch(now, c);
+    if (now.group != group) {
+      if (group < 0) pdl_wait();
+      group = now.group;
+      const moe_grad_tensor& mine = a.tensors[now.tensor];
+      const float norm = group_norm(a, mine, s_warp);
       const float q = __fdiv_rn(a.max_norm, norm + 1e-6f);
       k = q > 1.0f ? 1.0f : q;  // (a NaN stays one)
+      if (threadIdx.x == 0 && c0 <= mine.group_begin && mine.group_begin < c1) {
+        a.norms[group] = norm;
+        if (!(norm < __int_as_float(0x7F800000))) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);
+      }
     }
-    if (k == 1.0f && t.grad == t.out) continue;  // in place, and as it should be
-    if (t.type == MOE_DTYPE_BF16) scale_chunk<uint16_t>(t, c, k);
-    else scale_chunk<float>(t, c, k);
+    if (k != 1.0f || !now.in_place) {  // (in place, and as it should be: nothing to write)
+      if (now.type == MOE_DTYPE_BF16) scale_share<uint16_t>(now, k);
+      else scale_share<float>(now, k);
+    }
   }
   pdl_trigger();
 }
@@ -296,8 +305,17 @@ MOE_API moe_status moe_grad_plan(int32_t n_tensors, moe_grad_tensor* tensors, in
       return MOE_ERR_UNSUPPORTED;
     if (t.count > (int64_t(1) << 50)) return MOE_ERR_UNSUPPORTED;
     t.first_chunk = chunks;
-    chunks += ceil_div(t.count, kChunk);
+    chunks += ceil_div(t.count, chunk_elems(t.type));
     if (chunks > (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+  }
+  for (int32_t i = 0; i < n_tensors;) {  // the chunks of each group
+    int32_t j = i;
+    while (j < n_tensors && tensors[j].group == tensors[i].group) ++j;
+    const int64_t end = j < n_tensors ? tensors[j].first_chunk : chunks;
+    for (const int64_t begin = tensors[i].first_chunk; i < j; ++i) {
+      tensors[i].group_begin = begin;
+      tensors[i].group_end = end;
+    }
   }
   *n_chunks = chunks;
   return MOE_OK;
@@ -327,7 +345,7 @@ MOE_API moe_status moe_clip_grads(int32_t n_tensors, const moe_grad_tensor* tens
   const ClipArgs a{tensors, n_tensors, n_groups, n_chunks, static_cast<double*>(ws), max_norm, norms,
                    dev_status};
   const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>(n_chunks, std::min<int64_t>(4 * sm_count(), kMaxBlocks)));
+      std::min<int64_t>(n_chunks, std::min<int64_t>(kPerSm * sm_count(), kMaxBlocks)));
   launch(grad_squares_kernel, dim3(grid), dim3(kBlock), 0, s, a);
   launch(grad_scale_kernel, dim3(grid), dim3(kBlock), 0, s, a);
   return launch_status();

@@ -903,11 +903,12 @@ typedef struct {
   int64_t count;       /* elements                                               */
   int32_t type;        /* MOE_DTYPE_* of both                                    */
   int32_t group;       /* whose norm it counts in; non-decreasing over the table */
-  int64_t first_chunk; /* written by moe_grad_plan                               */
+  int64_t first_chunk; /* this and the two below: written by moe_grad_plan       */
+  int64_t group_begin, group_end;
 } moe_grad_tensor;
 
 /* Checks a table of n_tensors on the HOST (it may be copied to the device as it is
- * afterwards), fills in first_chunk and returns the number of chunks.  Tensors of a group
+ * afterwards), fills in its last three fields and returns the number of chunks.  Tensors of a group
  * stand together; a tensor may have no elements (its addresses may then be NULL), and a group
  * no tensors.  Addresses must be aligned to their type.                       */
 moe_status moe_grad_plan(int32_t n_tensors, moe_grad_tensor* tensors, int32_t n_groups,

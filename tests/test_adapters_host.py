@@ -73,9 +73,15 @@ def table(g, rows):
 
 
 def test_grad_plan(g):
-    t = table(g, [(16, 16, 8192, 1, 0), (None, None, 0, 0, 0), (18, 20, 8193, 0, 1), (16, 16, 1, 1, 4)])
-    assert g.moe_grad_plan(t, 5) == 4
-    assert [e.first_chunk for e in t] == [0, 1, 1, 3]
+    rows = [(16, 16, 100_000, 1, 0), (None, None, 0, 0, 0), (18, 20, 100_001, 0, 1), (16, 16, 1, 1, 1),
+            (16, 16, 5, 0, 4), (None, None, 0, 1, 4)]
+    t = table(g, rows)
+    n = g.moe_grad_plan(t, 5)
+    first = [e.first_chunk for e in t] + [n]
+    # whole chunks, none for a tensor without elements, one for a few elements
+    assert first[0] == 0 and 0 < first[1] == first[2] < first[3] == first[4] - 1 == first[5] - 2 == n - 2
+    assert [(e.group_begin, e.group_end) for e in t] == \
+        [(0, first[2])] * 2 + [(first[2], first[4])] * 2 + [(first[4], n)] * 2
     assert g.moe_grad_plan((g.GradTensor * 0)(), 1) == 0
     L, n = g.abi.lib(), ctypes.c_int64()
     ARG, UNS = g.MOE_ERR_INVALID_ARG, g.MOE_ERR_UNSUPPORTED
