@@ -178,9 +178,9 @@ shrink_kernel(const ShrinkArgs a, int split, int pieces_mode) {
 // ---------------------------------- grads ------------------------------------
 //
 // D_a[m, k] = sum over a's tokens of p[t, m] q[t, k], p fp32 [T, r] (u or v), q bf16 (dy or x).
-// A CTA takes one adapter and 128 columns (a cluster: parts of the adapter's tokens, added in
+// A CTA takes one adapter and 256 columns (128 with more than 64 ranks) (a cluster: parts of the adapter's tokens, added in
 // order).  p goes into the MMA as three bf16 numbers, the value and what each rounding left, and
-// every piece of kGradTokens rows is added to the sums in fp32 registers: the gradient is as
+// every 16 rows are added to the sums in fp32 registers: the gradient is as
 // exact as an fp32 sum.  Rows of other segments are never loaded: zeros stand in
 // their place in both operands.
 
@@ -195,17 +195,19 @@ struct GradArgs {
 };
 
 constexpr int kGradTokens = 32;
-constexpr int kGradCols = 128;
-constexpr int kGradStages = 4;
-constexpr int kGradRow = kGradCols * 2 + 16;  // bytes of a staged row of q
+constexpr int kGradStages = 3;
 
 template <int MB>
 struct Grad {
+  // columns of a CTA; a warp has an eighth of them
+  static constexpr int kCols = MB <= 4 ? 256 : 128;
+  static constexpr int kBlocks = kCols / 64;  // of 8 columns a warp
+  static constexpr int kRow = kCols * 2 + 16;  // bytes of a staged row of q
   static constexpr int kPRow = 16 * MB * 4;         // bytes of a staged row of p
-  static constexpr int kStageBytes = kGradTokens * (kGradRow + kPRow);
+  static constexpr int kStageBytes = kGradTokens * (kRow + kPRow);
   static constexpr int kSplitRow = 16 * MB * 2 + 16;  // of one of the three bf16 parts of p
   static constexpr int kSplitBytes = 3 * kGradTokens * kSplitRow;
-  static constexpr int kSum = 16 * MB * kGradCols * 4;
+  static constexpr int kSum = 16 * MB * kCols * 4;
   static constexpr int kRing = kGradStages * kStageBytes + kSplitBytes;
   static constexpr int kSmem = kRing > kSum ? kRing : kSum;
 };
@@ -224,7 +226,7 @@ grads_kernel(const GradArgs a, int split) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int col0 = static_cast<int>(blockIdx.x) / split * kGradCols;
+  const int col0 = static_cast<int>(blockIdx.x) / split * P::kCols;
   const int id = blockIdx.y;
   pdl_wait();
   pdl_trigger();
@@ -242,11 +244,11 @@ grads_kernel(const GradArgs a, int split) {
   }
   const int64_t part0 = count * rank / split, part1 = count * (rank + 1) / split;
 
-  float acc[MB][2][4];
+  float acc[MB][P::kBlocks][4];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < P::kBlocks; ++j)
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.0f;
 
@@ -284,13 +286,13 @@ grads_kernel(const GradArgs a, int split) {
   auto stage_ptr = [&](int s) { return s_raw + s * P::kStageBytes; };
   auto load = [&](int s, int row, int rows) {
     uint8_t* st = stage_ptr(s);
-    for (int i = threadIdx.x; i < kGradTokens * (kGradCols / 8); i += 256) {
-      const int t = i / (kGradCols / 8), c = i % (kGradCols / 8) * 8;
+    for (int i = threadIdx.x; i < kGradTokens * (P::kCols / 8); i += 256) {
+      const int t = i / (P::kCols / 8), c = i % (P::kCols / 8) * 8;
       const bool live = t < rows && col0 + c < a.K;
-      cp_async16(smem_u32(st + t * kGradRow + c * 2),
+      cp_async16(smem_u32(st + t * P::kRow + c * 2),
                  live ? a.q + (row + t) * a.q_stride + col0 + c : a.q, live);
     }
-    uint8_t* sp = st + kGradTokens * kGradRow;
+    uint8_t* sp = st + kGradTokens * P::kRow;
     for (int i = threadIdx.x; i < kGradTokens * 4 * MB; i += 256) {
       const int t = i / (4 * MB), m = i % (4 * MB) * 4;
       const bool live = t < rows && m < a.r;
@@ -324,7 +326,7 @@ grads_kernel(const GradArgs a, int split) {
     uint8_t* parts = s_raw + kGradStages * P::kStageBytes;
     for (int i = threadIdx.x; i < kGradTokens * 8 * MB; i += 256) {
       const int t = i / (8 * MB), m = i % (8 * MB) * 2;
-      float2 f = *reinterpret_cast<const float2*>(st + kGradTokens * kGradRow + t * P::kPRow + m * 4);
+      float2 f = *reinterpret_cast<const float2*>(st + kGradTokens * P::kRow + t * P::kPRow + m * 4);
 #pragma unroll
       for (int h = 0; h < 3; ++h) {
         const uint32_t w = pack_bf16x2(f.x, f.y);
@@ -334,29 +336,30 @@ grads_kernel(const GradArgs a, int split) {
       }
     }
     __syncthreads();
-    uint32_t bq[kGradTokens / 16][4];  // q: tokens x 16 columns of this warp, transposed on the way
 #pragma unroll
-    for (int kk = 0; kk < kGradTokens / 16; ++kk)
-      ldmatrix_trans(bq[kk], smem_u32(st + (kk * 16 + (lane & 15)) * kGradRow +
-                                      (warp * 16 + (lane >> 4) * 8) * 2));
+    for (int kk = 0; kk < kGradTokens / 16; ++kk) {
+      uint32_t bq[P::kBlocks / 2][4];  // q: 16 tokens x this warp's columns, transposed on the way
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      float d[2][4] = {};  // this piece's sums
+      for (int j = 0; j < P::kBlocks / 2; ++j)
+        ldmatrix_trans(bq[j], smem_u32(st + (kk * 16 + (lane & 15)) * P::kRow +
+                                       (warp * (P::kCols / 8) + 16 * j + (lane >> 4) * 8) * 2));
 #pragma unroll
-      for (int kk = 0; kk < kGradTokens / 16; ++kk)
+      for (int i = 0; i < MB; ++i) {
+        float d[P::kBlocks][4] = {};  // these 16 tokens' sums
 #pragma unroll
         for (int h = 0; h < 3; ++h) {
           uint32_t w[4];
           const int t = kk * 16 + (lane & 7) + (lane & 16 ? 8 : 0), m = 16 * i + (lane & 8);
           ldmatrix_trans(w, smem_u32(parts + (h * kGradTokens + t) * P::kSplitRow + m * 2));
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            mma_16816(d[j], w[0], w[1], w[2], w[3], bq[kk][2 * j], bq[kk][2 * j + 1]);
+          for (int j = 0; j < P::kBlocks; ++j)
+            mma_16816(d[j], w[0], w[1], w[2], w[3], bq[j / 2][2 * (j & 1)], bq[j / 2][2 * (j & 1) + 1]);
         }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < P::kBlocks; ++j)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] += d[j][v];
+          for (int v = 0; v < 4; ++v) acc[i][j][v] += d[j][v];
+      }
     }
     --ahead;
     s = (s + 1) % kGradStages;
@@ -371,15 +374,15 @@ grads_kernel(const GradArgs a, int split) {
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int m = 16 * i + g, c = warp * 16 + 8 * j + 2 * t4;
-        *reinterpret_cast<float2*>(s_sum + m * kGradCols + c) = make_float2(acc[i][j][0], acc[i][j][1]);
-        *reinterpret_cast<float2*>(s_sum + (m + 8) * kGradCols + c) =
+      for (int j = 0; j < P::kBlocks; ++j) {
+        const int m = 16 * i + g, c = warp * (P::kCols / 8) + 8 * j + 2 * t4;
+        *reinterpret_cast<float2*>(s_sum + m * P::kCols + c) = make_float2(acc[i][j][0], acc[i][j][1]);
+        *reinterpret_cast<float2*>(s_sum + (m + 8) * P::kCols + c) =
             make_float2(acc[i][j][2], acc[i][j][3]);
       }
     cluster_sync();
-    for (int i = rank * 256 + threadIdx.x; i < a.r * kGradCols; i += split * 256) {
-      const int m = i / kGradCols, c = i % kGradCols;
+    for (int i = rank * 256 + threadIdx.x; i < a.r * P::kCols; i += split * 256) {
+      const int m = i / P::kCols, c = i % P::kCols;
       const uint32_t addr = smem_u32(s_sum + i);
       float v = 0.0f;
       for (int o = 0; o < split; ++o) v += ld_cluster(map_to_rank(addr, o));
@@ -395,10 +398,10 @@ grads_kernel(const GradArgs a, int split) {
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < P::kBlocks; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int m = 16 * i + g + 8 * h, c = col0 + warp * 16 + 8 * j + 2 * t4;
+        const int m = 16 * i + g + 8 * h, c = col0 + warp * (P::kCols / 8) + 8 * j + 2 * t4;
         if (m < a.r && c < a.K) {
           float2* dst = reinterpret_cast<float2*>(out + static_cast<int64_t>(m) * a.K + c);
           float2 v = make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
@@ -451,12 +454,12 @@ moe_status launch_project(const ProjectArgs& a, const Operands& o, bool kmaj, cu
   const int64_t sms = sm_count();
   const int T = a.seg.T;
   if (T <= 64) {
-    const int split = pow2_at_most(std::min(sms / cols, steps), 8);
+    const int split = pow2_at_most(std::min(sms / cols, steps), 4);
     return kmaj ? project_flat64_kmaj(a, o, split, s) : project_flat64(a, o, split, s);
   }
   // Rounds of tiles, in units of a 128 x 128 tile's MMAs a step.
   const int64_t tiles = cols * ceil_div(T, 128);
-  const int split = pow2_at_most(std::min(sms / tiles, steps), 8);
+  const int split = pow2_at_most(std::min(sms / tiles, steps), 4);
   const int64_t flat = split > 1 ? ceil_div(steps, split) : ceil_div(tiles, sms) * steps;
   const int64_t pair = ceil_div(ceil_div(a.N, 256) * ceil_div(T, 256), sms / 2) * steps * 2;
   if (!a.y_fp32 && T >= 32 * static_cast<int64_t>(a.seg.n_seg) && 10 * pair <= 13 * flat) return project_pair(a, o, kmaj, s);
@@ -470,7 +473,7 @@ moe_status launch_grads_as(const GradArgs& a, cudaStream_t s) {
   static std::mutex mu;
   static bool done[64] = {};
   if (!opt_in(kern, P::kSmem, mu, done)) return MOE_ERR_CUDA;
-  const int64_t blocks = ceil_div(a.K, kGradCols);
+  const int64_t blocks = ceil_div(a.K, P::kCols);
   const int64_t active = std::min(a.seg.n_adapters, a.seg.n_seg);
   const int split =
       pow2_at_most(std::min<int64_t>(4 * sm_count() / (blocks * active), a.seg.T / 64), 8);

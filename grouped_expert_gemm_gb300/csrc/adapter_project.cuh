@@ -17,10 +17,11 @@ namespace {
 // The adapters' part is made by the epilogue warps, 32 tokens at a time: u B is r / d of the work
 // and a run of one adapter may be one token long, where tcgen05's narrowest tile is 16 columns
 // by 128 rows of the table.
-//   32 tokens of one adapter: mma.sync.  tcgen05's 16x256b loads give the accumulators in its
+//   32 tokens of one adapter, or of a few runs: mma.sync.  tcgen05's 16x256b loads give the accumulators in its
 //     layout, 16 weight columns by 8 tokens, so the table (16 columns, in registers, transposed
-//     by movmatrix, once a run) is multiplied with u onto the sums themselves.  u is split into
-//     two bf16 numbers a value by all warps together.
+//     by movmatrix, once a run) is multiplied with u onto the sums themselves, and every token
+//     takes the result of its own run.  u is split into two bf16 numbers a value by all warps
+//     together.
 //   otherwise: warp w takes tokens 4w .. 4w + 3, each with its own adapter's rows (four columns
 //     a lane, fp32), through shared memory.
 // Nothing of one request, not even 0 times an infinity, reaches another's rows.
@@ -59,19 +60,23 @@ struct Shape {
   static constexpr int kBars = 2 * kStages + 8;
   static constexpr int kTmem = CG == 2 ? 2 * TN : 4 * TN;  // two buffers, (flat) the sums
   static constexpr int kSmem =
-      1024 + kStages * kStageBytes + 2 * kPieceBytes + kRedBytes + kBars * 8 + 2 * (kOwn + 8) * 4 + 16;
+      1024 + kStages * kStageBytes + 2 * kPieceBytes + kRedBytes + kBars * 8 + 2 * (kOwn + 16) * 4 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOwn % 8 == 0 && kTmem <= 512, "shape");
   static_assert(kPieceBytes >= 2 * 32 * u_pitch(kMaxRank) && kPieceBytes >= 32 * kPartPitch * 4, "pieces");
 };
 
-constexpr int kSeveral = -3;  // 32 tokens of several kinds
+constexpr int kFew = -3;      // 32 tokens of up to kFewRuns runs
+constexpr int kSeveral = -4;  // of more
+constexpr int kFewRuns = 6;
 
-// First token of tile t, and first weight column of this CTA's part of it.
+// First token of tile t, and first weight column of this CTA's part of it.  (With tokens inner
+// each block of columns starts at another block of tokens: one whose adapters cost more does not
+// come to the same CTAs in every round.)
 template <int TN, int CG>
 __device__ __forceinline__ void tile_at(const ProjectArgs& a, int t, int rank, int& row0, int& n0) {
   const int nb = a.n_inner ? t % a.n_blocks : t / a.t_blocks;
-  const int tb = a.n_inner ? t / a.n_blocks : t % a.t_blocks;
+  const int tb = a.n_inner ? t / a.n_blocks : (t % a.t_blocks + nb) % a.t_blocks;
   row0 = tb * TN;
   n0 = nb * 128 * CG + (CG == 2 ? rank * 128 : 0);
 }
@@ -173,7 +178,8 @@ struct Epilogue {
   uint8_t* piece;   // [2][kPieceBytes]
   uint8_t* red;
   int* id;          // [2][kOwn]: adapter of a token
-  int* whole;       // [2][8]: of 32 tokens the adapter of all, kNone where none has one, or kSeveral
+  int* whole;       // [2][8]: of 32 tokens the adapter of all, kNone where none has one, kFew or kSeveral
+  uint32_t* starts; // [2][8]: where their runs start
   volatile int* abort_flag;
   uint32_t tfull, tempty, group_bar, red_bar;  // (tfull and tempty: two barriers each)
   uint32_t tmem;
@@ -219,23 +225,46 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
     }
     if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
   };
-  // 16 columns of the table of adapter `held`, mma.sync's first operand
-  uint32_t tab[RB][4];
-  int held = kNone, held_n = 0;
-  auto hold = [&](int e, int n) {
-    if (e == held && n == held_n) return;
-    held = e;
-    held_n = n;
+  // 16 columns of the table of adapter `held`, mma.sync's first operand; with up to 64 ranks the
+  // next run's are already on their way (`coming`, not yet transposed)
+  constexpr bool kAhead = RB <= 4;
+  uint32_t tab[RB][4], raw[kAhead ? RB : 1][4];
+  int held = kNone, coming = kNone, table_n = -1;
+  auto load_table = [&](uint32_t (&to)[RB][4], int e, int n) {
     const uint16_t* p = a.table + (static_cast<int64_t>(e) * a.r + g) * a.N + n + 2 * t4;
 #pragma unroll
     for (int k = 0; k < RB; ++k)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {  // columns + 8 (q & 1), ranks + 8 (q >> 1)
         const int rank_q = 16 * k + 8 * (q >> 1);
-        tab[k][q] = n + 8 * (q & 1) < a.N && rank_q < a.r
-                        ? __ldg(reinterpret_cast<const uint32_t*>(p + static_cast<int64_t>(rank_q) * a.N + 8 * (q & 1)))
-                        : 0u;
+        to[k][q] = n + 8 * (q & 1) < a.N && rank_q < a.r
+                       ? __ldg(reinterpret_cast<const uint32_t*>(p + static_cast<int64_t>(rank_q) * a.N + 8 * (q & 1)))
+                       : 0u;
       }
+  };
+  auto expect = [&](int e, int n) {  // adapter e is the next one
+    if constexpr (kAhead) {
+      if (e < 0 || e == held || e == coming) return;
+      coming = e;
+      load_table(raw, e, n);
+    }
+  };
+  auto hold = [&](int e, int n) {
+    if (e == held) return;
+    if constexpr (kAhead) {
+      if (e == coming) {
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tab[k][q] = raw[k][q];
+        coming = kNone;
+      } else {
+        load_table(tab, e, n);
+      }
+    } else {
+      load_table(tab, e, n);
+    }
+    held = e;
 #pragma unroll
     for (int k = 0; k < RB; ++k)
 #pragma unroll
@@ -248,7 +277,7 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
 #pragma unroll
     for (int e = 0; e < kLoads; ++e) {
       const int i = tid + 256 * e, q = i % kQuads * 4;
-      ahead[e] = i < 8 * kGroups * kQuads && q < a.r
+      ahead[e] = i < 8 * kGroups * kQuads && q < a.r && row + i / kQuads < a.seg.T
                      ? *reinterpret_cast<const float4*>(a.u + static_cast<int64_t>(row + i / kQuads) * a.r + q)
                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
@@ -256,6 +285,21 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
   // this lane's row of the four 8 x 8 blocks of an ldmatrix of u (two of the values, two of what
   // their rounding left): mma.sync's second operand of 8 tokens and 16 ranks
   const uint32_t lu = smem_u32(s.piece) + (lane & 7) * kPitch + (lane & 8) * 2 + (lane & 16 ? 32 * kPitch : 0);
+
+  // c += u B on the 32 tokens of a piece
+  auto multiply = [&](float (&c)[kGroups][4], uint32_t at) {
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      uint32_t u[kGroups][4];
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) ldmatrix(u[i], at + 8 * i * kPitch + k * 32);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+          mma_16816(c[i], tab[k][0], tab[k][1], tab[k][2], tab[k][3], u[i][2 * h], u[i][2 * h + 1]);
+    }
+  };
 
   for (int t = s.first; t < s.total; t += s.step) {
     int row0, n0;
@@ -268,17 +312,27 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
       const int id = row_adapters(a.seg, row_own + 32 * w, lane);
       constexpr uint32_t kIn = kOwn < 32 ? (1u << (kOwn & 31)) - 1 : kAll;
       const uint32_t has = __ballot_sync(kAll, id >= 0) & kIn;
-      const uint32_t same = __ballot_sync(kAll, id == __shfl_sync(kAll, id, 0)) & kIn;
+      const int before = __shfl_up_sync(kAll, id, 1);
+      const uint32_t starts = __ballot_sync(kAll, id >= 0 && (lane == 0 || id != before)) & kIn;
       if (32 * w + lane < kOwn) ids[32 * w + lane] = id;
-      if (lane == 0) whole[w] = has == 0 ? kNone : has == kIn && same == kIn ? id : kSeveral;
+      if (lane == 0) {
+        s.starts[par * 8 + w] = starts;
+        whole[w] = has == 0 ? kNone : has == kIn && starts == 1 ? id : __popc(starts) <= kFewRuns ? kFew : kSeveral;
+      }
     }
     if (!meet()) break;
-    if (whole[0] >= 0) hold(whole[0], n);
+    if (n != table_n) held = coming = kNone;  // other columns
+    table_n = n;
+    // the first adapter of 32 tokens that mma.sync takes
+    auto first_of = [&](int ch) {
+      return whole[ch] == kFew ? ids[32 * ch + __ffs(s.starts[par * 8 + ch]) - 1] : whole[ch];
+    };
+    expect(first_of(0), n);
     if (!waited) {
       pdl_wait();  // u; and what is written here may still be read by the kernels before
       waited = true;
     }
-    if (whole[0] >= 0) fetch_u(row_own);
+    if (whole[0] >= 0 || whole[0] == kFew) fetch_u(row_own);
     if constexpr (CG == 2)
       if (!sums_ready()) break;
 #pragma unroll 1
@@ -286,7 +340,7 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
       const int j = 32 * ch, kind = whole[ch];
       uint8_t* piece = s.piece + pb * kPieceBytes;
       const uint32_t at = lu + pb * kPieceBytes;
-      if (kind >= 0) {
+      if (kind >= 0 || kind == kFew) {
 #pragma unroll
         for (int e = 0; e < kLoads; ++e) {
           const int i = tid + 256 * e;
@@ -300,7 +354,7 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
             *reinterpret_cast<uint2*>(dst + 32 * kPitch) = make_uint2(l0, l1);
           }
         }
-        hold(kind, n);
+        hold(first_of(ch), n);
       } else if (kind == kSeveral && 4 * w < kOwn - j) {
         int id[4];
 #pragma unroll
@@ -319,7 +373,7 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
         if (!ok) break;
         pb ^= 1;  // (the other piece's readers have all come here)
       }
-      if (ch + 1 < kChunks && whole[ch + 1] >= 0) fetch_u(row_own + j + 32);
+      if (ch + 1 < kChunks && (whole[ch + 1] >= 0 || whole[ch + 1] == kFew)) fetch_u(row_own + j + 32);
       float c[kGroups][4];
       if constexpr (CG == 2) {
 #pragma unroll
@@ -333,16 +387,34 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
           for (int e = 0; e < 4; ++e) c[i][e] = 0.0f;
       }
       if (kind >= 0) {
+        multiply(c, at);
+      } else if (kind == kFew) {
+        uint32_t starts = s.starts[par * 8 + ch];
+#pragma unroll 1
+        while (starts != 0) {
+          const int b = __ffs(starts) - 1, mine = ids[j + b];  // tokens from b on, as long as they are mine
+          starts &= starts - 1;
+          const int end = starts != 0 ? __ffs(starts) - 1 : 8 * kGroups;
+          hold(mine, n);
+          if (starts != 0) expect(ids[j + __ffs(starts) - 1], n);
+          else if (ch + 1 < kChunks) expect(first_of(ch + 1), n);
+          // all 32 tokens (four products side by side), and each keeps its own run's
+          float d[kGroups][4];
 #pragma unroll
-        for (int k = 0; k < RB; ++k) {
-          uint32_t u[kGroups][4];
+          for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-          for (int i = 0; i < kGroups; ++i) ldmatrix(u[i], at + 8 * i * kPitch + k * 32);
+            for (int e = 0; e < 4; ++e) d[i][e] = c[i][e];
+          multiply(d, at);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i)
-              mma_16816(c[i], tab[k][0], tab[k][1], tab[k][2], tab[k][3], u[i][2 * h], u[i][2 * h + 1]);
+            for (int e = 0; e < 2; ++e) {
+              const int tok = 8 * i + 2 * t4 + e;
+              if (tok >= b && tok < end && ids[j + tok] == mine) {
+                c[i][e] = d[i][e];
+                c[i][2 + e] = d[i][2 + e];
+              }
+            }
         }
       } else if (kind == kSeveral) {
         const float* part = reinterpret_cast<const float*>(piece) + m0 + g;
@@ -462,10 +534,10 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   uint8_t* s_red = s_piece + 2 * kPieceBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_red + F::kRedBytes);
   int* s_id = reinterpret_cast<int*>(bars + F::kBars);  // [2][kOwn]: adapter of a token
-  // [2][8]: of 32 tokens the adapter of all, kNone where none has one, or kSeveral
   int* s_whole = s_id + 2 * kOwn;
-  volatile int* abort_flag = s_whole + 2 * 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_whole + 2 * 8) + 1;
+  uint32_t* s_starts = reinterpret_cast<uint32_t*>(s_whole + 2 * 8);
+  volatile int* abort_flag = s_whole + 4 * 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_whole + 4 * 8) + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCluster = S * CG;
   const int rank = kCluster > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -604,7 +676,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
       }
     }
   } else {
-    const Epilogue e{s_piece, s_red, s_id, s_whole, abort_flag, tfull_bar(0), tempty_bar(0), group_bar,
+    const Epilogue e{s_piece, s_red, s_id, s_whole, s_starts, abort_flag, tfull_bar(0), tempty_bar(0), group_bar,
                      red_bar, tmem, first, step, total, rank, k0, k1, piece};
     awaited = a.r <= 16   ? epilogue<TN, S, CG, 1>(a, e, warp, lane)
               : a.r <= 32 ? epilogue<TN, S, CG, 2>(a, e, warp, lane)
@@ -630,20 +702,20 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   pdl_trigger();
 }
 
-// Pairs of CTAs that can be resident at once, read once per kernel and device.
+// Clusters of `size` CTAs that can be resident at once, read once per kernel and device.
 template <typename Kernel>
-int resident_pairs(Kernel kern, int smem, std::mutex& mu, int (&cache)[64]) {
+int resident_clusters(Kernel kern, int size, int smem, std::mutex& mu, int (&cache)[64]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (cache[dev] == 0) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(sm_count() & ~1));
+    cfg.gridDim = dim3(static_cast<unsigned>(sm_count() / size * size));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -651,56 +723,65 @@ int resident_pairs(Kernel kern, int smem, std::mutex& mu, int (&cache)[64]) {
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
-      n = sm_count() / 2;
+      n = sm_count() / size;
     }
     cache[dev] = n;
   }
   return cache[dev];
 }
 
+// False, and nothing launched, where S CTAs were to share a tile's reduction and the tiles are
+// more than the clusters that are resident at once: a second wave of them takes longer than the
+// whole of fewer, longer ones (16 tiles of 7168 x 128, one token: clusters of eight, which do not
+// all fit, 18.9 us, of four 14.4, of two 22.7).
 template <int TN, int S, int CG, bool KMAJ>
-moe_status launch_project_as(ProjectArgs a, const Operands& o, cudaStream_t s) {
+bool launch_project_as(ProjectArgs a, const Operands& o, cudaStream_t s, moe_status& st) {
   using F = Shape<TN, S, CG>;
   auto kern = project_kernel<TN, S, CG, KMAJ>;
   static std::mutex mu;
   static bool done[64] = {};
-  if (!opt_in(kern, F::kSmem, mu, done)) return MOE_ERR_CUDA;
+  st = MOE_ERR_CUDA;
+  if (!opt_in(kern, F::kSmem, mu, done)) return true;
+  a.n_blocks = static_cast<int>(ceil_div(a.N, 128 * CG));
+  a.t_blocks = static_cast<int>(ceil_div(a.seg.T, TN));
+  const int64_t tiles = static_cast<int64_t>(a.n_blocks) * a.t_blocks;
+  int64_t clusters = std::min<int64_t>(tiles, sm_count());
+  if constexpr (S * CG > 1) {
+    static std::mutex mu2;
+    static int resident[64] = {};
+    const int n = resident_clusters(kern, S * CG, F::kSmem, mu2, resident);
+    if (n <= 0) return true;
+    if (S > 1 && tiles > n) return false;
+    clusters = std::min<int64_t>(tiles, n);
+  }
   CUtensorMap mw, mx;
   a.x_rows = static_cast<int>(std::min<int64_t>(TN / CG, ceil_div(a.seg.T, 8) * 8));
   // the weight is [K, N] (rows of N), or for the backward [N, K]
   if (!(KMAJ ? map_2d(&mw, o.w, a.N, a.K, a.K, 128) : map_2d(&mw, o.w, a.K, a.N, a.N, 64)) ||
       !map_2d(&mx, o.x, a.seg.T, a.K, o.x_stride, a.x_rows))
-    return MOE_ERR_CUDA;
-  a.n_blocks = static_cast<int>(ceil_div(a.N, 128 * CG));
-  a.t_blocks = static_cast<int>(ceil_div(a.seg.T, TN));
+    return true;
   // Tokens inner: the weight is read once, the rows stay in the L2.  Rows that outgrow it while
   // the weight does not: columns inner.
   constexpr int64_t kL2Budget = 80ll << 20;
   a.n_inner = static_cast<int64_t>(a.seg.T) * a.K * 2 > kL2Budget &&
               static_cast<int64_t>(a.N) * a.K * 2 <= kL2Budget;
-  const int64_t tiles = static_cast<int64_t>(a.n_blocks) * a.t_blocks;
-  int64_t clusters = tiles;
-  if constexpr (CG == 2) {
-    static std::mutex mu2;
-    static int pairs[64] = {};
-    const int n = resident_pairs(kern, F::kSmem, mu2, pairs);
-    if (n <= 0) return MOE_ERR_CUDA;
-    clusters = std::min<int64_t>(tiles, n);
-  } else if (S == 1) {
-    clusters = std::min<int64_t>(tiles, sm_count());
-  }
   launch_clustered(kern, dim3(static_cast<unsigned>(clusters * S * CG)), kThreads, F::kSmem, S * CG, s,
                    mw, mx, a);
-  return launch_status();
+  st = launch_status();
+  return true;
 }
 
 template <int TN, bool KMAJ>
 moe_status launch_flat(const ProjectArgs& a, const Operands& o, int split, cudaStream_t s) {
+  moe_status st = MOE_ERR_CUDA;
   switch (split) {
-    case 8: return launch_project_as<TN, 8, 1, KMAJ>(a, o, s);
-    case 4: return launch_project_as<TN, 4, 1, KMAJ>(a, o, s);
-    case 2: return launch_project_as<TN, 2, 1, KMAJ>(a, o, s);
-    default: return launch_project_as<TN, 1, 1, KMAJ>(a, o, s);
+    case 4:
+      if (launch_project_as<TN, 4, 1, KMAJ>(a, o, s, st)) return st;
+      [[fallthrough]];
+    case 2:
+      if (launch_project_as<TN, 2, 1, KMAJ>(a, o, s, st)) return st;
+      [[fallthrough]];
+    default: launch_project_as<TN, 1, 1, KMAJ>(a, o, s, st); return st;
   }
 }
 
