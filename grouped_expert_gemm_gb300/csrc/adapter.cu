@@ -175,246 +175,6 @@ shrink_kernel(const ShrinkArgs a, int split, int pieces_mode) {
   }
 }
 
-// ---------------------------------- grads ------------------------------------
-//
-// D_a[m, k] = sum over a's tokens of p[t, m] q[t, k], p fp32 [T, r] (u or v), q bf16 (dy or x).
-// A CTA takes one adapter and 256 columns (128 with more than 64 ranks) (a cluster: parts of the adapter's tokens, added in
-// order).  p goes into the MMA as three bf16 numbers, the value and what each rounding left, and
-// every 16 rows are added to the sums in fp32 registers: the gradient is as
-// exact as an fp32 sum.  Rows of other segments are never loaded: zeros stand in
-// their place in both operands.
-
-struct GradArgs {
-  Segments seg;
-  int K, r;
-  const float* p;
-  const uint16_t* q;
-  int64_t q_stride;
-  float* out;  // [n_adapters, r, K]
-  int accumulate;
-};
-
-constexpr int kGradTokens = 32;
-constexpr int kGradStages = 3;
-
-template <int MB>
-struct Grad {
-  // columns of a CTA; a warp has an eighth of them
-  static constexpr int kCols = MB <= 4 ? 256 : 128;
-  static constexpr int kBlocks = kCols / 64;  // of 8 columns a warp
-  static constexpr int kRow = kCols * 2 + 16;  // bytes of a staged row of q
-  static constexpr int kPRow = 16 * MB * 4;         // bytes of a staged row of p
-  static constexpr int kStageBytes = kGradTokens * (kRow + kPRow);
-  static constexpr int kSplitRow = 16 * MB * 2 + 16;  // of one of the three bf16 parts of p
-  static constexpr int kSplitBytes = 3 * kGradTokens * kSplitRow;
-  static constexpr int kSum = 16 * MB * kCols * 4;
-  static constexpr int kRing = kGradStages * kStageBytes + kSplitBytes;
-  static constexpr int kSmem = kRing > kSum ? kRing : kSum;
-};
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 16 : 0)
-               : "memory");
-}
-
-template <int MB>
-__global__ void __launch_bounds__(256)
-grads_kernel(const GradArgs a, int split) {
-  using P = Grad<MB>;
-  extern __shared__ __align__(16) uint8_t s_raw[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t4 = lane & 3;
-  const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int col0 = static_cast<int>(blockIdx.x) / split * P::kCols;
-  const int id = blockIdx.y;
-  pdl_wait();
-  pdl_trigger();
-
-  // the adapter's tokens, in order of its segments: this CTA's part of them
-  int64_t count = 0;
-  for (int q0 = 0; q0 < a.seg.n_seg; q0 += 32) {
-    int n = 0;
-    if (q0 + lane < a.seg.n_seg && __ldg(a.seg.adapter + q0 + lane) == id) {
-      int b, e;
-      seg_rows(a.seg, q0 + lane, b, e);
-      n = max(e - b, 0);
-    }
-    count += __reduce_add_sync(0xFFFFFFFFu, n);
-  }
-  const int64_t part0 = count * rank / split, part1 = count * (rank + 1) / split;
-
-  float acc[MB][P::kBlocks][4];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < P::kBlocks; ++j)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][j][v] = 0.0f;
-
-  // The pieces of kGradTokens rows, one after the other (every warp walks the same table):
-  // `next` finds the next one.
-  int q = -1, b = 0, e = 0, cand = 0;
-  uint32_t mask = 0;
-  int q_base = -32;
-  int64_t seen = 0;  // tokens of the adapter before the current segment
-  auto next = [&](int& row, int& rows) {
-    while (true) {
-      if (b < e) {
-        row = b;
-        rows = min(e - b, kGradTokens);
-        b += rows;
-        return true;
-      }
-      while (mask == 0) {
-        q_base += 32;
-        if (q_base >= a.seg.n_seg) return false;
-        cand = q_base + lane < a.seg.n_seg ? __ldg(a.seg.adapter + q_base + lane) : -1;
-        mask = __ballot_sync(0xFFFFFFFFu, cand == id);
-      }
-      q = q_base + __ffs(mask) - 1;
-      mask &= mask - 1;
-      seg_rows(a.seg, q, b, e);
-      if (e <= b) { e = b; continue; }
-      const int n = e - b;
-      const int64_t from = part0 > seen ? part0 - seen : 0, to = part1 - seen;
-      seen += n;
-      e = b + static_cast<int>(to < n ? (to > 0 ? to : 0) : n);
-      b += static_cast<int>(from < n ? from : n);
-    }
-  };
-  auto stage_ptr = [&](int s) { return s_raw + s * P::kStageBytes; };
-  auto load = [&](int s, int row, int rows) {
-    uint8_t* st = stage_ptr(s);
-    for (int i = threadIdx.x; i < kGradTokens * (P::kCols / 8); i += 256) {
-      const int t = i / (P::kCols / 8), c = i % (P::kCols / 8) * 8;
-      const bool live = t < rows && col0 + c < a.K;
-      cp_async16(smem_u32(st + t * P::kRow + c * 2),
-                 live ? a.q + (row + t) * a.q_stride + col0 + c : a.q, live);
-    }
-    uint8_t* sp = st + kGradTokens * P::kRow;
-    for (int i = threadIdx.x; i < kGradTokens * 4 * MB; i += 256) {
-      const int t = i / (4 * MB), m = i % (4 * MB) * 4;
-      const bool live = t < rows && m < a.r;
-      cp_async16(smem_u32(sp + t * P::kPRow + m * 4),
-                 live ? a.p + static_cast<int64_t>(row + t) * a.r + m : a.p, live);
-    }
-  };
-  int ahead = 0;  // pieces staged and not yet used
-  bool more = count > 0;
-  for (int s = 0; s < kGradStages - 1; ++s) {
-    int row, rows;
-    if (more && (more = next(row, rows))) {
-      load(s, row, rows);
-      ++ahead;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  int s = 0;
-  while (ahead > 0) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kGradStages - 2) : "memory");
-    __syncthreads();
-    {
-      int row, rows;
-      if (more && (more = next(row, rows))) {
-        load((s + kGradStages - 1) % kGradStages, row, rows);
-        ++ahead;
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    const uint8_t* st = stage_ptr(s);
-    uint8_t* parts = s_raw + kGradStages * P::kStageBytes;
-    for (int i = threadIdx.x; i < kGradTokens * 8 * MB; i += 256) {
-      const int t = i / (8 * MB), m = i % (8 * MB) * 2;
-      float2 f = *reinterpret_cast<const float2*>(st + kGradTokens * P::kRow + t * P::kPRow + m * 4);
-#pragma unroll
-      for (int h = 0; h < 3; ++h) {
-        const uint32_t w = pack_bf16x2(f.x, f.y);
-        f.x -= __uint_as_float(w << 16);
-        f.y -= __uint_as_float(w & 0xFFFF0000u);
-        *reinterpret_cast<uint32_t*>(parts + (h * kGradTokens + t) * P::kSplitRow + m * 2) = w;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kGradTokens / 16; ++kk) {
-      uint32_t bq[P::kBlocks / 2][4];  // q: 16 tokens x this warp's columns, transposed on the way
-#pragma unroll
-      for (int j = 0; j < P::kBlocks / 2; ++j)
-        ldmatrix_trans(bq[j], smem_u32(st + (kk * 16 + (lane & 15)) * P::kRow +
-                                       (warp * (P::kCols / 8) + 16 * j + (lane >> 4) * 8) * 2));
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        float d[P::kBlocks][4] = {};  // these 16 tokens' sums
-#pragma unroll
-        for (int h = 0; h < 3; ++h) {
-          uint32_t w[4];
-          const int t = kk * 16 + (lane & 7) + (lane & 16 ? 8 : 0), m = 16 * i + (lane & 8);
-          ldmatrix_trans(w, smem_u32(parts + (h * kGradTokens + t) * P::kSplitRow + m * 2));
-#pragma unroll
-          for (int j = 0; j < P::kBlocks; ++j)
-            mma_16816(d[j], w[0], w[1], w[2], w[3], bq[j / 2][2 * (j & 1)], bq[j / 2][2 * (j & 1) + 1]);
-        }
-#pragma unroll
-        for (int j = 0; j < P::kBlocks; ++j)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][j][v] += d[j][v];
-      }
-    }
-    --ahead;
-    s = (s + 1) % kGradStages;
-    __syncthreads();
-  }
-
-  float* out = a.out + static_cast<int64_t>(id) * a.r * a.K;
-  if (split > 1 && count > 0) {
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-    float* s_sum = reinterpret_cast<float*>(s_raw);  // [16 MB][128]
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-      for (int j = 0; j < P::kBlocks; ++j) {
-        const int m = 16 * i + g, c = warp * (P::kCols / 8) + 8 * j + 2 * t4;
-        *reinterpret_cast<float2*>(s_sum + m * P::kCols + c) = make_float2(acc[i][j][0], acc[i][j][1]);
-        *reinterpret_cast<float2*>(s_sum + (m + 8) * P::kCols + c) =
-            make_float2(acc[i][j][2], acc[i][j][3]);
-      }
-    cluster_sync();
-    for (int i = rank * 256 + threadIdx.x; i < a.r * P::kCols; i += split * 256) {
-      const int m = i / P::kCols, c = i % P::kCols;
-      const uint32_t addr = smem_u32(s_sum + i);
-      float v = 0.0f;
-      for (int o = 0; o < split; ++o) v += ld_cluster(map_to_rank(addr, o));
-      if (col0 + c < a.K) {
-        float* dst = out + static_cast<int64_t>(m) * a.K + col0 + c;
-        *dst = a.accumulate ? *dst + v : v;
-      }
-    }
-    cluster_sync();
-    return;
-  }
-  if (rank > 0 || (count == 0 && a.accumulate)) return;
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < P::kBlocks; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int m = 16 * i + g + 8 * h, c = col0 + warp * (P::kCols / 8) + 8 * j + 2 * t4;
-        if (m < a.r && c < a.K) {
-          float2* dst = reinterpret_cast<float2*>(out + static_cast<int64_t>(m) * a.K + c);
-          float2 v = make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
-          if (a.accumulate) {
-            const float2 old = *dst;
-            v.x += old.x;
-            v.y += old.y;
-          }
-          *dst = v;
-        }
-      }
-}
-
 // ------------------------------- host side -----------------------------------
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -464,30 +224,6 @@ moe_status launch_project(const ProjectArgs& a, const Operands& o, bool kmaj, cu
   const int64_t pair = ceil_div(ceil_div(a.N, 256) * ceil_div(T, 256), sms / 2) * steps * 2;
   if (!a.y_fp32 && T >= 32 * static_cast<int64_t>(a.seg.n_seg) && 10 * pair <= 13 * flat) return project_pair(a, o, kmaj, s);
   return kmaj ? project_flat128_kmaj(a, o, split, s) : project_flat128(a, o, split, s);
-}
-
-template <int MB>
-moe_status launch_grads_as(const GradArgs& a, cudaStream_t s) {
-  using P = Grad<MB>;
-  auto kern = grads_kernel<MB>;
-  static std::mutex mu;
-  static bool done[64] = {};
-  if (!opt_in(kern, P::kSmem, mu, done)) return MOE_ERR_CUDA;
-  const int64_t blocks = ceil_div(a.K, P::kCols);
-  const int64_t active = std::min(a.seg.n_adapters, a.seg.n_seg);
-  const int split =
-      pow2_at_most(std::min<int64_t>(4 * sm_count() / (blocks * active), a.seg.T / 64), 8);
-  launch_clustered(kern, dim3(static_cast<unsigned>(blocks * split), a.seg.n_adapters), 256, P::kSmem,
-                   split, s, a, split);
-  return launch_status();
-}
-
-moe_status launch_grads(const GradArgs& a, cudaStream_t s) {
-  const int mb = (a.r + 15) / 16;
-  if (mb == 1) return launch_grads_as<1>(a, s);
-  if (mb == 2) return launch_grads_as<2>(a, s);
-  if (mb <= 4) return launch_grads_as<4>(a, s);
-  return launch_grads_as<8>(a, s);
 }
 
 constexpr int64_t kMaxStride = int64_t(1) << 31;
@@ -594,9 +330,9 @@ MOE_API moe_status moe_adapter_project_backward(
     if (st != MOE_OK) return st;
   }
   if (da != nullptr) {
-    st = launch_grads(GradArgs{seg, p->d, p->r, v, x, p->x_stride, da, accumulate}, s);
+    st = table_grads(GradArgs{seg, p->d, p->r, v, x, p->x_stride, da, accumulate, dev_status}, s);
     if (st != MOE_OK) return st;
   }
-  if (db != nullptr) return launch_grads(GradArgs{seg, p->n, p->r, u, dy, p->y_stride, db, accumulate}, s);
+  if (db != nullptr) return table_grads(GradArgs{seg, p->n, p->r, u, dy, p->y_stride, db, accumulate, dev_status}, s);
   return MOE_OK;
 }

@@ -55,6 +55,20 @@ struct ShrinkArgs {
   uint32_t* dev_status;
 };
 
+// out[e, m, k] = (or +=) sum over e's tokens of p[t, m] q[t, k] (adapter_grads.cu).
+struct GradArgs {
+  Segments seg;
+  int K, r;
+  const float* p;     // [T, r]
+  const uint16_t* q;  // [T, K]
+  int64_t q_stride;
+  float* out;         // [n_adapters, r, K]
+  int accumulate;
+  uint32_t* dev_status;
+};
+
+moe_status table_grads(const GradArgs& a, cudaStream_t s);
+
 // Segments long enough for tiles of 128 rows (adapter_shrink.cu).
 moe_status shrink_long(const ShrinkArgs& a, cudaStream_t s);
 
