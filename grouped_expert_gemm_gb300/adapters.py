@@ -97,8 +97,8 @@ class AdapterProjection:
         return y
 
     def backward(self, dy, accumulate: bool = False, stream=None):
-        """Gradients of the last forward: (dx [T, d] bf16, da, db fp32 like the tables); dy is
-        [T, n] bf16.  The buffers are the object's own; with ``accumulate`` da and db are added
+        """Gradients of the last forward, whose x, segments and tables must be as they were:
+        (dx [T, d] bf16, da, db fp32 like the tables); dy is [T, n] bf16.  The buffers are the object's own; with ``accumulate`` da and db are added
         to what they hold (zeros at first).  The weight has no gradient."""
         abi.check_current_device(self.device)
         if self._last is None:

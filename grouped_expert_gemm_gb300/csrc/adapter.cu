@@ -162,8 +162,7 @@ shrink_kernel(const ShrinkArgs a, int split, int pieces_mode) {
       const int at = m * P::kPitch + row;
       float v = 0.0f;
       if (split > 1) {
-        const uint32_t addr = smem_u32(s_sum + at);
-        for (int o = 0; o < split; ++o) v += ld_cluster(map_to_rank(addr, o));
+        v = sum_of_ranks(smem_u32(s_sum + at), split);
       } else {
 #pragma unroll
         for (int s = 0; s < P::kSlices; ++s) v += s_part[s * P::kElems + at];

@@ -209,6 +209,18 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
+// The sum of a float at the same place in every CTA of a cluster of `split`, in the order of the
+// ranks.  (All loads are on their way before the first is used.)
+__device__ __forceinline__ float sum_of_ranks(uint32_t addr, int split) {
+  float v[8];
+#pragma unroll
+  for (int o = 0; o < 8; ++o) v[o] = o < split ? ld_cluster(map_to_rank(addr, o)) : 0.0f;
+  float sum = v[0];
+#pragma unroll
+  for (int o = 1; o < 8; ++o) sum += v[o];
+  return sum;
+}
+
 // The library's launch, with clusters of `cluster` CTAs along x.
 template <typename... KArgs, typename... Args>
 void launch_clustered(void (*kern)(KArgs...), dim3 grid, int threads, int smem, int cluster,

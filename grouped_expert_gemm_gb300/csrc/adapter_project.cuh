@@ -699,6 +699,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     if constexpr (CG == 2) umma_dealloc_pair(tmem, F::kTmem);
     else umma_dealloc(tmem, F::kTmem);
   }
+  pdl_wait();  // (where the epilogue gave up before its own)
   pdl_trigger();
 }
 

@@ -185,9 +185,8 @@ shrink_long_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     if (live && *abort_flag == 0) {
       const float scale = __ldg(a.scale + p.adapter);
       for (int i = rank * kThreads + threadIdx.x; i < p.rows * a.r; i += split * kThreads) {
-        const uint32_t at = smem_u32(reinterpret_cast<float*>(stage_base) + i / a.r * F::kSumPitch + i % a.r);
-        float v = 0.0f;
-        for (int o = 0; o < split; ++o) v += ld_cluster(map_to_rank(at, o));
+        const float v = sum_of_ranks(
+            smem_u32(reinterpret_cast<float*>(stage_base) + i / a.r * F::kSumPitch + i % a.r), split);
         a.u[static_cast<int64_t>(p.row) * a.r + i] = scale * v;
       }
     }

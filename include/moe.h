@@ -860,7 +860,8 @@ typedef struct {
  * and in y.  A segment may be empty, and several may name one adapter.  A row's result depends
  * on its own x, w and its own adapter only: a NaN or Inf in one adapter's tables or in one
  * row stays with the rows that use it.
- * fp32 y [T, E] of w [d, E] are router logits as moe_route takes them.
+ * fp32 y [T, E] of w [d, E] are router logits as moe_route takes them.  Where u is infinite (or
+ * beyond bf16's range) y is NaN or infinite.
  * Offsets out of order or range set MOE_DEV_BAD_MAP (results unspecified, nothing outside
  * the arrays is touched); an adapter outside [-1, n_adapters) sets MOE_DEV_BAD_ADAPTER and
  * counts as none.  A bounded wait that gives up sets MOE_DEV_TIMEOUT (outputs invalid).
