@@ -93,6 +93,12 @@ SHAPES = [
     # runs between rows without an adapter, inside 32 rows
     (2200, [0, 34, 50, 64, 70, 2180], [-1, 1, -1, 0, -1], 200, 2040, 24, 2),
     (100, [1, 4, 9, 40, 60, 97], [-1, 1, -1, 0, -1], 328, 136, 8, 2),
+    # single tokens beside long segments in tiles of two CTAs; more segments than are looked over
+    # piece by piece; reductions of several fp32 pieces, whole and shared by a cluster
+    (2290, list(range(41)) + [400, 1200, 2290], [q % 5 - 1 for q in range(43)], 200, 2040, 128, 4),
+    (3500, list(range(2900)) + [3100, 3490], [q % 7 - 1 for q in range(2901)], 64, 72, 16, 6),
+    (2290, [0, 700, 1300, 2290], [1, 0, 2], 2056, 2040, 8, 3),
+    (40, [0, 5, 39], [1, 0], 6000, 136, 48, 2),
     (700, [0] * 300 + [400] * 200 + [700], [q % 3 for q in range(500)], 128, 128, 8, 3),
 ]
 
