@@ -207,21 +207,29 @@ moe_status launch_shrink(const ShrinkArgs& a, cudaStream_t s) {
   return narrow ? launch_shrink_as<8, 1>(a, s) : launch_shrink_as<8, 4>(a, s);
 }
 
+// The shape of the projection.  Up to 64 tokens: narrow tiles, the reduction shared by up to
+// four CTAs until the SMs are full (one token: 16 tiles of 7168 x 128 on one / two / four CTAs each
+// 36.9 / 22.7 / 14.4 us; 64 tokens of as many adapters, 2048 x 2048: 19.3 / 15.4 / 13.6).
+// Above, what takes fewer cycles: a stage of 64 takes 575 in either shape (it has 32 KB a CTA), the
+// adapters' part and the stores 18,000 a tile of a pair, behind the last tile or where a tile's
+// MMAs are shorter, and 8,000 of 128 x 128.  Measured, flat / pair (us): 256 tokens, 4096 x 4096: 22.5
+// / 32.7; 512: 29.8 / 31.7; 1,024: 56.5 / 51.2; 1,024, 2048 x 2048: 19.2 / 22.5; 2,048: 31.0 / 27.7;
+// 4,096, 2048 x 1024: 32.7 / 29.6, 768 x 2048: 29.5 / 34.2.  Where segments have few rows flat
+// tiles make the adapters' part beside the MMAs: 1,000 tokens in 70 segments, 4096 x 4096: 105 / 117.
 moe_status launch_project(const ProjectArgs& a, const Operands& o, bool kmaj, cudaStream_t s) {
-  const int64_t cols = ceil_div(a.N, 128);
-  const int64_t steps = ceil_div(a.K, 64);
-  const int64_t sms = sm_count();
+  const int64_t sms = sm_count(), cols = ceil_div(a.N, 128);
   const int T = a.seg.T;
   if (T <= 64) {
-    const int split = pow2_at_most(std::min(sms / cols, steps), 4);
+    const int split = pow2_at_most(std::min(sms / cols, ceil_div(a.K, 128)), 4);
     return kmaj ? project_flat64_kmaj(a, o, split, s) : project_flat64(a, o, split, s);
   }
-  // Rounds of tiles, in units of a 128 x 128 tile's MMAs a step.
-  const int64_t tiles = cols * ceil_div(T, 128);
+  const int64_t steps = ceil_div(a.K, 64), tiles = cols * ceil_div(T, 128);
   const int split = pow2_at_most(std::min(sms / tiles, steps), 4);
-  const int64_t flat = split > 1 ? ceil_div(steps, split) : ceil_div(tiles, sms) * steps;
-  const int64_t pair = ceil_div(ceil_div(a.N, 256) * ceil_div(T, 256), sms / 2) * steps * 2;
-  if (!a.y_fp32 && T >= 32 * static_cast<int64_t>(a.seg.n_seg) && 10 * pair <= 13 * flat) return project_pair(a, o, kmaj, s);
+  const int64_t flat = ceil_div(tiles * split, sms) * std::max<int64_t>(575 * ceil_div(steps, split), 8000) + 6000;
+  const int64_t pair_tiles = ceil_div(a.N, 256) * ceil_div(T, 256);
+  const int64_t pair = ceil_div(pair_tiles, sms / 2) * std::max<int64_t>(575 * steps, 18000) + 18000;
+  if (!a.y_fp32 && T >= 32 * static_cast<int64_t>(a.seg.n_seg) && pair < flat)
+    return project_pair(a, o, kmaj, s);
   return kmaj ? project_flat128_kmaj(a, o, split, s) : project_flat128(a, o, split, s);
 }
 

@@ -23,7 +23,7 @@ constexpr int kTokens = 64;
 constexpr int kCols = 128;
 constexpr int kQBox = kTokens * 128;
 constexpr int kQBytes = 2 * kQBox;
-constexpr int kGroup = 4;
+constexpr int kGroup = 2;
 
 template <int RB>
 struct Grads {

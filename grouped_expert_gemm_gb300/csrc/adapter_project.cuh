@@ -11,8 +11,9 @@ namespace {
 //
 // D^T = W^T X^T: the weight's columns are the M operand, the tokens N, so a decode batch is a
 // narrow tile and the weight streams once.  Roles of the 320 threads:
-//   warp 0       TMA producer: [64 k x 128] of the weight (16 KB) and [tokens x 64 k] of x
-//   warp 1       tensor memory; lane 0 issues four MMAs (K = 16) a stage
+//   warp 0       TMA producer: [64 k x 128] of the weight (16 KB) and [tokens x 64 k] of x, once or
+//                (few tokens) twice a stage
+//   warp 1       tensor memory; lane 0 issues the MMAs (K = 16)
 //   warps 2..9   epilogue: warp (quad, sub) has the 16 weight columns at 32 quad + 16 sub
 // The adapters' part is made by the epilogue warps, 32 tokens at a time: u B is r / d of the work
 // and a run of one adapter may be one token long, where tcgen05's narrowest tile is 16 columns
@@ -40,7 +41,7 @@ namespace {
 constexpr int kThreads = 320;
 constexpr int kWBytes = 128 * 64 * 2;
 constexpr int kWBox = 64 * 64 * 2;
-constexpr int kPiece = 16;      // steps of 64 to a piece of an fp32 result's reduction
+constexpr int kPiece = 8;  // blocks of 64 to a piece of an fp32 result's reduction
 constexpr int kMaxRank = 128;
 
 // 32 tokens of u: [value, remainder][32][r, padded to 16 and 8 more], so that eight rows of an
@@ -52,8 +53,13 @@ constexpr int kPieceBytes = 18 * 1024;  // either of them
 
 template <int TN, int S, int CG>
 struct Shape {
-  static constexpr int kStageBytes = kWBytes + TN / CG * 128;
-  static constexpr int kStages = CG == 2 ? 5 : TN == 128 ? (S == 1 ? 5 : 4) : 6;
+  // Blocks of 64 k a stage.  Two where the weight streams for few tokens: half as many, larger
+  // boxes of it (128 k x 64).
+  static constexpr int kDepth = TN == 64 ? 2 : 1;
+  static constexpr int kXBlock = TN / CG * 128;
+  static constexpr int kXOff = kDepth * kWBytes;
+  static constexpr int kStageBytes = kDepth * (kWBytes + kXBlock);
+  static constexpr int kStages = CG == 2 ? 5 : TN == 128 ? (S == 1 ? 5 : 4) : 3;
   static constexpr int kOwn = TN / S;
   static constexpr int kRedBytes = (S - 1) * kOwn * 512;  // [S - 1][kOwn / 8][8][32] float4
   // full[st], empty[st], tfull[2], tempty[2], group, red, drain
@@ -545,10 +551,11 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   const int first = static_cast<int>(blockIdx.x) / kCluster;
   const int step = static_cast<int>(gridDim.x) / kCluster;
   const int total = a.n_blocks * a.t_blocks;
-  const int steps = (a.K + 63) / 64;
+  constexpr int kDepth = F::kDepth;
+  const int steps = (a.K + 64 * kDepth - 1) / (64 * kDepth);  // stages of the reduction
   const int k0 = S > 1 ? rank * steps / S : 0, k1 = S > 1 ? (rank + 1) * steps / S : steps;
-  const int piece = CG == 1 && a.y_fp32 ? kPiece : steps;
-  const uint32_t stage_tx = kWBytes + a.x_rows * 128;
+  const int piece = CG == 1 && a.y_fp32 ? kPiece / kDepth : steps;
+  const uint32_t stage_tx = kDepth * (kWBytes + a.x_rows * 128);
 
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto empty_bar = [&](int s) { return smem_u32(bars + kStages + s); };
@@ -612,12 +619,16 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
           } else {
             mbar_arrive_expect_tx(full_bar(s), stage_tx);
             if (KMAJ) {
-              tma_load_2d(st, &map_w, full_bar(s), k * 64, n0);
+#pragma unroll
+              for (int h = 0; h < kDepth; ++h)
+                tma_load_2d(st + h * kWBytes, &map_w, full_bar(s), (k * kDepth + h) * 64, n0);
             } else {
-              tma_load_2d(st, &map_w, full_bar(s), n0, k * 64);
-              tma_load_2d(st + kWBox, &map_w, full_bar(s), n0 + 64, k * 64);
+              tma_load_2d(st, &map_w, full_bar(s), n0, k * kDepth * 64);
+              tma_load_2d(st + kDepth * kWBox, &map_w, full_bar(s), n0 + 64, k * kDepth * 64);
             }
-            tma_load_2d(st + kWBytes, &map_x, full_bar(s), k * 64, row0);
+#pragma unroll
+            for (int h = 0; h < kDepth; ++h)
+              tma_load_2d(st + F::kXOff + h * F::kXBlock, &map_x, full_bar(s), (k * kDepth + h) * 64, row0);
           }
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
@@ -652,9 +663,10 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             umma_fence_after();
             const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t ad = KMAJ ? umma_desc(st + kk * 32) : umma_desc_mn(st + kk * 16 * 128, kWBox);
-              const uint64_t bd = umma_desc(st + kWBytes + kk * 32);
+            for (int kk = 0; kk < 4 * kDepth; ++kk) {
+              const uint64_t ad = KMAJ ? umma_desc(st + kk / 4 * kWBytes + kk % 4 * 32)
+                                       : umma_desc_mn(st + kk * 16 * 128, kDepth * kWBox);
+              const uint64_t bd = umma_desc(st + F::kXOff + kk / 4 * F::kXBlock + kk % 4 * 32);
               if constexpr (CG == 2) umma_bf16_pair(tmem + buf * TN, ad, bd, idesc, k > kp || kk > 0);
               else umma_bf16(tmem + buf * TN, ad, bd, idesc, k > kp || kk > 0);
             }
@@ -758,7 +770,7 @@ bool launch_project_as(ProjectArgs a, const Operands& o, cudaStream_t s, moe_sta
   CUtensorMap mw, mx;
   a.x_rows = static_cast<int>(std::min<int64_t>(TN / CG, ceil_div(a.seg.T, 8) * 8));
   // the weight is [K, N] (rows of N), or for the backward [N, K]
-  if (!(KMAJ ? map_2d(&mw, o.w, a.N, a.K, a.K, 128) : map_2d(&mw, o.w, a.K, a.N, a.N, 64)) ||
+  if (!(KMAJ ? map_2d(&mw, o.w, a.N, a.K, a.K, 128) : map_2d(&mw, o.w, a.K, a.N, a.N, 64 * F::kDepth)) ||
       !map_2d(&mx, o.x, a.seg.T, a.K, o.x_stride, a.x_rows))
     return true;
   // Tokens inner: the weight is read once, the rows stay in the L2.  Rows that outgrow it while

@@ -18,7 +18,7 @@ namespace {
 constexpr int kThreads = 192;
 constexpr int kRows = 128;
 constexpr int kXBytes = kRows * 128;
-constexpr int kPieceSteps = 8;
+constexpr int kPieceSteps = 4;
 
 template <int RB>
 struct Long {
