@@ -192,9 +192,9 @@ struct Epilogue {
   int first, step, total, rank, k0, k1, piece_steps;
 };
 
-// The epilogue warps' work; RB: blocks of 16 ranks.  True if partners' sums were awaited.
+// The epilogue warps' work; RB: blocks of 16 ranks.
 template <int TN, int S, int CG, int RB>
-__device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s, int warp, int lane) {
+__device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s, int warp, int lane) {
   constexpr int kOwn = TN / S, kChunks = (kOwn + 31) / 32, kGroups = kOwn < 32 ? kOwn / 8 : 4;
   constexpr int kQuads = 4 * RB;                              // groups of four values of a row of u
   constexpr int kLoads = (8 * kGroups * kQuads + 255) / 256;  // of them a thread
@@ -208,7 +208,7 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
   const uint32_t sums = taddr + 2 * TN;  // (flat) [kOwn], or in pieces [TN]
   int buf = 0, par = 0, pb = 0;
   uint32_t acc_ph = 0, group_ph = 0;
-  bool ok = true, waited = false, awaited = false;
+  bool ok = true, waited = false;
   // Barrier of the eight warps: false if one of them gave up.
   auto meet = [&]() {
     __syncwarp();
@@ -473,7 +473,6 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
       }
       if (!ok || !sums_ready()) break;
       if constexpr (S > 1) {
-        awaited = true;
         for (int i = 1; i < S; ++i) {  // the partners' tokens first
           const int owner = (s.rank + i) % S;
           const uint32_t bar = map_to_rank(s.red_bar, owner);
@@ -523,7 +522,6 @@ __device__ __forceinline__ bool epilogue(const ProjectArgs& a, const Epilogue& s
     }
     par ^= 1;
   }
-  return awaited;
 }
 
 template <int TN, int S, int CG, bool KMAJ>
@@ -591,7 +589,6 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   if constexpr (kCluster > 1) cluster_sync();  // the partners' barriers are initialised
   umma_fence_after();
   const uint32_t tmem = *tmem_slot;
-  bool awaited = false;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -690,10 +687,10 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   } else {
     const Epilogue e{s_piece, s_red, s_id, s_whole, s_starts, abort_flag, tfull_bar(0), tempty_bar(0), group_bar,
                      red_bar, tmem, first, step, total, rank, k0, k1, piece};
-    awaited = a.r <= 16   ? epilogue<TN, S, CG, 1>(a, e, warp, lane)
-              : a.r <= 32 ? epilogue<TN, S, CG, 2>(a, e, warp, lane)
-              : a.r <= 64 ? epilogue<TN, S, CG, 4>(a, e, warp, lane)
-                          : epilogue<TN, S, CG, 8>(a, e, warp, lane);
+    if (a.r <= 16) epilogue<TN, S, CG, 1>(a, e, warp, lane);
+    else if (a.r <= 32) epilogue<TN, S, CG, 2>(a, e, warp, lane);
+    else if (a.r <= 64) epilogue<TN, S, CG, 4>(a, e, warp, lane);
+    else epilogue<TN, S, CG, 8>(a, e, warp, lane);
   }
 
   // ---- teardown ----
@@ -702,8 +699,8 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   __syncthreads();
   if constexpr (kCluster > 1) {
     cluster_sync();  // no CTA leaves while a partner may still reach it
-    // (after a wait that gave up: nor before the sums that were on their way)
-    if (S > 1 && threadIdx.x == 64 && awaited && *abort_flag) wait_drain(red_bar, 0);
+    // (after a wait that gave up: nor before the partners' sums that may be on their way)
+    if (S > 1 && threadIdx.x == 64 && *abort_flag) wait_drain(red_bar, 0);
   }
   umma_fence_after();
   if (warp == 1) {

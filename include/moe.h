@@ -865,8 +865,9 @@ typedef struct {
  * Offsets out of order or range set MOE_DEV_BAD_MAP (results unspecified, nothing outside
  * the arrays is touched); an adapter outside [-1, n_adapters) sets MOE_DEV_BAD_ADAPTER and
  * counts as none.  A bounded wait that gives up sets MOE_DEV_TIMEOUT (outputs invalid).
- * The call enqueues two kernels; the second one reads x and w before the first has ended, so
- * nothing enqueued after the first may write them (the call itself enqueues both).
+ * The call enqueues two kernels; the second one reads x, w, the tables and the segments before
+ * the first has ended, so nothing enqueued after the first may write them (the call itself
+ * enqueues both).
  * Limits: d, n, r % 8 == 0, d, n <= 65536, r <= 128, n_adapters, n_seg <= 65535, strides % 8
  * == 0; 16-byte aligned x, w, a, b, u and y.  T = 0 does nothing.  y must not overlap the
  * inputs.                                                                     */
