@@ -714,7 +714,8 @@ def moe_adapter_project_backward(p: AdapterParams, seg_offsets, seg_adapter, x, 
         _ptr(scale), _ptr(u), _ptr(dy), _ptr(dx), _ptr(da), _ptr(db), accumulate, _ptr(ws),
         ws_bytes, _ptr(dev_status), _stream(stream)))
     if p.T > 0:
-        _count(int(dx is not None or da is not None) + sum(t is not None for t in (dx, da, db)))
+        _count(int(dx is not None or da is not None) + int(dx is not None) +
+               int(da is not None or db is not None))
 
 
 def moe_grad_plan(tensors, n_groups: int) -> int:

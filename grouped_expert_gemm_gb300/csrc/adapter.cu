@@ -336,10 +336,13 @@ MOE_API moe_status moe_adapter_project_backward(
                               Operands{dy, p->y_stride, w}, true, s);
     if (st != MOE_OK) return st;
   }
-  if (da != nullptr) {
-    st = table_grads(GradArgs{seg, p->d, p->r, v, x, p->x_stride, da, accumulate, dev_status}, s);
-    if (st != MOE_OK) return st;
-  }
-  if (db != nullptr) return table_grads(GradArgs{seg, p->n, p->r, u, dy, p->y_stride, db, accumulate, dev_status}, s);
+  if (da != nullptr || db != nullptr)
+    return table_grads(GradArgs{seg,
+                                p->r,
+                                {{da != nullptr ? p->d : 0, v, x, p->x_stride, da},
+                                 {db != nullptr ? p->n : 0, u, dy, p->y_stride, db}},
+                                accumulate,
+                                dev_status},
+                       s);
   return MOE_OK;
 }

@@ -55,14 +55,19 @@ struct ShrinkArgs {
   uint32_t* dev_status;
 };
 
-// out[e, m, k] = (or +=) sum over e's tokens of p[t, m] q[t, k] (adapter_grads.cu).
-struct GradArgs {
-  Segments seg;
-  int K, r;
+// out[e, m, k] = (or +=) sum over e's tokens of p[t, m] q[t, k], of up to two pairs of p and q
+// (adapter_grads.cu).
+struct GradSide {
+  int K;              // 0: left out
   const float* p;     // [T, r]
   const uint16_t* q;  // [T, K]
   int64_t q_stride;
   float* out;         // [n_adapters, r, K]
+};
+struct GradArgs {
+  Segments seg;
+  int r;
+  GradSide side[2];
   int accumulate;
   uint32_t* dev_status;
 };

@@ -1,5 +1,5 @@
 // The tables' gradients: out[e, m, k] = sum over e's tokens of p[t, m] q[t, k], p fp32 [T, r] (u or
-// v), q bf16 (dy or x).
+// v), q bf16 (dy or x); dA and dB in one launch, the columns of one behind the other's.
 //
 // D^T: 128 columns of q (M, their tokens the reduction, as TMA lays them down) against the r
 // columns of p (N).  A CTA takes one adapter and 128 columns, and of the adapter's tokens, cut
@@ -85,7 +85,8 @@ struct Walk {
 
 template <int RB>
 __global__ void __launch_bounds__(kThreads, Grads<RB>::kPerSm)
-grads_kernel(const __grid_constant__ CUtensorMap map_q, const GradArgs a, int split) {
+grads_kernel(const __grid_constant__ CUtensorMap map_q0, const __grid_constant__ CUtensorMap map_q1,
+             const GradArgs a, int split) {
   using F = Grads<RB>;
   constexpr int kStages = F::kStages, kN = F::kN;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -97,7 +98,11 @@ grads_kernel(const __grid_constant__ CUtensorMap map_q, const GradArgs a, int sp
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + F::kBars) + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int col0 = static_cast<int>(blockIdx.x) / split * kCols;
+  const int block = static_cast<int>(blockIdx.x) / split, blocks0 = (a.side[0].K + kCols - 1) / kCols;
+  const bool second = block >= blocks0;
+  const CUtensorMap* map_q = second ? &map_q1 : &map_q0;
+  const int K = a.side[second].K, col0 = (second ? block - blocks0 : block) * kCols;
+  const float* p = a.side[second].p;
   const int id = blockIdx.y;
   auto full_bar = [&](int s) { return smem_u32(bars + s); };
   auto ready_bar = [&](int s) { return smem_u32(bars + kStages + s); };
@@ -119,11 +124,11 @@ grads_kernel(const __grid_constant__ CUtensorMap map_q, const GradArgs a, int sp
     }
     count += __reduce_add_sync(kAll, n);
   }
-  float* out = a.out + static_cast<int64_t>(id) * a.r * a.K;
+  float* out = a.side[second].out + static_cast<int64_t>(id) * a.r * K;
   if (count == 0) {  // (the same in every CTA of a cluster)
     if (rank == 0 && !a.accumulate)
       for (int i = threadIdx.x; i < a.r * kCols; i += kThreads)
-        if (col0 + i % kCols < a.K) out[static_cast<int64_t>(i / kCols) * a.K + col0 + i % kCols] = 0.0f;
+        if (col0 + i % kCols < K) out[static_cast<int64_t>(i / kCols) * K + col0 + i % kCols] = 0.0f;
     return;
   }
   const int64_t part0 = count * rank / split, part1 = count * (rank + 1) / split;
@@ -161,8 +166,8 @@ grads_kernel(const __grid_constant__ CUtensorMap map_q, const GradArgs a, int sp
       if (lane == 0) {
         const uint32_t st = smem_u32(stage_base + s * F::kStageBytes);
         mbar_arrive_expect_tx(full_bar(s), kQBytes);
-        tma_load_2d(st, &map_q, full_bar(s), col0, row);
-        tma_load_2d(st + kQBox, &map_q, full_bar(s), col0 + 64, row);
+        tma_load_2d(st, map_q, full_bar(s), col0, row);
+        tma_load_2d(st + kQBox, map_q, full_bar(s), col0 + 64, row);
       }
       if (++s == kStages) { s = 0; ph ^= 1u; }
     }
@@ -250,7 +255,7 @@ grads_kernel(const __grid_constant__ CUtensorMap map_q, const GradArgs a, int sp
         const int item = tid + 128 * i, m = item % kN, t0 = item / kN * 8;
 #pragma unroll
         for (int t = 0; t < 8; ++t)
-          ahead[f][i][t] = m < a.r && t0 + t < rows ? a.p[static_cast<int64_t>(row + t0 + t) * a.r + m] : 0.0f;
+          ahead[f][i][t] = m < a.r && t0 + t < rows ? p[static_cast<int64_t>(row + t0 + t) * a.r + m] : 0.0f;
       }
     };
     int s = 0;
@@ -306,11 +311,11 @@ grads_kernel(const __grid_constant__ CUtensorMap map_q, const GradArgs a, int sp
     while (ok && done < pieces) ok = take();
     const int c = quad * 32 + lane;
     if (ok && split == 1) {
-      if (col0 + c < a.K) {
+      if (col0 + c < K) {
 #pragma unroll
         for (int m = 0; m < kN; ++m)
           if (m < a.r) {
-            float* dst = out + static_cast<int64_t>(m) * a.K + col0 + c;
+            float* dst = out + static_cast<int64_t>(m) * K + col0 + c;
             *dst = a.accumulate ? *dst + acc[m] : acc[m];
           }
       }
@@ -326,8 +331,8 @@ grads_kernel(const __grid_constant__ CUtensorMap map_q, const GradArgs a, int sp
     if (*abort_flag == 0)
       for (int i = rank * kThreads + threadIdx.x; i < a.r * kCols; i += split * kThreads) {
         const float v = sum_of_ranks(smem_u32(reinterpret_cast<float*>(stage_base) + i), split);
-        if (col0 + i % kCols < a.K) {
-          float* dst = out + static_cast<int64_t>(i / kCols) * a.K + col0 + i % kCols;
+        if (col0 + i % kCols < K) {
+          float* dst = out + static_cast<int64_t>(i / kCols) * K + col0 + i % kCols;
           *dst = a.accumulate ? *dst + v : v;
         }
       }
@@ -350,9 +355,13 @@ moe_status launch_grads(const GradArgs& a, cudaStream_t s) {
   static std::mutex mu;
   static bool done[64] = {};
   if (!opt_in(kern, F::kSmem, mu, done)) return MOE_ERR_CUDA;
-  CUtensorMap mq;
-  if (!map_2d(&mq, a.q, a.seg.T, a.K, a.q_stride, kTokens)) return MOE_ERR_CUDA;
-  const int64_t blocks = ceil_div(a.K, kCols);
+  CUtensorMap mq[2] = {};
+  int64_t blocks = 0;
+  for (int i = 0; i < 2; ++i) {
+    const GradSide& g = a.side[i];
+    if (g.K > 0 && !map_2d(&mq[i], g.q, a.seg.T, g.K, g.q_stride, kTokens)) return MOE_ERR_CUDA;
+    blocks += ceil_div(g.K, kCols);
+  }
   // Adapters that can have tokens.  Their tokens are split until the CTAs are twice what the SMs
   // hold, two pieces a CTA at least: adapters have more and less of them (4,096 tokens x 7168, of
   // which one adapter of four has 2,345: 26 us where the CTAs just fit).
@@ -360,7 +369,7 @@ moe_status launch_grads(const GradArgs& a, cudaStream_t s) {
   const int split = pow2_at_most(
       std::min<int64_t>(2 * F::kPerSm * sm_count() / (blocks * active), a.seg.T / (2 * kTokens)), 8);
   launch_clustered(kern, dim3(static_cast<unsigned>(blocks * split), a.seg.n_adapters), kThreads, F::kSmem,
-                   split, s, mq, a, split);
+                   split, s, mq[0], mq[1], a, split);
   return launch_status();
 }
 
