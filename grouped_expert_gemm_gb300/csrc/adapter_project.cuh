@@ -23,6 +23,10 @@ namespace {
 //     by movmatrix, once a run) is multiplied with u onto the sums themselves, and every token
 //     takes the result of its own run.  u is split into two bf16 numbers a value by all warps
 //     together.
+//   256 tokens of one adapter of up to 32 ranks (pairs): the reduction goes on over the ranks, u as
+//     value and remainder against the table twice, both laid down in shared memory by the
+//     epilogue warps while the tile's MMAs run.  (Beside running MMAs the products above take
+//     2,000 cycles for 32 tokens.)
 //   otherwise: warp w takes tokens 4w .. 4w + 3, each with its own adapter's rows (four columns
 //     a lane, fp32), through shared memory.
 // Nothing of one request, not even 0 times an infinity, reaches another's rows.
@@ -51,6 +55,9 @@ __host__ __device__ constexpr int u_pitch(int rp) { return rp * 2 + 16; }
 constexpr int kPartPitch = 132;
 constexpr int kPieceBytes = 18 * 1024;  // either of them
 
+constexpr int kMoreU = 128 * 128;
+constexpr int kMoreTable = 2 * 32 * 128;
+
 template <int TN, int S, int CG>
 struct Shape {
   // Blocks of 64 k a stage.  Two where the weight streams for few tokens: half as many, larger
@@ -62,11 +69,14 @@ struct Shape {
   static constexpr int kStages = CG == 2 ? 5 : TN == 128 ? (S == 1 ? 5 : 4) : 3;
   static constexpr int kOwn = TN / S;
   static constexpr int kRedBytes = (S - 1) * kOwn * 512;  // [S - 1][kOwn / 8][8][32] float4
-  // full[st], empty[st], tfull[2], tempty[2], group, red, drain
+  // (pair) the tile's further reduction: [128 tokens][64] of u, [2][32 ranks][64 columns] of the table
+  static constexpr int kMoreBytes = CG == 2 ? kMoreU + kMoreTable : 0;
+  // full[st], empty[st], tfull[2], tempty[2], group, red, drain, more
   static constexpr int kBars = 2 * kStages + 8;
   static constexpr int kTmem = CG == 2 ? 2 * TN : 4 * TN;  // two buffers, (flat) the sums
   static constexpr int kSmem =
-      1024 + kStages * kStageBytes + 2 * kPieceBytes + kRedBytes + kBars * 8 + 2 * (kOwn + 16) * 4 + 16;
+      1024 + kStages * kStageBytes + kMoreBytes + 2 * kPieceBytes + kRedBytes + kBars * 8 +
+      3 * (kOwn + 20) * 4 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOwn % 8 == 0 && kTmem <= 512, "shape");
   static_assert(kPieceBytes >= 2 * 32 * u_pitch(kMaxRank) && kPieceBytes >= 32 * kPartPitch * 4, "pieces");
@@ -183,11 +193,13 @@ __device__ __forceinline__ void put_frags(const ProjectArgs& a, const float (&c)
 struct Epilogue {
   uint8_t* piece;   // [2][kPieceBytes]
   uint8_t* red;
-  int* id;          // [2][kOwn]: adapter of a token
-  int* whole;       // [2][8]: of 32 tokens the adapter of all, kNone where none has one, kFew or kSeveral
-  uint32_t* starts; // [2][8]: where their runs start
+  uint8_t* more;    // kMoreU, then kMoreTable bytes
+  // Three of each, tile by tile: the next tile's are made while other warps may still be at the last.
+  int* id;          // [3][kOwn]: adapter of a token
+  int* whole;       // [3][8]: of 32 tokens the adapter of all, kNone where none has one, kFew or kSeveral
+  uint32_t* starts; // [3][8]: where their runs start
   volatile int* abort_flag;
-  uint32_t tfull, tempty, group_bar, red_bar;  // (tfull and tempty: two barriers each)
+  uint32_t tfull, tempty, group_bar, red_bar, more_bar;  // (tfull and tempty: two barriers each)
   uint32_t tmem;
   int first, step, total, rank, k0, k1, piece_steps;
 };
@@ -208,7 +220,7 @@ __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s
   const uint32_t sums = taddr + 2 * TN;  // (flat) [kOwn], or in pieces [TN]
   int buf = 0, par = 0, pb = 0;
   uint32_t acc_ph = 0, group_ph = 0;
-  bool ok = true, waited = false;
+  bool ok = true;
   // Barrier of the eight warps: false if one of them gave up.
   auto meet = [&]() {
     __syncwarp();
@@ -307,43 +319,108 @@ __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s
     }
   };
 
-  for (int t = s.first; t < s.total; t += s.step) {
-    int row0, n0;
-    tile_at<TN, CG>(a, t, s.rank, row0, n0);
-    const int n = n0 + m0, row_own = row0 + own0;
-    // ---- whose are the tokens: warp w finds out for 32 of them ----
-    int* ids = s.id + par * kOwn;
-    int* whole = s.whole + par * 8;
+  // Whose are the tokens of tile t: warp w finds out for 32 of them.
+  auto look = [&](int t, int to) {
     if (w < kChunks) {
-      const int id = row_adapters(a.seg, row_own + 32 * w, lane);
+      int row0, n0;
+      tile_at<TN, CG>(a, t, s.rank, row0, n0);
+      const int id = row_adapters(a.seg, row0 + own0 + 32 * w, lane);
       constexpr uint32_t kIn = kOwn < 32 ? (1u << (kOwn & 31)) - 1 : kAll;
       const uint32_t has = __ballot_sync(kAll, id >= 0) & kIn;
       const int before = __shfl_up_sync(kAll, id, 1);
       const uint32_t starts = __ballot_sync(kAll, id >= 0 && (lane == 0 || id != before)) & kIn;
-      if (32 * w + lane < kOwn) ids[32 * w + lane] = id;
+      if (32 * w + lane < kOwn) s.id[to * kOwn + 32 * w + lane] = id;
       if (lane == 0) {
-        s.starts[par * 8 + w] = starts;
-        whole[w] = has == 0 ? kNone : has == kIn && starts == 1 ? id : __popc(starts) <= kFewRuns ? kFew : kSeveral;
+        s.starts[to * 8 + w] = starts;
+        s.whole[to * 8 + w] =
+            has == 0 ? kNone : has == kIn && starts == 1 ? id : __popc(starts) <= kFewRuns ? kFew : kSeveral;
       }
     }
-    if (!meet()) break;
+    return meet();
+  };
+  // The adapter of a whole tile (kNone: not of one adapter, or too many ranks).
+  constexpr bool kMore = CG == 2 && RB <= 2;
+  auto tile_adapter = [&](int of) {
+    if constexpr (!kMore) return kNone;
+    const int e = s.whole[of * 8];
+    bool same = e >= 0;
+#pragma unroll
+    for (int ch = 1; ch < kChunks; ++ch) same = same && s.whole[of * 8 + ch] == e;
+    return same ? e : kNone;
+  };
+  // The further reduction of tile t, if it is of one adapter: this CTA's half of the tokens' u and
+  // its columns of the table, both zero behind rank r, as the MMAs take them.  The issuer is told
+  // either way.
+  auto lay_more = [&](int t, int of) {
+    if constexpr (kMore) {
+      const int e = tile_adapter(of);
+      if (e >= 0) {
+        int row0, n0;
+        tile_at<TN, CG>(a, t, s.rank, row0, n0);
+        row0 += s.rank * 128;
+#pragma unroll
+        for (int i = tid; i < 128 * 4 * RB; i += 256) {  // four values of a token
+          const int tok = i / (4 * RB), q = i % (4 * RB);
+          const float4 f = 4 * q < a.r ? *reinterpret_cast<const float4*>(
+                                             a.u + static_cast<int64_t>(row0 + tok) * a.r + 4 * q)
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
+          const uint32_t l0 = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
+          const uint32_t l1 = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+          // 16-byte chunks of a row of 128: the values' first, then (2 RB on) the remainders'
+          uint8_t* row = s.more + tok * 128 + (q & 1) * 8;
+          *reinterpret_cast<uint2*>(row + (((q >> 1) ^ (tok & 7)) << 4)) = make_uint2(h0, h1);
+          *reinterpret_cast<uint2*>(row + (((2 * RB + (q >> 1)) ^ (tok & 7)) << 4)) = make_uint2(l0, l1);
+        }
+#pragma unroll
+        for (int i = tid; i < 16 * RB * 16; i += 256) {  // eight columns of a rank
+          const int k = i / 16, c = i % 16, col = n0 + 8 * c;
+          const uint4 v = k < a.r && col < a.N
+                              ? __ldg(reinterpret_cast<const uint4*>(
+                                    a.table + (static_cast<int64_t>(e) * a.r + k) * a.N + col))
+                              : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(s.more + kMoreU + (c >> 3) * (16 * RB * 128) + k * 128 +
+                                    (((c & 7) ^ (k & 7)) << 4)) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(s.more_bar, 0));
+    }
+  };
+
+  if (s.first < s.total && !look(s.first, 0)) return;
+  bool waited = false;
+  for (int t = s.first; t < s.total; t += s.step) {
+    int row0, n0;
+    tile_at<TN, CG>(a, t, s.rank, row0, n0);
+    const int n = n0 + m0, row_own = row0 + own0;
+    int* ids = s.id + par * kOwn;
+    int* whole = s.whole + par * 8;
+    const int coming_up = par == 2 ? 0 : par + 1;
+    const bool more = t + s.step < s.total;
     if (n != table_n) held = coming = kNone;  // other columns
     table_n = n;
     // the first adapter of 32 tokens that mma.sync takes
     auto first_of = [&](int ch) {
       return whole[ch] == kFew ? ids[32 * ch + __ffs(s.starts[par * 8 + ch]) - 1] : whole[ch];
     };
-    expect(first_of(0), n);
+    const bool done = tile_adapter(par) >= 0;  // the adapter's part is in the sums already
+    if (!done) expect(first_of(0), n);
     if (!waited) {
       pdl_wait();  // u; and what is written here may still be read by the kernels before
       waited = true;
+      lay_more(t, par);
     }
-    if (whole[0] >= 0 || whole[0] == kFew) fetch_u(row_own);
-    if constexpr (CG == 2)
+    if (!done && (whole[0] >= 0 || whole[0] == kFew)) fetch_u(row_own);
+    if (more && !look(t + s.step, coming_up)) break;
+    if constexpr (CG == 2) {
       if (!sums_ready()) break;
+      if (more) lay_more(t + s.step, coming_up);  // (this tile's MMAs have read theirs)
+    }
 #pragma unroll 1
     for (int ch = 0; ch < kChunks; ++ch) {
-      const int j = 32 * ch, kind = whole[ch];
+      const int j = 32 * ch, kind = done ? kNone : whole[ch];
       uint8_t* piece = s.piece + pb * kPieceBytes;
       const uint32_t at = lu + pb * kPieceBytes;
       if (kind >= 0 || kind == kFew) {
@@ -379,7 +456,7 @@ __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s
         if (!ok) break;
         pb ^= 1;  // (the other piece's readers have all come here)
       }
-      if (ch + 1 < kChunks && (whole[ch + 1] >= 0 || whole[ch + 1] == kFew)) fetch_u(row_own + j + 32);
+      if (!done && ch + 1 < kChunks && (whole[ch + 1] >= 0 || whole[ch + 1] == kFew)) fetch_u(row_own + j + 32);
       float c[kGroups][4];
       if constexpr (CG == 2) {
 #pragma unroll
@@ -520,7 +597,7 @@ __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s
       }
       sums_read();
     }
-    par ^= 1;
+    par = coming_up;
   }
 }
 
@@ -534,14 +611,15 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stage_base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* s_piece = stage_base + kStages * F::kStageBytes;  // two
+  uint8_t* s_more = stage_base + kStages * F::kStageBytes;
+  uint8_t* s_piece = s_more + F::kMoreBytes;  // two
   uint8_t* s_red = s_piece + 2 * kPieceBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_red + F::kRedBytes);
-  int* s_id = reinterpret_cast<int*>(bars + F::kBars);  // [2][kOwn]: adapter of a token
-  int* s_whole = s_id + 2 * kOwn;
-  uint32_t* s_starts = reinterpret_cast<uint32_t*>(s_whole + 2 * 8);
-  volatile int* abort_flag = s_whole + 4 * 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_whole + 4 * 8) + 1;
+  int* s_id = reinterpret_cast<int*>(bars + F::kBars);
+  int* s_whole = s_id + 3 * kOwn;
+  uint32_t* s_starts = reinterpret_cast<uint32_t*>(s_whole + 3 * 8);
+  volatile int* abort_flag = s_whole + 6 * 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_whole + 6 * 8) + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCluster = S * CG;
   const int rank = kCluster > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -561,7 +639,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   auto tempty_bar = [&](int b) { return smem_u32(bars + 2 * kStages + 2 + b); };
   const uint32_t group_bar = smem_u32(bars + 2 * kStages + 4);
   const uint32_t red_bar = group_bar + 8;
-  const uint32_t drain_bar = red_bar + 8;
+  const uint32_t drain_bar = red_bar + 8, more_bar = drain_bar + 8;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full_bar(s), 1);
@@ -574,6 +652,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     mbar_init(group_bar, 8);
     mbar_init(red_bar, 1);
     mbar_init(drain_bar, 1);
+    mbar_init(more_bar, 16);  // the epilogue warps of both CTAs
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (S > 1) mbar_arrive_expect_tx(red_bar, F::kRedBytes);
@@ -647,8 +726,8 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     if (lane == 0 && leader) {
       // ---- MMA issuer ----
       constexpr uint32_t idesc = umma_idesc_bf16(128 * CG, TN, !KMAJ);
-      int s = 0, buf = 0;
-      uint32_t ph = 0, acc_ph = 0;
+      int s = 0, buf = 0, par = 0;
+      uint32_t ph = 0, acc_ph = 0, more_ph = 0;
       bool ok = true, issued = false;
       for (int t = first; t < total && ok; t += step) {
         for (int kp = k0; kp < k1 && ok; kp += piece) {
@@ -673,6 +752,25 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             if (++s == kStages) { s = 0; ph ^= 1u; }
           }
           if (!ok) break;
+          if constexpr (CG == 2) {
+            if (a.r <= 32) {  // the ranks of a tile of one adapter
+              if (!wait_bounded<true>(more_bar, more_ph, abort_flag, a.dev_status)) { ok = false; break; }
+              more_ph ^= 1u;
+              umma_fence_after();
+              const int* whole = s_whole + par * 8;
+              par = par == 2 ? 0 : par + 1;
+              bool same = whole[0] >= 0;
+              for (int ch = 1; ch < 8; ++ch) same = same && whole[ch] == whole[0];
+              if (same) {
+                const int rb = a.r <= 16 ? 1 : 2;
+                const uint32_t mu = smem_u32(s_more), mt = mu + kMoreU;
+                constexpr uint32_t more_idesc = umma_idesc_bf16(128 * CG, TN, true);
+                for (int q = 0; q < 2 * rb; ++q)
+                  umma_bf16_pair(tmem + buf * TN, umma_desc_mn(mt + q % rb * 2048, 16 * rb * 128),
+                                 umma_desc(mu + q * 32), more_idesc, 1);
+              }
+            }
+          }
           if constexpr (CG == 2) umma_commit_pair(tfull_bar(buf), 0x3);
           else umma_commit(tfull_bar(buf));
           if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
@@ -685,8 +783,8 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
       }
     }
   } else {
-    const Epilogue e{s_piece, s_red, s_id, s_whole, s_starts, abort_flag, tfull_bar(0), tempty_bar(0), group_bar,
-                     red_bar, tmem, first, step, total, rank, k0, k1, piece};
+    const Epilogue e{s_piece, s_red, s_more, s_id, s_whole, s_starts, abort_flag, tfull_bar(0), tempty_bar(0), group_bar,
+                     red_bar, more_bar, tmem, first, step, total, rank, k0, k1, piece};
     if (a.r <= 16) epilogue<TN, S, CG, 1>(a, e, warp, lane);
     else if (a.r <= 32) epilogue<TN, S, CG, 2>(a, e, warp, lane);
     else if (a.r <= 64) epilogue<TN, S, CG, 4>(a, e, warp, lane);

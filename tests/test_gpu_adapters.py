@@ -99,6 +99,11 @@ SHAPES = [
     (3500, list(range(2900)) + [3100, 3490], [q % 7 - 1 for q in range(2901)], 64, 72, 16, 6),
     (2290, [0, 700, 1300, 2290], [1, 0, 2], 2056, 2040, 8, 3),
     (40, [0, 5, 39], [1, 0], 6000, 136, 48, 2),
+    # whole tiles of two CTAs with one adapter, of 8, 16, 24 and 32 ranks, and beside others
+    (2304, [0, 2304], [1], 320, 2048, 16, 2),
+    (2304, [0, 1024, 2000, 2304], [0, 1, 0], 320, 1928, 8, 2),
+    (2300, [0, 600, 2290], [2, 0], 264, 2048, 24, 3),
+    (2304, [0, 256, 512, 1500, 2304], [1, -1, 0, 1], 2048, 264, 32, 2),
     (700, [0] * 300 + [400] * 200 + [700], [q % 3 for q in range(500)], 128, 128, 8, 3),
 ]
 
