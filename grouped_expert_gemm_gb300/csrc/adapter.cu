@@ -212,9 +212,9 @@ moe_status launch_shrink(const ShrinkArgs& a, cudaStream_t s) {
 // 36.9 / 22.7 / 14.4 us; 64 tokens of as many adapters, 2048 x 2048: 19.3 / 15.4 / 13.6).
 // Above, what takes fewer cycles: a stage of 64 takes 575 in either shape (it has 32 KB a CTA), the
 // adapters' part and the stores 18,000 a tile of a pair, behind the last tile or where a tile's
-// MMAs are shorter, and 8,000 of 128 x 128.  Measured, flat / pair (us): 256 tokens, 4096 x 4096: 22.5
-// / 32.7; 512: 29.8 / 31.7; 1,024: 56.5 / 51.2; 1,024, 2048 x 2048: 19.2 / 22.5; 2,048: 31.0 / 27.7;
-// 4,096, 2048 x 1024: 32.7 / 29.6, 768 x 2048: 29.5 / 34.2.  Where segments have few rows flat
+// MMAs are shorter, and 8,000 of 128 x 128.  Measured, flat / pair (us): 256 tokens, 4096 x 4096: 22.4
+// / 34.1; 512: 29.7 / 33.0; 1,024 (r 64): 52.0 / 48.8; 1,024, 2048 x 2048: 19.3 / 21.4; 2,048: 31.2 /
+// 26.7; 4,096, 2048 x 1024: 33.0 / 28.7, 768 x 2048: 30.5 / 29.3.  Where segments have few rows flat
 // tiles make the adapters' part beside the MMAs: 1,000 tokens in 70 segments, 4096 x 4096: 105 / 117.
 moe_status launch_project(const ProjectArgs& a, const Operands& o, bool kmaj, cudaStream_t s) {
   const int64_t sms = sm_count(), cols = ceil_div(a.N, 128);

@@ -261,6 +261,44 @@ def test_same_bits_captured_and_on_another_stream(T, off, ids, d, n, r, N):
             assert torch.equal(p, q)
 
 
+def test_two_streams_at_once():
+    """Objects of their own on two streams, their kernels side by side: each gives what it gives
+    alone."""
+    g = G()
+    shapes = [SHAPES[6], SHAPES[9]]
+    mods, args, alone = [], [], []
+    for i, (T, off, ids, d, n, r, N) in enumerate(shapes):
+        x, w, a, b, scale, rnd = make(T, d, n, r, N, seed=20 + i)
+        m = g.AdapterProjection(T, w, a, b, scale, device=DEV)
+        mods.append(m)
+        args.append((x, i32(ids), None if off is None else i32(off), rnd(T, n).to(torch.bfloat16)))
+        y = m.forward(*args[i][:3])
+        alone.append([t.clone() for t in (y, m.u) + m.backward(args[i][3])])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for m, (x, ids, off, dy), s in zip(mods, args, streams):
+            got = (m.forward(x, ids, off, stream=s), m.u) + m.backward(dy, stream=s)
+            m.last = got
+    torch.cuda.synchronize()
+    for m, want in zip(mods, alone):
+        assert int(m.dev_status.item()) == 0
+        assert all(torch.equal(p, q) for p, q in zip(m.last, want))
+
+
+def test_results_into_a_slice():
+    g = G()
+    T, d, n, r, N = 130, 136, 264, 16, 2
+    x, w, a, b, scale, _ = make(T, d, n, r, N, seed=9, x_stride=d + 8)
+    m = g.AdapterProjection(T, w, a, b, scale, y_dtype=torch.float32, device=DEV)
+    off, ids = i32([0, 100, 130]), i32([1, 0])
+    want = m.forward(x, ids, off).clone()
+    wide = torch.full((T, n + 48), MARK, device=DEV)
+    assert m.forward(x, ids, off, out=wide[:, 16:16 + n]).data_ptr() == wide.data_ptr() + 64
+    assert torch.equal(wide[:, 16:16 + n], want)
+    assert (wide[:, :16] == MARK).all() and (wide[:, 16 + n:] == MARK).all()
+
+
 def test_bad_tables_are_reported():
     g = G()
     *t, rnd = make(64, 128, 136, 16, 3)
