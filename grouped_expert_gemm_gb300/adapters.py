@@ -126,7 +126,7 @@ class AdapterProjection:
 class GradientClip:
     """Scales gradients so that the norm of each group of them is at most max_norm.
 
-    grads: bf16 and fp32 tensors (contiguous; no two may overlap).  out: where the scaled ones
+    grads: bf16 and fp32 tensors (contiguous; tensors that overlap are refused).  out: where the scaled ones
     go, like grads (default: in place).  groups: the group of each (default: one group of all);
     n_groups: how many there are.  ``clip()`` returns ``norms`` [n_groups], the norms before
     scaling.  The table of the tensors is made once, here, and names their memory: the tensors
@@ -152,6 +152,13 @@ class GradientClip:
                 raise ValueError(f"grads[{i}] must be a bfloat16 or float32 tensor")
             check_tensor(f"grads[{i}]", g, g.shape, g.dtype, self.device)
             check_tensor(f"out[{i}]", o, g.shape, g.dtype, self.device)
+        # Each tensor's bytes once (in place: gradient and result are the same ones): elements that
+        # two blocks read and write would be scaled in any order, or twice.
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                       for g, o in zip(self.grads, self.out)
+                       for t in ((g,) if g.data_ptr() == o.data_ptr() else (g, o)) if t.numel())
+        if any(end > begin for (_, end), (begin, _) in zip(spans, spans[1:])):
+            raise ValueError("gradients and their results must not overlap")
         table = (abi.GradTensor * len(self.grads))()
         for t, i in zip(table, sorted(range(len(self.grads)), key=lambda i: groups[i])):
             g, o = self.grads[i], self.out[i]

@@ -148,6 +148,20 @@ def test_objects_refuse(g):
             g.GradientClip(**{**dict(grads=[t], max_norm=1.0, device="cpu"), **kw})
 
 
+def test_clip_refuses_overlapping_tensors(g):
+    flat = torch.ones(64)
+    make = lambda grads, out=None: g.GradientClip(grads, 1.0, out=out, device="cpu")  # noqa: E731
+    make([flat[:32], flat[32:]])  # neighbours
+    make([flat[:32]], out=[flat[32:]])
+    make([flat[:32], flat[8:8]])  # no elements
+    for grads, out in (([flat, flat], None), ([flat[:33], flat[32:]], None),
+                       ([flat[:32]], [flat[1:33]]),  # a result behind its own gradient
+                       ([flat[:16], flat[16:32]], [flat[16:32], flat[32:48]]),
+                       ([flat[:16], flat[16:32]], [flat[40:56], flat[40:56]])):
+        with pytest.raises(ValueError, match="overlap"):
+            make(grads, out)
+
+
 def test_formulas_against_differences():
     """The gradients' formulas, by central differences in 64 bits."""
     gen = torch.Generator().manual_seed(0)
