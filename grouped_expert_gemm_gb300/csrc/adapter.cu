@@ -90,7 +90,6 @@ shrink_kernel(const ShrinkArgs a, int split, int pieces_mode) {
     const int e = min(stops != 0 ? __ffs(stops) - 1 : 32, P::kRows);
     if (nth % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
     const int adapter = __shfl_sync(kAll, id, b);
-    const float scale = __ldg(a.scale + adapter);
     float acc[P::kMB][NB][4];
 #pragma unroll
     for (int i = 0; i < P::kMB; ++i)
@@ -146,6 +145,7 @@ shrink_kernel(const ShrinkArgs a, int split, int pieces_mode) {
               make_float2(acc[i][j][2], acc[i][j][3]);
         }
     __syncthreads();
+    const float scale = __ldg(a.scale + adapter);
     const int n = (e - b) * a.r;
     if (split > 1) {
       for (int i = threadIdx.x; i < n; i += blockDim.x) {

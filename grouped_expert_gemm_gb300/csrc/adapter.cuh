@@ -103,18 +103,6 @@ __device__ __forceinline__ int seg_adapter(const Segments& s, int q) {
 // the other as it has steps), then the ends of the segments behind it, 32 at a time.
 __device__ __forceinline__ int row_adapters(const Segments& s, int row0, int lane) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  if (s.n_seg <= 32) {  // the whole table at once: one load's latency instead of three
-    const bool in = lane < s.n_seg;
-    const int begin = in ? seg_begin(s, lane) : 0, end = in ? seg_begin(s, lane + 1) : 0x7FFFFFFF;
-    const int id = in ? seg_adapter(s, lane) : kOutside;
-    const int row = row0 + lane;
-    int c = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) c += __shfl_sync(kAll, end, i) <= row;
-    const int mine = __shfl_sync(kAll, id, c & 31);
-    const bool before = row < __shfl_sync(kAll, begin, 0);
-    return row >= s.T || before || c >= s.n_seg ? kOutside : mine;
-  }
   int lo = 0, n = s.n_seg;  // the last segment that starts at or before row0 is in [lo, lo + n)
   while (n > 1) {
     const int stride = (n + 31) / 32;
@@ -166,11 +154,8 @@ __device__ __forceinline__ Piece piece_of(const Segments& s, int index, int size
   int64_t before = 0;  // pieces of the segments in front of this round's
   for (int q0 = 0; q0 < s.n_seg; q0 += THREADS) {
     const int q = q0 + static_cast<int>(threadIdx.x);
-    int b = 0, e = 0, id = kNone;
-    if (q < s.n_seg) {
-      seg_rows(s, q, b, e);
-      id = seg_adapter(s, q);
-    }
+    int b = 0, e = 0;
+    if (q < s.n_seg) seg_rows(s, q, b, e);
     const int n = e > b ? (e - b + size - 1) / size : 0;
     int incl = n;
 #pragma unroll
@@ -189,7 +174,7 @@ __device__ __forceinline__ Piece piece_of(const Segments& s, int index, int size
     }
     if (index >= at && index < at + n) {
       const int row = b + static_cast<int>(index - at) * size;
-      s_piece = Piece{row, min(size, e - row), id};
+      s_piece = Piece{row, min(size, e - row), seg_adapter(s, q)};
     }
     before = total;
     if (total > index) break;

@@ -117,10 +117,10 @@ grads_kernel(const __grid_constant__ CUtensorMap map_q0, const __grid_constant__
   int64_t count = 0;
   for (int q0 = 0; q0 < a.seg.n_seg; q0 += 32) {
     int n = 0;
-    if (q0 + lane < a.seg.n_seg) {
+    if (q0 + lane < a.seg.n_seg && __ldg(a.seg.adapter + q0 + lane) == id) {
       int b, e;
       seg_rows(a.seg, q0 + lane, b, e);
-      n = e > b && __ldg(a.seg.adapter + q0 + lane) == id ? (e - b + kTokens - 1) / kTokens : 0;
+      n = e > b ? (e - b + kTokens - 1) / kTokens : 0;
     }
     count += __reduce_add_sync(kAll, n);
   }

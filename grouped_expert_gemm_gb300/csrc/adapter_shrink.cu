@@ -81,7 +81,6 @@ shrink_long_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   umma_fence_after();
   const uint32_t tmem = *tmem_slot;
   const bool live = p.rows > 0 && p.adapter >= 0;
-  const float scale = live ? __ldg(a.scale + p.adapter) : 0.0f;
 
   float acc[kN];
   bool ok = true;
@@ -165,6 +164,7 @@ shrink_long_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const int row = quad * 32 + lane;
     if (ok && split == 1) {
       if (row < p.rows) {
+        const float scale = __ldg(a.scale + p.adapter);
         float* out = a.u + static_cast<int64_t>(p.row + row) * a.r;
 #pragma unroll
         for (int c = 0; c < kN; c += 4)
@@ -182,12 +182,14 @@ shrink_long_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   }
   if (split > 1) {
     cluster_sync();
-    if (live && *abort_flag == 0)
+    if (live && *abort_flag == 0) {
+      const float scale = __ldg(a.scale + p.adapter);
       for (int i = rank * kThreads + threadIdx.x; i < p.rows * a.r; i += split * kThreads) {
         const float v = sum_of_ranks(
             smem_u32(reinterpret_cast<float*>(stage_base) + i / a.r * F::kSumPitch + i % a.r), split);
         a.u[static_cast<int64_t>(p.row) * a.r + i] = scale * v;
       }
+    }
     cluster_sync();  // no CTA leaves while a partner may still read its sums
   }
   __syncwarp();
