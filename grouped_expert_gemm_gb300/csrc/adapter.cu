@@ -215,7 +215,7 @@ moe_status launch_shrink(const ShrinkArgs& a, cudaStream_t s) {
 // MMAs are shorter, and 8,000 of 128 x 128.  Measured, flat / pair (us): 256 tokens, 4096 x 4096: 22.4
 // / 34.1; 512: 29.7 / 33.0; 1,024 (r 64): 52.0 / 48.8; 1,024, 2048 x 2048: 19.3 / 21.4; 2,048: 31.2 /
 // 26.7; 4,096, 2048 x 1024: 33.0 / 28.7, 768 x 2048: 30.5 / 29.3.  Where segments have few rows flat
-// tiles make the adapters' part beside the MMAs: 1,000 tokens in 70 segments, 4096 x 4096: 105 / 117.
+// tiles make the adapters' part beside the MMAs: 1,000 tokens in 70 segments, 4096 x 4096: 73 / 81.
 moe_status launch_project(const ProjectArgs& a, const Operands& o, bool kmaj, cudaStream_t s) {
   const int64_t sms = sm_count(), cols = ceil_div(a.N, 128);
   const int T = a.seg.T;
