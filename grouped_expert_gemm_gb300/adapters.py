@@ -18,7 +18,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import abi
-from .block import _KIND, _device, _memory_of, check_tensor
+from .block import _KIND, _device, check_tensor
 
 
 def _check_rows(name, t, shape, dtype, device):
@@ -39,11 +39,18 @@ class AdapterProjection:
     ``forward(x, seg_adapter, seg_offsets)``: segment q holds rows [seg_offsets[q],
     seg_offsets[q+1]) of x [T, d] and has adapter seg_adapter[q] (-1: none); int32 tensors
     [n_seg] and [n_seg + 1] (None: one segment of all rows).  Returns y [T, n]; rows of no
-    segment keep what they held (zeros at first).  ``u`` [T, r] is what the backward needs."""
+    segment keep what they held (zeros at first).  ``u`` [T, r] is what the backward needs.
+
+    ``gradients``: make the backward's buffers (dx, da, db and a workspace) too; a program that
+    serves alone can do without them.  They are made here and not by the first backward: one that is
+    captured would clear them in every replay."""
 
     def __init__(self, T: int, weight: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
-                 scale: torch.Tensor, y_dtype=torch.bfloat16, device="cuda"):
+                 scale: torch.Tensor, y_dtype=torch.bfloat16, device="cuda",
+                 gradients: bool = True):
         self.device = _device(device)
+        if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            raise ValueError("the object's buffers must be made before a capture begins")
         if y_dtype not in _KIND:
             raise ValueError("y_dtype must be bfloat16 or float32")
         for name, t, dims in (("weight", weight, 2), ("a", a, 3), ("b", b, 3)):
@@ -65,7 +72,11 @@ class AdapterProjection:
         self.y = torch.zeros((T, self.n), dtype=y_dtype, **new)
         self.dev_status = torch.zeros((1,), dtype=torch.int32, **new)
         self._last = None
-        self._grads = None
+        self._grads = None if not gradients else (
+            torch.zeros((T, self.d), dtype=torch.bfloat16, **new),
+            torch.zeros(a.shape, dtype=torch.float32, **new),
+            torch.zeros(b.shape, dtype=torch.float32, **new),
+            torch.empty((self.ws_bytes,), dtype=torch.uint8, **new))
 
     def _segments(self, seg_adapter, seg_offsets):
         n_seg = seg_adapter.shape[0] if isinstance(seg_adapter, torch.Tensor) and \
@@ -98,20 +109,16 @@ class AdapterProjection:
 
     def backward(self, dy, accumulate: bool = False, stream=None):
         """Gradients of the last forward, whose x, segments and tables must be as they were:
-        (dx [T, d] bf16, da, db fp32 like the tables); dy is [T, n] bf16.  The buffers are the object's own; with ``accumulate`` da and db are added
-        to what they hold (zeros at first).  The weight has no gradient."""
+        (dx [T, d] bf16, da, db fp32 like the tables); dy is [T, n] bf16.  The buffers are the
+        object's own; with ``accumulate`` da and db are added to what they hold (zeros at first),
+        in a captured call by every replay.  The weight has no gradient."""
         abi.check_current_device(self.device)
+        if self._grads is None:
+            raise ValueError("the object was made without gradients")
         if self._last is None:
             raise ValueError("backward needs a forward before it")
         _check_rows("dy", dy, (self.T, self.n), torch.bfloat16, self.device)
         x, seg_adapter, seg_offsets = self._last
-        if self._grads is None:
-            new = dict(device=self.device)
-            with _memory_of(stream, self.device):
-                self._grads = (torch.zeros((self.T, self.d), dtype=torch.bfloat16, **new),
-                               torch.zeros(self.a.shape, dtype=torch.float32, **new),
-                               torch.zeros(self.b.shape, dtype=torch.float32, **new),
-                               torch.empty((self.ws_bytes,), dtype=torch.uint8, **new))
         dx, da, db, ws = self._grads
         p = self.params
         p.n_seg = self._segments(seg_adapter, seg_offsets)

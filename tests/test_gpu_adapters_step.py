@@ -1,0 +1,97 @@
+"""AdapterProjection as a training program uses it: gradients summed over replays of a captured
+step, and several micro-batches."""
+import pytest
+import torch
+
+import adapter_reference as ref
+from test_gpu_adapters import DEV, G, MARK, i32, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from grouped_expert_gemm_gb300 import build
+    build.build()
+
+
+T, D, N_OUT, R, N = 150, 264, 136, 16, 3
+OFF, IDS = [4, 30, 31, 140], [2, 0, 2]
+
+
+def step(seed):
+    x, w, a, b, scale, rnd = make(T, D, N_OUT, R, N, seed=seed)
+    return x, w, a, b, scale, rnd(T, N_OUT).to(torch.bfloat16)
+
+
+def gradients(x, w, a, b, scale, dy):
+    """da and db of an object of their own that adds nothing up."""
+    m = G().AdapterProjection(T, w, a, b, scale, device=DEV)
+    m.forward(x, i32(IDS), i32(OFF))
+    dx, da, db = m.backward(dy)
+    return dx.clone(), da.clone(), db.clone()
+
+
+def test_replays_of_a_first_backward_add_up():
+    """The first backward of an object is captured, with accumulate: K replays hold the sum of K
+    gradients, in fp32 additions in that order, and rows of no segment of dx are not written."""
+    g = G()
+    x, w, a, b, scale, dy = step(11)
+    dx1, da1, db1 = gradients(x, w, a, b, scale, dy)
+    ids, off = i32(IDS), i32(OFF)
+    m = g.AdapterProjection(T, w, a, b, scale, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.forward(x, ids, off)
+        dx, da, db = m.backward(dy, accumulate=True)
+    torch.cuda.synchronize()
+    assert not da.any() and not db.any()  # zeros at first; a capture runs nothing
+    dx.fill_(MARK)
+    want_a, want_b = torch.zeros_like(da1), torch.zeros_like(db1)
+    for _ in range(3):
+        graph.replay()
+        want_a, want_b = want_a + da1, want_b + db1
+    torch.cuda.synchronize()
+    assert torch.equal(da, want_a) and torch.equal(db, want_b)
+    assert (dx[:OFF[0]] == MARK).all() and (dx[OFF[-1]:] == MARK).all()
+    assert torch.equal(dx[OFF[0]:OFF[-1]], dx1[OFF[0]:OFF[-1]])
+    # and eagerly onto the same sums
+    m.forward(x, ids, off)
+    m.backward(dy, accumulate=True)
+    assert torch.equal(da, want_a + da1) and torch.equal(db, want_b + db1)
+
+
+def test_micro_batches_add_up():
+    g = G()
+    x, w, a, b, scale, _ = step(12)
+    m = g.AdapterProjection(T, w, a, b, scale, device=DEV)
+    want_a = want_b = 0.0
+    for seed in (12, 13, 14):
+        x, _, _, _, _, dy = step(seed)
+        _, da1, db1 = gradients(x, w, a, b, scale, dy)
+        want_a, want_b = want_a + da1, want_b + db1
+        m.forward(x, i32(IDS), i32(OFF))
+        _, da, db = m.backward(dy, accumulate=True)
+        torch.cuda.synchronize()
+        assert torch.equal(da, want_a) and torch.equal(db, want_b)
+    _, da, db = m.backward(dy)  # without it they start again
+    assert torch.equal(da, da1) and torch.equal(db, db1)
+
+
+def test_gradients_of_a_captured_step_against_the_definition():
+    g = G()
+    x, w, a, b, scale, dy = step(16)
+    m = g.AdapterProjection(T, w, a, b, scale, device=DEV)
+    ids, off = i32(IDS), i32(OFF)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.forward(x, ids, off)
+        dx, da, db = m.backward(dy, accumulate=True)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    _, (da64, dar), (db64, dbr) = ref.backward(x, w, a, b, scale, ref.segments(OFF, IDS, T), dy)
+    assert ((da.double() - 2 * da64).abs() <= 2 * dar).all()
+    assert ((db.double() - 2 * db64).abs() <= 2 * dbr).all()
