@@ -77,6 +77,8 @@ class AdapterProjection:
             torch.zeros(a.shape, dtype=torch.float32, **new),
             torch.zeros(b.shape, dtype=torch.float32, **new),
             torch.empty((self.ws_bytes,), dtype=torch.uint8, **new))
+        if self.device.type == "cuda":  # the buffers are clear whatever stream uses them
+            torch.cuda.current_stream(self.device).synchronize()
 
     def _segments(self, seg_adapter, seg_offsets):
         n_seg = seg_adapter.shape[0] if isinstance(seg_adapter, torch.Tensor) and \

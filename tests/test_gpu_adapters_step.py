@@ -95,3 +95,25 @@ def test_gradients_of_a_captured_step_against_the_definition():
     _, (da64, dar), (db64, dbr) = ref.backward(x, w, a, b, scale, ref.segments(OFF, IDS, T), dy)
     assert ((da.double() - 2 * da64).abs() <= 2 * dar).all()
     assert ((db.double() - 2 * db64).abs() <= 2 * dbr).all()
+
+
+def test_first_forward_on_another_stream():
+    """Results do not race with the clearing of the buffers that hold them, which the current stream
+    does behind other work."""
+    g = G()
+    x, w, a, b, scale, dy = step(17)
+    busy = torch.empty((1 << 30,), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    ids, off = i32(IDS), i32(OFF)
+    torch.cuda.synchronize()
+    for _ in range(100):
+        busy.fill_(1)
+    m = g.AdapterProjection(T, w, a, b, scale, device=DEV)
+    y = m.forward(x, ids, off, stream=side)
+    dx, da, db = m.backward(dy, stream=side)
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (y, m.u, dx, da, db)]
+    m.forward(x, ids, off)
+    m.backward(dy)
+    assert all(torch.equal(p, q) for p, q in zip(got, (y, m.u, dx, da, db)))
+    assert y[OFF[0]:OFF[-1]].any() and da.any() and int(m.dev_status.item()) == 0
