@@ -28,6 +28,35 @@ def _check_rows(name, t, shape, dtype, device):
         raise ValueError(f"rows of {name} must be a multiple of 8 values apart")
 
 
+def _overlap(p, q) -> bool:
+    """Whether two tensors with contiguous rows share memory.  Slices of the columns of one wider
+    buffer may stand side by side in its rows."""
+    if p.numel() == 0 or q.numel() == 0:
+        return False
+    at, size = [], []
+    for t in (p, q):
+        at.append(t.data_ptr())
+        rows = t.dim() == 2 and t.shape[0] > 1
+        values = (t.shape[0] - 1) * t.stride(0) + t.shape[1] if rows else t.numel()
+        size.append(values * t.element_size())
+    if at[0] + size[0] <= at[1] or at[1] + size[1] <= at[0]:
+        return False
+    if p.dim() == q.dim() == 2 and min(p.shape[0], q.shape[0]) > 1:
+        row = p.stride(0) * p.element_size()
+        if row == q.stride(0) * q.element_size():
+            ahead = (at[1] - at[0]) % row  # of q's rows to p's, inside a row of the buffer
+            return ahead < p.shape[1] * p.element_size() or \
+                ahead + q.shape[1] * q.element_size() > row
+    return True
+
+
+def _apart(name, written, *read):
+    """What a call writes must not be what other blocks of it still read."""
+    for t in read:
+        if t is not None and _overlap(written, t):
+            raise ValueError(f"{name} must not overlap what the call reads")
+
+
 def _stride(t, width):
     return t.stride(0) if t.shape[0] > 1 else width
 
@@ -95,7 +124,7 @@ class AdapterProjection:
     def forward(self, x, seg_adapter, seg_offsets=None, out: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
         """``out``: write there instead of ``y`` (rows at any multiple of 8 values apart, a
-        slice of a wider buffer for example)."""
+        slice of a wider buffer for example).  Neither may overlap what the call reads."""
         abi.check_current_device(self.device)
         _check_rows("x", x, (self.T, self.d), torch.bfloat16, self.device)
         p = self.params
@@ -103,6 +132,9 @@ class AdapterProjection:
         y = self.y if out is None else out
         if out is not None:
             _check_rows("out", out, (self.T, self.n), self.y_dtype, self.device)
+            _apart("out", out, self.weight, self.a, self.b, self.scale, self.u, seg_adapter,
+                   seg_offsets)
+        _apart("y", y, x)
         p.n_seg, p.x_stride, p.y_stride = n_seg, _stride(x, self.d), _stride(y, self.n)
         abi.moe_adapter_project(p, seg_offsets, seg_adapter, x, self.weight, self.a, self.b,
                                 self.scale, self.u, y, self.dev_status, stream)
@@ -121,6 +153,7 @@ class AdapterProjection:
             raise ValueError("backward needs a forward before it")
         _check_rows("dy", dy, (self.T, self.n), torch.bfloat16, self.device)
         x, seg_adapter, seg_offsets = self._last
+        _apart("dx", self._grads[0], dy, x)
         dx, da, db, ws = self._grads
         p = self.params
         p.n_seg = self._segments(seg_adapter, seg_offsets)

@@ -869,8 +869,8 @@ typedef struct {
  * the first has ended, so nothing enqueued after the first may write them (the call itself
  * enqueues both).
  * Limits: d, n, r % 8 == 0, d, n <= 65536, r <= 128, n_adapters, n_seg <= 65535, strides % 8
- * == 0; 16-byte aligned x, w, a, b, u and y.  T = 0 does nothing.  y must not overlap the
- * inputs.                                                                     */
+ * == 0; 16-byte aligned x, w, a, b, u and y.  T = 0 does nothing.  u and y must not overlap
+ * each other or the inputs.                                                   */
 moe_status moe_adapter_project(const moe_adapter_params* p, const int32_t* seg_offsets,
                                const int32_t* seg_adapter, const moe_bf16* x, const moe_bf16* w,
                                const moe_bf16* a, const moe_bf16* b, const float* scale, float* u,
@@ -888,7 +888,8 @@ moe_status moe_adapter_project(const moe_adapter_params* p, const int32_t* seg_o
  * ws: moe_adapter_project_backward_workspace_size() bytes (0 = invalid parameters), 16-byte
  * aligned; calls, and replays of graphs that captured them, that overlap on the GPU must not
  * share it.  T = 0 writes zero gradients (accumulate = 0).  16-byte aligned dy, dx, da and db;
- * other limits and errors as the forward.                                    */
+ * dx, da, db and ws must not overlap each other or the inputs; other limits and errors as the
+ * forward.                                                                   */
 size_t moe_adapter_project_backward_workspace_size(const moe_adapter_params* p);
 moe_status moe_adapter_project_backward(
     const moe_adapter_params* p, const int32_t* seg_offsets, const int32_t* seg_adapter,

@@ -29,3 +29,43 @@ def test_gradient_buffers_are_made_with_the_object(g):
     assert m._grads is None
     with pytest.raises(ValueError, match="without gradients"):
         m.backward(torch.zeros(4, 72, dtype=BF))
+
+
+def test_overlap_of_rows():
+    from grouped_expert_gemm_gb300.adapters import _overlap
+    wide = torch.zeros(6, 48, dtype=BF)
+    for p, q, want in (
+            (wide[:, :16], wide[:, 16:], False), (wide[:, 16:], wide[:, :16], False),
+            (wide[:, :16], wide[:, 8:24], True), (wide[:, 8:24], wide[:, :16], True),
+            (wide[:, 16:32], wide[:, 16:32], True), (wide[:, :16], wide[:, 40:], False),
+            (wide[:3, :16], wide[3:, :16], False), (wide[:3], wide[2:5], True),
+            (wide[:, :16], wide[1:, 16:], False), (wide[1:, :24], wide[:5, 16:40], True),
+            (wide, wide.view(-1)[5:6], True), (wide[:2], wide.view(-1)[96:], False),
+            (wide[0:1, :16], wide[0:1, 16:], False), (wide[0:1], wide[0:1, 40:], True),
+            (wide[:, 1:47].view(torch.int16), wide[:, 46:], True), (wide[:0], wide, False),
+            (wide[:, :8], torch.zeros(6, 48, dtype=BF), False),
+            # a row's slice that goes on into the next row of the other
+            (wide[:, 40:], wide.view(-1)[44:188].view(3, 48), True)):
+        assert _overlap(p, q) == _overlap(q, p) == want
+
+
+def test_outputs_that_a_call_reads_are_refused(g):
+    d = 64
+    t = tables(d, d)
+    m = g.AdapterProjection(4, **t, device="cpu")
+    ids, off = torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    wide = torch.zeros(4, 3 * d, dtype=BF)
+    for x, out in ((m.y, None),                          # the result of the last call as the next one's rows
+                   (wide[:, :d], wide[:, d - 8:2 * d - 8]), (wide[:, :d], wide[:, :d]),
+                   (wide[:, :d], t["weight"][8:12]), (wide[:, :d], t["b"][1, 2:6])):
+        with pytest.raises(ValueError, match="overlap"):
+            m.forward(x, ids, off, out=out)
+    f = g.AdapterProjection(4, **tables(d, 8), y_dtype=torch.float32, device="cpu")
+    with pytest.raises(ValueError, match="overlap"):
+        f.forward(torch.zeros(4, d, dtype=BF), ids, off, out=f.u)
+    m._last = (torch.zeros(4, d, dtype=BF), ids, off)
+    with pytest.raises(ValueError, match="overlap"):
+        m.backward(m._grads[0])                          # the last dx as the next dy
+    m._last = (m._grads[0], ids, off)
+    with pytest.raises(ValueError, match="overlap"):
+        m.backward(torch.zeros(4, d, dtype=BF))

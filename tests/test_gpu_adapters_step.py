@@ -117,3 +117,20 @@ def test_first_forward_on_another_stream():
     m.backward(dy)
     assert all(torch.equal(p, q) for p, q in zip(got, (y, m.u, dx, da, db)))
     assert y[OFF[0]:OFF[-1]].any() and da.any() and int(m.dev_status.item()) == 0
+
+
+def test_rows_and_results_side_by_side_in_one_buffer():
+    g = G()
+    x, w, a, b, scale, dy = step(18)
+    m = g.AdapterProjection(T, w, a, b, scale, device=DEV)
+    ids, off = i32(IDS), i32(OFF)
+    want = m.forward(x, ids, off).clone()
+    grads = [t.clone() for t in m.backward(dy)]
+    wide = torch.full((T, 8 + D + N_OUT), MARK, dtype=torch.bfloat16, device=DEV)
+    wide[:, :D] = x
+    m.forward(wide[:, :D], ids, off, out=wide[:, D + 8:])
+    live = slice(OFF[0], OFF[-1])
+    assert torch.equal(wide[live, D + 8:], want[live]) and torch.equal(wide[:, :D], x)
+    assert (wide[:, D:D + 8] == MARK).all()
+    wide[:, D + 8:] = dy
+    assert all(torch.equal(p, q) for p, q in zip(m.backward(wide[:, D + 8:]), grads))
