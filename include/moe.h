@@ -913,7 +913,8 @@ typedef struct {
 /* Checks a table of n_tensors on the HOST (it may be copied to the device as it is
  * afterwards), fills in its last three fields and returns the number of chunks.  Tensors of a group
  * stand together; a tensor may have no elements (its addresses may then be NULL), and a group
- * no tensors.  Addresses must be aligned to their type.                       */
+ * no tensors.  Addresses must be aligned to their type.  Tensors must not overlap (a tensor in
+ * place with itself alone); norms and ws of the call below must not overlap them either.  */
 moe_status moe_grad_plan(int32_t n_tensors, moe_grad_tensor* tensors, int32_t n_groups,
                          int64_t* n_chunks);
 

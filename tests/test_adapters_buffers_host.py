@@ -69,3 +69,12 @@ def test_outputs_that_a_call_reads_are_refused(g):
     m._last = (m._grads[0], ids, off)
     with pytest.raises(ValueError, match="overlap"):
         m.backward(torch.zeros(4, d, dtype=BF))
+
+
+def test_norms_apart_from_the_gradients(g):
+    flat = torch.ones(64)
+    g.GradientClip([flat[:32]], 1.0, norms=flat[32:33], device="cpu")
+    for grads, out, norms in (([flat[:32]], None, flat[31:32]), ([flat[:32]], [flat[32:]], flat[40:41]),
+                              ([flat.view(8, 8)], None, flat[:1])):
+        with pytest.raises(ValueError, match="overlap"):
+            g.GradientClip(grads, 1.0, out=out, norms=norms, device="cpu")
