@@ -342,6 +342,7 @@ MOE_API moe_status moe_adapter_project_backward(
                                 {{da != nullptr ? p->d : 0, v, x, p->x_stride, da},
                                  {db != nullptr ? p->n : 0, u, dy, p->y_stride, db}},
                                 accumulate,
+                                dx == nullptr && da == nullptr,  // (no shrink)
                                 dev_status},
                        s);
   return MOE_OK;

@@ -69,6 +69,7 @@ struct GradArgs {
   int r;
   GradSide side[2];
   int accumulate;
+  int check;  // look the segment table over: no kernel before this one has
   uint32_t* dev_status;
 };
 

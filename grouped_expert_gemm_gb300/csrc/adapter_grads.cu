@@ -113,6 +113,7 @@ grads_kernel(const __grid_constant__ CUtensorMap map_q0, const __grid_constant__
 
   pdl_wait();
   pdl_trigger();
+  if (a.check && blockIdx.x == 0 && blockIdx.y == 0) check_segments(a.seg, a.dev_status);
   // the adapter's pieces: this CTA's part of them
   int64_t count = 0;
   for (int q0 = 0; q0 < a.seg.n_seg; q0 += 32) {

@@ -1,5 +1,5 @@
 """AdapterProjection as a training program uses it: gradients summed over replays of a captured
-step, and several micro-batches."""
+step, several micro-batches, and what each kind of backward reports."""
 import pytest
 import torch
 
@@ -77,6 +77,27 @@ def test_micro_batches_add_up():
         assert torch.equal(da, want_a) and torch.equal(db, want_b)
     _, da, db = m.backward(dy)  # without it they start again
     assert torch.equal(da, da1) and torch.equal(db, db1)
+
+
+@pytest.mark.parametrize("want", ["x", "a", "b", "ab", "xab"])
+def test_every_backward_reports_bad_tables(want):
+    g = G()
+    x, w, a, b, scale, dy = step(15)
+    u = torch.zeros((T, R), device=DEV)
+    out = dict(x=torch.zeros((T, D), dtype=torch.bfloat16, device=DEV),
+               a=torch.zeros(a.shape, device=DEV), b=torch.zeros(b.shape, device=DEV))
+    p = g.AdapterParams(T, D, N_OUT, R, N, 3)
+    nb = g.moe_adapter_project_backward_workspace_size(p)
+    ws = torch.zeros((nb,), dtype=torch.uint8, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for off, ids, bit in (([0, 20, 40, T], [0, 1, 2], 0), ([0, 40, 20, T], [0, 1, 2], g.MOE_DEV_BAD_MAP),
+                          ([0, 20, 40, T + 1], [0, 1, 2], g.MOE_DEV_BAD_MAP),
+                          ([0, 20, 40, T], [0, N, 2], g.MOE_DEV_BAD_ADAPTER),
+                          ([0, 20, 40, T], [0, -2, 2], g.MOE_DEV_BAD_ADAPTER)):
+        st.zero_()
+        g.moe_adapter_project_backward(p, i32(off), i32(ids), x, w, a, b, scale, u, dy,
+                                       *(out[k] if k in want else None for k in "xab"), 0, ws, nb, st)
+        assert int(st.item()) == bit
 
 
 def test_gradients_of_a_captured_step_against_the_definition():
