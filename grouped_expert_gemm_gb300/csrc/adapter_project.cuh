@@ -420,6 +420,7 @@ __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s
     }
 #pragma unroll 1
     for (int ch = 0; ch < kChunks; ++ch) {
+      __syncwarp();  // (behind the last tokens' masked stores: loads of sums want whole warps)
       const int j = 32 * ch, kind = done ? kNone : whole[ch];
       uint8_t* piece = s.piece + pb * kPieceBytes;
       const uint32_t at = lu + pb * kPieceBytes;
