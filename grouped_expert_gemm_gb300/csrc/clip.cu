@@ -12,7 +12,8 @@
 // order.  No atomics, no counters: the same bits on every run, and nothing to clear.  The
 // second pass walks every part backwards: its end is what the first pass read last.
 //
-// Squares are summed in fp32 over a thread's 16 or 32 values of a chunk and in fp64 from there on;
+// Squares are summed in fp32 over a thread's share of four chunks (32 fp32 or 64 bf16 values and at most one
+// beside them) in chains of eight, so that a sum's path has 12 roundings at most, and in fp64 from there on;
 // where those squares leave fp32's range (values beyond 2^60 or below 2^-40) the values are
 // scaled by a power of two first, so any finite tensor has its norm.
 #include <algorithm>
@@ -116,16 +117,22 @@ struct Share {
   }
   template <int PER>
   __device__ __forceinline__ float sum(float k) const {
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s[PER];  // a chain for each place in a vector: kVecs additions
+#pragma unroll
+    for (int e = 0; e < PER; ++e) s[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       float f[PER];
       spread(v[i], f);
 #pragma unroll
-      for (int e = 0; e < PER; ++e) s[e & 3] = fmaf(f[e] * k, f[e] * k, s[e & 3]);
+      for (int e = 0; e < PER; ++e) s[e] = fmaf(f[e] * k, f[e] * k, s[e]);
     }
     s[0] = fmaf(edge * k, edge * k, s[0]);
-    return (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int o = PER / 2; o > 0; o /= 2)
+#pragma unroll
+      for (int e = 0; e < o; ++e) s[e] += s[e + o];
+    return s[0];
   }
   template <int PER>
   __device__ __forceinline__ double squares_as() const {

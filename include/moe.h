@@ -921,9 +921,9 @@ moe_status moe_grad_plan(int32_t n_tensors, moe_grad_tensor* tensors, int32_t n_
 /* One norm per group and the tensors scaled to it, with a planned table on the DEVICE:
  *   norms[g] = sqrt(sum of squares over g's tensors)            fp32 [n_groups]
  *   c_g = min(1, max_norm / (norms[g] + 1e-6)),  out = round(grad * c_g), to the tensor's type
- * A tensor in place whose c_g is 1 is not written.  Sums of squares are held in fp64 (over 32
- * values at a time fp32, scaled where they leave its range), in an order that the table and
- * the GPU fix: the same bits on every run.  A norm that is not finite in fp32 sets
+ * A tensor in place whose c_g is 1 is not written.  Sums of squares are held in fp64 (over 65
+ * values at most fp32, 12 roundings deep, scaled where they leave its range), in an order that
+ * the table and the GPU fix: the same bits on every run.  A norm that is not finite in fp32 sets
  * MOE_DEV_NONFINITE_INPUT; the formula is followed (NaN: NaN everywhere in the group, Inf:
  * zeros, and NaN where the gradient was infinite).
  * max_norm > 0 (infinity: norms alone matter).  ws: moe_clip_grads_workspace_size(n_groups)
