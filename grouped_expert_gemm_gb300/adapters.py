@@ -168,11 +168,12 @@ class AdapterProjection:
 class GradientClip:
     """Scales gradients so that the norm of each group of them is at most max_norm.
 
-    grads: bf16 and fp32 tensors (contiguous; tensors that overlap are refused).  out: where the scaled ones
-    go, like grads (default: in place).  groups: the group of each (default: one group of all);
-    n_groups: how many there are.  ``clip()`` returns ``norms`` [n_groups], the norms before
-    scaling.  The table of the tensors is made once, here, and names their memory: the tensors
-    are kept alive, and a program that replaces one makes another object."""
+    grads: bf16 and fp32 tensors (contiguous; tensors that overlap are refused).  max_norm:
+    infinity scales nothing, whatever the norm.  out: where the scaled ones go, like grads
+    (default: in place).  groups: the group of each (default: one group of all); n_groups: how
+    many there are.  ``clip()`` returns ``norms`` [n_groups], the norms before scaling.  The table
+    of the tensors is made once, here, and names their memory: the tensors are kept alive, and a
+    program that replaces one makes another object."""
 
     def __init__(self, grads: Sequence[torch.Tensor], max_norm: float, out=None, groups=None,
                  n_groups: Optional[int] = None, norms: Optional[torch.Tensor] = None,

@@ -1,6 +1,7 @@
 // Gradient norms over groups of many tensors, and the tensors scaled to a largest norm.
 //
 //   norm_g = sqrt(sum x^2 over g's tensors),  c_g = min(1, max_norm / (norm_g + 1e-6))
+//   (1 where max_norm is infinite)
 //   out = round(x c_g)
 //
 // Bound: HBM (the tensors twice in, once out, less what the second pass finds in the L2).
@@ -268,7 +269,8 @@ __global__ void __launch_bounds__(kBlock, kPerSm) grad_scale_kernel(const ClipAr
       const moe_grad_tensor& mine = a.tensors[now.tensor];
       const float norm = group_norm(a, mine, s_warp);
       const float q = __fdiv_rn(a.max_norm, norm + 1e-6f);
-      k = q > 1.0f ? 1.0f : q;  // (a NaN stays one)
+      // (a NaN stays one; without a limit nothing is scaled, whatever the norm)
+      k = q > 1.0f || a.max_norm == __int_as_float(0x7F800000) ? 1.0f : q;
       if (threadIdx.x == 0 && c0 <= mine.group_begin && mine.group_begin < c1) {
         a.norms[group] = norm;
         if (!(norm < __int_as_float(0x7F800000))) report(a.dev_status, MOE_DEV_NONFINITE_INPUT);

@@ -926,9 +926,10 @@ moe_status moe_grad_plan(int32_t n_tensors, moe_grad_tensor* tensors, int32_t n_
  * the table and the GPU fix: the same bits on every run.  A norm that is not finite in fp32 sets
  * MOE_DEV_NONFINITE_INPUT; the formula is followed (NaN: NaN everywhere in the group, Inf:
  * zeros, and NaN where the gradient was infinite).
- * max_norm > 0 (infinity: norms alone matter).  ws: moe_clip_grads_workspace_size(n_groups)
- * bytes, 8-byte aligned, no state kept in it between calls; calls, and replays of graphs that
- * captured them, that overlap on the GPU must not share it.  Limits: n_groups <= 2^20.      */
+ * max_norm > 0 (infinity: c_g = 1 whatever the norm, which is all that is asked for).  ws:
+ * moe_clip_grads_workspace_size(n_groups) bytes, 8-byte aligned, no state kept in it between
+ * calls; calls, and replays of graphs that captured them, that overlap on the GPU must not share
+ * it.  Limits: n_groups <= 2^20.                                             */
 size_t moe_clip_grads_workspace_size(int32_t n_groups);
 moe_status moe_clip_grads(int32_t n_tensors, const moe_grad_tensor* tensors, int64_t n_chunks,
                           int32_t n_groups, float max_norm, float* norms, void* ws,

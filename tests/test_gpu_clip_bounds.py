@@ -1,4 +1,5 @@
-"""moe_clip_grads at the edges of its arithmetic: the longest chain of fp32 roundings."""
+"""moe_clip_grads at the edges of its arithmetic: the longest chain of fp32 roundings, and a limit
+that is infinite."""
 import math
 
 import pytest
@@ -44,3 +45,31 @@ def test_norm_where_every_rounding_loses(kind):
     want = float(g.double().square().sum().sqrt())
     norm = float(G().GradientClip([g], math.inf, device=DEV).clip())
     assert abs(norm - want) <= want * 8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("kind", [F32, BF])
+@pytest.mark.parametrize("bad", [math.inf, math.nan, None])
+def test_infinite_limit_scales_nothing(bad, kind, in_place):
+    """Norms alone are asked for: also where one is not finite, for an element's sake or because the
+    norm of finite values passes fp32's range, every value stays what it was."""
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    grads = [torch.randn(c, generator=gen, device=DEV).to(kind) for c in (100, 9000, 300)]
+    if bad is None:
+        grads[1].fill_(1e37)  # norm 9.5e38
+    else:
+        grads[1][8500] = bad
+    before = [x.clone() for x in grads]
+    out = None if in_place else [torch.zeros_like(x) for x in grads]
+    clip = G().GradientClip(grads, math.inf, out=out, groups=[0, 1, 2], device=DEV)
+    norms = clip.clip()
+    bits = lambda t: t.view(torch.int32 if kind is F32 else torch.int16)  # noqa: E731
+    for got, want in zip(clip.out, before):
+        if bad is not None and math.isnan(bad):
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
+            keep = ~torch.isnan(want)
+            assert torch.equal(got[keep], want[keep])
+        else:
+            assert torch.equal(bits(got), bits(want))
+    assert torch.isfinite(norms[[0, 2]]).all() and not torch.isfinite(norms[1])
+    assert int(clip.dev_status.item()) == G().MOE_DEV_NONFINITE_INPUT
