@@ -21,8 +21,8 @@ namespace {
 //   32 tokens of one adapter, or of a few runs: mma.sync.  tcgen05's 16x256b loads give the accumulators in its
 //     layout, 16 weight columns by 8 tokens, so the table (16 columns, in registers, transposed
 //     by movmatrix, once a run) is multiplied with u onto the sums themselves, and every token
-//     takes the result of its own run.  u is split into two bf16 numbers a value by all warps
-//     together.
+//     takes the result of its own run.  u is split into bf16 numbers by all warps together: two a
+//     value (16 bits) for bf16 results, which keep eight, three (all 24) for fp32 ones.
 //   256 tokens of one adapter of up to 32 ranks (pairs): the reduction goes on over the ranks, u as
 //     value and remainder against the table twice, both laid down in shared memory by the
 //     epilogue warps while the tile's MMAs run.  (Beside running MMAs the products above take
@@ -48,12 +48,11 @@ constexpr int kWBox = 64 * 64 * 2;
 constexpr int kPiece = 8;  // blocks of 64 to a piece of an fp32 result's reduction
 constexpr int kMaxRank = 128;
 
-// 32 tokens of u: [value, remainder][32][r, padded to 16 and 8 more], so that eight rows of an
+// 32 tokens of u: [value, remainder(s)][32][r, padded to 16 and 8 more], so that eight rows of an
 // ldmatrix lie in other banks.
 __host__ __device__ constexpr int u_pitch(int rp) { return rp * 2 + 16; }
 // 32 tokens of the adapters' part: [32][128 columns and 4 more] fp32.
 constexpr int kPartPitch = 132;
-constexpr int kPieceBytes = 18 * 1024;  // either of them
 
 constexpr int kMoreU = 128 * 128;
 constexpr int kMoreTable = 2 * 32 * 128;
@@ -71,15 +70,21 @@ struct Shape {
   static constexpr int kRedBytes = (S - 1) * kOwn * 512;  // [S - 1][kOwn / 8][8][32] float4
   // (pair) the tile's further reduction: [128 tokens][64] of u, [2][32 ranks][64 columns] of the table
   static constexpr int kMoreBytes = CG == 2 ? kMoreU + kMoreTable : 0;
+  // bf16 numbers a value of u (pairs have bf16 results alone), the bytes of 32 tokens of u or of the
+  // adapters' part, and buffers of them: a cluster that shares a tile has one, and a CTA whose tokens
+  // are 32 at most fills one buffer once.
+  static constexpr int kParts = CG == 2 ? 2 : 3;
+  static constexpr int kPieceBytes = (CG == 2 ? 18 : 26) * 1024;
+  static constexpr int kPieces = S > 1 && kOwn <= 32 ? 1 : 2;
   // full[st], empty[st], tfull[2], tempty[2], group, red, drain, more
   static constexpr int kBars = 2 * kStages + 8;
   static constexpr int kTmem = CG == 2 ? 2 * TN : 4 * TN;  // two buffers, (flat) the sums
   static constexpr int kSmem =
-      1024 + kStages * kStageBytes + kMoreBytes + 2 * kPieceBytes + kRedBytes + kBars * 8 +
+      1024 + kStages * kStageBytes + kMoreBytes + kPieces * kPieceBytes + kRedBytes + kBars * 8 +
       3 * (kOwn + 20) * 4 + 16;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kOwn % 8 == 0 && kTmem <= 512, "shape");
-  static_assert(kPieceBytes >= 2 * 32 * u_pitch(kMaxRank) && kPieceBytes >= 32 * kPartPitch * 4, "pieces");
+  static_assert(kPieceBytes >= kParts * 32 * u_pitch(kMaxRank) && kPieceBytes >= 32 * kPartPitch * 4, "pieces");
 };
 
 constexpr int kFew = -3;      // 32 tokens of up to kFewRuns runs
@@ -148,6 +153,12 @@ __device__ __forceinline__ void expand(const ProjectArgs& a, const int (&id)[4],
   }
 }
 
+// What the rounding of four values to bf16 left of them.
+__device__ __forceinline__ float4 left_of(const float4& f, uint32_t h0, uint32_t h1) {
+  return make_float4(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u),
+                     f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+}
+
 // Stores 16 weight columns from n by 8 G tokens from row (the layout of umma_ld_frag); id: the
 // tokens'.
 template <int G>
@@ -191,7 +202,7 @@ __device__ __forceinline__ void put_frags(const ProjectArgs& a, const float (&c)
 
 // What the epilogue warps share.
 struct Epilogue {
-  uint8_t* piece;   // [2][kPieceBytes]
+  uint8_t* piece;   // [kPieces][kPieceBytes]
   uint8_t* red;
   uint8_t* more;    // kMoreU, then kMoreTable bytes
   // Three of each, tile by tile: the next tile's are made while other warps may still be at the last.
@@ -208,6 +219,8 @@ struct Epilogue {
 template <int TN, int S, int CG, int RB>
 __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s, int warp, int lane) {
   constexpr int kOwn = TN / S, kChunks = (kOwn + 31) / 32, kGroups = kOwn < 32 ? kOwn / 8 : 4;
+  constexpr int kPieceBytes = Shape<TN, S, CG>::kPieceBytes;
+  const bool whole_u = CG == 1 && a.y_fp32;  // u as three numbers
   constexpr int kQuads = 4 * RB;                              // groups of four values of a row of u
   constexpr int kLoads = (8 * kGroups * kQuads + 255) / 256;  // of them a thread
   constexpr int kPitch = u_pitch(16 * RB);
@@ -316,6 +329,16 @@ __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s
 #pragma unroll
         for (int i = 0; i < kGroups; ++i)
           mma_16816(c[i], tab[k][0], tab[k][1], tab[k][2], tab[k][3], u[i][2 * h], u[i][2 * h + 1]);
+      if (whole_u) {  // the third numbers of two groups of eight tokens at once
+        const uint32_t third = at + 64 * kPitch - (lane & 16 ? 24 * kPitch : 0);
+#pragma unroll
+        for (int i = 0; i < kGroups; i += 2) {
+          uint32_t l[4];
+          ldmatrix(l, third + 8 * i * kPitch + k * 32);
+          mma_16816(c[i], tab[k][0], tab[k][1], tab[k][2], tab[k][3], l[0], l[1]);
+          mma_16816(c[i + 1], tab[k][0], tab[k][1], tab[k][2], tab[k][3], l[2], l[3]);
+        }
+      }
     }
   };
 
@@ -365,8 +388,8 @@ __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s
                                              a.u + static_cast<int64_t>(row0 + tok) * a.r + 4 * q)
                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
-          const uint32_t l0 = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
-          const uint32_t l1 = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+          const float4 d = left_of(f, h0, h1);
+          const uint32_t l0 = pack_bf16x2(d.x, d.y), l1 = pack_bf16x2(d.z, d.w);
           // 16-byte chunks of a row of 128: the values' first, then (2 RB on) the remainders'
           uint8_t* row = s.more + tok * 128 + (q & 1) * 8;
           *reinterpret_cast<uint2*>(row + (((q >> 1) ^ (tok & 7)) << 4)) = make_uint2(h0, h1);
@@ -430,12 +453,16 @@ __device__ __forceinline__ void epilogue(const ProjectArgs& a, const Epilogue& s
           const int i = tid + 256 * e;
           const float4 f = ahead[e];
           const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
-          const uint32_t l0 = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
-          const uint32_t l1 = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+          const float4 d = left_of(f, h0, h1);
+          const uint32_t l0 = pack_bf16x2(d.x, d.y), l1 = pack_bf16x2(d.z, d.w);
           if (i < 8 * kGroups * kQuads) {
             uint8_t* dst = piece + i / kQuads * kPitch + i % kQuads * 8;
             *reinterpret_cast<uint2*>(dst) = make_uint2(h0, h1);
             *reinterpret_cast<uint2*>(dst + 32 * kPitch) = make_uint2(l0, l1);
+            if (whole_u) {
+              const float4 q = left_of(d, l0, l1);
+              *reinterpret_cast<uint2*>(dst + 64 * kPitch) = make_uint2(pack_bf16x2(q.x, q.y), pack_bf16x2(q.z, q.w));
+            }
           }
         }
         hold(first_of(ch), n);
@@ -613,8 +640,8 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   uint8_t* stage_base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_more = stage_base + kStages * F::kStageBytes;
-  uint8_t* s_piece = s_more + F::kMoreBytes;  // two
-  uint8_t* s_red = s_piece + 2 * kPieceBytes;
+  uint8_t* s_piece = s_more + F::kMoreBytes;
+  uint8_t* s_red = s_piece + F::kPieces * F::kPieceBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_red + F::kRedBytes);
   int* s_id = reinterpret_cast<int*>(bars + F::kBars);
   int* s_whole = s_id + 3 * kOwn;

@@ -855,11 +855,13 @@ typedef struct {
  *   u[t] = scale[e] * (x[t] a[e]^T)          fp32 [T, r]; zero rows without an adapter
  *   y[t] = round(x[t] w + u[t] b[e])         one rounding, to y_type
  * with x, w [d, n], a [n_adapters, r, d], b [n_adapters, r, n] bf16 and scale fp32
- * [n_adapters].  Products are of bf16 numbers (u enters as fp32, or as the sum of two bf16
- * numbers that holds 16 bits of it), sums fp32.  Rows of no segment are left as they are, in u
- * and in y.  A segment may be empty, and several may name one adapter.  A row's result depends
- * on its own x, w and its own adapter only: a NaN or Inf in one adapter's tables or in one
- * row stays with the rows that use it.
+ * [n_adapters].  Products are of bf16 numbers (u enters with all of fp32's bits where y is
+ * fp32, with 16 or all where y is bf16), sums fp32.  Rows of no segment are left as they are, in u
+ * and in y.  A segment may be empty, and several may name one adapter.  A row's result is made
+ * of its own x, w and its own adapter only: a NaN or Inf in one adapter's tables or in one row
+ * stays with the rows that use it.  Its last bits may differ with the batch that it is in, whose
+ * segments decide the order of sums and the form in which u enters; of the same batch they are the
+ * same on every run.
  * fp32 y [T, E] of w [d, E] are router logits as moe_route takes them.  Where u is infinite (or
  * beyond bf16's range) y is NaN or infinite.
  * Offsets out of order or range set MOE_DEV_BAD_MAP (results unspecified, nothing outside

@@ -90,6 +90,26 @@ def exact_u(T, d, n, r, N):
     return x, w, a, keep, scale, rnd
 
 
+@pytest.mark.parametrize("T,off,ids", [
+    (1, [0, 1], [1]), (40, [0, 40], [2]), (40, [0, 10, 40], [0, 2]),         # whole, few runs
+    (64, list(range(65)), [q % 3 for q in range(64)]),                       # many runs
+    (300, [0, 300], [1]), (300, [0, 100, 110, 300], [1, -1, 2]),
+    (300, list(range(40)) + [300], [q % 3 for q in range(40)])])
+@pytest.mark.parametrize("r", [8, 24, 40, 128])
+def test_all_of_u_enters_fp32_results(T, off, ids, r):
+    """y is one product u b: three parts of u, each added exactly or cut by one last bit."""
+    d, n = 72, 136
+    x, w, a, b, scale, _ = exact_u(T, d, n, r, 3)
+    u, y, _ = project((x, w, a, b, scale), off, ids, F32)
+    for p, q, e in ref.segments(off, ids, T):
+        if e < 0:
+            assert not y[p:q].any()
+            continue
+        assert (u[p:q] == scale[e]).all()
+        want = scale[e].double() * b[e, 3].double()
+        assert ((y[p:q].double() - want).abs() <= 4 * 2.0 ** -23 * want.abs()).all()
+
+
 @pytest.mark.parametrize("r", [8, 24, 64, 128])
 def test_all_of_u_and_v_enters_the_gradients(r):
     """One token: db = u^T dy and da = v^T x are single products."""
