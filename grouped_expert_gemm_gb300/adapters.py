@@ -9,7 +9,8 @@
 
 As the layers: each object owns its buffers, a call only enqueues kernels on the given stream
 (default: the current one) and can be captured into a CUDA graph; arguments are checked with
-ValueError, and the object's device must be the current one.
+ValueError, and the object's device must be the current one.  Calls of one object share its
+buffers: they follow one another on the GPU.  An object is made outside of captures.
 """
 from __future__ import annotations
 
@@ -19,6 +20,11 @@ import torch
 
 from . import abi
 from .block import _KIND, _device, check_tensor
+
+
+def _not_capturing(device):
+    if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        raise ValueError("the object must be made before a capture begins")
 
 
 def _check_rows(name, t, shape, dtype, device):
@@ -78,8 +84,7 @@ class AdapterProjection:
                  scale: torch.Tensor, y_dtype=torch.bfloat16, device="cuda",
                  gradients: bool = True):
         self.device = _device(device)
-        if self.device.type == "cuda" and torch.cuda.is_current_stream_capturing():
-            raise ValueError("the object's buffers must be made before a capture begins")
+        _not_capturing(self.device)
         if y_dtype not in _KIND:
             raise ValueError("y_dtype must be bfloat16 or float32")
         for name, t, dims in (("weight", weight, 2), ("a", a, 3), ("b", b, 3)):
@@ -179,6 +184,7 @@ class GradientClip:
                  n_groups: Optional[int] = None, norms: Optional[torch.Tensor] = None,
                  device="cuda"):
         self.device = _device(device)
+        _not_capturing(self.device)
         self.grads = list(grads)
         self.out = self.grads if out is None else list(out)
         groups = [0] * len(self.grads) if groups is None else [int(g) for g in groups]

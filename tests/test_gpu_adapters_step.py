@@ -155,3 +155,24 @@ def test_rows_and_results_side_by_side_in_one_buffer():
     assert (wide[:, D:D + 8] == MARK).all()
     wide[:, D + 8:] = dy
     assert all(torch.equal(p, q) for p, q in zip(m.backward(wide[:, D + 8:]), grads))
+
+
+def test_objects_are_refused_inside_a_capture():
+    """(and the capture goes on)"""
+    g = G()
+    x, w, a, b, scale, dy = step(19)
+    m = g.AdapterProjection(T, w, a, b, scale, device=DEV)
+    ids, off = i32(IDS), i32(OFF)
+    want = m.forward(x, ids, off).clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="capture"):
+            g.AdapterProjection(T, w, a, b, scale, device=DEV)
+        with pytest.raises(ValueError, match="capture"):
+            g.GradientClip([scale], 1.0, device=DEV)
+        m.forward(x, ids, off)
+    m.y.fill_(MARK)
+    graph.replay()
+    live = slice(OFF[0], OFF[-1])
+    assert torch.equal(m.y[live], want[live]) and (m.y[:OFF[0]] == MARK).all()
