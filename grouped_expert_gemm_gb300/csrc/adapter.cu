@@ -4,13 +4,15 @@
 //   v = s (dy B^T)             dx = round(dy W^T + v A)
 //   dA = sum_t v_t^T x_t       dB = sum_t u_t^T dy_t
 // with an adapter (A [r, d], B [r, n], s) or none for every segment of token rows.  u and v
-// are fp32, so an adapter's part of y is as exact as the projection itself.
+// are fp32; they enter the products of fp32 results with all their bits, those of bf16 results with 16.
 //
-// Three kernels serve both directions (A and B, d and n, x and dy change places):
-//   shrink   u: rows against the r rows of one table, reduction over the long side.
-//   project  y: the projection on the tensor cores, the adapter's part added before the one
-//            rounding.
-//   grads    dA, dB: the sums over an adapter's tokens.
+// Four kernels serve both directions (A and B, d and n, x and dy change places):
+//   shrink       u of segments of few rows against the r rows of one table, reduction over the
+//                long side;
+//   shrink_long  u of segments of many rows (adapter_shrink.cu);
+//   project      y: the projection on the tensor cores, the adapter's part added before the one
+//                rounding (adapter_project.cuh);
+//   grads        dA, dB: the sums over an adapter's tokens (adapter_grads.cu).
 #include "adapter.cuh"
 
 namespace moe {

@@ -39,7 +39,7 @@ namespace {
 //          CTA a part of the reduction; the CTA of rank c finishes its S-th of the tokens and
 //          gets the others' sums through distributed shared memory.
 // fp32 results of long reductions are summed in pieces of kPiece: the tensor cores' own fp32
-// sums lose 2^-26 a step (7168: 8e-6 of the result, in pieces of 1024 1e-6).
+// sums lose 2^-26 a step (7168: 8e-6 of the result, in these pieces 4.6e-7).
 // The weight, x and the tables are read before shrink has ended; u is waited for.
 
 constexpr int kThreads = 320;
