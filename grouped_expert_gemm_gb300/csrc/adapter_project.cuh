@@ -648,6 +648,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   uint32_t* s_starts = reinterpret_cast<uint32_t*>(s_whole + 3 * 8);
   volatile int* abort_flag = s_whole + 6 * 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_whole + 6 * 8) + 1;
+  uint32_t* ring_end = tmem_slot + 1;  // where the producer stopped, and whether MMAs were issued
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kCluster = S * CG;
   const int rank = kCluster > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -737,18 +738,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
       }
-      if (!ok) {  // copies in flight land before the shared memory is given up
-        if (leader) {
-          for (int i = 0; i < kStages; ++i) {
-            if (--s < 0) { s = kStages - 1; ph ^= 1u; }
-            wait_drain(full_bar(s), ph);
-          }
-        } else {  // they are counted on the leader's barriers: a fixed window
-          const uint64_t t0 = global_timer_ns();
-          while (global_timer_ns() - t0 < 2000000ull) {
-          }
-        }
-      }
+      ring_end[0] = static_cast<uint32_t>(s) << 1 | ph;
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
@@ -804,11 +794,7 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
           if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
         }
       }
-      if (!ok && issued) {
-        if constexpr (CG == 2) umma_commit_pair(drain_bar, 0x1);
-        else umma_commit(drain_bar);
-        wait_drain(drain_bar, 0);
-      }
+      ring_end[1] = issued;
     }
   } else {
     const Epilogue e{s_piece, s_red, s_more, s_id, s_whole, s_starts, abort_flag, tfull_bar(0), tempty_bar(0), group_bar,
@@ -823,6 +809,30 @@ project_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
   __syncwarp();
   umma_fence_before();
   __syncthreads();
+  // No role gives up behind this barrier.  Where one has, whichever it was, MMAs and copies in flight end before
+  // the memory that they use is given up.
+  if (*abort_flag) {
+    if (threadIdx.x == 32 && leader && ring_end[1]) {
+      if constexpr (CG == 2) umma_commit_pair(drain_bar, 0x1);
+      else umma_commit(drain_bar);
+      wait_drain(drain_bar, 0);
+    }
+    if (threadIdx.x == 0) {
+      if (leader) {
+        int s = static_cast<int>(ring_end[0] >> 1);
+        uint32_t ph = ring_end[0] & 1u;
+        for (int i = 0; i < kStages; ++i) {
+          if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+          wait_drain(full_bar(s), ph);
+        }
+      } else {  // they are counted on the leader's barriers: a fixed window
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  }
   if constexpr (kCluster > 1) {
     cluster_sync();  // no CTA leaves while a partner may still reach it
     // (after a wait that gave up: nor before the partners' sums that may be on their way)

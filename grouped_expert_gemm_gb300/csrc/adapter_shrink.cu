@@ -46,6 +46,7 @@ shrink_long_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage_base + kStages * F::kStageBytes);
   volatile int* abort_flag = reinterpret_cast<int*>(bars + F::kBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + F::kBars) + 1;
+  uint32_t* ring_end = tmem_slot + 1;  // where the producer stopped, and whether MMAs were issued
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int steps = (a.K + 63) / 64;
@@ -100,12 +101,7 @@ shrink_long_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         tma_load_3d(st + kXBytes, &map_t, full_bar(s), k * 64, 0, p.adapter);
         if (++s == kStages) { s = 0; ph ^= 1u; }
       }
-      if (!ok) {  // copies in flight land before the shared memory is given up
-        for (int i = 0; i < kStages; ++i) {
-          if (--s < 0) { s = kStages - 1; ph ^= 1u; }
-          wait_drain(full_bar(s), ph);
-        }
-      }
+      ring_end[0] = static_cast<uint32_t>(s) << 1 | ph;
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -132,10 +128,7 @@ shrink_long_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
         umma_commit(tfull_bar(buf));
         if (++buf == 2) { buf = 0; acc_ph ^= 1u; }
       }
-      if (!ok && issued) {
-        umma_commit(drain_bar);
-        wait_drain(drain_bar, 0);
-      }
+      ring_end[1] = issued;
     }
   } else {
     const int quad = warp & 3;
@@ -195,6 +188,23 @@ shrink_long_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   __syncwarp();
   umma_fence_before();
   __syncthreads();
+  // No role gives up behind this barrier.  Where one has, whichever it was, MMAs and copies in flight end before
+  // the memory that they use is given up.
+  if (*abort_flag) {
+    if (threadIdx.x == 32 && ring_end[1]) {
+      umma_commit(drain_bar);
+      wait_drain(drain_bar, 0);
+    }
+    if (threadIdx.x == 0) {
+      int s = static_cast<int>(ring_end[0] >> 1);
+      uint32_t ph = ring_end[0] & 1u;
+      for (int i = 0; i < kStages; ++i) {
+        if (--s < 0) { s = kStages - 1; ph ^= 1u; }
+        wait_drain(full_bar(s), ph);
+      }
+    }
+    __syncwarp();
+  }
   umma_fence_after();
   if (warp == 1) {
     __syncwarp();
