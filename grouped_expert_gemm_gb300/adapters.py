@@ -14,6 +14,7 @@ buffers: they follow one another on the GPU.  An object is made outside of captu
 """
 from __future__ import annotations
 
+import math
 from typing import Optional, Sequence
 
 import torch
@@ -48,11 +49,11 @@ def _overlap(p, q) -> bool:
     if at[0] + size[0] <= at[1] or at[1] + size[1] <= at[0]:
         return False
     if p.dim() == q.dim() == 2 and min(p.shape[0], q.shape[0]) > 1:
-        row = p.stride(0) * p.element_size()
-        if row == q.stride(0) * q.element_size():
-            ahead = (at[1] - at[0]) % row  # of q's rows to p's, inside a row of the buffer
-            return ahead < p.shape[1] * p.element_size() or \
-                ahead + q.shape[1] * q.element_size() > row
+        # every row of either starts at its place in a row of this many bytes
+        row = math.gcd(p.stride(0) * p.element_size(), q.stride(0) * q.element_size())
+        ahead = (at[1] - at[0]) % row
+        return ahead < p.shape[1] * p.element_size() or \
+            ahead + q.shape[1] * q.element_size() > row
     return True
 
 

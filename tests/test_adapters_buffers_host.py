@@ -44,6 +44,8 @@ def test_overlap_of_rows():
             (wide[0:1, :16], wide[0:1, 16:], False), (wide[0:1], wide[0:1, 40:], True),
             (wide[:, 1:47].view(torch.int16), wide[:, 46:], True), (wide[:0], wide, False),
             (wide[:, :8], torch.zeros(6, 48, dtype=BF), False),
+            (wide[::2, :16], wide[:3, 16:], False), (wide[::2, :16], wide[1::2, :16], False),
+            (wide[::2, :16], wide[:3, 8:], True), (wide[::3, :16], wide[:4:2, 16:32], False),
             # a row's slice that goes on into the next row of the other
             (wide[:, 40:], wide.view(-1)[44:188].view(3, 48), True)):
         assert _overlap(p, q) == _overlap(q, p) == want
